@@ -14,12 +14,14 @@ Tensor layouts (see ``include/pd.h``):
     qo_indptr       int32 [B+1]; kv_len int32 [B]; page_indptr int32 [B+1];
     page_indices    int32 [nnz]
     lse             fp32 [total_qo][Hq], natural log
+    positions       int32 [total_qo]; slot_map int64 [total_qo] (page * P + slot, -1: padding)
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -31,11 +33,12 @@ PD_F32, PD_BF16 = 0, 1
 PD_LAYOUT_HND, PD_LAYOUT_NHD = 0, 1
 PD_KIND_DECODE, PD_KIND_PREFILL, PD_KIND_MIXED, PD_KIND_MIXED_SPLIT = 0, 1, 2, 3
 DEVICE_STATUS = {0: "ok", 1: "bad indptr", 2: "bad length", 3: "bad page table", 4: "not a decode",
-                 5: "timeout", 6: "bad offset"}
+                 5: "timeout", 6: "bad offset", 7: "no free pages", 8: "bad row"}
 
 # Every symbol include/pd.h declares.
 EXPORTS = ("pd_attn_workspace_size", "pd_attn_decode", "pd_attn_decode_static", "pd_attn_prefill",
-           "pd_attn_mixed", "pd_attn_mixed_split", "pd_mla_workspace_size", "pd_mla_decode",
+           "pd_attn_mixed", "pd_attn_mixed_split", "pd_attn_chunk_workspace_size", "pd_attn_chunk",
+           "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_mla_workspace_size", "pd_mla_decode",
            "pd_kv_append", "pd_kv_pack", "pd_kv_unpack", "pd_kv_pack_heads", "pd_kv_unpack_heads",
            "pd_kv_pack_layers", "pd_counter_alloc", "pd_counter_free", "pd_layer_signal",
            "pd_messenger_start_pack", "pd_messenger_join",
@@ -76,6 +79,30 @@ class MlaDesc(ctypes.Structure):
                 ("sm_scale", ctypes.c_float)]
 
 
+class TablesDesc(ctypes.Structure):
+    _fields_ = [("batch_size", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("table_rows", ctypes.c_int32), ("table_cols", ctypes.c_int32), ("total_qo", ctypes.c_int32),
+                ("max_page_indices", ctypes.c_int32), ("free_capacity", ctypes.c_int32)]
+
+
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("num_qo_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
+
+
+class BatchTables(NamedTuple):
+    """What pd_batch_tables writes: the batch of the attention calls, and each new token's place."""
+    qo_indptr: torch.Tensor     # int32 [B+1]
+    kv_len: torch.Tensor        # int32 [B], -1 for a request that could not be served
+    page_indptr: torch.Tensor   # int32 [B+1]
+    page_indices: torch.Tensor  # int32 [max_page_indices]
+    positions: torch.Tensor     # int32 [total_qo]
+    slot_map: torch.Tensor      # int64 [total_qo], -1 for padding rows
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -97,6 +124,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.pd_attn_mixed_split.restype = ctypes.c_int
             lib.pd_attn_workspace_size.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(Batch), I32]
             lib.pd_attn_workspace_size.restype = S
+            lib.pd_attn_chunk_workspace_size.argtypes = attn[:2]
+            lib.pd_attn_chunk_workspace_size.restype = S
+            lib.pd_attn_chunk.argtypes = attn[:2] + [I32, ctypes.c_int64] + attn[2:]
+            lib.pd_batch_tables.argtypes = [ctypes.POINTER(TablesDesc)] + [P] * 15
+            lib.pd_slot_map.argtypes = [ctypes.POINTER(Batch), I32, P, P, P, P]
+            lib.pd_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + [P] * 9
+            lib.pd_qk_norm_rope_append.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + [P] * 13
+            for name in ("pd_attn_chunk", "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope",
+                         "pd_qk_norm_rope_append"):
+                getattr(lib, name).restype = ctypes.c_int
             lib.pd_mla_workspace_size.argtypes = [ctypes.POINTER(MlaDesc), ctypes.POINTER(Batch)]
             lib.pd_mla_workspace_size.restype = S
             lib.pd_mla_decode.argtypes = [ctypes.POINTER(MlaDesc), ctypes.POINTER(Batch), P, P, P, P, P, S, P, P]
@@ -298,6 +335,251 @@ def pd_attn_mixed_split(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo
                                  _ptr(dev_status), _stream(stream, q.get_device()))
     _check(rc, "pd_attn_mixed_split")
     return o, lse
+
+
+def _device_of(**tensors):
+    """The CUDA device that all the given tensors (None: absent) are on, as an index."""
+    dev = -1
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise PdError(f"{name} must be a CUDA tensor")
+        if dev >= 0 and d != dev:
+            raise PdError(f"{name} is on device {d}, the arguments before it on device {dev}")
+        dev = d
+    return dev
+
+
+def _launch(device: int, what: str, fn, *args) -> int:
+    """Calls fn(*args) with `device` current (kernels are launched on the current device)."""
+    if device == torch.cuda.current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != PD_OK and rc != PD_ERR_WORKSPACE:
+        _check(rc, what)
+    return rc
+
+
+def _vector(t, name, dtype, n=None):
+    """A contiguous tensor of `dtype`, with at least n entries."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise PdError(f"{name} must be a contiguous {dtype} tensor")
+    if n is not None and t.numel() < n:
+        raise PdError(f"{name} has {t.numel()} entries, {n} are needed")
+
+
+def _rows(t, name, heads=None, dim=None, dtype=None):
+    """Token stride of a [tokens][heads][dim] tensor whose heads lie one after another."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise PdError(f"{name} must be [tokens][heads][dim] with contiguous heads")
+    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise PdError(f"{name} has the shape {tuple(t.shape)}, not [tokens][{heads}][{dim}]")
+    if dtype is not None and t.dtype != dtype:
+        raise PdError(f"{name} is {t.dtype}, not {dtype}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, *, causal=True, window_left=-1,
+                  sm_scale=None, max_qo_len=None, max_kv_len=None, o=None, lse=True, o_dtype=None, workspace=None,
+                  dev_status=None, stream=None, layout="HND"):
+    """Attention of each request's new tokens (one or many) over its pages, causal by default, with
+    an optional sliding window of window_left keys before each token. q [total_qo][Hq][D] may be a
+    slice of a wider row. Without max_qo_len / max_kv_len they are read from the device (a
+    synchronisation). Returns (o, lse)."""
+    lib = load_library()
+    device = _device_of(q=q, k_pool=k_pool, v_pool=v_pool, kv_len=kv_len, page_indptr=page_indptr,
+                        page_indices=page_indices, qo_indptr=qo_indptr, o=o,
+                        lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace, dev_status=dev_status)
+    if not k_pool.is_contiguous() or not v_pool.is_contiguous() or k_pool.shape != v_pool.shape or k_pool.dim() != 4:
+        raise PdError("k_pool and v_pool must be contiguous pools of the same shape")
+    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise PdError("q and the pools differ in dtype")
+    stride = _rows(q, "q", dim=k_pool.shape[3])
+    B = kv_len.numel()
+    _vector(qo_indptr, "qo_indptr", torch.int32, B + 1)
+    _vector(page_indptr, "page_indptr", torch.int32, B + 1)
+    if max_qo_len is None:
+        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if B else 0
+    shape = q.shape
+    if o is None:
+        o = torch.empty(shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
+    elif o.shape != shape or not o.is_contiguous():
+        raise PdError("o must be contiguous and shaped like q")
+    if lse is True:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    if lse is not None:
+        _vector(lse, "lse", torch.float32, shape[0] * shape[1])
+    desc = make_attn_desc(q, k_pool, causal=causal, sm_scale=sm_scale, o_dtype=o.dtype, layout=layout)
+    batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr, total_qo=shape[0],
+                       max_qo_len=max_qo_len, max_kv_len=max_kv_len)
+    dref, bref = ctypes.byref(desc), ctypes.byref(batch)
+    args = (dref, bref, int(window_left) if window_left is not None else -1, stride, q.data_ptr(), k_pool.data_ptr(),
+            v_pool.data_ptr(), o.data_ptr(), _ptr(lse))
+    tail = (_ptr(dev_status), _stream(stream, device))
+    rc = PD_ERR_WORKSPACE
+    if workspace is not None:
+        rc = _launch(device, "pd_attn_chunk", lib.pd_attn_chunk, *args, workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size(), *tail)
+    if rc == PD_ERR_WORKSPACE:  # none, or one too small for this batch
+        with torch.cuda.device(device):
+            size = int(lib.pd_attn_chunk_workspace_size(dref, bref))
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=q.device)
+        rc = _launch(device, "pd_attn_chunk", lib.pd_attn_chunk, *args, workspace.data_ptr(), workspace.numel(), *tail)
+    _check(rc, "pd_attn_chunk")
+    return o, lse
+
+
+def pd_batch_tables(new_len, cached_len, block_table, *, page_size, num_pages, total_qo, max_page_indices, rows=None,
+                    free_pages=None, free_count=None, free_count_out=None, out=None, dev_status=None, stream=None):
+    """Page table, positions and slots of a step from the requests' lengths: request r has
+    cached_len[r] tokens in row rows[r] (r without `rows`) of block_table and brings new_len[r];
+    the pages it lacks are taken from the end of free_pages and entered there. free_count (int32,
+    one entry) counts the free pages; free_count_out gets what is left (free_count itself: in
+    place). `out` may hold the six result tensors. Returns BatchTables."""
+    lib = load_library()
+    B = new_len.numel()
+    device = _device_of(new_len=new_len, cached_len=cached_len, block_table=block_table, rows=rows,
+                        free_pages=free_pages, free_count=free_count, free_count_out=free_count_out,
+                        dev_status=dev_status)
+    i32 = torch.int32
+    _vector(new_len, "new_len", i32)
+    _vector(cached_len, "cached_len", i32, B)
+    if block_table.dim() != 2:
+        raise PdError("block_table must be [rows][pages]")
+    _vector(block_table, "block_table", i32)
+    if rows is not None:
+        _vector(rows, "rows", i32, B)
+    if free_pages is not None:
+        if free_count is None:
+            raise PdError("free_pages needs free_count")
+        _vector(free_pages, "free_pages", i32)
+        _vector(free_count, "free_count", i32, 1)
+        if free_count_out is None:
+            free_count_out = torch.empty_like(free_count)
+        _vector(free_count_out, "free_count_out", i32, 1)
+    total_qo, nnz = int(total_qo), int(max_page_indices)
+    if out is None:
+        sizes = ((B + 1, i32), (B, i32), (B + 1, i32), (nnz, i32), (total_qo, i32), (total_qo, torch.int64))
+        out = tuple(torch.empty(n, dtype=t, device=new_len.device) for n, t in sizes)
+    out = BatchTables(*out)
+    _device_of(new_len=new_len, **out._asdict())
+    for name, n in (("qo_indptr", B + 1), ("kv_len", B), ("page_indptr", B + 1), ("page_indices", nnz),
+                    ("positions", total_qo)):
+        _vector(getattr(out, name), name, i32, n)
+    _vector(out.slot_map, "slot_map", torch.int64, total_qo)
+    desc = TablesDesc(B, int(page_size), int(num_pages), block_table.shape[0], block_table.shape[1], total_qo, nnz,
+                      free_pages.numel() if free_pages is not None else 0)
+    _launch(device, "pd_batch_tables", lib.pd_batch_tables, ctypes.byref(desc), _ptr(rows), cached_len.data_ptr(),
+            new_len.data_ptr(), block_table.data_ptr(), _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
+            *(t.data_ptr() for t in out), _ptr(dev_status), _stream(stream, device))
+    return out
+
+
+def pd_slot_map(qo_indptr, kv_len, page_indptr, page_indices, *, page_size, num_pages, total_qo, max_kv_len=None,
+                positions=None, slot_map=None, dev_status=None, stream=None):
+    """Position and slot of every new token of a batch whose page table is there: the rows
+    qo_indptr[r] .. qo_indptr[r+1] are the last positions of kv_len[r]; rows past the last request's
+    get slot -1. Returns (positions int32, slot_map int64)."""
+    lib = load_library()
+    device = _device_of(qo_indptr=qo_indptr, kv_len=kv_len, page_indptr=page_indptr, page_indices=page_indices,
+                        positions=positions, slot_map=slot_map, dev_status=dev_status)
+    B, total_qo = kv_len.numel(), int(total_qo)
+    _vector(qo_indptr, "qo_indptr", torch.int32, B + 1)
+    _vector(page_indptr, "page_indptr", torch.int32, B + 1)
+    if positions is None:
+        positions = torch.empty(total_qo, dtype=torch.int32, device=kv_len.device)
+    if slot_map is None:
+        slot_map = torch.empty(total_qo, dtype=torch.int64, device=kv_len.device)
+    _vector(positions, "positions", torch.int32, total_qo)
+    _vector(slot_map, "slot_map", torch.int64, total_qo)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, qo_indptr=qo_indptr, total_qo=total_qo,
+                       max_kv_len=max_kv_len)
+    _launch(device, "pd_slot_map", lib.pd_slot_map, ctypes.byref(batch), int(page_size), positions.data_ptr(),
+            slot_map.data_ptr(), _ptr(dev_status), _stream(stream, device))
+    return positions, slot_map
+
+
+def _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
+    """Checks what both forms of the norm and rotation share; returns the descriptor and the token count."""
+    tokens, hq, dim = q.shape
+    dt = q.dtype
+    qs, ks = _rows(q, "q"), _rows(k, "k", dim=dim, dtype=dt)
+    if k.shape[0] != tokens:
+        raise PdError("q and k differ in tokens")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vector(w, name, dt, dim)
+    rope = 0
+    if inv_freq is not None:
+        _vector(inv_freq, "inv_freq", torch.float32)
+        rope = 2 * inv_freq.numel()
+        if positions is None:
+            raise PdError("a rotation needs positions")
+        _vector(positions, "positions", torch.int32, tokens)
+    return NormRopeDesc(hq, k.shape[1], dim, rope, int(bool(interleaved)), _dtype_code(dt), 0, 0, 0, float(eps), qs,
+                        ks, 0, 0, 0), tokens
+
+
+def pd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, interleaved=False, q_out=None,
+                    k_out=None, stream=None):
+    """Per-head RMS norm (None as weight: no norm) and position rotation (inv_freq None: none; its
+    2 * numel first values of each head, pairs of halves or, interleaved, neighbours) of q
+    [T][Hq][D] and k [T][Hkv][D], which may be slices of a wider row. q_out / k_out may be q / k
+    themselves. Returns (q_out, k_out)."""
+    lib = load_library()
+    device = _device_of(q=q, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
+                        q_out=q_out, k_out=k_out)
+    desc, tokens = _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t.shape != like.shape:
+            raise PdError(f"{name} has the shape {tuple(t.shape)}, not {tuple(like.shape)}")
+    desc.q_out_stride = _rows(q_out, "q_out", dtype=q.dtype)
+    desc.k_out_stride = _rows(k_out, "k_out", dtype=q.dtype)
+    _launch(device, "pd_qk_norm_rope", lib.pd_qk_norm_rope, ctypes.byref(desc), tokens, q.data_ptr(), k.data_ptr(),
+            _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(),
+            _stream(stream, device))
+    return q_out, k_out
+
+
+def pd_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, slot_map, k_pool, v_pool, *, eps=1e-6,
+                           interleaved=False, q_out=None, dev_status=None, stream=None, layout="HND"):
+    """pd_qk_norm_rope whose k, and v as it is, go straight into their slots of the pools (slot_map
+    int64 [T], from pd_batch_tables or pd_slot_map; rows with a negative slot are left alone).
+    Returns q_out."""
+    lib = load_library()
+    device = _device_of(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
+                        slot_map=slot_map, k_pool=k_pool, v_pool=v_pool, q_out=q_out, dev_status=dev_status)
+    desc, tokens = _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    if v.shape != k.shape:
+        raise PdError("k and v differ in shape")
+    desc.v_stride = _rows(v, "v", dtype=q.dtype)
+    _vector(slot_map, "slot_map", torch.int64, tokens)
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or not k_pool.is_contiguous() or not v_pool.is_contiguous():
+        raise PdError("k_pool and v_pool must be contiguous pools of the same shape")
+    num_pages, hkv, page, dim = _pool_dims(k_pool, layout)
+    if (hkv, dim) != (k.shape[1], k.shape[2]) or k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise PdError("the pools' heads, head_dim or dtype are not those of k")
+    desc.page_size, desc.num_pages, desc.layout = page, num_pages, _layout_code(layout)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise PdError(f"q_out has the shape {tuple(q_out.shape)}, not {tuple(q.shape)}")
+    desc.q_out_stride = _rows(q_out, "q_out", dtype=q.dtype)
+    _launch(device, "pd_qk_norm_rope_append", lib.pd_qk_norm_rope_append, ctypes.byref(desc), tokens, q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
+            slot_map.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_status),
+            _stream(stream, device))
+    return q_out
 
 
 def pd_mla_decode(q, kv_pool, kv_len, page_indptr, page_indices, *, kv_lora_rank=512, sm_scale=None,

@@ -187,6 +187,8 @@ const char* pd_device_status_string(int32_t code) {
     case PD_DEV_NOT_DECODE: return "decode request with qo_len != 1";
     case PD_DEV_TIMEOUT: return "bounded wait timed out inside a kernel";
     case PD_DEV_BAD_OFFSET: return "pack/unpack block misaligned or outside the packed buffer";
+    case PD_DEV_NO_PAGES: return "not enough free pages for a request's new tokens";
+    case PD_DEV_BAD_ROW: return "block-table row out of range or listed twice";
     default: return "unknown device status";
   }
 }
@@ -485,6 +487,252 @@ int pd_kv_unpack(const pd_kv_desc* desc, const pd_batch* batch, const void* src,
   if (desc == nullptr) return PD_ERR_INVALID_ARG;
   return pd_kv_unpack_heads(desc, batch, 0, desc->num_kv_heads, src, src_bytes, src_offsets, k_pool, v_pool,
                             dev_status, stream);
+}
+
+namespace {
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + bn && y < x + an;
+}
+
+}  // namespace
+
+int pd_batch_tables(const pd_tables_desc* d, const int32_t* rows, const int32_t* cached_len, const int32_t* new_len,
+                    int32_t* block_table, const int32_t* free_pages, const int32_t* free_count,
+                    int32_t* free_count_out, int32_t* qo_indptr, int32_t* kv_len, int32_t* page_indptr,
+                    int32_t* page_indices, int32_t* positions, int64_t* slot_map, int32_t* dev_status,
+                    void* stream) {
+  if (d == nullptr) return PD_ERR_INVALID_ARG;
+  if (d->batch_size < 0 || d->page_size <= 0 || d->num_pages <= 0 || d->table_rows <= 0 || d->table_cols <= 0 ||
+      d->total_qo < 0 || d->max_page_indices < 0 || d->free_capacity < 0)
+    return PD_ERR_INVALID_ARG;
+  if (d->batch_size > kTablesMaxBatch) return PD_ERR_UNSUPPORTED;
+  if (rows == nullptr && d->batch_size > d->table_rows) return PD_ERR_INVALID_ARG;
+  if (qo_indptr == nullptr || page_indptr == nullptr) return PD_ERR_INVALID_ARG;
+  if (d->batch_size > 0 &&
+      (cached_len == nullptr || new_len == nullptr || block_table == nullptr || kv_len == nullptr))
+    return PD_ERR_INVALID_ARG;
+  if (d->max_page_indices > 0 && page_indices == nullptr) return PD_ERR_INVALID_ARG;
+  if (d->total_qo > 0 && (positions == nullptr || slot_map == nullptr)) return PD_ERR_INVALID_ARG;
+  if (free_pages != nullptr && (free_count == nullptr || free_count_out == nullptr)) return PD_ERR_INVALID_ARG;
+  // CTAs read the inputs while others write the results: no result may lie on an input or on another result.
+  // The one exception, the free count in place, is a launch of its own.
+  const size_t b4 = 4 * (size_t)d->batch_size, t = (size_t)d->total_qo;
+  const struct { const void* p; size_t n; bool out; } bufs[] = {
+      {rows, b4, false}, {cached_len, b4, false}, {new_len, b4, false},
+      {free_pages, 4 * (size_t)d->free_capacity, false},
+      {free_count_out == free_count ? nullptr : free_count, 4, false},
+      {free_pages != nullptr ? free_count_out : nullptr, 4, true},
+      {block_table, 4 * (size_t)d->table_rows * (size_t)d->table_cols, true},
+      {qo_indptr, b4 + 4, true}, {kv_len, b4, true}, {page_indptr, b4 + 4, true},
+      {page_indices, 4 * (size_t)d->max_page_indices, true}, {positions, 4 * t, true}, {slot_map, 8 * t, true}};
+  const int nb = sizeof(bufs) / sizeof(bufs[0]);
+  for (int i = 0; i < nb; ++i) {
+    if (reinterpret_cast<uintptr_t>(bufs[i].p) % (bufs[i].p == slot_map ? 8 : 4) != 0) return PD_ERR_INVALID_ARG;
+    for (int j = i + 1; j < nb; ++j)
+      if ((bufs[i].out || bufs[j].out) && bufs[i].n > 0 && bufs[j].n > 0 &&
+          overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
+        return PD_ERR_INVALID_ARG;
+  }
+  TablesParams p{};
+  p.batch = d->batch_size;
+  p.page_size = d->page_size;
+  p.num_pages = d->num_pages;
+  p.table_rows = d->table_rows;
+  p.table_cols = d->table_cols;
+  p.total_qo = d->total_qo;
+  p.max_page_indices = d->max_page_indices;
+  p.free_capacity = d->free_capacity;
+  p.rows = rows;
+  p.cached_len = cached_len;
+  p.new_len = new_len;
+  p.block_table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.free_count_out = free_count_out;
+  p.qo_indptr = qo_indptr;
+  p.kv_len = kv_len;
+  p.page_indptr = page_indptr;
+  p.page_indices = page_indices;
+  p.positions = positions;
+  p.slot_map = slot_map;
+  p.status = dev_status;
+  return launch_batch_tables(p, static_cast<cudaStream_t>(stream));
+}
+
+int pd_slot_map(const pd_batch* b, int32_t page_size, int32_t* positions, int64_t* slot_map, int32_t* dev_status,
+                void* stream) {
+  if (b == nullptr || page_size <= 0 || b->batch_size < 0 || b->total_qo < 0 || b->max_kv_len < 0)
+    return PD_ERR_INVALID_ARG;
+  if (b->total_qo == 0) return PD_OK;
+  if (positions == nullptr || slot_map == nullptr || reinterpret_cast<uintptr_t>(slot_map) % 8 != 0)
+    return PD_ERR_INVALID_ARG;
+  if (b->batch_size > 0 && (b->qo_indptr == nullptr || b->kv_len == nullptr || b->page_indptr == nullptr ||
+                            b->page_indices == nullptr || b->num_pages <= 0))
+    return PD_ERR_INVALID_ARG;
+  SlotMapParams p{};
+  p.batch = b->batch_size;
+  p.page_size = page_size;
+  p.num_pages = b->num_pages;
+  p.total_qo = b->total_qo;
+  p.max_kv_len = b->max_kv_len;
+  p.qo_indptr = b->qo_indptr;
+  p.kv_len = b->kv_len;
+  p.page_indptr = b->page_indptr;
+  p.page_indices = b->page_indices;
+  p.positions = positions;
+  p.slot_map = slot_map;
+  p.status = dev_status;
+  return launch_slot_map(p, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// Checks and launches either form of the norm and rotation; with a slot map, k and v go to pools.
+int run_norm_rope(const pd_norm_rope_desc* d, int32_t num_tokens, const void* q, const void* k, const void* v,
+                  const void* q_weight, const void* k_weight, const float* inv_freq, const int32_t* positions,
+                  const int64_t* slot_map, void* q_out, void* k_out, void* v_out, bool paged, int32_t* dev_status,
+                  void* stream) {
+  if (d == nullptr || num_tokens < 0) return PD_ERR_INVALID_ARG;
+  const int es = elem_size(d->dtype);
+  if (es == 0 || d->num_qo_heads < 0 || d->num_kv_heads < 0 || d->num_qo_heads + (int64_t)d->num_kv_heads == 0 ||
+      d->head_dim <= 0)
+    return PD_ERR_INVALID_ARG;
+  if (d->rope_dim < 0 || d->rope_dim > d->head_dim || d->rope_dim % 2 != 0) return PD_ERR_INVALID_ARG;
+  if (!isfinite(d->eps) || d->eps < 0.f) return PD_ERR_INVALID_ARG;
+  if (paged && (d->layout != PD_LAYOUT_HND && d->layout != PD_LAYOUT_NHD)) return PD_ERR_INVALID_ARG;
+  if (paged && (d->page_size <= 0 || d->num_pages <= 0 || d->num_kv_heads == 0)) return PD_ERR_INVALID_ARG;
+  if ((int64_t)d->num_qo_heads + 2 * (int64_t)d->num_kv_heads > (1 << 20)) return PD_ERR_UNSUPPORTED;
+  const int64_t qrow = (int64_t)d->num_qo_heads * d->head_dim, krow = (int64_t)d->num_kv_heads * d->head_dim;
+  NormRopeParams p{};
+  p.q_stride = d->q_stride != 0 ? d->q_stride : qrow;
+  p.k_stride = d->k_stride != 0 ? d->k_stride : krow;
+  p.v_stride = d->v_stride != 0 ? d->v_stride : krow;
+  p.q_out_stride = d->q_out_stride != 0 ? d->q_out_stride : qrow;
+  p.k_out_stride = d->k_out_stride != 0 && !paged ? d->k_out_stride : krow;
+  // Reads of a token may repeat another's (a broadcast row), but no two tokens may share a result.
+  if (p.q_stride < 0 || p.k_stride < 0 || p.v_stride < 0) return PD_ERR_INVALID_ARG;
+  if (p.q_out_stride < qrow || p.k_out_stride < krow) return PD_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PD_OK;
+  if (d->num_qo_heads > 0 && (q == nullptr || q_out == nullptr)) return PD_ERR_INVALID_ARG;
+  if (d->num_kv_heads > 0 && (k == nullptr || k_out == nullptr)) return PD_ERR_INVALID_ARG;
+  if (paged && (v == nullptr || v_out == nullptr || slot_map == nullptr)) return PD_ERR_INVALID_ARG;
+  if (d->rope_dim > 0 && (inv_freq == nullptr || positions == nullptr)) return PD_ERR_INVALID_ARG;
+  p.tokens = num_tokens;
+  p.hq = d->num_qo_heads;
+  p.hkv = d->num_kv_heads;
+  p.head_dim = d->head_dim;
+  p.rope_dim = d->rope_dim;
+  p.interleaved = d->interleaved ? 1 : 0;
+  p.page_size = d->page_size;
+  p.num_pages = d->num_pages;
+  p.nhd = d->layout == PD_LAYOUT_NHD;
+  p.heads = d->num_qo_heads + d->num_kv_heads * (paged ? 2 : 1);
+  p.eps = d->eps;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.slot_map = paged ? slot_map : nullptr;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.status = dev_status;
+  uintptr_t low = 0;  // all addresses' low bits
+  for (const void* a : {q, k, paged ? v : nullptr, q_weight, k_weight, (const void*)q_out, (const void*)k_out,
+                        paged ? (const void*)v_out : nullptr})
+    low |= reinterpret_cast<uintptr_t>(a);
+  const int vec = norm_rope_vec(p, es, low);
+  if (vec == 0) return PD_ERR_UNSUPPORTED;
+  return launch_norm_rope(p, es, vec, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+int pd_qk_norm_rope(const pd_norm_rope_desc* desc, int32_t num_tokens, const void* q, const void* k,
+                    const void* q_weight, const void* k_weight, const float* inv_freq, const int32_t* positions,
+                    void* q_out, void* k_out, void* stream) {
+  return run_norm_rope(desc, num_tokens, q, k, nullptr, q_weight, k_weight, inv_freq, positions, nullptr, q_out,
+                       k_out, nullptr, false, nullptr, stream);
+}
+
+int pd_qk_norm_rope_append(const pd_norm_rope_desc* desc, int32_t num_tokens, const void* q, const void* k,
+                           const void* v, const void* q_weight, const void* k_weight, const float* inv_freq,
+                           const int32_t* positions, const int64_t* slot_map, void* q_out, void* k_pool,
+                           void* v_pool, int32_t* dev_status, void* stream) {
+  return run_norm_rope(desc, num_tokens, q, k, v, q_weight, k_weight, inv_freq, positions, slot_map, q_out, k_pool,
+                       v_pool, true, dev_status, stream);
+}
+
+namespace {
+
+ChunkParams chunk_params(const pd_attn_desc* d, const pd_batch* b, int32_t window_left, int64_t q_stride) {
+  ChunkParams p{};
+  p.batch = b->batch_size;
+  p.hq = d->num_qo_heads;
+  p.hkv = d->num_kv_heads;
+  p.group = p.hq / p.hkv;
+  p.head_dim = d->head_dim;
+  p.page_size = d->page_size;
+  p.num_pages = b->num_pages;
+  p.total_qo = b->total_qo;
+  p.max_qo_len = b->max_qo_len;
+  p.max_kv_len = b->max_kv_len;
+  p.causal = d->causal ? 1 : 0;
+  // a window past every key is none; the bound also keeps position - window inside 32 bits
+  p.window = window_left >= 0 && window_left < (1 << 30) ? window_left : -1;
+  p.o_dtype = d->o_dtype;
+  p.nhd = d->layout == PD_LAYOUT_NHD;
+  p.scale_log2 = scale_of(d) * kLog2e;
+  p.q_stride = q_stride != 0 ? q_stride : (int64_t)p.hq * p.head_dim;
+  p.qo_indptr = b->qo_indptr;
+  p.kv_len = b->kv_len;
+  p.page_indptr = b->page_indptr;
+  p.page_indices = b->page_indices;
+  return p;
+}
+
+}  // namespace
+
+size_t pd_attn_chunk_workspace_size(const pd_attn_desc* desc, const pd_batch* batch) {
+  if (check_attn(desc, batch, false) != PD_OK) return 0;
+  ChunkParams p = chunk_params(desc, batch, -1, 0);
+  return chunk_layout(p, desc->kv_dtype).total;
+}
+
+int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t window_left, int64_t q_stride,
+                  const void* q, const void* k_pool, const void* v_pool, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_attn(desc, batch, true);
+  if (rc != PD_OK) return rc;
+  ChunkParams p = chunk_params(desc, batch, window_left, q_stride);
+  if (p.q_stride < (int64_t)p.hq * p.head_dim || p.q_stride * elem_size(desc->kv_dtype) % 16 != 0)
+    return PD_ERR_INVALID_ARG;
+  if (batch->batch_size == 0 || batch->total_qo == 0 || batch->max_qo_len == 0) return PD_OK;
+  if (q == nullptr || k_pool == nullptr || v_pool == nullptr || o == nullptr || workspace == nullptr)
+    return PD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(workspace))
+    return PD_ERR_INVALID_ARG;
+  const ChunkLayout L = chunk_layout(p, desc->kv_dtype);
+  if (workspace_bytes < L.total) return PD_ERR_WORKSPACE;
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.o = o;
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.hdr = reinterpret_cast<int64_t*>(ws + L.hdr);
+  p.req_first = reinterpret_cast<int32_t*>(ws + L.req_first);
+  p.pre = reinterpret_cast<int64_t*>(ws + L.pre);
+  p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.status = dev_status;
+  return launch_chunk(p, desc->kv_dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,469 @@
+// pd_chunk.cu -- attention of a chunk of new tokens over a paged KV cache: the
+// plan of the work line, the kernel for fp32 and for pages that the tensor-core
+// kernel does not take, and the merge of items cut between CTAs.
+//
+// Sections "Prefill vs Decode performance" (attention parallelises over requests
+// and over the KV length) and "Qwen3-Coder" (grouped-query heads). For token i
+// of n new ones at position t = kv_len - n + i and a query head h on KV head
+// h / group, over the keys j < kv_len with j <= t (causal) and j >= t - window:
+//   s_j = scale <q_ih, k_j>,  o_ih = sum_j softmax(s)_j v_j,  lse = ln sum_j e^{s_j}
+// and o = 0, lse = -inf where no key is left.
+#include <math.h>
+
+#include <atomic>
+
+#include "pd_chunk.cuh"
+
+namespace pd {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr long long kChunkMinUnits = 2;  // least units of a part
+
+__device__ bool chunk_request_ok(const ChunkParams& p, int r) {
+  const int a = p.qo_indptr[r], b = p.qo_indptr[r + 1], n = p.kv_len[r];
+  const int pa = p.page_indptr[r], pb = p.page_indptr[r + 1];
+  int code = PD_DEV_OK;
+  if (a < 0 || b < a || b > p.total_qo || pa < 0 || pb < pa) code = PD_DEV_BAD_INDPTR;
+  else if (n < 0 || n > p.max_kv_len || b - a > p.max_qo_len) code = PD_DEV_BAD_LENGTH;
+  else if ((long long)(pb - pa) * p.page_size < n) code = PD_DEV_BAD_PAGE_TABLE;
+  if (code != PD_DEV_OK) report(p.status, code);
+  return code == PD_DEV_OK;
+}
+
+// Exclusive scan over the CTA, and the total.
+__device__ long long scan_exclusive(long long v, long long* warp_tot, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // the totals of an earlier scan have been read
+  if (lane == 31) warp_tot[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = warp_tot[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    warp_tot[lane] = w;
+  }
+  __syncthreads();
+  total = warp_tot[kPlanThreads / 32 - 1];
+  return (warp > 0 ? warp_tot[warp - 1] : 0) + x - v;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------- plan
+// One CTA: checks the requests, numbers their token blocks and sums the blocks' units.
+__global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p) {
+  __shared__ long long warp_tot[kPlanThreads / 32];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x;
+  long long carry = 0, total;
+  for (int r0 = 0; r0 < p.batch; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    long long n = 0;
+    if (r < p.batch && chunk_request_ok(p, r))
+      n = (p.qo_indptr[r + 1] - p.qo_indptr[r] + p.item_tokens - 1) / p.item_tokens;
+    const long long at = carry + scan_exclusive(n, warp_tot, total);
+    // rows of different requests do not overlap in a sound batch, so the bound holds there
+    if (r < p.batch) p.req_first[r] = (int)min(at, (long long)p.max_blocks);
+    carry += total;
+  }
+  const int blocks = (int)min(carry, (long long)p.max_blocks);
+  if (tid == 0) p.req_first[p.batch] = blocks;
+  __syncthreads();
+  carry = 0;
+  for (int b0 = 0; b0 < blocks; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long units = 0;
+    if (b < blocks) {
+      int lo = 0, hi = p.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.req_first[mid] <= b) lo = mid;
+        else hi = mid;
+      }
+      const int qo = p.qo_indptr[lo + 1] - p.qo_indptr[lo], t0 = (b - p.req_first[lo]) * p.item_tokens;
+      units = p.item_cost +
+              chunk_tiles(p, chunk_keys(p, qo, p.kv_len[lo], t0, min(qo, t0 + p.item_tokens)));
+    }
+    const long long at = carry + scan_exclusive(units, warp_tot, total);
+    if (b < blocks) p.pre[b] = at;
+    carry += total;
+  }
+  if (tid == 0) {
+    p.pre[blocks] = carry;
+    const long long units = carry * p.item_heads;
+    // at least kChunkMinUnits of work a part
+    long long parts = (units + kChunkMinUnits - 1) / kChunkMinUnits;
+    if (parts > p.max_parts) parts = p.max_parts;
+    p.hdr[0] = units;
+    p.hdr[1] = parts < 1 ? 1 : parts;
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// o and lse of the items that the line's cuts fell into: block x looks at the
+// cut behind part x, and works if an item's first cut is there. One warp a row.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
+  pdl_wait_primary();
+  const int64_t units = p.hdr[0], parts = p.hdr[1];
+  const int c = blockIdx.x;
+  if (c + 1 >= parts || units == 0) return;
+  const int64_t from = part_start(units, parts, c), cut = part_start(units, parts, c + 1);
+  ChunkWalk w;
+  w.seek(p, cut, units);
+  const int64_t s = w.item_start;
+  const int n = (int)(p.pre[w.b + 1] - p.pre[w.b]) - p.item_cost;
+  if (s < from || s >= cut || cut >= s + n) return;  // an earlier part's item, or no tile behind the cut
+  int64_t last = c + 1;  // the part that holds the item's last tile
+  while (last + 1 < parts && part_start(units, parts, last + 1) < s + n) ++last;
+  const int a = p.qo_indptr[w.r], qo = p.qo_indptr[w.r + 1] - a;
+  const int tok0 = (w.b - w.b0) * p.item_tokens;
+  const int rows = min(p.item_tokens, qo - tok0) * p.tile_heads;
+  const int lane = threadIdx.x & 31;
+  constexpr int E = D / 32;
+  for (int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); m < rows;
+       m += gridDim.y * (kMergeThreads / 32)) {
+    float best = -INFINITY;
+    for (int64_t x = c; x <= last; ++x)
+      best = fmaxf(best, p.part_lse[(2 * x + (x == c ? 1 : 0)) * p.rows + m]);
+    if (best == -INFINITY) best = 0.f;  // no part has a key: every factor below is 0
+    float sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int64_t x = c; x <= last; ++x) {
+      const int64_t slot = (2 * x + (x == c ? 1 : 0)) * p.rows + m;
+      const float f = exp2f(p.part_lse[slot] - best);
+      const float* o = p.part_o + slot * D + lane * E;
+      sum += f;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+        acc[2] += f * v.z;
+        acc[3] += f * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+      }
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const int tok = m / p.tile_heads;
+    const int64_t row = (int64_t)(a + tok0 + tok) * p.hq + w.h * p.tile_heads + (m - tok * p.tile_heads);
+    if (p.o_dtype == PD_BF16) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) o[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    } else {
+      float* o = static_cast<float*>(p.o) + row * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+    }
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = sum != 0.f ? (best + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// ----------------------------------------------------------------- kernel
+// fp32 arithmetic on the CUDA cores: R query rows (tokens x heads of a KV head)
+// against tiles of 64 keys, K then V of a tile in one shared buffer as fp32.
+// 256 threads as 16 x 16: a thread has R / 16 rows and every 16th key of the
+// scores, the same rows and D / 16 columns of the output; a row's maximum and
+// sum go over its 16 lanes by shuffles.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 64;
+
+template <int R, int D>
+constexpr size_t simt_smem() {
+  return sizeof(float) * (size_t)(R * (D + 4) + kSimtKeys * (D + 4) + kSimtKeys * (R + 4));
+}
+
+template <typename T, int R, int D>
+__global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkParams p) {
+  constexpr int RT = R / 16, LD = D + 4, LP = R + 4, CT = D / 64;  // CT: float4 columns of a thread
+  extern __shared__ float4 simt_smem_raw[];
+  float* sQ = reinterpret_cast<float*>(simt_smem_raw);
+  float* sKV = sQ + R * LD;
+  float* sP = sKV + kSimtKeys * LD;  // [key][row]
+  pdl_wait_primary();
+  const int64_t units = p.hdr[0], parts = p.hdr[1];
+  if (blockIdx.x >= parts) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  ChunkWalk walk;
+  walk.seek(p, part_start(units, parts, blockIdx.x), part_start(units, parts, blockIdx.x + 1));
+  constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
+  ChunkItem I;
+  while (walk.next(p, I)) {
+    const int rows = I.tokens * p.tile_heads;
+    __syncthreads();  // the last item's shared rows have been read
+    for (int i = tid; i < R * VR; i += kSimtThreads) {
+      const int m = i / VR, c = i - m * VR;
+      float f[VE] = {};
+      if (m < rows) {
+        const int tok = m / p.tile_heads;
+        const T* q = static_cast<const T*>(p.q) + (int64_t)(I.q0 + tok) * p.q_stride +
+                     (int64_t)(I.h + m - tok * p.tile_heads) * D + c * VE;
+        const uint4 v = *reinterpret_cast<const uint4*>(q);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 4) {
+            f[e] = __uint_as_float(w[e]);
+          } else {
+            f[2 * e] = bf16_lo(w[e]);
+            f[2 * e + 1] = bf16_hi(w[e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) sQ[m * LD + c * VE + e] = f[e];
+    }
+    float m_run[RT], l_run[RT], acc[RT][CT * 4];
+    int lo[RT], hi[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      m_run[i] = -INFINITY;
+      l_run[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < CT * 4; ++e) acc[i][e] = 0.f;
+      const int m = ty * RT + i;
+      const int tok = I.first_tok + m / p.tile_heads;
+      const KeyRange k = chunk_keys(p, I.qo, I.kv, tok, tok + 1);
+      lo[i] = k.lo;
+      hi[i] = m < rows ? k.hi : 0;
+    }
+    const int kv_head = I.h / p.group;
+    // rows of tile keys [k0, k0 + 64) of a pool to shared memory; keys that no row of the item sees are zero
+    auto load = [&](const void* pool, int k0) {
+      for (int i = tid; i < kSimtKeys * VR; i += kSimtThreads) {
+        const int key = i / VR, c = i - key * VR, j = k0 + key;
+        float f[VE] = {};
+        if (j >= I.keys.lo && j < I.keys.hi) {
+          const int page = p.page_indices[I.pbase + j / p.page_size], slot = j % p.page_size;
+          if (page >= 0 && page < p.num_pages) {
+            const int64_t row = p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head
+                                      : ((int64_t)page * p.hkv + kv_head) * p.page_size + slot;
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(T) == 4) {
+                f[e] = __uint_as_float(w[e]);
+              } else {
+                f[2 * e] = bf16_lo(w[e]);
+                f[2 * e + 1] = bf16_hi(w[e]);
+              }
+            }
+          } else {
+            report(p.status, PD_DEV_BAD_PAGE_TABLE);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < VE; e += 4)
+          *reinterpret_cast<float4*>(sKV + key * LD + c * VE + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+      }
+    };
+    for (int t = I.t0; t < I.t1; ++t) {
+      const int k0 = (I.tile0 + t) * kSimtKeys;
+      __syncthreads();
+      load(p.k_pool, k0);
+      __syncthreads();
+      float s[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 qv[RT], kv[4];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * LD + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * j) * LD + d);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+            s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+            s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = k0 + tx + 16 * j;
+          s[i][j] = key >= lo[i] && key < hi[i] ? s[i][j] * p.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float m_new = fmaxf(m_run[i], mx);
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = exp2f(m_run[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float w = exp2f(s[i][j] - base);
+          sum += w;
+          sP[(tx + 16 * j) * LP + ty * RT + i] = w;
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l_run[i] = l_run[i] * alpha + sum;
+        m_run[i] = m_new;
+#pragma unroll
+        for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
+      }
+      __syncthreads();  // the scores have read K, and the weights are written
+      load(p.v_pool, k0);
+      __syncthreads();
+#pragma unroll 4
+      for (int key = 0; key < kSimtKeys; ++key) {
+        float w[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) w[i] = sP[key * LP + ty * RT + i];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(sKV + key * LD + tx * 4 + 64 * c);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            acc[i][4 * c + 0] = fmaf(w[i], v.x, acc[i][4 * c + 0]);
+            acc[i][4 * c + 1] = fmaf(w[i], v.y, acc[i][4 * c + 1]);
+            acc[i][4 * c + 2] = fmaf(w[i], v.z, acc[i][4 * c + 2]);
+            acc[i][4 * c + 3] = fmaf(w[i], v.w, acc[i][4 * c + 3]);
+          }
+        }
+      }
+    }
+    const int64_t slot = part_slot(I, blockIdx.x);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int m = ty * RT + i;
+      if (m >= rows) continue;
+      const float inv = l_run[i] != 0.f ? 1.f / l_run[i] : 0.f;
+      const float lse2 = l_run[i] != 0.f ? m_run[i] + log2f(l_run[i]) : -INFINITY;
+      const int tok = m / p.tile_heads;
+      const int64_t row = (int64_t)(I.q0 + tok) * p.hq + I.h + m - tok * p.tile_heads;
+      if (slot < 0 && p.o_dtype == PD_BF16) {
+        uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + tx * 4);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          o[16 * c] = make_uint2(pack_bf16x2(acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv),
+                                 pack_bf16x2(acc[i][4 * c + 2] * inv, acc[i][4 * c + 3] * inv));
+      } else {
+        float* o = slot < 0 ? static_cast<float*>(p.o) + row * D : p.part_o + (slot * p.rows + m) * D;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          *reinterpret_cast<float4*>(o + tx * 4 + 64 * c) =
+              make_float4(acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv, acc[i][4 * c + 2] * inv,
+                          acc[i][4 * c + 3] * inv);
+      }
+      if (tx == 0) {
+        if (slot >= 0) p.part_lse[slot * p.rows + m] = lse2;
+        else if (p.lse != nullptr) p.lse[row] = lse2 * kLn2;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
+  (void)kv_dtype;
+  // Rows of an item: 16 where no request has more, else 64 (a 64-row tile with
+  // few rows would spend its time on rows that are not there).
+  const int64_t most = (int64_t)p.max_qo_len * p.group;
+  p.rows = most <= 16 ? 16 : 64;
+  p.tile_heads = p.group <= p.rows ? p.group : 1;
+  p.item_tokens = p.rows / p.tile_heads;
+  p.item_heads = p.hq / p.tile_heads;
+  p.key_tile = kSimtKeys;
+  p.item_cost = 1;
+  p.max_parts = device_sm_count() * 2;
+  const int64_t by_len = (int64_t)p.batch * (((int64_t)p.max_qo_len + p.item_tokens - 1) / p.item_tokens);
+  const int64_t by_rows = (int64_t)p.total_qo / p.item_tokens + p.batch;
+  p.max_blocks = (int32_t)(by_len < by_rows ? by_len : by_rows);
+  ChunkLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  L.hdr = take(32 * sizeof(int64_t));
+  L.req_first = take(sizeof(int32_t) * ((size_t)p.batch + 1));
+  L.pre = take(sizeof(int64_t) * ((size_t)p.max_blocks + 1));
+  L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
+  L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);
+  L.total = off;
+  return L;
+}
+
+namespace {
+
+// Launches `kernel` as a programmatic dependent of the kernel before it on the stream.
+template <typename K>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const ChunkParams& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, int R, int D>
+cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
+  auto kernel = chunk_simt_kernel<T, R, D>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<R, D>());
+  if (e != cudaSuccess) return e;
+  last_kernel() = "chunk_simt_kernel";
+  profile_begin(stream);
+  e = launch_dependent(kernel, dim3(p.max_parts), kSimtThreads, simt_smem<R, D>(), stream, p);
+  profile_end(stream);
+  return e;
+}
+
+}  // namespace
+
+int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
+  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  cudaError_t e;
+  const bool d64 = p.head_dim == 64, few = p.rows == 16;
+  if (kv_dtype == PD_BF16)
+    e = d64 ? (few ? launch_simt<uint16_t, 16, 64>(p, stream) : launch_simt<uint16_t, 64, 64>(p, stream))
+            : (few ? launch_simt<uint16_t, 16, 128>(p, stream) : launch_simt<uint16_t, 64, 128>(p, stream));
+  else
+    e = d64 ? (few ? launch_simt<float, 16, 64>(p, stream) : launch_simt<float, 64, 64>(p, stream))
+            : (few ? launch_simt<float, 16, 128>(p, stream) : launch_simt<float, 64, 128>(p, stream));
+  if (e != cudaSuccess) return PD_ERR_CUDA;
+  if (p.max_parts > 1) {
+    const dim3 grid(p.max_parts - 1, (p.rows + 31) / 32);
+    e = d64 ? launch_dependent(chunk_merge_kernel<64>, grid, kMergeThreads, 0, stream, p)
+            : launch_dependent(chunk_merge_kernel<128>, grid, kMergeThreads, 0, stream, p);
+  }
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+}
+
+}  // namespace pd

@@ -169,6 +169,105 @@ int mla_pairs();
 MlaLayout mla_layout(int32_t batch, int32_t hq);
 int launch_mla(MlaParams& p, const void* q, const void* kv_pool, cudaStream_t stream);
 
+// ------------------------------------------------------------------ tables
+struct TablesParams {
+  int32_t batch, page_size, num_pages, table_rows, table_cols, total_qo, max_page_indices, free_capacity;
+  int32_t hash_size;  // entries of the duplicate-row table in shared memory (0: rows == NULL)
+  const int32_t* rows;
+  const int32_t* cached_len;
+  const int32_t* new_len;
+  int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* qo_indptr;
+  int32_t* kv_len;
+  int32_t* page_indptr;
+  int32_t* page_indices;
+  int32_t* positions;
+  int64_t* slot_map;
+  int32_t* status;
+};
+constexpr int32_t kTablesMaxBatch = 8192;  // the sums of a batch stay in shared memory
+int launch_batch_tables(TablesParams& p, cudaStream_t stream);
+
+struct SlotMapParams {
+  int32_t batch, page_size, num_pages, total_qo, max_kv_len;
+  const int32_t* qo_indptr;
+  const int32_t* kv_len;
+  const int32_t* page_indptr;
+  const int32_t* page_indices;
+  int32_t* positions;
+  int64_t* slot_map;
+  int32_t* status;
+};
+int launch_slot_map(const SlotMapParams& p, cudaStream_t stream);
+
+// ----------------------------------------------------------- norm and rope
+struct NormRopeParams {
+  int32_t tokens, hq, hkv, head_dim, rope_dim, interleaved, page_size, num_pages, nhd;
+  int32_t heads;  // heads a token's work covers: q, k and (with a slot map) v
+  // set by the launcher: lanes of a head, heads of a warp's group, groups of a
+  // token, groups a work item covers, work items of a token
+  int32_t lanes, heads_per_group, groups, groups_per_block, blocks;
+  float eps, inv_dim;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements between tokens
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_weight;
+  const void* k_weight;
+  const float* inv_freq;
+  const int32_t* positions;
+  const int64_t* slot_map;  // null: k goes to rows of k_out
+  void* q_out;
+  void* k_out;  // rows or pool
+  void* v_out;  // pool
+  int32_t* status;
+};
+int32_t norm_rope_vec(const NormRopeParams& p, int32_t elem_size, uintptr_t addresses);
+int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStream_t stream);
+
+// --------------------------------------------------------- chunk attention
+// An item is (request, block of item_tokens query tokens, tile_heads query
+// heads of one KV head); its keys are cut into tiles of key_tile. All items
+// form one line of units, a tile costing one and an item item_cost more; the
+// line is cut into equal parts, one per CTA (see pd_chunk.cuh).
+// Workspace (offsets 256-byte aligned):
+//   hdr        int64[32]        hdr[0] = units in total, hdr[1] = parts
+//   req_first  int32[B + 1]     first block of every request
+//   pre        int64[max_blocks + 1]  units of one head before every block
+//   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
+//   part_o     float[2 * parts][rows][D]  its normalised output
+struct ChunkParams {
+  int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
+  int32_t causal, window, o_dtype, nhd;
+  int32_t tile_heads, item_heads, item_tokens, key_tile, item_cost, rows, max_blocks, max_parts;
+  float scale_log2;  // softmax scale times log2(e)
+  int64_t q_stride;  // elements between query tokens
+  const int32_t* qo_indptr;
+  const int32_t* kv_len;
+  const int32_t* page_indptr;
+  const int32_t* page_indices;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  void* o;
+  float* lse;
+  int64_t* hdr;
+  int32_t* req_first;
+  int64_t* pre;
+  float* part_lse;
+  float* part_o;
+  int32_t* status;
+};
+struct ChunkLayout {
+  size_t hdr, req_first, pre, part_lse, part_o, total;
+};
+// Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
+ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
+int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
+
 // ------------------------------------------------------------ tensor maps
 bool make_pool_map(CUtensorMap* map, const void* pool, int32_t dtype, int32_t num_pages, int32_t hkv,
                    int32_t page_size, int32_t head_dim, int32_t box_cols, int32_t box_rows, bool swizzle128,

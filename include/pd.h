@@ -95,7 +95,9 @@ typedef enum {
   PD_DEV_BAD_PAGE_TABLE = 3, /* fewer pages than ceil(kv_len / page_size), or a page id outside [0, num_pages) */
   PD_DEV_NOT_DECODE = 4,     /* pd_attn_decode given a request with qo_len != 1 */
   PD_DEV_TIMEOUT = 5,        /* a bounded wait inside a kernel ran out; the kernel returned early */
-  PD_DEV_BAD_OFFSET = 6      /* a pack / unpack block misaligned or outside the packed buffer */
+  PD_DEV_BAD_OFFSET = 6,     /* a pack / unpack block misaligned or outside the packed buffer */
+  PD_DEV_NO_PAGES = 7,       /* pd_batch_tables: too few free pages for a request's new tokens */
+  PD_DEV_BAD_ROW = 8         /* pd_batch_tables: a block-table row out of range or listed twice */
 } pd_device_status;
 
 typedef enum { PD_F32 = 0, PD_BF16 = 1 } pd_dtype;
@@ -258,6 +260,39 @@ PD_API int pd_attn_mixed_split(const pd_attn_desc *desc, const pd_batch *batch, 
                                int32_t *dev_status, void *stream);
 
 /*
+ * Attention of a chunk of new tokens over the paged cache: any number of new
+ * tokens per request from one (a decode, the verification of drafted tokens) to
+ * thousands (a chunked prefill), whose K/V are in the cache already. (Section
+ * "Prefill vs Decode performance": attention parallelises over requests and over
+ * kv_len; the KV axis is cut over the SMs wherever query rows alone would leave
+ * some idle, and the pieces are merged by log-sum-exp.)
+ * Token i of a request with n new tokens is at position t = kv_len - n + i and
+ * sees the keys j < kv_len with
+ *   j <= t                  if desc->causal
+ *   j >= t - window_left    if window_left >= 0 (sliding window)
+ * A row that sees no key (kv_len = 0, or t < 0 because n > kv_len under the
+ * causal mask) gives o = 0, lse = -inf.
+ *   q        device, row i at q + i * q_stride elements, [Hq][D] (kv_dtype); q_stride 0
+ *            means Hq * D; a slice of a fused projection has a larger one. q_stride
+ *            times the element size must be a multiple of 16 bytes.
+ *   k_pool, v_pool, o, lse, dev_status: as pd_attn_prefill (o and lse are contiguous)
+ *   workspace: pd_attn_chunk_workspace_size(desc, batch) bytes
+ * batch->qo_indptr is required; rows of q past qo_indptr[B] are not used and
+ * their o and lse are left as they were. Supported: fp32 and bf16, D 64 or 128,
+ * any page size, any group. bf16 with pages a power of two of at least 8 runs on
+ * the tensor cores (the softmax weights enter the product with V as bf16); other
+ * calls run in fp32 on the CUDA cores. Keys that no token of the request sees
+ * (past kv_len, or before the first token's window) may hold anything, also NaN;
+ * V rows that some token of the request sees must be finite for all its tokens.
+ * The call can be captured into a CUDA graph; lengths may change between replays
+ * within the host bounds max_qo_len and max_kv_len.
+ */
+PD_API size_t pd_attn_chunk_workspace_size(const pd_attn_desc *desc, const pd_batch *batch);
+PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_t window_left, int64_t q_stride,
+                         const void *q, const void *k_pool, const void *v_pool, void *o, float *lse,
+                         void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * MLA decode (section "Disaggregated Deployments", "DeepSeek-R1": multi-head
  * latent attention compresses the KV heads of a token into one latent vector
  * that every query head reads, so the cache holds one row per token and is
@@ -294,6 +329,110 @@ PD_API size_t pd_mla_workspace_size(const pd_mla_desc *desc, const pd_batch *bat
 PD_API int pd_mla_decode(const pd_mla_desc *desc, const pd_batch *batch, const void *q, const void *kv_pool,
                          void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status,
                          void *stream);
+
+/*
+ * Block tables, page lists, positions and slots of a serving step, built on the
+ * GPU from the requests' lengths (section "KV Messenger": the model appends a
+ * layer's new KV entries to their pages; this call says which pages). Request r
+ * has cached_len[r] tokens in the cache and brings new_len[r] more; its pages are
+ * the first ceil(cached_len / page_size) entries of block_table row rows[r] (row
+ * r when rows is NULL), and the pages its new tokens need beyond those are taken
+ * from the end of free_pages, in request order, and entered into its row:
+ *   page j = free_pages[*free_count - 1 - (pages taken so far)].
+ * With free_pages NULL nothing is taken: the rows hold every page already.
+ * Results, all written by the call:
+ *   qo_indptr   int32 [B+1], kv_len int32 [B] (cached + new), page_indptr int32 [B+1],
+ *   page_indices int32 [max_page_indices]: the batch that the attention calls take
+ *   positions   int32 [total_qo]: each new token's position in its request
+ *   slot_map    int64 [total_qo]: page * page_size + slot of each new token
+ *   free_count_out int32: the free pages left
+ * Rows past the last request's (a padded batch) get position 0 and slot -1;
+ * entries of page_indices past page_indptr[B] are left as they were.
+ * A request that cannot be served gets kv_len -1 (which the attention calls skip
+ * and report), slot -1 and page -1 throughout, takes no page and is reported:
+ * PD_DEV_BAD_LENGTH (a negative length, or more pages than table_cols),
+ * PD_DEV_BAD_ROW (its row out of range or listed by an earlier request),
+ * PD_DEV_BAD_INDPTR (rows past total_qo or pages past max_page_indices),
+ * PD_DEV_NO_PAGES (too few free pages left; later requests that need none are
+ * served). A page id outside [0, num_pages) is entered as it is and reported
+ * (PD_DEV_BAD_PAGE_TABLE); its tokens get slot -1. *free_count is read clamped to
+ * [0, free_capacity]. free_count_out may be free_count (one launch more);
+ * otherwise no result may overlap an input or another result
+ * (PD_ERR_INVALID_ARG). Calls with free_count_out apart from free_count can be
+ * repeated: they give the same results. batch_size at most 8192
+ * (PD_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  int32_t batch_size;       /* B >= 0 */
+  int32_t page_size;        /* P >= 1 */
+  int32_t num_pages;        /* pages in each pool (bound for page ids) */
+  int32_t table_rows;       /* rows of block_table */
+  int32_t table_cols;       /* its columns: pages of a request at most */
+  int32_t total_qo;         /* host: rows of positions and slot_map */
+  int32_t max_page_indices; /* host: entries of page_indices */
+  int32_t free_capacity;    /* host: entries of free_pages */
+} pd_tables_desc;
+PD_API int pd_batch_tables(const pd_tables_desc *desc, const int32_t *rows, const int32_t *cached_len,
+                           const int32_t *new_len, int32_t *block_table, const int32_t *free_pages,
+                           const int32_t *free_count, int32_t *free_count_out, int32_t *qo_indptr,
+                           int32_t *kv_len, int32_t *page_indptr, int32_t *page_indices, int32_t *positions,
+                           int64_t *slot_map, int32_t *dev_status, void *stream);
+
+/*
+ * Positions and slots (as pd_batch_tables) of a batch whose page table the caller
+ * has: the rows qo_indptr[r] .. qo_indptr[r+1] are the last positions of kv_len[r].
+ * Rows of no request, and rows of a request that is reported, get position 0 and
+ * slot -1; a token whose page id is out of range gets slot -1.
+ */
+PD_API int pd_slot_map(const pd_batch *batch, int32_t page_size, int32_t *positions, int64_t *slot_map,
+                       int32_t *dev_status, void *stream);
+
+/*
+ * Per-head RMS norms of queries and keys and the position rotation in one pass
+ * (section "Qwen3-Coder": a model family that norms each head before rotating
+ * it), and with it the append of section "KV Messenger". For a head x of
+ * head_dim values:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *   (z_a, z_b) = (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
+ *   t = positions[token] * inv_freq[i], i < rope_dim / 2,
+ *   (a, b) = (i, rope_dim / 2 + i), or (2i, 2i + 1) if interleaved
+ * and values past rope_dim stay y. Computed in fp32 (angles exactly modulo a
+ * turn) and rounded once.
+ *   q, k, v   device, token t at + t * stride elements, [heads][head_dim]; stride 0 means
+ *             contiguous (heads * head_dim); slices of one projection's rows have its width
+ *   q_weight, k_weight  device [head_dim] (dtype) or NULL
+ *   inv_freq  device fp32 [rope_dim / 2]; positions device int32 [num_tokens];
+ *             both may be NULL if rope_dim is 0
+ * pd_qk_norm_rope writes q_out and k_out rows (strides as above; each may be its
+ * input itself, with the same stride). pd_qk_norm_rope_append writes q_out rows,
+ * and k and v into their slots of the pools: token t goes to page slot_map[t] /
+ * page_size, slot slot_map[t] % page_size. A negative slot marks a padding row,
+ * of which nothing is written, q_out neither; a slot past the pools is reported
+ * (PD_DEV_BAD_PAGE_TABLE), its k and v dropped. Slots must be distinct.
+ * Supported (otherwise PD_ERR_UNSUPPORTED): head_dim and rope_dim multiples of
+ * 2 v elements, head_dim at most 64 v, strides multiples of v and addresses
+ * aligned to v elements, for one v of 2, 4 and (bf16) 8; the largest is taken.
+ */
+typedef struct {
+  int32_t num_qo_heads;  /* Hq; 0: no queries */
+  int32_t num_kv_heads;  /* Hkv; 0: no keys (not in pd_qk_norm_rope_append) */
+  int32_t head_dim;      /* D */
+  int32_t rope_dim;      /* R, even, 0 .. D */
+  int32_t interleaved;   /* 0: pairs (i, R/2 + i); 1: pairs (2i, 2i + 1) */
+  int32_t dtype;         /* pd_dtype of q, k, v, the weights, the results and the pools */
+  int32_t page_size;     /* pools (pd_qk_norm_rope_append): tokens per page */
+  int32_t num_pages;     /* pages in each pool */
+  int32_t layout;        /* pd_layout of the pools */
+  float eps;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride; /* elements; 0: contiguous */
+} pd_norm_rope_desc;
+PD_API int pd_qk_norm_rope(const pd_norm_rope_desc *desc, int32_t num_tokens, const void *q, const void *k,
+                           const void *q_weight, const void *k_weight, const float *inv_freq,
+                           const int32_t *positions, void *q_out, void *k_out, void *stream);
+PD_API int pd_qk_norm_rope_append(const pd_norm_rope_desc *desc, int32_t num_tokens, const void *q, const void *k,
+                                  const void *v, const void *q_weight, const void *k_weight,
+                                  const float *inv_freq, const int32_t *positions, const int64_t *slot_map,
+                                  void *q_out, void *k_pool, void *v_pool, int32_t *dev_status, void *stream);
 
 /*
  * KV append (section "KV Messenger": page copies of a layer start once the
