@@ -1,0 +1,101 @@
+"""A serving step as it is used: tables from lengths, norm + rotation + append into the pages, attention
+of the new tokens, over several steps of a ragged batch; against fp64 attention over a dense cache."""
+import random
+
+import pytest
+import torch
+
+import step_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import decode_ragged_paged_gb300 as pd
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dt,hq,hkv,d,page,layout,window,captured", [
+    (torch.float32, 8, 2, 64, 16, "HND", -1, False),
+    (torch.bfloat16, 32, 8, 128, 16, "HND", -1, False),
+    (torch.bfloat16, 8, 8, 128, 64, "NHD", 50, False),
+    (torch.bfloat16, 28, 4, 128, 16, "HND", -1, True),
+    (torch.bfloat16, 8, 2, 64, 24, "NHD", -1, True),
+])
+def test_steps(dt, hq, hkv, d, page, layout, window, captured):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rng = random.Random(2)
+    B, steps, cap = 9, 5, 260
+    plan = [[rng.choice([0, 1, 1, 3, 40]) for _ in range(B)] for _ in range(steps)]
+    plan[0] = [1, 100, 17, 16, 0, 33, 2, 5, 64]
+    num_pages = sum(ref.ceil_div(sum(p[r] for p in plan), page) for r in range(B)) + 5
+    shape = (num_pages, hkv, page, d) if layout == "HND" else (num_pages, page, hkv, d)
+    kp, vp = (torch.full(shape, float("nan"), device="cuda").to(dt) for _ in range(2))
+    free = torch.randperm(num_pages, device="cuda", generator=g).to(torch.int32)
+    count, table = i32([num_pages]), torch.full((B + 3, 40), -1, dtype=torch.int32, device="cuda")
+    rows = torch.randperm(B + 3, device="cuda", generator=g)[:B].to(torch.int32)
+    cached, new = torch.zeros(B, dtype=torch.int32, device="cuda"), i32(plan[0])
+    inv_freq = (10000.0 ** (-torch.arange(d // 2, device="cuda", dtype=torch.float64) / (d // 2))).float()
+    qw, kw = ((1 + 0.2 * torch.randn(d, device="cuda", generator=g)).to(dt) for _ in range(2))
+    qkv = torch.zeros(cap, (hq + 2 * hkv) * d, device="cuda").to(dt)
+    q, k, v = (x.view(cap, -1, d) for x in qkv.split([hq * d, hkv * d, hkv * d], 1))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out, o = (torch.zeros(cap, hq, d, device="cuda").to(dt) for _ in range(2))
+    lse = torch.zeros(cap, hq, device="cuda")
+    ws = torch.empty(96 << 20, dtype=torch.uint8, device="cuda")
+    out = pd.BatchTables(*(torch.zeros(n, dtype=t, device="cuda") for n, t in (
+        (B + 1, torch.int32), (B, torch.int32), (B + 1, torch.int32), (num_pages, torch.int32), (cap, torch.int32),
+        (cap, torch.int64))))
+
+    def step():
+        t = pd.pd_batch_tables(new, cached, table, page_size=page, num_pages=num_pages, total_qo=cap,
+                               max_page_indices=num_pages, rows=rows, free_pages=free, free_count=count,
+                               free_count_out=count, out=out, dev_status=status)
+        pd.pd_qk_norm_rope_append(q, k, v, qw, kw, inv_freq, t.positions, t.slot_map, kp, vp, q_out=q_out,
+                                  dev_status=status, layout=layout)
+        pd.pd_attn_chunk(q_out, kp, vp, t.kv_len, t.page_indptr, t.page_indices, t.qo_indptr, window_left=window,
+                         max_qo_len=100, max_kv_len=400, o=o, lse=lse, workspace=ws, dev_status=status, layout=layout)
+
+    graph = None
+    past_k, past_v = [[] for _ in range(B)], [[] for _ in range(B)]
+    have = [0] * B
+    for i, ns in enumerate(plan):
+        new.copy_(i32(ns))
+        qkv.copy_(torch.randn(qkv.shape, device="cuda", generator=g))
+        torch.cuda.synchronize()
+        if not captured or i == 0:
+            step()
+        else:
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    step()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        at = 0
+        for r, n in enumerate(ns):
+            pos = torch.arange(have[r], have[r] + n, device="cuda")
+            kn, size = ref.norm_rope(k[at:at + n], kw, inv_freq, pos, eps=1e-6, interleaved=False)
+            qn, qsize = ref.norm_rope(q[at:at + n], qw, inv_freq, pos, eps=1e-6, interleaved=False)
+            assert bool(((q_out[at:at + n].double() - qn).abs() <= ref.norm_rope_bound(qn, qsize, dt)).all())
+            past_k[r].append((kn, size))
+            past_v[r].append(v[at:at + n].clone())
+            have[r] += n
+            ids = out.page_indices[int(out.page_indptr[r]):int(out.page_indptr[r + 1])]
+            got_k, got_v = (ref.gather(x, ids, have[r], layout) for x in (kp, vp))
+            if have[r]:
+                want, size = (torch.cat([p[e] for p in past_k[r]]) for e in (0, 1))
+                assert bool(((got_k - want).abs() <= ref.norm_rope_bound(want, size, dt)).all())
+                assert torch.equal(got_v, torch.cat(past_v[r]).double())
+            at += n
+        assert out.kv_len.tolist() == have and int(count.item()) == num_pages - sum(
+            ref.ceil_div(h, page) for h in have)
+        # attention over what the cache holds, through the plain form's own dense gather
+        qo = [sum(ns[:r]) for r in range(B + 1)]
+        want = ref.attention(q_out[:at], kp, vp, qo, have, out.page_indptr.tolist(), out.page_indices, window=window,
+                             layout=layout)
+        ref.check_attention(o[:at], lse[:at], want)
+        cached.copy_(out.kv_len)
