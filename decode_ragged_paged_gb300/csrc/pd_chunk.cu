@@ -19,7 +19,6 @@ namespace pd {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr long long kChunkMinUnits = 2;  // least units of a part
 
 __device__ bool chunk_request_ok(const ChunkParams& p, int r) {
   const int a = p.qo_indptr[r], b = p.qo_indptr[r + 1], n = p.kv_len[r];
@@ -102,8 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   if (tid == 0) {
     p.pre[blocks] = carry;
     const long long units = carry * p.item_heads;
-    // at least kChunkMinUnits of work a part
-    long long parts = (units + kChunkMinUnits - 1) / kChunkMinUnits;
+    long long parts = (units + p.min_units - 1) / p.min_units;  // at least so many units a part
     if (parts > p.max_parts) parts = p.max_parts;
     p.hdr[0] = units;
     p.hdr[1] = parts < 1 ? 1 : parts;
@@ -384,17 +382,30 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
 
 // ------------------------------------------------------------------- host
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
-  (void)kv_dtype;
-  // Rows of an item: 16 where no request has more, else 64 (a 64-row tile with
-  // few rows would spend its time on rows that are not there).
-  const int64_t most = (int64_t)p.max_qo_len * p.group;
-  p.rows = most <= 16 ? 16 : 64;
-  p.tile_heads = p.group <= p.rows ? p.group : 1;
-  p.item_tokens = p.rows / p.tile_heads;
+  // The tensor cores take bf16, in pages whose boxes fill a tile (and whose
+  // rows keep the swizzle's groups of 8 whole); the CUDA cores take the rest.
+  p.tc = kv_dtype == PD_BF16 && p.page_size >= 8 && (p.page_size & (p.page_size - 1)) == 0;
+  if (p.tc) {
+    p.tile_heads = p.group <= 128 ? p.group : 1;
+    p.item_tokens = 2 * (128 / p.tile_heads);  // two query tiles
+    p.rows = p.item_tokens * p.tile_heads;
+    p.key_tile = kChunkTcKeys;
+    p.item_cost = 1;
+    p.min_units = 2;
+    p.max_parts = device_sm_count();
+  } else {
+    // Rows of an item: 16 where no request has more, else 64 (a 64-row tile with
+    // few rows would spend its time on rows that are not there).
+    const int64_t most = (int64_t)p.max_qo_len * p.group;
+    p.rows = most <= 16 ? 16 : 64;
+    p.tile_heads = p.group <= p.rows ? p.group : 1;
+    p.item_tokens = p.rows / p.tile_heads;
+    p.key_tile = kSimtKeys;
+    p.item_cost = 1;
+    p.min_units = 2;
+    p.max_parts = device_sm_count() * 2;
+  }
   p.item_heads = p.hq / p.tile_heads;
-  p.key_tile = kSimtKeys;
-  p.item_cost = 1;
-  p.max_parts = device_sm_count() * 2;
   const int64_t by_len = (int64_t)p.batch * (((int64_t)p.max_qo_len + p.item_tokens - 1) / p.item_tokens);
   const int64_t by_rows = (int64_t)p.total_qo / p.item_tokens + p.batch;
   p.max_blocks = (int32_t)(by_len < by_rows ? by_len : by_rows);
@@ -451,7 +462,9 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e;
   const bool d64 = p.head_dim == 64, few = p.rows == 16;
-  if (kv_dtype == PD_BF16)
+  if (p.tc)
+    e = launch_chunk_tc(p, stream);
+  else if (kv_dtype == PD_BF16)
     e = d64 ? (few ? launch_simt<uint16_t, 16, 64>(p, stream) : launch_simt<uint16_t, 64, 64>(p, stream))
             : (few ? launch_simt<uint16_t, 16, 128>(p, stream) : launch_simt<uint16_t, 64, 128>(p, stream));
   else

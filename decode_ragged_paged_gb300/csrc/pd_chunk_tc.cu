@@ -1,0 +1,578 @@
+// pd_chunk_tc.cu -- the tensor-core kernel of the chunk attention (bf16, pages
+// a power of two of at least 8 slots): tcgen05 products with S, P and O in
+// tensor memory, tiles fetched by TMA.
+//
+// One persistent CTA per SM walks its part of the work line (pd_chunk.cuh). Two
+// groups of four softmax warps, each with its own S / P buffer and O accumulator
+// in TMEM, keep the tensor cores and the exponential units busy in turn: while
+// one group turns its scores into weights, the other group's products run. What
+// the two groups share depends on the item:
+//   more tokens than a tile holds: group g takes query tile g, both against the
+//     same K and V tiles, so a K/V tile fetched once serves 256 query rows;
+//   one query tile: the groups take alternate key tiles of it, each with its own
+//     running maximum, sum and output, and are merged at the end.
+// A query tile packs the query heads of a KV head: row m is token m /
+// tile_heads, head m % tile_heads.
+// Warps: 0 loads Q and K, 2 loads V; 1 and 3 issue the products of group 0 and
+// 1; 4-7 and 8-11 are the groups, one query row a thread.
+//
+// Softmax. Weights are 2^(s scale log2 e - m) with a running maximum m that may
+// be stale: a tile's weights are computed with the m of the tiles before, in one
+// pass over its scores, and kept if every row's weights sum to at most 2^8;
+// otherwise the tile is done again with its own maximum, and O is rescaled.
+// Sums are fp32. The weights enter the product with V as bf16, as the tensor
+// cores want V's own type there; the sum that divides takes them unrounded, so
+// a result is off by the average of its weights' rounding errors, each at most
+// half a bf16 step.
+//
+// Every wait is bounded; on a timeout the CTA records PD_DEV_TIMEOUT, drains
+// and frees its TMEM.
+#include <math.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "pd_chunk.cuh"
+#include "pd_tc.cuh"
+
+namespace pd {
+
+namespace {
+
+constexpr int kCtThreads = 384;
+constexpr int kM = 128;  // query rows of a tile
+constexpr int kN = kChunkTcKeys;
+constexpr float kSumLimit = 256.0f;   // 2^8: largest row sum of weights taken with a stale maximum
+constexpr float kRaise = 8.0f;        // log2 of it: a maximum is raised when it grew by more
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;                // 64-column halves of a row (128 bytes each)
+  static constexpr uint32_t kHalf = kM * 128;           // one half of a 128-row tile
+  static constexpr uint32_t kTile = kHalves * kHalf;    // one Q, K or V tile
+  static constexpr int kKS = D == 128 ? 3 : 5;          // K ring
+  static constexpr int kVS = D == 128 ? 2 : 5;          // V ring
+  static constexpr uint32_t kOffK = 2 * kTile, kOffV = kOffK + kKS * kTile, kOffBar = kOffV + kVS * kTile;
+  static constexpr size_t kSmem = kOffBar + 512 + 128 * 2 * sizeof(float) + 1024;
+};
+static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t ml_ready, merged;  // group 1's maxima and sums are in shared memory; its output has been read
+  uint64_t drain;
+  uint32_t tmem_slot;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__device__ __forceinline__ uint32_t col_s(int g) { return (uint32_t)g * 128; }
+__device__ __forceinline__ uint32_t col_o(int g) { return 256u + (uint32_t)g * 128; }
+
+// Whether the item has a second query tile (else its groups share the first).
+__device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem& I) {
+  return I.tokens > p.item_tokens / 2;
+}
+
+// Key tiles of the piece that group g multiplies: all of them, or every second.
+__device__ __forceinline__ int first_tile(bool two, int g) { return two ? 0 : g; }
+
+// Lane l < boxes of a tile: the page its box lies in (read a tile ahead).
+__device__ __forceinline__ int box_page(const ChunkParams& p, const ChunkItem& I, int tile, int lane, int boxes) {
+  const int idx = tile * kN / p.page_size + lane;
+  return lane < boxes && idx < I.need ? __ldg(p.page_indices + I.pbase + idx) : 0;
+}
+
+// The halves of one 128-key tile of a pool, a box per page and half. Pages past
+// the request's end, and ids outside the pools, become page num_pages, which TMA
+// reads as zeros.
+template <int D>
+__device__ __forceinline__ void load_tile(const ChunkParams& p, const CUtensorMap* map, const ChunkItem& I, int tile,
+                                          int page, uint8_t* dst, uint64_t* bar, int lane) {
+  const int pb = p.page_size < kN ? p.page_size : kN, boxes = kN / pb;
+  const int kv_head = I.h / p.group;
+  if (tile * kN / p.page_size + lane >= I.need) {
+    page = p.num_pages;
+  } else if (page < 0 || page >= p.num_pages) {
+    if (lane < boxes) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+    page = p.num_pages;
+  }
+  if (lane == 0) mbar_arrive_expect_tx(bar, Shape<D>::kTile);
+  __syncwarp();
+  if (lane < boxes) {
+    const int soff = p.page_size > kN ? tile * kN % p.page_size : 0;
+    const int c1 = p.nhd ? kv_head : soff, c2 = p.nhd ? soff : kv_head;
+#pragma unroll
+    for (int h = 0; h < Shape<D>::kHalves; ++h)
+      tma_load_4d(dst + h * Shape<D>::kHalf + lane * pb * 128, map, 64 * h, c1, c2, page, bar);
+  }
+}
+
+// V rows of keys that no row of the item sees become zeros, so that nothing of
+// what they hold reaches O through a zero weight.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int lane) {
+  constexpr int kVec = Shape<D>::kHalves * 8;
+  for (int i = lane; i < (to - from) * kVec; i += 32) {
+    const int r = from + i / kVec, c = i % kVec;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (c / 8) * Shape<D>::kHalf + r * 128 +
+                                                                (c % 8) * 16),
+                 "r"(0)
+                 : "memory");
+  }
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kCtThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+  using S = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = base, *sK = base + S::kOffK, *sV = base + S::kOffV;
+  Bars* bars = reinterpret_cast<Bars*>(base + S::kOffBar);
+  float2* sML = reinterpret_cast<float2*>(base + S::kOffBar + 512);  // group 1's (m, l) of every row
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 2);  // each group's products are done with the item's Q
+    for (int i = 0; i < S::kKS; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 2);  // two arrivals: one of each group, or two of the only one that reads it
+    }
+    for (int i = 0; i < S::kVS; ++i) {
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bars->s_full[g], 1);
+      mbar_init(&bars->p_full[g], 4);
+      mbar_init(&bars->pv_done[g], 1);
+    }
+    mbar_init(&bars->ml_ready, 4);
+    mbar_init(&bars->merged, 4);
+    mbar_init(&bars->drain, 2);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+  pdl_wait_primary();  // the plan's work line
+  const int64_t units = p.hdr[0], parts = p.hdr[1];
+  ChunkWalk walk;
+  walk.u = walk.u1 = 0;
+  if (blockIdx.x < parts)
+    walk.seek(p, part_start(units, parts, blockIdx.x), part_start(units, parts, blockIdx.x + 1));
+  ChunkItem I;
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------- producers
+    const bool is_v = warp == 2;
+    const int boxes = p.page_size < kN ? kN / p.page_size : 1;
+    const uint32_t ring = is_v ? S::kVS : S::kKS;
+    uint32_t items = 0, ctr = 0, slot = 0, turn = 0;
+    bool ok = true;
+    while (ok && walk.next(p, I)) {
+      if (I.t1 <= I.t0) continue;
+      int page = box_page(p, I, I.tile0 + I.t0, lane, boxes);
+      if (!is_v) {
+        ok = warp_mbar_wait(&bars->q_empty, (items & 1u) ^ 1u, abort, p.status);
+        if (!ok) break;
+        ++items;
+        if (lane == 0) {
+          const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.item_tokens / 2;
+          mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(tiles * S::kHalves * tok * p.tile_heads * 128));
+          for (int x = 0; x < tiles; ++x)
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_3d(sQ + x * S::kTile + h * S::kHalf, &tm_q, 64 * h, I.h, I.q0 + x * tok, &bars->q_full);
+        }
+        __syncwarp();
+      }
+      for (int t = I.t0; t < I.t1; ++t, ++ctr) {
+        const int tile = I.tile0 + t;
+        const int next = t + 1 < I.t1 ? box_page(p, I, tile + 1, lane, boxes) : 0;
+        ok = warp_mbar_wait(is_v ? &bars->v_empty[slot] : &bars->k_empty[slot], (turn & 1u) ^ 1u, abort, p.status);
+        if (!ok) break;
+        if (is_v) load_tile<D>(p, &tm_v, I, tile, page, sV + slot * S::kTile, &bars->v_full[slot], lane);
+        else load_tile<D>(p, &tm_k, I, tile, page, sK + slot * S::kTile, &bars->k_full[slot], lane);
+        page = next;
+        if (++slot == ring) {
+          slot = 0;
+          ++turn;
+        }
+      }
+    }
+  } else if (warp == 1 || warp == 3) {
+    // -------------------------------------------------------------- products
+    const int g = warp >> 1;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0), idesc_pv = idesc_bf16_f32(kM, D, 1);
+    const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
+    const uint32_t t_s = tmem + col_s(g), t_o = tmem + col_o(g);
+    uint32_t items = 0, own = 0;                // items, and this group's tiles, so far
+    uint32_t ks = 0, kturn = 0, vs = 0, vturn = 0;  // ring places of the next tile (of either group)
+    bool ok = true;
+    while (ok && walk.next(p, I)) {
+      const int nt = I.t1 - I.t0;
+      if (nt <= 0) continue;
+      const bool two = two_tiles(p, I);
+      const int step = two ? 1 : 2;
+      ok = warp_mbar_wait(&bars->q_full, items & 1u, abort, p.status);
+      if (!ok) break;
+      ++items;
+      const uint64_t dq = sw128_desc(sQa + (two ? g : 0) * S::kTile, 16, 1024);
+      const int i0 = first_tile(two, g);
+      if (i0 >= nt && lane == 0) mbar_arrive(&bars->q_empty);
+      for (int i = 0; i < nt; ++i) {
+        if (!two && (i & 1) != g) {  // the other group's tile
+          if (++ks == S::kKS) ks = 0, ++kturn;
+          if (++vs == S::kVS) vs = 0, ++vturn;
+          continue;
+        }
+        // S = Q K^T, once the group's last product has read the weights out of the same columns
+        ok = warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status) &&
+             (own == 0 || warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dk = sw128_desc(sKa + ks * S::kTile, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
+            tc_mma_f16(t_s, desc_advance(dq, off), desc_advance(dk, off), idesc_s, kk > 0);
+          }
+          tc_commit(&bars->s_full[g]);
+          tc_commit(&bars->k_empty[ks]);
+          if (!two) tc_commit(&bars->k_empty[ks]);
+          if (i + step >= nt) tc_commit(&bars->q_empty);
+        }
+        __syncwarp();
+        // O += P V
+        ok = warp_mbar_wait(&bars->p_full[g], own & 1u, abort, p.status) &&
+             warp_mbar_wait(&bars->v_full[vs], vturn & 1u, abort, p.status);
+        if (!ok) break;
+        const int k0 = (I.tile0 + I.t0 + i) * kN;
+        const int from = max(I.keys.lo - k0, 0), to = min(I.keys.hi - k0, kN);
+        if (from > 0 || to < kN) {
+          // with two tiles both groups' warps write the same zeros
+          zero_rows<D>(sVa + vs * S::kTile, 0, from, lane);
+          zero_rows<D>(sVa + vs * S::kTile, to, kN, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dv = sw128_desc(sVa + vs * S::kTile, S::kHalf, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            tc_mma_f16_tmem_a(t_o, t_s + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, (i > i0 || kk > 0) ? 1u : 0u);
+          tc_commit(&bars->pv_done[g]);
+          tc_commit(&bars->v_empty[vs]);
+          if (!two) tc_commit(&bars->v_empty[vs]);
+        }
+        __syncwarp();
+        ++own;
+        if (++ks == S::kKS) ks = 0, ++kturn;
+        if (++vs == S::kVS) vs = 0, ++vturn;
+      }
+    }
+    // every product of this thread completes before TMEM is released
+    if (lane == 0) {
+      tc_commit(&bars->drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars->drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ----------------------------------------------------- softmax, epilogue
+    const int g = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t t_s = tmem + lanes + col_s(g);
+    uint32_t own = 0, merges = 0;
+    bool ok = true;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    while (ok && walk.next(p, I)) {
+      const int nt = max(I.t1 - I.t0, 0);
+      const bool two = two_tiles(p, I);
+      const int half_tok = p.item_tokens / 2;
+      const int tokens = two ? (g == 0 ? half_tok : I.tokens - half_tok) : I.tokens;  // of this group's tile
+      const int tok0 = two && g == 1 ? half_tok : 0;
+      const bool valid = tok_row < tokens;
+      const bool warp_valid = wq * 32 < tokens * p.tile_heads;
+      int lo = 0, hi = 0x7fffffff;  // rows that are not there are never masked and never stored
+      if (valid) {
+        const int tok = I.first_tok + tok0 + tok_row;
+        const KeyRange k = chunk_keys(p, I.qo, I.kv, tok, tok + 1);
+        lo = k.lo;
+        hi = k.hi;
+      }
+      float m = valid ? -INFINITY : 0.f, l = 0.f;
+      for (int i = first_tile(two, g); i < nt; i += two ? 1 : 2, ++own) {
+        ok = warp_mbar_wait(&bars->s_full[g], own & 1u, abort, p.status);
+        if (!ok) break;
+        if (warp_valid) {
+          tc_fence_after();
+          const int k0 = (I.tile0 + I.t0 + i) * kN;
+          const int c_lo = lo - k0, c_hi = hi - k0;
+          const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
+          // columns [c_lo, c_hi) of 32-column chunk c as a bit mask
+          auto mask_of = [&](int c) -> uint32_t {
+            const int a = min(max(c_lo - 32 * c, 0), 32), b = min(max(c_hi - 32 * c, 0), 32);
+            const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
+            const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+            return below_b & ~below_a;
+          };
+          auto load_chunk = [&](int c, uint32_t (&v)[32]) {
+            tmem_ld32(t_s + 32 * c, v);
+            tmem_wait_ld();
+            if (!full) {
+              const uint32_t keep = mask_of(c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = (keep >> e) & 1u ? v[e] : 0xff800000u;
+            }
+          };
+          uint32_t w[kN / 2];
+          float2 sum[2];
+          // weights of the tile with maximum m, as bf16 pairs, and their sum
+          auto weights = [&](float nm) {
+            const float2 nm2 = make_float2(nm, nm);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kN / 32; ++c) {
+              uint32_t v[32];
+              load_chunk(c, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nm2);
+                const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                w[16 * c + e / 2] = pack_bf16x2(pe.x, pe.y);
+                sum[(e / 2) & 1] = fadd2(sum[(e / 2) & 1], pe);
+              }
+            }
+          };
+          bool stale = __all_sync(0xffffffffu, m > -INFINITY);
+          if (stale) {
+            weights(-m);
+            const float s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            stale = !__any_sync(0xffffffffu, valid && s > kSumLimit);
+          }
+          if (!stale) {
+            // the tile's own maximum
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kN / 32; ++c) {
+              uint32_t v[32];
+              load_chunk(c, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            }
+            const float ms = mx * p.scale_log2;
+            float alpha = 1.f;
+            if (valid && mx > -INFINITY) {
+              if (m == -INFINITY) {
+                m = ms;
+              } else if (ms > m + kRaise) {
+                alpha = exp2f(m - ms);
+                m = ms;
+              }
+            }
+            // O of the tiles before is complete: this tile's scores were issued after their products
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              l *= alpha;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lanes + col_o(g) + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(tmem + lanes + col_o(g) + 32 * c, o);
+              }
+              tmem_wait_st();
+            }
+            weights(m == -INFINITY ? 0.f : -m);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_st32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(w + 0));
+          tmem_st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+        }
+        // warps without rows leave what is there: only rows that are not stored read it
+        if (lane == 0) mbar_arrive(&bars->p_full[g]);
+      }
+      if (!ok) break;
+      const bool other = !two && nt > 1;  // group 1 has tiles of the same rows
+      if (g == 1 && !two) {
+        if (nt < 2) continue;
+        ok = warp_mbar_wait(&bars->pv_done[1], (own - 1) & 1u, abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        sML[row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->ml_ready);
+        // group 0 has read this group's output: its accumulator may be written again
+        ok = warp_mbar_wait(&bars->merged, merges & 1u, abort, p.status);
+        tc_fence_after();
+        ++merges;
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (nt > 0) {
+        ok = warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status);
+        if (!ok) break;
+      }
+      if (other) {
+        ok = warp_mbar_wait(&bars->ml_ready, merges & 1u, abort, p.status);
+        if (!ok) break;
+        const float2 b = sML[row];
+        const float top = fmaxf(m, b.x), at = top == -INFINITY ? 0.f : top;
+        f0 = exp2f(m - at);
+        f1 = exp2f(b.x - at);
+        l = l * f0 + b.y * f1;
+        m = top;
+      }
+      tc_fence_after();
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const float lse2 = l != 0.f ? m + log2f(l) : -INFINITY;
+      const int64_t slot = part_slot(I, blockIdx.x);
+      const int mrow = tok0 * p.tile_heads + row;
+      const int64_t orow = (int64_t)(I.q0 + tok0 + tok_row) * p.hq + I.h + head;
+      f0 *= inv;
+      f1 *= inv;
+      if (warp_valid) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (nt > 0) {
+            tmem_ld32(tmem + lanes + col_o(g) + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          }
+          if (other) {
+            uint32_t b[32];
+            tmem_ld32(tmem + lanes + col_o(1) + 32 * c, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(b[e]) * f1);
+          }
+          if (valid) {
+            if (slot < 0 && p.o_dtype == PD_BF16) {
+              uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 u;
+                u.x = pack_bf16x2(__uint_as_float(v[8 * e + 0]), __uint_as_float(v[8 * e + 1]));
+                u.y = pack_bf16x2(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+                u.z = pack_bf16x2(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+                u.w = pack_bf16x2(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+                o[e] = u;
+              }
+            } else {
+              float* o = (slot < 0 ? static_cast<float*>(p.o) + orow * D : p.part_o + (slot * p.rows + mrow) * D) +
+                         32 * c;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(o + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+          }
+        }
+      }
+      if (valid) {
+        if (slot >= 0) p.part_lse[slot * p.rows + mrow] = lse2;
+        else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (other) {
+        if (lane == 0) mbar_arrive(&bars->merged);
+        ++merges;
+      }
+    }
+  }
+
+  // Normally every copy has been consumed here. After an abort, copies may still
+  // be in flight: give them a bounded 2 ms to land before shared memory is freed.
+  if (*abort && warp == 0 && lane == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+
+template <int D>
+cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t stream) {
+  auto kernel = chunk_tc_kernel<D>;
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.max_parts);
+  cfg.blockDim = dim3(kCtThreads);
+  cfg.dynamicSmemBytes = Shape<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  const int pb = p.page_size < kN ? p.page_size : kN;
+  if (!make_rows_map(&tq, p.q, PD_BF16, p.total_qo, p.hq, p.head_dim, 64, p.item_tokens / 2, true, p.tile_heads,
+                     p.q_stride) ||
+      !make_pool_map(&tk, p.k_pool, PD_BF16, p.num_pages, p.hkv, p.page_size, p.head_dim, 64, pb, true, p.nhd != 0) ||
+      !make_pool_map(&tv, p.v_pool, PD_BF16, p.num_pages, p.hkv, p.page_size, p.head_dim, 64, pb, true, p.nhd != 0))
+    return cudaErrorInvalidValue;
+  last_kernel() = "chunk_tc_kernel";
+  profile_begin(stream);
+  const cudaError_t e = p.head_dim == 64 ? launch_d<64>(p, tq, tk, tv, stream) : launch_d<128>(p, tq, tk, tv, stream);
+  profile_end(stream);
+  return e;
+}
+
+}  // namespace pd

@@ -242,7 +242,8 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 struct ChunkParams {
   int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
   int32_t causal, window, o_dtype, nhd;
-  int32_t tile_heads, item_heads, item_tokens, key_tile, item_cost, rows, max_blocks, max_parts;
+  int32_t tc;  // the tensor-core kernel takes the call
+  int32_t tile_heads, item_heads, item_tokens, key_tile, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)
   int64_t q_stride;  // elements between query tokens
   const int32_t* qo_indptr;
@@ -267,13 +268,16 @@ struct ChunkLayout {
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
+constexpr int kChunkTcKeys = 128;  // keys of a tensor-core tile
+cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
 bool make_pool_map(CUtensorMap* map, const void* pool, int32_t dtype, int32_t num_pages, int32_t hkv,
                    int32_t page_size, int32_t head_dim, int32_t box_cols, int32_t box_rows, bool swizzle128,
                    bool nhd = false);
 bool make_rows_map(CUtensorMap* map, const void* base, int32_t dtype, int32_t total, int32_t hq, int32_t head_dim,
-                   int32_t box_cols, int32_t box_rows, bool swizzle128, int32_t box_heads = 1);
+                   int32_t box_cols, int32_t box_rows, bool swizzle128, int32_t box_heads = 1,
+                   int64_t row_stride = 0);
 
 // ------------------------------------------------------------------- misc
 // SMs of the device, or of the SM partition (green context) the calling thread
