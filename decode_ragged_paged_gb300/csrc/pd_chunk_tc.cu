@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     mbar_init(&bars->q_empty, 2);  // each group's products are done with the item's Q
     for (int i = 0; i < S::kKS; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 2);  // two arrivals: one of each group, or two of the only one that reads it
+      mbar_init(&bars->k_empty[i], 2);  // one of each group, or two of the only one that reads it
     }
     for (int i = 0; i < S::kVS; ++i) {
       mbar_init(&bars->v_full[i], 1);
@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int g = warp >> 1;
     constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0), idesc_pv = idesc_bf16_f32(kM, D, 1);
     const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-    const uint32_t t_s = tmem + col_s(g), t_o = tmem + col_o(g);
-    uint32_t items = 0, own = 0;                // items, and this group's tiles, so far
+    const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g), 0);
+    const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
+    uint32_t items = 0, own = 0;                    // items, and this group's tiles, so far
     uint32_t ks = 0, kturn = 0, vs = 0, vturn = 0;  // ring places of the next tile (of either group)
     bool ok = true;
     while (ok && walk.next(p, I)) {
@@ -236,9 +237,19 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       ok = warp_mbar_wait(&bars->q_full, items & 1u, abort, p.status);
       if (!ok) break;
       ++items;
-      const uint64_t dq = sw128_desc(sQa + (two ? g : 0) * S::kTile, 16, 1024);
+      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + (two ? g : 0) * S::kTile, 0), 16, 1024);
       const int i0 = first_tile(two, g);
       if (i0 >= nt && lane == 0) mbar_arrive(&bars->q_empty);
+      uint32_t held = 0;  // V slot of the group's product under way
+      // That product done: its V slot, and the columns that held its weights, are free.
+      auto finish = [&]() -> bool {
+        if (!warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status)) return false;
+        if (lane == 0) {
+          mbar_arrive(&bars->v_empty[held]);
+          if (!two) mbar_arrive(&bars->v_empty[held]);
+        }
+        return true;
+      };
       for (int i = 0; i < nt; ++i) {
         if (!two && (i & 1) != g) {  // the other group's tile
           if (++ks == S::kKS) ks = 0, ++kturn;
@@ -246,20 +257,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           continue;
         }
         // S = Q K^T, once the group's last product has read the weights out of the same columns
-        ok = warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status) &&
-             (own == 0 || warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status));
+        ok = (i == i0 || finish()) && warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dk = sw128_desc(sKa + ks * S::kTile, 16, 1024);
+        const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, sKa + ks * S::kTile, 0), 16, 1024);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
             tc_mma_f16(t_s, desc_advance(dq, off), desc_advance(dk, off), idesc_s, kk > 0);
           }
           tc_commit(&bars->s_full[g]);
-          tc_commit(&bars->k_empty[ks]);
-          if (!two) tc_commit(&bars->k_empty[ks]);
           if (i + step >= nt) tc_commit(&bars->q_empty);
         }
         __syncwarp();
@@ -277,23 +285,24 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           __syncwarp();
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dv = sw128_desc(sVa + vs * S::kTile, S::kHalf, 1024);
+        const uint64_t dv = sw128_desc(__shfl_sync(0xffffffffu, sVa + vs * S::kTile, 0), S::kHalf, 1024);
+        const uint32_t more = __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kN / 16; ++kk)
-            tc_mma_f16_tmem_a(t_o, t_s + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, (i > i0 || kk > 0) ? 1u : 0u);
+            tc_mma_f16_tmem_a(t_o, t_s + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
           tc_commit(&bars->pv_done[g]);
-          tc_commit(&bars->v_empty[vs]);
-          if (!two) tc_commit(&bars->v_empty[vs]);
         }
         __syncwarp();
+        held = vs;
         ++own;
         if (++ks == S::kKS) ks = 0, ++kturn;
         if (++vs == S::kVS) vs = 0, ++vturn;
       }
+      if (ok && i0 < nt) ok = finish();
     }
-    // every product of this thread completes before TMEM is released
-    if (lane == 0) {
+    // every product completes before TMEM is released; after an abort some may be under way
+    if (elect_one()) {
       tc_commit(&bars->drain);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(&bars->drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t t_s = tmem + lanes + col_s(g);
-    uint32_t own = 0, merges = 0;
+    uint32_t own = 0, merges = 0, ks = 0;  // ks: K slot of the next tile (of either group)
     bool ok = true;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     while (ok && walk.next(p, I)) {
@@ -325,9 +334,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         hi = k.hi;
       }
       float m = valid ? -INFINITY : 0.f, l = 0.f;
-      for (int i = first_tile(two, g); i < nt; i += two ? 1 : 2, ++own) {
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t slot = ks;
+        if (++ks == S::kKS) ks = 0;
+        if (!two && (i & 1) != g) continue;  // the other group's tile
         ok = warp_mbar_wait(&bars->s_full[g], own & 1u, abort, p.status);
         if (!ok) break;
+        ++own;
+        if (wq == 0 && lane == 0) {  // the scores are there: the group is done with the K tile
+          mbar_arrive(&bars->k_empty[slot]);
+          if (!two) mbar_arrive(&bars->k_empty[slot]);
+        }
         if (warp_valid) {
           tc_fence_after();
           const int k0 = (I.tile0 + I.t0 + i) * kN;
@@ -340,14 +357,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
             return below_b & ~below_a;
           };
-          auto load_chunk = [&](int c, uint32_t (&v)[32]) {
-            tmem_ld32(t_s + 32 * c, v);
-            tmem_wait_ld();
-            if (!full) {
-              const uint32_t keep = mask_of(c);
+          auto hide = [&](int c, uint32_t (&v)[32]) {
+            if (full) return;
+            const uint32_t keep = mask_of(c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (keep >> e) & 1u ? v[e] : 0xff800000u;
-            }
+            for (int e = 0; e < 32; ++e) v[e] = (keep >> e) & 1u ? v[e] : 0xff800000u;
           };
           uint32_t w[kN / 2];
           float2 sum[2];
@@ -355,17 +369,23 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           auto weights = [&](float nm) {
             const float2 nm2 = make_float2(nm, nm);
             sum[0] = sum[1] = make_float2(0.f, 0.f);
+            // the next 32 scores are on their way while these are worked on
+            uint32_t v[2][32];
+            tmem_ld32(t_s, v[0]);
+            tmem_wait_ld(v[0]);
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-              uint32_t v[32];
-              load_chunk(c, v);
+              if (c + 1 < kN / 32) tmem_ld32(t_s + 32 * (c + 1), v[(c + 1) & 1]);
+              hide(c, v[c & 1]);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nm2);
+                const float2 x = ffma2(
+                    make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])), sc2, nm2);
                 const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 w[16 * c + e / 2] = pack_bf16x2(pe.x, pe.y);
                 sum[(e / 2) & 1] = fadd2(sum[(e / 2) & 1], pe);
               }
+              if (c + 1 < kN / 32) tmem_wait_ld(v[(c + 1) & 1]);
             }
           };
           bool stale = __all_sync(0xffffffffu, m > -INFINITY);
@@ -380,7 +400,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
               uint32_t v[32];
-              load_chunk(c, v);
+              tmem_ld32(t_s + 32 * c, v);
+              tmem_wait_ld(v);
+              hide(c, v);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
             }
@@ -401,7 +423,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lanes + col_o(g) + 32 * c, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                 tmem_st32(tmem + lanes + col_o(g) + 32 * c, o);
@@ -466,7 +488,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           uint32_t v[32];
           if (nt > 0) {
             tmem_ld32(tmem + lanes + col_o(g) + 32 * c, v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
           } else {
@@ -476,7 +498,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           if (other) {
             uint32_t b[32];
             tmem_ld32(tmem + lanes + col_o(1) + 32 * c, b);
-            tmem_wait_ld();
+            tmem_wait_ld(b);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(b[e]) * f1);
