@@ -390,8 +390,8 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.item_tokens = 2 * (128 / p.tile_heads);  // two query tiles
     p.rows = p.item_tokens * p.tile_heads;
     p.key_tile = kChunkTcKeys;
-    p.item_cost = 1;
-    p.min_units = 2;
+    p.item_cost = 2;
+    p.min_units = 4;
     p.max_parts = device_sm_count();
   } else {
     // Rows of an item: 16 where no request has more, else 64 (a 64-row tile with

@@ -48,19 +48,18 @@ constexpr float kRaise = 8.0f;        // log2 of it: a maximum is raised when it
 template <int D>
 struct Shape {
   static constexpr int kHalves = D / 64;                // 64-column halves of a row (128 bytes each)
-  static constexpr uint32_t kHalf = kM * 128;           // one half of a 128-row tile
-  static constexpr uint32_t kTile = kHalves * kHalf;    // one Q, K or V tile
-  static constexpr int kKS = D == 128 ? 3 : 5;          // K ring
-  static constexpr int kVS = D == 128 ? 2 : 5;          // V ring
-  static constexpr uint32_t kOffK = 2 * kTile, kOffV = kOffK + kKS * kTile, kOffBar = kOffV + kVS * kTile;
+  static constexpr uint32_t kQHalf = kM * 128, kQTile = kHalves * kQHalf;  // query tiles
+  static constexpr uint32_t kHalf = kN * 128, kTile = kHalves * kHalf;     // K and V tiles
+  static constexpr int kRing = D == 128 ? 5 : 8;        // slots of the K ring and of the V ring
+  static constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kRing * kTile, kOffBar = kOffV + kRing * kTile;
   static constexpr size_t kSmem = kOffBar + 512 + 128 * 2 * sizeof(float) + 1024;
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [group][S buffer]
   uint64_t ml_ready, merged;  // group 1's maxima and sums are in shared memory; its output has been read
   uint64_t drain;
   uint32_t tmem_slot;
@@ -68,16 +67,14 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-__device__ __forceinline__ uint32_t col_s(int g) { return (uint32_t)g * 128; }
+// TMEM: two S / P buffers of 64 columns a group, then the groups' O accumulators.
+__device__ __forceinline__ uint32_t col_s(int g, uint32_t buf) { return (uint32_t)(2 * g + buf) * kN; }
 __device__ __forceinline__ uint32_t col_o(int g) { return 256u + (uint32_t)g * 128; }
 
 // Whether the item has a second query tile (else its groups share the first).
 __device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem& I) {
   return I.tokens > p.item_tokens / 2;
 }
-
-// Key tiles of the piece that group g multiplies: all of them, or every second.
-__device__ __forceinline__ int first_tile(bool two, int g) { return two ? 0 : g; }
 
 // Lane l < boxes of a tile: the page its box lies in (read a tile ahead).
 __device__ __forceinline__ int box_page(const ChunkParams& p, const ChunkItem& I, int tile, int lane, int boxes) {
@@ -142,18 +139,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 2);  // each group's products are done with the item's Q
-    for (int i = 0; i < S::kKS; ++i) {
+    for (int i = 0; i < S::kRing; ++i) {
       mbar_init(&bars->k_full[i], 1);
       mbar_init(&bars->k_empty[i], 2);  // one of each group, or two of the only one that reads it
-    }
-    for (int i = 0; i < S::kVS; ++i) {
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 2);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(&bars->s_full[g], 1);
-      mbar_init(&bars->p_full[g], 4);
-      mbar_init(&bars->pv_done[g], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
+      mbar_init(&bars->p_full[i >> 1][i & 1], 4);
+      mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
     mbar_init(&bars->ml_ready, 4);
     mbar_init(&bars->merged, 4);
@@ -186,7 +181,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // ------------------------------------------------------------- producers
     const bool is_v = warp == 2;
     const int boxes = p.page_size < kN ? kN / p.page_size : 1;
-    const uint32_t ring = is_v ? S::kVS : S::kKS;
     uint32_t items = 0, ctr = 0, slot = 0, turn = 0;
     bool ok = true;
     while (ok && walk.next(p, I)) {
@@ -201,7 +195,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(tiles * S::kHalves * tok * p.tile_heads * 128));
           for (int x = 0; x < tiles; ++x)
             for (int h = 0; h < S::kHalves; ++h)
-              tma_load_3d(sQ + x * S::kTile + h * S::kHalf, &tm_q, 64 * h, I.h, I.q0 + x * tok, &bars->q_full);
+              tma_load_3d(sQ + x * S::kQTile + h * S::kQHalf, &tm_q, 64 * h, I.h, I.q0 + x * tok, &bars->q_full);
         }
         __syncwarp();
       }
@@ -213,7 +207,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (is_v) load_tile<D>(p, &tm_v, I, tile, page, sV + slot * S::kTile, &bars->v_full[slot], lane);
         else load_tile<D>(p, &tm_k, I, tile, page, sK + slot * S::kTile, &bars->k_full[slot], lane);
         page = next;
-        if (++slot == ring) {
+        if (++slot == S::kRing) {
           slot = 0;
           ++turn;
         }
@@ -221,58 +215,71 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
   } else if (warp == 1 || warp == 3) {
     // -------------------------------------------------------------- products
+    // A group's scores run two tiles ahead of its weights, in two buffers: tile
+    // n + 2's are issued once tile n's product with V has read its weights out
+    // of the same columns.
     const int g = warp >> 1;
     constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0), idesc_pv = idesc_bf16_f32(kM, D, 1);
     const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-    const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g), 0);
     const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
-    uint32_t items = 0, own = 0;                    // items, and this group's tiles, so far
-    uint32_t ks = 0, kturn = 0, vs = 0, vturn = 0;  // ring places of the next tile (of either group)
+    uint32_t items = 0, own = 0;                    // items, and this group's products with V, so far
+    uint32_t ks = 0, kturn = 0, vs = 0, vturn = 0;  // ring places of the next K and V tile (of either group)
     bool ok = true;
     while (ok && walk.next(p, I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const bool two = two_tiles(p, I);
-      const int step = two ? 1 : 2;
+      const int step = two ? 1 : 2, i0 = two ? 0 : g;
       ok = warp_mbar_wait(&bars->q_full, items & 1u, abort, p.status);
       if (!ok) break;
       ++items;
-      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + (two ? g : 0) * S::kTile, 0), 16, 1024);
-      const int i0 = first_tile(two, g);
+      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + (two ? g : 0) * S::kQTile, 0), 16, 1024);
       if (i0 >= nt && lane == 0) mbar_arrive(&bars->q_empty);
-      uint32_t held = 0;  // V slot of the group's product under way
-      // That product done: its V slot, and the columns that held its weights, are free.
-      auto finish = [&]() -> bool {
-        if (!warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status)) return false;
-        if (lane == 0) {
-          mbar_arrive(&bars->v_empty[held]);
-          if (!two) mbar_arrive(&bars->v_empty[held]);
-        }
-        return true;
+      // moves n tiles on in a ring
+      auto advance = [](uint32_t& slot, uint32_t& turn, int n) {
+        slot += n;
+        if (slot >= S::kRing) slot -= S::kRing, ++turn;
       };
-      for (int i = 0; i < nt; ++i) {
-        if (!two && (i & 1) != g) {  // the other group's tile
-          if (++ks == S::kKS) ks = 0, ++kturn;
-          if (++vs == S::kVS) vs = 0, ++vturn;
-          continue;
-        }
-        // S = Q K^T, once the group's last product has read the weights out of the same columns
-        ok = (i == i0 || finish()) && warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status);
-        if (!ok) break;
+      uint32_t issued = own;  // scores issued so far
+      // S = Q K^T of the piece's tile i
+      auto scores = [&](int i) -> bool {
+        if (!warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status)) return false;
         tc_fence_after();
         const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, sKa + ks * S::kTile, 0), 16, 1024);
+        const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g, issued & 1u), 0);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
-            tc_mma_f16(t_s, desc_advance(dq, off), desc_advance(dk, off), idesc_s, kk > 0);
-          }
-          tc_commit(&bars->s_full[g]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_f16(t_s, desc_advance(dq, (kk / 4) * S::kQHalf + (kk % 4) * 32),
+                       desc_advance(dk, (kk / 4) * S::kHalf + (kk % 4) * 32), idesc_s, kk > 0);
+          tc_commit(&bars->s_full[g][issued & 1u]);
           if (i + step >= nt) tc_commit(&bars->q_empty);
         }
         __syncwarp();
+        ++issued;
+        // the other group's tile between is passed over; the last step may end past the piece
+        advance(ks, kturn, i + step <= nt ? step : nt - i);
+        return true;
+      };
+      uint32_t held[2] = {0, 0};  // V slots of the last two products
+      // Product n (of the group) done: its V slot, and the columns that held its weights, are free.
+      auto finish = [&](uint32_t n) -> bool {
+        if (!warp_mbar_wait(&bars->pv_done[g][n & 1u], (n >> 1) & 1u, abort, p.status)) return false;
+        if (lane == 0) {
+          const uint32_t slot = (n & 1u) ? held[1] : held[0];
+          mbar_arrive(&bars->v_empty[slot]);
+          if (!two) mbar_arrive(&bars->v_empty[slot]);
+        }
+        return true;
+      };
+      advance(ks, kturn, min(i0, nt));
+      advance(vs, vturn, min(i0, nt));
+      for (int i = i0; ok && i < min(nt, i0 + 2 * step); i += step) ok = scores(i);
+      const uint32_t first = own;
+      for (int i = i0; ok && i < nt; i += step) {
         // O += P V
-        ok = warp_mbar_wait(&bars->p_full[g], own & 1u, abort, p.status) &&
+        const uint32_t buf = own & 1u;
+        ok = warp_mbar_wait(&bars->p_full[g][buf], (own >> 1) & 1u, abort, p.status) &&
              warp_mbar_wait(&bars->v_full[vs], vturn & 1u, abort, p.status);
         if (!ok) break;
         const int k0 = (I.tile0 + I.t0 + i) * kN;
@@ -286,20 +293,23 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tc_fence_after();
         const uint64_t dv = sw128_desc(__shfl_sync(0xffffffffu, sVa + vs * S::kTile, 0), S::kHalf, 1024);
+        const uint32_t t_p = __shfl_sync(0xffffffffu, tmem + col_s(g, buf), 0);
         const uint32_t more = __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kN / 16; ++kk)
-            tc_mma_f16_tmem_a(t_o, t_s + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
-          tc_commit(&bars->pv_done[g]);
+            tc_mma_f16_tmem_a(t_o, t_p + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
+          tc_commit(&bars->pv_done[g][buf]);
         }
         __syncwarp();
-        held = vs;
+        if (buf) held[1] = vs;
+        else held[0] = vs;
+        advance(vs, vturn, i + step <= nt ? step : nt - i);
         ++own;
-        if (++ks == S::kKS) ks = 0, ++kturn;
-        if (++vs == S::kVS) vs = 0, ++vturn;
+        if (i + 2 * step < nt) ok = finish(own - 1) && scores(i + 2 * step);
       }
-      if (ok && i0 < nt) ok = finish();
+      // the products whose columns no score of this item has taken
+      for (uint32_t n = own - min(own - first, 2u); ok && n < own; ++n) ok = finish(n);
     }
     // every product completes before TMEM is released; after an abort some may be under way
     if (elect_one()) {
@@ -314,7 +324,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int g = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t t_s = tmem + lanes + col_s(g);
     uint32_t own = 0, merges = 0, ks = 0;  // ks: K slot of the next tile (of either group)
     bool ok = true;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
@@ -336,9 +345,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       float m = valid ? -INFINITY : 0.f, l = 0.f;
       for (int i = 0; i < nt; ++i) {
         const uint32_t slot = ks;
-        if (++ks == S::kKS) ks = 0;
+        if (++ks == S::kRing) ks = 0;
         if (!two && (i & 1) != g) continue;  // the other group's tile
-        ok = warp_mbar_wait(&bars->s_full[g], own & 1u, abort, p.status);
+        const uint32_t buf = own & 1u, t_s = tmem + lanes + col_s(g, buf);
+        ok = warp_mbar_wait(&bars->s_full[g][buf], (own >> 1) & 1u, abort, p.status);
         if (!ok) break;
         ++own;
         if (wq == 0 && lane == 0) {  // the scores are there: the group is done with the K tile
@@ -369,23 +379,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           auto weights = [&](float nm) {
             const float2 nm2 = make_float2(nm, nm);
             sum[0] = sum[1] = make_float2(0.f, 0.f);
-            // the next 32 scores are on their way while these are worked on
             uint32_t v[2][32];
             tmem_ld32(t_s, v[0]);
+            tmem_ld32(t_s + 32, v[1]);
             tmem_wait_ld(v[0]);
+            tmem_wait_ld(v[1]);
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-              if (c + 1 < kN / 32) tmem_ld32(t_s + 32 * (c + 1), v[(c + 1) & 1]);
-              hide(c, v[c & 1]);
+              hide(c, v[c]);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float2 x = ffma2(
-                    make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])), sc2, nm2);
+                const float2 x =
+                    ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
                 const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 w[16 * c + e / 2] = pack_bf16x2(pe.x, pe.y);
                 sum[(e / 2) & 1] = fadd2(sum[(e / 2) & 1], pe);
               }
-              if (c + 1 < kN / 32) tmem_wait_ld(v[(c + 1) & 1]);
             }
           };
           bool stale = __all_sync(0xffffffffu, m > -INFINITY);
@@ -416,8 +425,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 m = ms;
               }
             }
-            // O of the tiles before is complete: this tile's scores were issued after their products
             if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              // the product of the tile before (own counts this one already) is under way
+              ok = warp_mbar_wait(&bars->pv_done[g][(own - 2) & 1u], ((own - 2) >> 1) & 1u, abort, p.status);
+              if (!ok) break;
+              tc_fence_after();
               l *= alpha;
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
@@ -433,20 +445,19 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             weights(m == -INFINITY ? 0.f : -m);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          tmem_st32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(w + 0));
-          tmem_st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+          tmem_st32(t_s, w);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
         }
         // warps without rows leave what is there: only rows that are not stored read it
-        if (lane == 0) mbar_arrive(&bars->p_full[g]);
+        if (lane == 0) mbar_arrive(&bars->p_full[g][buf]);
       }
       if (!ok) break;
       const bool other = !two && nt > 1;  // group 1 has tiles of the same rows
       if (g == 1 && !two) {
         if (nt < 2) continue;
-        ok = warp_mbar_wait(&bars->pv_done[1], (own - 1) & 1u, abort, p.status);
+        ok = warp_mbar_wait(&bars->pv_done[1][(own - 1) & 1u], ((own - 1) >> 1) & 1u, abort, p.status);
         if (!ok) break;
         tc_fence_after();
         sML[row] = make_float2(m, l);
@@ -461,7 +472,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       }
       float f0 = 1.f, f1 = 0.f;
       if (nt > 0) {
-        ok = warp_mbar_wait(&bars->pv_done[g], (own - 1) & 1u, abort, p.status);
+        ok = warp_mbar_wait(&bars->pv_done[g][(own - 1) & 1u], ((own - 1) >> 1) & 1u, abort, p.status);
         if (!ok) break;
       }
       if (other) {

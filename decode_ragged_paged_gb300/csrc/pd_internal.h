@@ -268,7 +268,7 @@ struct ChunkLayout {
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
-constexpr int kChunkTcKeys = 128;  // keys of a tensor-core tile
+constexpr int kChunkTcKeys = 64;  // keys of a tensor-core tile
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
