@@ -13,8 +13,10 @@
 //     running maximum, sum and output, and are merged at the end.
 // A query tile packs the query heads of a KV head: row m is token m /
 // tile_heads, head m % tile_heads.
-// Warps: 0 loads Q and K, 2 loads V; 1 and 3 issue the products of group 0 and
-// 1; 4-7 and 8-11 are the groups, one query row a thread.
+// Warps: 0 loads K, 2 V and 4 Q; 1 and 5 issue the products with K of group 0
+// and 1, 3 and 7 those with V (each issuer waits only for its own group: with one
+// for both, a group that is late held up the other); 8-11 and 12-15 are the
+// groups, one query row a thread.
 //
 // Softmax. Weights are 2^(s scale log2 e - m) with a running maximum m that may
 // be stale: a tile's weights are computed with the m of the tiles before, in one
@@ -39,7 +41,7 @@ namespace pd {
 
 namespace {
 
-constexpr int kCtThreads = 384;
+constexpr int kCtThreads = 512;
 constexpr int kM = 128;  // query rows of a tile
 constexpr int kN = kChunkTcKeys;
 constexpr float kSumLimit = 256.0f;   // 2^8: largest row sum of weights taken with a stale maximum
@@ -51,13 +53,18 @@ struct Shape {
   static constexpr uint32_t kQHalf = kM * 128, kQTile = kHalves * kQHalf;  // query tiles
   static constexpr uint32_t kHalf = kN * 128, kTile = kHalves * kHalf;     // K and V tiles
   static constexpr int kRing = D == 128 ? 5 : 8;        // slots of the K ring and of the V ring
-  static constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kRing * kTile, kOffBar = kOffV + kRing * kTile;
+  static constexpr int kQ = D == 128 ? 2 : 4;           // slots of the Q ring
+  static constexpr uint32_t kOffK = kQ * kQTile, kOffV = kOffK + kRing * kTile, kOffBar = kOffV + kRing * kTile;
   static constexpr size_t kSmem = kOffBar + 512 + 128 * 2 * sizeof(float) + 1024;
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
+// Slots of the Q, K and V rings are freed by one arrival of each group. A group
+// waits for every slot's every fill, its own or not, and then frees it, at once
+// if the tile is the other group's: were it to pass over a fill without waiting,
+// it could look at a barrier two phases early, where a parity wait lets it by.
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[4], q_empty[4];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [group][S buffer]
   uint64_t ml_ready, merged;  // group 1's maxima and sums are in shared memory; its output has been read
@@ -76,13 +83,8 @@ __device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem&
   return I.tokens > p.item_tokens / 2;
 }
 
-// Lane l < boxes of a tile: the page its box lies in (read a tile ahead).
-__device__ __forceinline__ int box_page(const ChunkParams& p, const ChunkItem& I, int tile, int lane, int boxes) {
-  const int idx = tile * kN / p.page_size + lane;
-  return lane < boxes && idx < I.need ? __ldg(p.page_indices + I.pbase + idx) : 0;
-}
-
-// The halves of one 128-key tile of a pool, a box per page and half. Pages past
+// The halves of one key tile of a pool, a box per page and half: lane l loads
+// the box of the tile's page l. Pages past
 // the request's end, and ids outside the pools, become page num_pages, which TMA
 // reads as zeros.
 template <int D>
@@ -137,11 +139,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 2);  // each group's products are done with the item's Q
+    for (int i = 0; i < S::kQ; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 2);  // the tile's last scores are there
+    }
     for (int i = 0; i < S::kRing; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 2);  // one of each group, or two of the only one that reads it
+      mbar_init(&bars->k_empty[i], 2);
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 2);
     }
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
     mbar_init(&bars->ml_ready, 4);
     mbar_init(&bars->merged, 4);
-    mbar_init(&bars->drain, 2);
+    mbar_init(&bars->drain, 4);
     bars->abort = 0;
     fence_barrier_init();
   }
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
   }
-  if (warp == 1) {
+  if (warp == 6) {
     tmem_alloc(&bars->tmem_slot, 512);
     tmem_relinquish();
   }
@@ -175,142 +179,160 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   walk.u = walk.u1 = 0;
   if (blockIdx.x < parts)
     walk.seek(p, part_start(units, parts, blockIdx.x), part_start(units, parts, blockIdx.x + 1));
-  ChunkItem I;
+  ChunkItem I{};
 
   if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------- producers
+    // ----------------------------------------------------------- K, V loads
+    // Page ids are read 32 at a time, a window ahead: lane l holds the id of the
+    // request's page 32 w + l.
     const bool is_v = warp == 2;
     const int boxes = p.page_size < kN ? kN / p.page_size : 1;
-    uint32_t items = 0, ctr = 0, slot = 0, turn = 0;
+    uint32_t slot = 0, turn = 0;
     bool ok = true;
+    auto window = [&](int w) -> int {
+      const int idx = 32 * w + lane;
+      return idx < I.need ? __ldg(p.page_indices + I.pbase + idx) : 0;
+    };
     while (ok && walk.next(p, I)) {
       if (I.t1 <= I.t0) continue;
-      int page = box_page(p, I, I.tile0 + I.t0, lane, boxes);
-      if (!is_v) {
-        ok = warp_mbar_wait(&bars->q_empty, (items & 1u) ^ 1u, abort, p.status);
-        if (!ok) break;
-        ++items;
-        if (lane == 0) {
-          const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.item_tokens / 2;
-          mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(tiles * S::kHalves * tok * p.tile_heads * 128));
-          for (int x = 0; x < tiles; ++x)
-            for (int h = 0; h < S::kHalves; ++h)
-              tma_load_3d(sQ + x * S::kQTile + h * S::kQHalf, &tm_q, 64 * h, I.h, I.q0 + x * tok, &bars->q_full);
+      int win = (I.tile0 + I.t0) * kN / p.page_size >> 5;
+      int ids = window(win), ahead = window(win + 1);
+      for (int t = I.t0; t < I.t1; ++t) {
+        const int tile = I.tile0 + t, idx = tile * kN / p.page_size;
+        if ((idx >> 5) != win) {
+          win = idx >> 5;
+          ids = ahead;
+          ahead = window(win + 1);
         }
-        __syncwarp();
-      }
-      for (int t = I.t0; t < I.t1; ++t, ++ctr) {
-        const int tile = I.tile0 + t;
-        const int next = t + 1 < I.t1 ? box_page(p, I, tile + 1, lane, boxes) : 0;
+        // a tile's pages lie in one window: there is one, or a power of two of them up to 8
+        const int page = __shfl_sync(0xffffffffu, ids, (idx + (lane < boxes ? lane : 0)) & 31);
         ok = warp_mbar_wait(is_v ? &bars->v_empty[slot] : &bars->k_empty[slot], (turn & 1u) ^ 1u, abort, p.status);
         if (!ok) break;
         if (is_v) load_tile<D>(p, &tm_v, I, tile, page, sV + slot * S::kTile, &bars->v_full[slot], lane);
         else load_tile<D>(p, &tm_k, I, tile, page, sK + slot * S::kTile, &bars->k_full[slot], lane);
-        page = next;
-        if (++slot == S::kRing) {
-          slot = 0;
-          ++turn;
-        }
+        if (++slot == S::kRing) slot = 0, ++turn;
       }
     }
-  } else if (warp == 1 || warp == 3) {
-    // -------------------------------------------------------------- products
-    // A group's scores run two tiles ahead of its weights, in two buffers: tile
-    // n + 2's are issued once tile n's product with V has read its weights out
-    // of the same columns.
-    const int g = warp >> 1;
-    constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0), idesc_pv = idesc_bf16_f32(kM, D, 1);
-    const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-    const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
-    uint32_t items = 0, own = 0;                    // items, and this group's products with V, so far
-    uint32_t ks = 0, kturn = 0, vs = 0, vturn = 0;  // ring places of the next K and V tile (of either group)
+  } else if (warp == 4) {
+    // --------------------------------------------------------------- Q loads
+    uint32_t q = 0, qturn = 0;
+    bool ok = true;
+    while (ok && walk.next(p, I)) {
+      if (I.t1 <= I.t0) continue;
+      const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.item_tokens / 2;
+      for (int x = 0; ok && x < tiles; ++x) {
+        ok = warp_mbar_wait(&bars->q_empty[q], (qturn & 1u) ^ 1u, abort, p.status);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[q], (uint32_t)(S::kHalves * tok * p.tile_heads * 128));
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(sQ + q * S::kQTile + h * S::kQHalf, &tm_q, 64 * h, I.h, I.q0 + x * tok, &bars->q_full[q]);
+        }
+        __syncwarp();
+        if (++q == S::kQ) q = 0, ++qturn;
+      }
+    }
+  } else if (warp == 1 || warp == 5) {
+    // -------------------------------------------------------------- S = Q K^T
+    // A group's scores run two tiles ahead of its weights, in two buffers: a
+    // tile's are issued once the product with V of the tile two before has read
+    // its weights out of the same columns.
+    const int g = warp >> 2;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);
+    const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
+    uint32_t q = 0, qturn = 0, ks = 0, kturn = 0;
+    uint32_t own = 0;  // scores issued
     bool ok = true;
     while (ok && walk.next(p, I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const bool two = two_tiles(p, I);
-      const int step = two ? 1 : 2, i0 = two ? 0 : g;
-      ok = warp_mbar_wait(&bars->q_full, items & 1u, abort, p.status);
-      if (!ok) break;
-      ++items;
-      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + (two ? g : 0) * S::kQTile, 0), 16, 1024);
-      if (i0 >= nt && lane == 0) mbar_arrive(&bars->q_empty);
-      // moves n tiles on in a ring
-      auto advance = [](uint32_t& slot, uint32_t& turn, int n) {
-        slot += n;
-        if (slot >= S::kRing) slot -= S::kRing, ++turn;
-      };
-      uint32_t issued = own;  // scores issued so far
-      // S = Q K^T of the piece's tile i
-      auto scores = [&](int i) -> bool {
-        if (!warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status)) return false;
-        tc_fence_after();
-        const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, sKa + ks * S::kTile, 0), 16, 1024);
-        const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g, issued & 1u), 0);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_f16(t_s, desc_advance(dq, (kk / 4) * S::kQHalf + (kk % 4) * 32),
-                       desc_advance(dk, (kk / 4) * S::kHalf + (kk % 4) * 32), idesc_s, kk > 0);
-          tc_commit(&bars->s_full[g][issued & 1u]);
-          if (i + step >= nt) tc_commit(&bars->q_empty);
-        }
-        __syncwarp();
-        ++issued;
-        // the other group's tile between is passed over; the last step may end past the piece
-        advance(ks, kturn, i + step <= nt ? step : nt - i);
-        return true;
-      };
-      uint32_t held[2] = {0, 0};  // V slots of the last two products
-      // Product n (of the group) done: its V slot, and the columns that held its weights, are free.
-      auto finish = [&](uint32_t n) -> bool {
-        if (!warp_mbar_wait(&bars->pv_done[g][n & 1u], (n >> 1) & 1u, abort, p.status)) return false;
-        if (lane == 0) {
-          const uint32_t slot = (n & 1u) ? held[1] : held[0];
-          mbar_arrive(&bars->v_empty[slot]);
-          if (!two) mbar_arrive(&bars->v_empty[slot]);
-        }
-        return true;
-      };
-      advance(ks, kturn, min(i0, nt));
-      advance(vs, vturn, min(i0, nt));
-      for (int i = i0; ok && i < min(nt, i0 + 2 * step); i += step) ok = scores(i);
-      const uint32_t first = own;
-      for (int i = i0; ok && i < nt; i += step) {
-        // O += P V
-        const uint32_t buf = own & 1u;
-        ok = warp_mbar_wait(&bars->p_full[g][buf], (own >> 1) & 1u, abort, p.status) &&
-             warp_mbar_wait(&bars->v_full[vs], vturn & 1u, abort, p.status);
-        if (!ok) break;
-        const int k0 = (I.tile0 + I.t0 + i) * kN;
-        const int from = max(I.keys.lo - k0, 0), to = min(I.keys.hi - k0, kN);
-        if (from > 0 || to < kN) {
-          // with two tiles both groups' warps write the same zeros
-          zero_rows<D>(sVa + vs * S::kTile, 0, from, lane);
-          zero_rows<D>(sVa + vs * S::kTile, to, kN, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        const uint64_t dv = sw128_desc(__shfl_sync(0xffffffffu, sVa + vs * S::kTile, 0), S::kHalf, 1024);
-        const uint32_t t_p = __shfl_sync(0xffffffffu, tmem + col_s(g, buf), 0);
-        const uint32_t more = __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk)
-            tc_mma_f16_tmem_a(t_o, t_p + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
-          tc_commit(&bars->pv_done[g][buf]);
-        }
-        __syncwarp();
-        if (buf) held[1] = vs;
-        else held[0] = vs;
-        advance(vs, vturn, i + step <= nt ? step : nt - i);
-        ++own;
-        if (i + 2 * step < nt) ok = finish(own - 1) && scores(i + 2 * step);
+      const int step = two ? 1 : 2;
+      uint32_t q_slot = q;  // of the group's query tile
+      for (int x = 0; ok && x < (two ? 2 : 1); ++x) {
+        ok = warp_mbar_wait(&bars->q_full[q], qturn & 1u, abort, p.status);
+        if (x == g || !two) q_slot = q;
+        else if (ok && lane == 0) mbar_arrive(&bars->q_empty[q]);  // the other group's
+        if (++q == S::kQ) q = 0, ++qturn;
       }
-      // the products whose columns no score of this item has taken
-      for (uint32_t n = own - min(own - first, 2u); ok && n < own; ++n) ok = finish(n);
+      if (!ok) break;
+      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + q_slot * S::kQTile, 0), 16, 1024);
+      for (int i = 0; i < nt; ++i) {
+        ok = warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status);
+        if (!ok) break;
+        if (two || (i & 1) == g) {
+          const uint32_t buf = own & 1u;
+          ok = own < 2 || warp_mbar_wait(&bars->pv_done[g][buf], ((own - 2) >> 1) & 1u, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, sKa + ks * S::kTile, 0), 16, 1024);
+          const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g, buf), 0);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_f16(t_s, desc_advance(dq, (kk / 4) * S::kQHalf + (kk % 4) * 32),
+                         desc_advance(dk, (kk / 4) * S::kHalf + (kk % 4) * 32), idesc_s, kk > 0);
+            tc_commit(&bars->s_full[g][buf]);
+            if (i + step >= nt) tc_commit(&bars->q_empty[q_slot]);  // the group's last of this item
+          }
+          __syncwarp();
+          ++own;
+        } else if (lane == 0) {
+          mbar_arrive(&bars->k_empty[ks]);
+        }
+        if (++ks == S::kRing) ks = 0, ++kturn;
+      }
+      if (ok && !two && g >= nt && lane == 0) mbar_arrive(&bars->q_empty[q_slot]);  // no tile of the item is its own
     }
+  } else if (warp == 3 || warp == 7) {
+    // --------------------------------------------------------------- O += P V
+    const int g = warp >> 2;
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kM, D, 1);
+    const uint32_t sVa = smem_u32(sV);
+    const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
+    uint32_t vs = 0, vturn = 0, own = 0;
+    bool ok = true;
+    while (ok && walk.next(p, I)) {
+      const int nt = I.t1 - I.t0;
+      const bool two = two_tiles(p, I);
+      const int i0 = two ? 0 : g;
+      for (int i = 0; i < nt; ++i) {
+        ok = warp_mbar_wait(&bars->v_full[vs], vturn & 1u, abort, p.status);
+        if (!ok) break;
+        if (two || (i & 1) == g) {
+          const uint32_t buf = own & 1u;
+          const int k0 = (I.tile0 + I.t0 + i) * kN;
+          const int from = max(I.keys.lo - k0, 0), to = min(I.keys.hi - k0, kN);
+          if (from > 0 || to < kN) {
+            // with two tiles both groups' warps write the same zeros
+            zero_rows<D>(sVa + vs * S::kTile, 0, from, lane);
+            zero_rows<D>(sVa + vs * S::kTile, to, kN, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          ok = warp_mbar_wait(&bars->p_full[g][buf], (own >> 1) & 1u, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = sw128_desc(__shfl_sync(0xffffffffu, sVa + vs * S::kTile, 0), S::kHalf, 1024);
+          const uint32_t t_p = __shfl_sync(0xffffffffu, tmem + col_s(g, buf), 0);
+          const uint32_t more = __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+              tc_mma_f16_tmem_a(t_o, t_p + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
+            tc_commit(&bars->pv_done[g][buf]);
+          }
+          __syncwarp();
+          // the V slot is free once the product is done: a wait and a plain arrival here cost less than a second commit
+          ok = warp_mbar_wait(&bars->pv_done[g][buf], (own >> 1) & 1u, abort, p.status);
+          if (!ok) break;
+          ++own;
+        }
+        if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
+        if (++vs == S::kRing) vs = 0, ++vturn;
+      }
+    }
+  }
+  if (warp < 8 && (warp & 1)) {
     // every product completes before TMEM is released; after an abort some may be under way
     if (elect_one()) {
       tc_commit(&bars->drain);
@@ -319,9 +341,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  if (warp >= 8) {
     // ----------------------------------------------------- softmax, epilogue
-    const int g = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const int g = (warp - 8) >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     uint32_t own = 0, merges = 0, ks = 0;  // ks: K slot of the next tile (of either group)
@@ -351,10 +374,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         ok = warp_mbar_wait(&bars->s_full[g][buf], (own >> 1) & 1u, abort, p.status);
         if (!ok) break;
         ++own;
-        if (wq == 0 && lane == 0) {  // the scores are there: the group is done with the K tile
-          mbar_arrive(&bars->k_empty[slot]);
-          if (!two) mbar_arrive(&bars->k_empty[slot]);
-        }
+        if (wq == 0 && lane == 0) mbar_arrive(&bars->k_empty[slot]);  // the scores are there: the tile has been read
         if (warp_valid) {
           tc_fence_after();
           const int k0 = (I.tile0 + I.t0 + i) * kN;
@@ -559,7 +579,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 6) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------- host
