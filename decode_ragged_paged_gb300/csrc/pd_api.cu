@@ -629,7 +629,6 @@ int run_norm_rope(const pd_norm_rope_desc* d, int32_t num_tokens, const void* q,
   p.page_size = d->page_size;
   p.num_pages = d->num_pages;
   p.nhd = d->layout == PD_LAYOUT_NHD;
-  p.heads = d->num_qo_heads + d->num_kv_heads * (paged ? 2 : 1);
   p.eps = d->eps;
   p.q = q;
   p.k = k;

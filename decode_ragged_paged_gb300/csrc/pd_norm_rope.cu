@@ -16,20 +16,30 @@
 // products of far positions would be off by whole turns. The fraction comes from
 // a double, so an angle is off by at most position * 2^-53 of its frequency.
 //
-// Bound: HBM. Every element is read once and written once; a head is D / (2 V)
-// lanes, each with V elements of both halves of its pairs, so both loads and
-// both stores of a lane are wide and no lane needs another's elements; the sum
-// of squares is the only exchange. Cosines and sines are made once per token
-// and reused over the heads that the warp takes.
+// Bound: HBM; every element is read once and written once. What stands in the
+// way is the instructions (at one warp a head group, a first form with scalar
+// arithmetic was held at half of HBM's rate by them), so:
+//   a head is D / (2 V) lanes, each with V elements of both halves of its pairs:
+//     loads and stores are wide and the sum of squares is the only exchange;
+//   the weights are multiplied into the token's cosines and sines once, for all
+//     the heads that the warp takes: z_a = (x_a (c w_a) - x_b (s w_b)) / rms;
+//   the lanes of the heads that a warp holds side by side share the cosines out;
+//   the arithmetic is in packed pairs.
 #include "pd_common.cuh"
 #include "pd_internal.h"
+#include "pd_tc.cuh"
 
 namespace pd {
 
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrUnroll = 2;  // head groups of a token in flight per warp
+constexpr int kNrUnroll = 4;  // head groups of a token in flight per warp (without staging)
+// With staging: shared-memory stages of a warp, and the head groups (1 KiB each
+// at most) that a stage holds.
+constexpr int kNrStages = 2, kNrStageGroups = 7;
+constexpr uint32_t kNrStageBytes = kNrStageGroups * 1024;
+constexpr size_t kNrSmem = (size_t)(kNrThreads / 32) * kNrStages * (kNrStageBytes + sizeof(uint64_t)) + 128;
 
 template <int BYTES>
 struct Vec;
@@ -50,27 +60,19 @@ struct Pack {
   __device__ __forceinline__ void store(T* p) const {
     *reinterpret_cast<typename Vec<V * sizeof(T)>::type*>(p) = raw;
   }
-  __device__ __forceinline__ void unpack(float* f) const {
+  // Elements 2 i and 2 i + 1.
+  __device__ __forceinline__ float2 get(int i) const {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = __uint_as_float(w[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        f[2 * e] = bf16_lo(w[e]);
-        f[2 * e + 1] = bf16_hi(w[e]);
-      }
-    }
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else return make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
   }
-  __device__ __forceinline__ void pack(const float* f) {
+  __device__ __forceinline__ void set(int i, float2 v) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
     if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = __float_as_uint(f[e]);
+      w[2 * i] = __float_as_uint(v.x);
+      w[2 * i + 1] = __float_as_uint(v.y);
     } else {
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+      w[i] = pack_bf16x2(v.x, v.y);
     }
   }
 };
@@ -93,8 +95,16 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t turns, float& c, float& s
 
 }  // namespace
 
-template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
+// C: heads side by side in a warp that share a token's cosines out (a lane makes
+// V / C of its unit's V pairs).
+// STAGED: a warp's inputs come through shared memory by bulk copies, a stage per
+// work item and kNrStages items under way, so that what is in flight is not
+// limited by registers; its rows must be 16-byte aligned.
+template <typename T, int V, bool INTERLEAVED, int C, bool STAGED>
+__global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int U = STAGED ? 1 : kNrUnroll, H = V / 2;  // groups loaded together, packed pairs of a run
+  extern __shared__ __align__(128) uint8_t nr_smem[];
+  __shared__ int give_up;
   const int lane = threadIdx.x & 31;
   const int warp = (blockIdx.x * kNrThreads + threadIdx.x) >> 5;
   const int nwarps = gridDim.x * (kNrThreads / 32);
@@ -114,127 +124,254 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
     eb = rot ? half + u * V : ea + V;
   }
   rot = rot && active;
-  uint64_t freq[V];
+  uint64_t freq[V / C];  // of pairs C j + sub % C
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    freq[e] = 0;
+  for (int j = 0; j < V / C; ++j) {
+    freq[j] = 0;
     if (rot) {
-      double x = (double)p.inv_freq[u * V + e] * 0.15915494309189535;  // 1 / (2 pi)
+      double x = (double)p.inv_freq[u * V + C * j + (sub & (C - 1))] * 0.15915494309189535;  // 1 / (2 pi)
       x -= floor(x);
-      freq[e] = (uint64_t)(x * 18446744073709551616.0);
+      freq[j] = (uint64_t)(x * 18446744073709551616.0);
     }
   }
-  Pack<T, V> qwa, qwb, kwa, kwb;
-  if (p.q_weight != nullptr && active) {
-    qwa.load(static_cast<const T*>(p.q_weight) + ea);
-    qwb.load(static_cast<const T*>(p.q_weight) + eb);
+  const int kinds = p.slot_map != nullptr ? 3 : 2;
+  uint8_t* stages = nr_smem + (threadIdx.x >> 5) * (kNrStages * kNrStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(nr_smem + (kNrThreads / 32) * kNrStages * kNrStageBytes) +
+                   (threadIdx.x >> 5) * kNrStages;
+  // Groups [a0, a1) of a kind's heads that the item's groups [g0, g1) cover; `first` is the kind's first group.
+  auto cover = [&](int kind, int first, int g0, int g1, int& a0, int& a1) -> int {
+    const int count = kind == 0 ? p.hq : p.hkv, groups = (count + p.heads_per_group - 1) / p.heads_per_group;
+    a0 = max(g0 - first, 0);
+    a1 = min(g1 - first, groups);
+    return groups;
+  };
+  auto source = [&](int kind, int64_t t) -> const T* {
+    return kind == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
+           : kind == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
+                       : static_cast<const T*>(p.v) + t * p.v_stride;
+  };
+  // A warp's items are nwarps apart: (token, block) moves on by (step_t, step_b), without a division.
+  const int step_t = nwarps / p.blocks, step_b = nwarps - step_t * p.blocks;
+  auto move_on = [&](int& t, int& blk) {
+    blk += step_b;
+    t += step_t;
+    if (blk >= p.blocks) blk -= p.blocks, ++t;
+  };
+  // Starts the copies of an item into stage `st` (one lane).
+  auto fetch = [&](int t, int blk, int st) {
+    if (t >= p.tokens) return;
+    const int g0 = blk * p.groups_per_block, g1 = min(g0 + p.groups_per_block, p.groups);
+    const void* from[3];
+    uint32_t bytes[3], total = 0;
+    int first = 0, a0, a1;
+#pragma unroll
+    for (int kind = 0; kind < 3; ++kind) {
+      bytes[kind] = 0;
+      if (kind >= kinds) continue;
+      first += cover(kind, first, g0, g1, a0, a1);
+      if (a0 >= a1) continue;
+      const int h0 = a0 * p.heads_per_group, h1 = min(a1 * p.heads_per_group, kind == 0 ? p.hq : p.hkv);
+      from[kind] = source(kind, t) + (int64_t)h0 * D;
+      bytes[kind] = (uint32_t)((h1 - h0) * D * sizeof(T));
+      total += bytes[kind];
+    }
+    mbar_arrive_expect_tx(&full[st], total);
+    uint8_t* to = stages + st * kNrStageBytes;
+    const uint64_t once = make_evict_first();
+#pragma unroll
+    for (int kind = 0; kind < 3; ++kind) {
+      if (bytes[kind] == 0) continue;
+      bulk_g2s_hint(to, from[kind], bytes[kind], &full[st], once);
+      to += bytes[kind];
+    }
+  };
+  if constexpr (STAGED) {
+    if (threadIdx.x == 0) give_up = 0;
+    if (lane == 0) {
+      for (int i = 0; i < kNrStages; ++i) mbar_init(&full[i], 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
   }
-  if (p.k_weight != nullptr && active) {
-    kwa.load(static_cast<const T*>(p.k_weight) + ea);
-    kwb.load(static_cast<const T*>(p.k_weight) + eb);
+  int t = warp / p.blocks, blk = warp - t * p.blocks;
+  int ft = t, fb = blk;  // the next item to fetch
+  if constexpr (STAGED) {
+    for (int i = 0; i < kNrStages; ++i) {
+      if (lane == 0) fetch(ft, fb, i);
+      move_on(ft, fb);
+    }
   }
-
-  const int heads = p.heads;  // q heads, then k heads, then v heads (when v is written)
-  const int64_t items = (int64_t)p.tokens * p.blocks;
-  for (int64_t it = warp; it < items; it += nwarps) {
-    const int t = (int)(it / p.blocks), blk = (int)(it - (int64_t)t * p.blocks);
-    int64_t page_at = 0;  // element offset of the token's slot, head 0
-    bool cached = false;
+  int st = 0;
+  uint32_t parity = 0;
+  int64_t next_slot = p.slot_map != nullptr && t < p.tokens ? p.slot_map[t] : 0;
+  int32_t next_pos = p.rope_dim > 0 && t < p.tokens ? p.positions[t] : 0;
+  while (t < p.tokens) {
+    const int64_t slot = next_slot;
+    const int32_t position = next_pos;
+    int tn = t, bn = blk;
+    move_on(tn, bn);
+    if (tn < p.tokens) {  // read an item ahead
+      if (p.slot_map != nullptr) next_slot = p.slot_map[tn];
+      if (p.rope_dim > 0) next_pos = p.positions[tn];
+    }
+    int64_t place = 0;  // element offset of the token's k and v, head 0
+    bool cached = true;
     if (p.slot_map != nullptr) {
-      const int64_t slot = p.slot_map[t];
-      if (slot < 0) continue;  // a padding row: nothing of it is written
-      const int64_t page = slot <= 0xffffffffLL ? (int64_t)((uint32_t)slot / (uint32_t)p.page_size)
-                                                : slot / p.page_size;
-      cached = page < p.num_pages;
-      const int64_t s = slot - page * p.page_size;
-      page_at = (p.nhd ? slot * p.hkv : page * p.hkv * p.page_size + s) * D;
-      if (!cached && lane == 0) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+      const int64_t page = (uint64_t)slot <= 0xffffffffULL ? (int64_t)((uint32_t)slot / (uint32_t)p.page_size)
+                                                           : slot / p.page_size;
+      cached = slot >= 0 && page < p.num_pages;
+      place = (p.nhd ? slot * p.hkv : page * p.hkv * p.page_size + (slot - page * p.page_size)) * D;
+      if (slot >= 0 && !cached && lane == 0) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+    } else {
+      place = (int64_t)t * p.k_out_stride;
     }
+    const int64_t head_step = p.slot_map != nullptr && !p.nhd ? (int64_t)p.page_size * D : D;
     float cs[V], sn[V];
-    if (rot) {
-      const uint64_t pos = (uint64_t)(int64_t)p.positions[t];
+    if (p.rope_dim > 0) {
+      const uint64_t pos = (uint64_t)(int64_t)position;
+      float c[V / C], s[V / C];
 #pragma unroll
-      for (int e = 0; e < V; ++e) cos_sin_turns(freq[e] * pos, cs[e], sn[e]);
+      for (int j = 0; j < V / C; ++j) cos_sin_turns(freq[j] * pos, c[j], s[j]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int from = (e % C) * p.lanes + u;
+        cs[e] = C == 1 ? c[e / C] : __shfl_sync(0xffffffffu, c[e / C], from);
+        sn[e] = C == 1 ? s[e / C] : __shfl_sync(0xffffffffu, s[e / C], from);
+      }
     }
-    const int g0 = blk * p.groups_per_block;
-    const int g1 = min(g0 + p.groups_per_block, p.groups);
-    for (int g = g0; g < g1; g += kNrUnroll) {
-      Pack<T, V> a[kNrUnroll], b[kNrUnroll];
-      T* out[kNrUnroll];
-      int kind[kNrUnroll];  // 0 q, 1 k, 2 v
-#pragma unroll
-      for (int x = 0; x < kNrUnroll; ++x) {
-        const int head = (g + x) * p.heads_per_group + sub;
-        const T* src = nullptr;
-        out[x] = nullptr;
-        kind[x] = 0;
-        if (g + x < g1 && head < heads && active) {
-          if (head < p.hq) {
-            src = static_cast<const T*>(p.q) + (int64_t)t * p.q_stride + (int64_t)head * D;
-            out[x] = static_cast<T*>(p.q_out) + (int64_t)t * p.q_out_stride + (int64_t)head * D;
-          } else {
-            const bool is_v = head >= p.hq + p.hkv;
-            const int h = head - p.hq - (is_v ? p.hkv : 0);
-            kind[x] = is_v ? 2 : 1;
-            src = static_cast<const T*>(is_v ? p.v : p.k) + (int64_t)t * (is_v ? p.v_stride : p.k_stride) +
-                  (int64_t)h * D;
-            T* dst = static_cast<T*>(is_v ? p.v_out : p.k_out);
-            if (p.slot_map == nullptr) out[x] = dst + (int64_t)t * p.k_out_stride + (int64_t)h * D;
-            else if (cached) out[x] = dst + page_at + (int64_t)h * (p.nhd ? D : (int64_t)p.page_size * D);
-          }
+    const int g0 = blk * p.groups_per_block, g1 = min(g0 + p.groups_per_block, p.groups);
+    const T* staged = reinterpret_cast<const T*>(stages + st * kNrStageBytes);
+    if constexpr (STAGED) {
+      if (!warp_mbar_wait(&full[st], parity, &give_up, p.status)) break;
+    }
+    int first = 0;  // the kind's first group
+    // q heads, then k heads, then v heads: one body, or its registers would add up
+#pragma unroll 1
+    for (int kind = 0; kind < kinds; ++kind) {
+      const int count = kind == 0 ? p.hq : p.hkv;
+      int a0, a1;
+      first += cover(kind, first, g0, g1, a0, a1);
+      if (a0 >= a1) continue;
+      const T* src;  // head 0, were it there
+      if constexpr (STAGED) {
+        src = staged - a0 * p.heads_per_group * D;
+        staged += (min(a1 * p.heads_per_group, count) - a0 * p.heads_per_group) * D;
+      } else {
+        src = source(kind, t);
+      }
+      // a padding row: nothing of it is written; a slot past the pools: no k and v
+      if (slot < 0 || (kind > 0 && !cached)) continue;
+      T* dst = kind == 0 ? static_cast<T*>(p.q_out) + t * p.q_out_stride
+                         : static_cast<T*>(kind == 1 ? p.k_out : p.v_out) + place;
+      const int64_t step = kind == 0 ? D : head_step;
+      const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
+      const bool turn = kind < 2 && p.rope_dim > 0;
+      // the rotation of this token, weights multiplied in
+      float2 aa[H], ab[H], ba[H], bb[H];
+      const bool mix = turn && rot;
+      {
+        Pack<T, V> wa, wb;
+        if (weight != nullptr && active) {
+          wa.load(weight + ea);
+          wb.load(weight + eb);
         }
-        if (out[x] != nullptr) {
-          a[x].load(src + ea);
-          b[x].load(src + eb);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const float2 one = make_float2(1.f, 1.f);
+          const float2 fa = weight != nullptr ? wa.get(i) : one, fb = weight != nullptr ? wb.get(i) : one;
+          aa[i] = fa;
+          bb[i] = fb;
+          if (!mix) continue;
+          if constexpr (INTERLEAVED) {
+            // pairs i of run a and i of run b: z = (x0 c - x1 s, x0 s + x1 c), in four products
+            const float ca = cs[i], sa = sn[i], cb = cs[H + i], sb = sn[H + i];
+            aa[i] = make_float2(fa.x * ca, fa.y * ca);   // x0 -> z0, x1 -> z1
+            ab[i] = make_float2(-fa.y * sa, fa.x * sa);  // x1 -> z0, x0 -> z1
+            bb[i] = make_float2(fb.x * cb, fb.y * cb);
+            ba[i] = make_float2(-fb.y * sb, fb.x * sb);
+          } else {
+            const float2 c2 = make_float2(cs[2 * i], cs[2 * i + 1]), s2 = make_float2(sn[2 * i], sn[2 * i + 1]);
+            aa[i] = fmul2(fa, c2);
+            ab[i] = fmul2(fb, make_float2(-s2.x, -s2.y));  // of x_b in z_a
+            ba[i] = fmul2(fa, s2);                         // of x_a in z_b
+            bb[i] = fmul2(fb, c2);
+          }
         }
       }
+      for (int g = a0; g < a1; g += U) {
+        Pack<T, V> a[U], b[U];
+        const int head0 = g * p.heads_per_group + sub;
 #pragma unroll
-      for (int x = 0; x < kNrUnroll; ++x) {
-        float fa[V], fb[V];
-        float ss = 0.f;
-        if (out[x] != nullptr) {
-          a[x].unpack(fa);
-          b[x].unpack(fb);
-#pragma unroll
-          for (int e = 0; e < V; ++e) ss += fa[e] * fa[e] + fb[e] * fb[e];
+        for (int x = 0; x < U; ++x) {
+          const int head = head0 + x * p.heads_per_group;
+          if (g + x < a1 && head < count && active) {
+            a[x].load(src + (int64_t)head * D + ea);
+            b[x].load(src + (int64_t)head * D + eb);
+          }
         }
-        for (int d = p.lanes >> 1; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        if (out[x] == nullptr) continue;
-        if (kind[x] < 2) {
-          if ((kind[x] == 0 ? p.q_weight : p.k_weight) != nullptr) {
-            const float inv = rsqrtf(ss * p.inv_dim + p.eps);
-            float ga[V], gb[V];
-            (kind[x] == 0 ? qwa : kwa).unpack(ga);
-            (kind[x] == 0 ? qwb : kwb).unpack(gb);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              fa[e] *= inv * ga[e];
-              fb[e] *= inv * gb[e];
+        for (int x = 0; x < U; ++x) {
+          if (g + x >= a1) break;
+          const int head = head0 + x * p.heads_per_group;
+          const bool here = head < count && active;
+          if (turn || weight != nullptr) {
+            float2 xa[H], xb[H], sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              xa[i] = a[x].get(i);
+              xb[i] = b[x].get(i);
+            }
+            float inv = 1.f;
+            if (weight != nullptr) {
+#pragma unroll
+              for (int i = 0; i < H; ++i) {
+                sum = ffma2(xa[i], xa[i], sum);
+                sum = ffma2(xb[i], xb[i], sum);
+              }
+              float ss = active ? sum.x + sum.y : 0.f;  // lanes past the head's units have nothing
+              for (int d = p.lanes >> 1; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+              inv = rsqrtf(ss * p.inv_dim + p.eps);
+            }
+            const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              float2 za = fmul2(xa[i], aa[i]), zb = fmul2(xb[i], bb[i]);
+              if (mix) {
+                if constexpr (INTERLEAVED) {
+                  za = ffma2(make_float2(xa[i].y, xa[i].x), ab[i], za);
+                  zb = ffma2(make_float2(xb[i].y, xb[i].x), ba[i], zb);
+                } else {
+                  za = ffma2(xb[i], ab[i], za);
+                  zb = ffma2(xa[i], ba[i], zb);
+                }
+              }
+              a[x].set(i, fmul2(za, inv2));
+              b[x].set(i, fmul2(zb, inv2));
             }
           }
-          if (rot) {
-            if constexpr (INTERLEAVED) {
-#pragma unroll
-              for (int e = 0; e < V; ++e) {
-                float* f = e < V / 2 ? fa + 2 * e : fb + 2 * e - V;
-                const float y0 = f[0], y1 = f[1];
-                f[0] = y0 * cs[e] - y1 * sn[e];
-                f[1] = y0 * sn[e] + y1 * cs[e];
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < V; ++e) {
-                const float y0 = fa[e], y1 = fb[e];
-                fa[e] = y0 * cs[e] - y1 * sn[e];
-                fb[e] = y0 * sn[e] + y1 * cs[e];
-              }
-            }
+          if (here) {
+            a[x].store(dst + head * step + ea);
+            b[x].store(dst + head * step + eb);
           }
-          a[x].pack(fa);
-          b[x].pack(fb);
         }
-        a[x].store(out[x] + ea);
-        b[x].store(out[x] + eb);
+      }
+    }
+    if constexpr (STAGED) {
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) fetch(ft, fb, st);
+      move_on(ft, fb);
+      if (++st == kNrStages) {
+        st = 0;
+        parity ^= 1u;
+      }
+    }
+    t = tn;
+    blk = bn;
+  }
+  if constexpr (STAGED) {
+    if (*static_cast<volatile int*>(&give_up)) {  // copies may be under way: let them land before shared memory is freed
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
       }
     }
   }
@@ -243,10 +380,29 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 // ------------------------------------------------------------------- host
 namespace {
 
+template <typename T, int V, int C, bool STAGED>
+cudaError_t launch_s(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
+  auto kernel = p.interleaved ? norm_rope_kernel<T, V, true, C, STAGED> : norm_rope_kernel<T, V, false, C, STAGED>;
+  if (STAGED) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNrSmem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, kNrThreads, STAGED ? kNrSmem : 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int C>
+cudaError_t launch_c(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
+  if constexpr (V * sizeof(T) == 16)
+    if (p.staged) return launch_s<T, V, C, true>(p, grid, stream);
+  return launch_s<T, V, C, false>(p, grid, stream);
+}
+
 template <typename T, int V>
-void launch_v(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
-  if (p.interleaved) norm_rope_kernel<T, V, true><<<grid, kNrThreads, 0, stream>>>(p);
-  else norm_rope_kernel<T, V, false><<<grid, kNrThreads, 0, stream>>>(p);
+cudaError_t launch_v(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
+  if (V >= 4 && p.heads_per_group >= 4) return launch_c<T, V, V >= 4 ? 4 : 2>(p, grid, stream);
+  if (p.heads_per_group >= 2) return launch_c<T, V, 2>(p, grid, stream);
+  return launch_c<T, V, 1>(p, grid, stream);
 }
 
 }  // namespace
@@ -269,33 +425,35 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
   p.lanes = 1;
   while (p.lanes < units) p.lanes <<= 1;
   p.heads_per_group = 32 / p.lanes;
-  p.groups = (p.heads + p.heads_per_group - 1) / p.heads_per_group;
+  // groups of q heads, of k heads, and (with a slot map) of v heads
+  p.groups = (p.hq + p.heads_per_group - 1) / p.heads_per_group +
+             (p.slot_map != nullptr ? 2 : 1) * ((p.hkv + p.heads_per_group - 1) / p.heads_per_group);
   p.inv_dim = 1.0f / (float)p.head_dim;
-  // A warp takes as many of a token's head groups as leave every SM 32 warps:
-  // more would reuse its cosines further, but leave SMs without work.
-  const int64_t warps = (int64_t)device_sm_count() * 32;
-  int64_t blocks = (warps + p.tokens - 1) / p.tokens;
-  const int max_blocks = (p.groups + kNrUnroll - 1) / kNrUnroll;
-  if (blocks > max_blocks) blocks = max_blocks;
+  p.staged = vec * elem_size == 16;
+  // A warp takes as many of a token's head groups as leave every SM its resident
+  // warps (more would reuse its cosines further, but leave SMs without work), and
+  // no more than a stage holds.
+  const int64_t resident = (int64_t)device_sm_count() * 2;  // CTAs
+  int64_t blocks = (resident * (kNrThreads / 32) + p.tokens - 1) / p.tokens;
+  if (p.staged && blocks < (p.groups + kNrStageGroups - 1) / kNrStageGroups)
+    blocks = (p.groups + kNrStageGroups - 1) / kNrStageGroups;
+  if (blocks > p.groups) blocks = p.groups;
   p.groups_per_block = (int32_t)((p.groups + blocks - 1) / blocks);
-  p.groups_per_block = (p.groups_per_block + kNrUnroll - 1) / kNrUnroll * kNrUnroll;
   p.blocks = (p.groups + p.groups_per_block - 1) / p.groups_per_block;
   const int64_t items = (int64_t)p.tokens * p.blocks;
   int64_t grid = (items * 32 + kNrThreads - 1) / kNrThreads;
-  const int64_t most = (int64_t)device_sm_count() * (2048 / kNrThreads);
-  if (grid > most) grid = most;
+  if (grid > resident) grid = resident;
   last_kernel() = "norm_rope_kernel";
   profile_begin(stream);
-  if (elem_size == 2) {
-    if (vec == 8) launch_v<uint16_t, 8>(p, (unsigned)grid, stream);
-    else if (vec == 4) launch_v<uint16_t, 4>(p, (unsigned)grid, stream);
-    else launch_v<uint16_t, 2>(p, (unsigned)grid, stream);
-  } else {
-    if (vec == 4) launch_v<float, 4>(p, (unsigned)grid, stream);
-    else launch_v<float, 2>(p, (unsigned)grid, stream);
-  }
+  cudaError_t e;
+  if (elem_size == 2)
+    e = vec == 8   ? launch_v<uint16_t, 8>(p, (unsigned)grid, stream)
+        : vec == 4 ? launch_v<uint16_t, 4>(p, (unsigned)grid, stream)
+                   : launch_v<uint16_t, 2>(p, (unsigned)grid, stream);
+  else
+    e = vec == 4 ? launch_v<float, 4>(p, (unsigned)grid, stream) : launch_v<float, 2>(p, (unsigned)grid, stream);
   profile_end(stream);
-  return cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // namespace pd
