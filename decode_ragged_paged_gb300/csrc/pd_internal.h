@@ -208,7 +208,7 @@ struct NormRopeParams {
   int32_t tokens, hq, hkv, head_dim, rope_dim, interleaved, page_size, num_pages, nhd;
   // set by the launcher: lanes of a head, heads of a warp's group, groups of a
   // token, groups a work item covers, work items of a token
-  int32_t lanes, heads_per_group, groups, groups_per_block, blocks;
+  int32_t lanes, heads_per_group, q_groups, kv_groups, groups, groups_per_block, blocks;
   int32_t staged;  // inputs through shared memory
   float eps, inv_dim;
   int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements between tokens

@@ -138,9 +138,10 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
   uint8_t* stages = nr_smem + (threadIdx.x >> 5) * (kNrStages * kNrStageBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(nr_smem + (kNrThreads / 32) * kNrStages * kNrStageBytes) +
                    (threadIdx.x >> 5) * kNrStages;
+  const int hpg = p.heads_per_group;
   // Groups [a0, a1) of a kind's heads that the item's groups [g0, g1) cover; `first` is the kind's first group.
   auto cover = [&](int kind, int first, int g0, int g1, int& a0, int& a1) -> int {
-    const int count = kind == 0 ? p.hq : p.hkv, groups = (count + p.heads_per_group - 1) / p.heads_per_group;
+    const int groups = kind == 0 ? p.q_groups : p.kv_groups;
     a0 = max(g0 - first, 0);
     a1 = min(g1 - first, groups);
     return groups;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
       if (kind >= kinds) continue;
       first += cover(kind, first, g0, g1, a0, a1);
       if (a0 >= a1) continue;
-      const int h0 = a0 * p.heads_per_group, h1 = min(a1 * p.heads_per_group, kind == 0 ? p.hq : p.hkv);
+      const int h0 = a0 * hpg, h1 = min(a1 * hpg, kind == 0 ? p.hq : p.hkv);
       from[kind] = source(kind, t) + (int64_t)h0 * D;
       bytes[kind] = (uint32_t)((h1 - h0) * D * sizeof(T));
       total += bytes[kind];
@@ -252,12 +253,12 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
       int a0, a1;
       first += cover(kind, first, g0, g1, a0, a1);
       if (a0 >= a1) continue;
-      const T* src;  // head 0, were it there
+      const T* src;  // of head a0 * hpg
       if constexpr (STAGED) {
-        src = staged - a0 * p.heads_per_group * D;
-        staged += (min(a1 * p.heads_per_group, count) - a0 * p.heads_per_group) * D;
+        src = staged;
+        staged += (min(a1 * hpg, count) - a0 * hpg) * D;
       } else {
-        src = source(kind, t);
+        src = source(kind, t) + (int64_t)a0 * hpg * D;
       }
       // a padding row: nothing of it is written; a slot past the pools: no k and v
       if (slot < 0 || (kind > 0 && !cached)) continue;
@@ -298,21 +299,24 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
           }
         }
       }
+      const T* s_at = src + sub * D + ea;
+      T* d_at = dst + (int64_t)(a0 * hpg + sub) * step + ea;
+      const int run = eb - ea, s_step = hpg * D;
+      const int64_t d_step = hpg * step;
+      int head = a0 * hpg + sub;
       for (int g = a0; g < a1; g += U) {
         Pack<T, V> a[U], b[U];
-        const int head0 = g * p.heads_per_group + sub;
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-          const int head = head0 + x * p.heads_per_group;
-          if (g + x < a1 && head < count && active) {
-            a[x].load(src + (int64_t)head * D + ea);
-            b[x].load(src + (int64_t)head * D + eb);
+          if (g + x < a1 && head + x * hpg < count && active) {
+            a[x].load(s_at + x * s_step);
+            b[x].load(s_at + x * s_step + run);
           }
         }
+        s_at += U * s_step;
 #pragma unroll
-        for (int x = 0; x < U; ++x) {
+        for (int x = 0; x < U; ++x, head += hpg, d_at += d_step) {
           if (g + x >= a1) break;
-          const int head = head0 + x * p.heads_per_group;
           const bool here = head < count && active;
           if (turn || weight != nullptr) {
             float2 xa[H], xb[H], sum = make_float2(0.f, 0.f);
@@ -350,8 +354,8 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
             }
           }
           if (here) {
-            a[x].store(dst + head * step + ea);
-            b[x].store(dst + head * step + eb);
+            a[x].store(d_at);
+            b[x].store(d_at + run);
           }
         }
       }
@@ -426,8 +430,9 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
   while (p.lanes < units) p.lanes <<= 1;
   p.heads_per_group = 32 / p.lanes;
   // groups of q heads, of k heads, and (with a slot map) of v heads
-  p.groups = (p.hq + p.heads_per_group - 1) / p.heads_per_group +
-             (p.slot_map != nullptr ? 2 : 1) * ((p.hkv + p.heads_per_group - 1) / p.heads_per_group);
+  p.q_groups = (p.hq + p.heads_per_group - 1) / p.heads_per_group;
+  p.kv_groups = (p.hkv + p.heads_per_group - 1) / p.heads_per_group;
+  p.groups = p.q_groups + (p.slot_map != nullptr ? 2 : 1) * p.kv_groups;
   p.inv_dim = 1.0f / (float)p.head_dim;
   p.staged = vec * elem_size == 16;
   // A warp takes as many of a token's head groups as leave every SM its resident
