@@ -4,7 +4,10 @@ A thin Python binding over the C ABI in ``include/pd.h`` (``libpd.so``, built
 in-tree by ``decode_ragged_paged_gb300.build``). The functions carry the C
 names and only marshal arguments: torch tensors give device pointers, shapes
 and the current CUDA stream; every step of the computation runs in the
-library's CUDA kernels. There is no CPU path: if ``libpd.so`` is missing or a
+library's CUDA kernels. The calls of a serving step (pd_batch_tables,
+pd_qk_norm_rope*, pd_attn_chunk) are checked and marshalled by a small extension
+module (``csrc/pd_bind.cpp``), as a short step's calls would otherwise take longer
+in Python than on the GPU. There is no CPU path: if ``libpd.so`` is missing or a
 call fails, an exception is raised.
 
 Tensor layouts (see ``include/pd.h``):
@@ -104,12 +107,13 @@ class BatchTables(NamedTuple):
 
 
 _lib = None
+_bind = None  # the module of pd_bind.cpp
 _lock = threading.Lock()
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libpd.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _bind
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -167,6 +171,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.pd_last_kernel.restype = ctypes.c_char_p
             lib.pd_profile_events.argtypes = [P, P]
             lib.pd_profile_events.restype = ctypes.c_int
+            from . import _pd_bind
+            _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), P).value for n in (
+                "pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
+                "pd_attn_chunk_workspace_size")))
+            _bind = _pd_bind
             _lib = lib
         return _lib
 
@@ -372,15 +381,24 @@ def _vector(t, name, dtype, n=None):
         raise PdError(f"{name} has {t.numel()} entries, {n} are needed")
 
 
-def _rows(t, name, heads=None, dim=None, dtype=None):
-    """Token stride of a [tokens][heads][dim] tensor whose heads lie one after another."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise PdError(f"{name} must be [tokens][heads][dim] with contiguous heads")
-    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise PdError(f"{name} has the shape {tuple(t.shape)}, not [tokens][{heads}][{dim}]")
-    if dtype is not None and t.dtype != dtype:
-        raise PdError(f"{name} is {t.dtype}, not {dtype}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _bound(name, stream, *args):
+    """Calls a function of the binding module on the tensors' device: None, or (value, pd_status)."""
+    if _lib is None:
+        load_library()
+    fn = getattr(_bind, name)
+    handle = None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    try:
+        device = _current()
+    except Exception:  # no GPU here: the tensors are refused below
+        device = -1
+    rc = fn(device, handle if handle is not None else _stream(None, device) if device >= 0 else 0, *args)
+    if rc is not None and rc[1] == 1:  # they are on another device than the current one
+        with torch.cuda.device(rc[0]):
+            rc = fn(rc[0], handle if handle is not None else _stream(None, rc[0]), *args)
+    return rc
 
 
 def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, *, causal=True, window_left=-1,
@@ -390,48 +408,24 @@ def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
     an optional sliding window of window_left keys before each token. q [total_qo][Hq][D] may be a
     slice of a wider row. Without max_qo_len / max_kv_len they are read from the device (a
     synchronisation). Returns (o, lse)."""
-    lib = load_library()
-    device = _device_of(q=q, k_pool=k_pool, v_pool=v_pool, kv_len=kv_len, page_indptr=page_indptr,
-                        page_indices=page_indices, qo_indptr=qo_indptr, o=o,
-                        lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace, dev_status=dev_status)
-    if not k_pool.is_contiguous() or not v_pool.is_contiguous() or k_pool.shape != v_pool.shape or k_pool.dim() != 4:
-        raise PdError("k_pool and v_pool must be contiguous pools of the same shape")
-    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
-        raise PdError("q and the pools differ in dtype")
-    stride = _rows(q, "q", dim=k_pool.shape[3])
-    B = kv_len.numel()
-    _vector(qo_indptr, "qo_indptr", torch.int32, B + 1)
-    _vector(page_indptr, "page_indptr", torch.int32, B + 1)
-    if max_qo_len is None:
-        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if B else 0
-    shape = q.shape
     if o is None:
-        o = torch.empty(shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
-    elif o.shape != shape or not o.is_contiguous():
-        raise PdError("o must be contiguous and shaped like q")
+        o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
     if lse is True:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     elif lse is False:
         lse = None
-    if lse is not None:
-        _vector(lse, "lse", torch.float32, shape[0] * shape[1])
-    desc = make_attn_desc(q, k_pool, causal=causal, sm_scale=sm_scale, o_dtype=o.dtype, layout=layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr, total_qo=shape[0],
-                       max_qo_len=max_qo_len, max_kv_len=max_kv_len)
-    dref, bref = ctypes.byref(desc), ctypes.byref(batch)
-    args = (dref, bref, int(window_left) if window_left is not None else -1, stride, q.data_ptr(), k_pool.data_ptr(),
-            v_pool.data_ptr(), o.data_ptr(), _ptr(lse))
-    tail = (_ptr(dev_status), _stream(stream, device))
-    rc = PD_ERR_WORKSPACE
-    if workspace is not None:
-        rc = _launch(device, "pd_attn_chunk", lib.pd_attn_chunk, *args, workspace.data_ptr(),
-                     workspace.numel() * workspace.element_size(), *tail)
-    if rc == PD_ERR_WORKSPACE:  # none, or one too small for this batch
-        with torch.cuda.device(device):
-            size = int(lib.pd_attn_chunk_workspace_size(dref, bref))
-        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=q.device)
-        rc = _launch(device, "pd_attn_chunk", lib.pd_attn_chunk, *args, workspace.data_ptr(), workspace.numel(), *tail)
-    _check(rc, "pd_attn_chunk")
+    if max_qo_len is None:
+        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if qo_indptr.numel() > 1 else 0
+    if max_kv_len is None:
+        max_kv_len = int(kv_len.max().item()) if kv_len.numel() else 0
+    head = (q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, o, lse)
+    tail = (dev_status, causal, window_left, sm_scale or None, max_qo_len, max_kv_len, _layout_code(layout))
+    rc = _bound("attn_chunk", stream, *head, workspace, *tail)
+    if rc is not None and rc[1] == PD_ERR_WORKSPACE:  # none, or one too small for this batch
+        workspace = torch.empty(max(rc[0], 16), dtype=torch.uint8, device=q.device)
+        rc = _bound("attn_chunk", stream, *head, workspace, *tail)
+    if rc is not None:
+        _check(rc[1], "pd_attn_chunk")
     return o, lse
 
 
@@ -442,42 +436,18 @@ def pd_batch_tables(new_len, cached_len, block_table, *, page_size, num_pages, t
     the pages it lacks are taken from the end of free_pages and entered there. free_count (int32,
     one entry) counts the free pages; free_count_out gets what is left (free_count itself: in
     place). `out` may hold the six result tensors. Returns BatchTables."""
-    lib = load_library()
-    B = new_len.numel()
-    device = _device_of(new_len=new_len, cached_len=cached_len, block_table=block_table, rows=rows,
-                        free_pages=free_pages, free_count=free_count, free_count_out=free_count_out,
-                        dev_status=dev_status)
-    i32 = torch.int32
-    _vector(new_len, "new_len", i32)
-    _vector(cached_len, "cached_len", i32, B)
-    if block_table.dim() != 2:
-        raise PdError("block_table must be [rows][pages]")
-    _vector(block_table, "block_table", i32)
-    if rows is not None:
-        _vector(rows, "rows", i32, B)
-    if free_pages is not None:
-        if free_count is None:
-            raise PdError("free_pages needs free_count")
-        _vector(free_pages, "free_pages", i32)
-        _vector(free_count, "free_count", i32, 1)
-        if free_count_out is None:
-            free_count_out = torch.empty_like(free_count)
-        _vector(free_count_out, "free_count_out", i32, 1)
-    total_qo, nnz = int(total_qo), int(max_page_indices)
+    if free_pages is not None and free_count_out is None and free_count is not None:
+        free_count_out = torch.empty_like(free_count)
     if out is None:
-        sizes = ((B + 1, i32), (B, i32), (B + 1, i32), (nnz, i32), (total_qo, i32), (total_qo, torch.int64))
-        out = tuple(torch.empty(n, dtype=t, device=new_len.device) for n, t in sizes)
+        B, i32 = new_len.numel(), torch.int32
+        sizes = ((B + 1, i32), (B, i32), (B + 1, i32), (max_page_indices, i32), (total_qo, i32),
+                 (total_qo, torch.int64))
+        out = (torch.empty(n, dtype=t, device=new_len.device) for n, t in sizes)
     out = BatchTables(*out)
-    _device_of(new_len=new_len, **out._asdict())
-    for name, n in (("qo_indptr", B + 1), ("kv_len", B), ("page_indptr", B + 1), ("page_indices", nnz),
-                    ("positions", total_qo)):
-        _vector(getattr(out, name), name, i32, n)
-    _vector(out.slot_map, "slot_map", torch.int64, total_qo)
-    desc = TablesDesc(B, int(page_size), int(num_pages), block_table.shape[0], block_table.shape[1], total_qo, nnz,
-                      free_pages.numel() if free_pages is not None else 0)
-    _launch(device, "pd_batch_tables", lib.pd_batch_tables, ctypes.byref(desc), _ptr(rows), cached_len.data_ptr(),
-            new_len.data_ptr(), block_table.data_ptr(), _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
-            *(t.data_ptr() for t in out), _ptr(dev_status), _stream(stream, device))
+    rc = _bound("batch_tables", stream, new_len, cached_len, block_table, rows, free_pages, free_count, free_count_out,
+                *out, dev_status, page_size, num_pages, total_qo, max_page_indices)
+    if rc is not None:
+        _check(rc[1], "pd_batch_tables")
     return out
 
 
@@ -505,49 +475,19 @@ def pd_slot_map(qo_indptr, kv_len, page_indptr, page_indices, *, page_size, num_
     return positions, slot_map
 
 
-def _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
-    """Checks what both forms of the norm and rotation share; returns the descriptor and the token count."""
-    tokens, hq, dim = q.shape
-    dt = q.dtype
-    qs, ks = _rows(q, "q"), _rows(k, "k", dim=dim, dtype=dt)
-    if k.shape[0] != tokens:
-        raise PdError("q and k differ in tokens")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _vector(w, name, dt, dim)
-    rope = 0
-    if inv_freq is not None:
-        _vector(inv_freq, "inv_freq", torch.float32)
-        rope = 2 * inv_freq.numel()
-        if positions is None:
-            raise PdError("a rotation needs positions")
-        _vector(positions, "positions", torch.int32, tokens)
-    return NormRopeDesc(hq, k.shape[1], dim, rope, int(bool(interleaved)), _dtype_code(dt), 0, 0, 0, float(eps), qs,
-                        ks, 0, 0, 0), tokens
-
-
 def pd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, interleaved=False, q_out=None,
                     k_out=None, stream=None):
     """Per-head RMS norm (None as weight: no norm) and position rotation (inv_freq None: none; its
     2 * numel first values of each head, pairs of halves or, interleaved, neighbours) of q
     [T][Hq][D] and k [T][Hkv][D], which may be slices of a wider row. q_out / k_out may be q / k
     themselves. Returns (q_out, k_out)."""
-    lib = load_library()
-    device = _device_of(q=q, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
-                        q_out=q_out, k_out=k_out)
-    desc, tokens = _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if t.shape != like.shape:
-            raise PdError(f"{name} has the shape {tuple(t.shape)}, not {tuple(like.shape)}")
-    desc.q_out_stride = _rows(q_out, "q_out", dtype=q.dtype)
-    desc.k_out_stride = _rows(k_out, "k_out", dtype=q.dtype)
-    _launch(device, "pd_qk_norm_rope", lib.pd_qk_norm_rope, ctypes.byref(desc), tokens, q.data_ptr(), k.data_ptr(),
-            _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(),
-            _stream(stream, device))
+    rc = _bound("norm_rope", stream, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved)
+    if rc is not None:
+        _check(rc[1], "pd_qk_norm_rope")
     return q_out, k_out
 
 
@@ -556,29 +496,12 @@ def pd_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, slo
     """pd_qk_norm_rope whose k, and v as it is, go straight into their slots of the pools (slot_map
     int64 [T], from pd_batch_tables or pd_slot_map; rows with a negative slot are left alone).
     Returns q_out."""
-    lib = load_library()
-    device = _device_of(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
-                        slot_map=slot_map, k_pool=k_pool, v_pool=v_pool, q_out=q_out, dev_status=dev_status)
-    desc, tokens = _norm_rope_desc(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    if v.shape != k.shape:
-        raise PdError("k and v differ in shape")
-    desc.v_stride = _rows(v, "v", dtype=q.dtype)
-    _vector(slot_map, "slot_map", torch.int64, tokens)
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or not k_pool.is_contiguous() or not v_pool.is_contiguous():
-        raise PdError("k_pool and v_pool must be contiguous pools of the same shape")
-    num_pages, hkv, page, dim = _pool_dims(k_pool, layout)
-    if (hkv, dim) != (k.shape[1], k.shape[2]) or k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
-        raise PdError("the pools' heads, head_dim or dtype are not those of k")
-    desc.page_size, desc.num_pages, desc.layout = page, num_pages, _layout_code(layout)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise PdError(f"q_out has the shape {tuple(q_out.shape)}, not {tuple(q.shape)}")
-    desc.q_out_stride = _rows(q_out, "q_out", dtype=q.dtype)
-    _launch(device, "pd_qk_norm_rope_append", lib.pd_qk_norm_rope_append, ctypes.byref(desc), tokens, q.data_ptr(),
-            k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
-            slot_map.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_status),
-            _stream(stream, device))
+    rc = _bound("norm_rope_append", stream, q, k, q_weight, k_weight, inv_freq, positions, v, slot_map, k_pool, v_pool,
+                q_out, dev_status, eps, interleaved, _layout_code(layout))
+    if rc is not None:
+        _check(rc[1], "pd_qk_norm_rope_append")
     return q_out
 
 

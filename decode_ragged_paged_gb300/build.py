@@ -1,7 +1,9 @@
-"""Builds libpd.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Builds libpd.so (the C-ABI library) in-tree for sm_103a with nvcc, and the
+Python binding's extension module with g++.
 
 Each .cu translation unit is compiled in parallel, then linked into
-``decode_ragged_paged_gb300/libpd.so``. Re-running is cheap: objects newer
+``decode_ragged_paged_gb300/libpd.so``; ``csrc/pd_bind.cpp`` becomes
+``decode_ragged_paged_gb300/_pd_bind.so``. Re-running is cheap: objects newer
 than their sources and headers are reused.
 
     python -m decode_ragged_paged_gb300.build [--force] [--verbose-ptxas]
@@ -21,6 +23,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpd.so")
+BIND = os.path.join(HERE, "_pd_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -61,6 +64,25 @@ def _host_stamp() -> str:
     return f"{platform.machine()} {nvcc()}"
 
 
+def _bind() -> None:
+    """Compiles the binding module (csrc/pd_bind.cpp) with g++ against torch's headers."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pd_bind.cpp"), "-o", tmp,
+           "-L", os.path.join(home, "lib"), f"-Wl,-rpath,{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on pd_bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     """Compile every kernel and the C ABI into libpd.so; returns its path."""
     os.makedirs(OBJ, exist_ok=True)
@@ -72,11 +94,15 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     deps = _deps()
     todo = [s for s in sources
             if force or verbose_ptxas or _stale(os.path.join(OBJ, os.path.basename(s) + ".o"), [s, *deps])]
+    bind = force or _stale(BIND, [os.path.join(CSRC, "pd_bind.cpp"), *deps])
     logs = []
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo), os.cpu_count() or 4)) as ex:
+    if todo or bind:
+        with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo) + 1, os.cpu_count() or 4)) as ex:
+            bound = ex.submit(_bind) if bind else None
             for obj, log in ex.map(lambda s: _compile(s, verbose_ptxas), todo):
                 logs.append(log)
+            if bound is not None:
+                bound.result()
     objs = [os.path.join(OBJ, os.path.basename(s) + ".o") for s in sources]
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
