@@ -64,6 +64,7 @@ __device__ long long scan_exclusive(long long v, long long* warp_tot, long long&
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p) {
   __shared__ long long warp_tot[kPlanThreads / 32];
   pdl_launch_dependents();
+  pdl_wait_primary();
   const int tid = threadIdx.x;
   long long carry = 0, total;
   for (int r0 = 0; r0 < p.batch; r0 += kPlanThreads) {
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
+  pdl_launch_dependents();
   pdl_wait_primary();
   const int64_t units = p.hdr[0], parts = p.hdr[1];
   const int c = blockIdx.x;
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   float* sQ = reinterpret_cast<float*>(simt_smem_raw);
   float* sKV = sQ + R * LD;
   float* sP = sKV + kSimtKeys * LD;  // [key][row]
+  pdl_launch_dependents();
   pdl_wait_primary();
   const int64_t units = p.hdr[0], parts = p.hdr[1];
   if (blockIdx.x >= parts) return;
@@ -427,23 +430,6 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
 
 namespace {
 
-// Launches `kernel` as a programmatic dependent of the kernel before it on the stream.
-template <typename K>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                             const ChunkParams& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <typename T, int R, int D>
 cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
   auto kernel = chunk_simt_kernel<T, R, D>;
@@ -459,8 +445,8 @@ cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
 }  // namespace
 
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  cudaError_t e;
+  cudaError_t e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  if (e != cudaSuccess) return PD_ERR_CUDA;
   const bool d64 = p.head_dim == 64, few = p.rows == 16;
   if (p.tc)
     e = launch_chunk_tc(p, stream);

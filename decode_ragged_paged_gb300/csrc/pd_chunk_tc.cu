@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
+  pdl_launch_dependents();
   pdl_wait_primary();  // the plan's work line
   const int64_t units = p.hdr[0], parts = p.hdr[1];
   ChunkWalk walk;
@@ -598,17 +599,7 @@ cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensor
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.max_parts);
-  cfg.blockDim = dim3(kCtThreads);
-  cfg.dynamicSmemBytes = Shape<D>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+  return launch_dependent(kernel, dim3((unsigned)p.max_parts), kCtThreads, Shape<D>::kSmem, stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -302,6 +302,26 @@ inline void profile_end(cudaStream_t s) {
   if (profile_events().stop) cudaEventRecord(profile_events().stop, s);
 }
 
+// Launches a kernel as a programmatic dependent of the one before it on the
+// stream: its CTAs are placed while that one drains, and wait for it (with
+// pdl_wait_primary(), before they touch global memory). Not while launches are
+// timed alone through the profiling events.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace pd

@@ -124,16 +124,6 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
     eb = rot ? half + u * V : ea + V;
   }
   rot = rot && active;
-  uint64_t freq[V / C];  // of pairs C j + sub % C
-#pragma unroll
-  for (int j = 0; j < V / C; ++j) {
-    freq[j] = 0;
-    if (rot) {
-      double x = (double)p.inv_freq[u * V + C * j + (sub & (C - 1))] * 0.15915494309189535;  // 1 / (2 pi)
-      x -= floor(x);
-      freq[j] = (uint64_t)(x * 18446744073709551616.0);
-    }
-  }
   const int kinds = p.slot_map != nullptr ? 3 : 2;
   uint8_t* stages = nr_smem + (threadIdx.x >> 5) * (kNrStages * kNrStageBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(nr_smem + (kNrThreads / 32) * kNrStages * kNrStageBytes) +
@@ -186,6 +176,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
       to += bytes[kind];
     }
   };
+  pdl_launch_dependents();
   if constexpr (STAGED) {
     if (threadIdx.x == 0) give_up = 0;
     if (lane == 0) {
@@ -194,6 +185,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
     }
     __syncthreads();
   }
+  pdl_wait_primary();
   int t = warp / p.blocks, blk = warp - t * p.blocks;
   int ft = t, fb = blk;  // the next item to fetch
   if constexpr (STAGED) {
@@ -206,6 +198,17 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
   uint32_t parity = 0;
   int64_t next_slot = p.slot_map != nullptr && t < p.tokens ? p.slot_map[t] : 0;
   int32_t next_pos = p.rope_dim > 0 && t < p.tokens ? p.positions[t] : 0;
+  // (made while the first inputs are on their way)
+  uint64_t freq[V / C];  // of pairs C j + sub % C
+#pragma unroll
+  for (int j = 0; j < V / C; ++j) {
+    freq[j] = 0;
+    if (rot) {
+      double x = (double)p.inv_freq[u * V + C * j + (sub & (C - 1))] * 0.15915494309189535;  // 1 / (2 pi)
+      x -= floor(x);
+      freq[j] = (uint64_t)(x * 18446744073709551616.0);
+    }
+  }
   while (t < p.tokens) {
     const int64_t slot = next_slot;
     const int32_t position = next_pos;
@@ -391,8 +394,7 @@ cudaError_t launch_s(const NormRopeParams& p, unsigned grid, cudaStream_t stream
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNrSmem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, kNrThreads, STAGED ? kNrSmem : 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3(grid), kNrThreads, STAGED ? kNrSmem : 0, stream, p);
 }
 
 template <typename T, int V, int C>

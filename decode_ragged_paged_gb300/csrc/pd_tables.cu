@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kTabThreads = 1024;
 constexpr int kTabWarps = kTabThreads / 32;
-constexpr int kEntriesPerCta = 4096;  // entries of the page list and rows a CTA is launched for
+constexpr int kFill = 4;  // entries of the page list or rows that a thread works on together
 
 // Prefix sums over the batch.
 struct Sums {
@@ -106,18 +106,32 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
   int* pg = qo + B + 1;             // [B + 1] pages before it, at most max_page_indices
   int* need = pg + B + 1;           // [B] free pages taken before it
   int* old_pages = need + B;        // [B] pages it holds already, -1 for a refused request
-  int* hash = old_pages + B;        // [hash_size] first request of every block-table row
+  int* table_row = old_pages + B;   // [B] its row of the block table
+  int* hash = table_row + B;        // [hash_size] first request of every block-table row
   const bool pops = p.free_pages != nullptr;
+  pdl_launch_dependents();
+  pdl_wait_primary();
   int avail = pops ? *p.free_count : 0;
   avail = min(max(avail, 0), p.free_capacity);
   if (tid == 0) taken = 0;
+
+  // Every thread takes a run of consecutive requests. The first of them (the only
+  // one up to 1024 requests) is read here, ahead of what the rows go through.
+  const int per = (B + kTabThreads - 1) / kTabThreads;
+  const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
+  struct Req {
+    int n, c, row;
+  };
+  auto read = [&](int r) -> Req { return {p.new_len[r], p.cached_len[r], p.rows != nullptr ? p.rows[r] : r}; };
+  Req mine0{};
+  if (r0 < r1) mine0 = read(r0);
 
   if (p.rows != nullptr) {
     for (int i = tid; i < p.hash_size; i += kTabThreads) hash[i] = -1;
     __syncthreads();
     // a row listed twice belongs to the first request that lists it
-    for (int r = tid; r < B; r += kTabThreads) {
-      const int row = p.rows[r];
+    for (int r = r0; r < r1; ++r) {
+      const int row = r == r0 ? mine0.row : p.rows[r];
       if (row < 0 || row >= p.table_rows) continue;
       for (unsigned h = (unsigned)row * 2654435761u;; ++h) {
         int* at = &hash[h & (unsigned)(p.hash_size - 1)];
@@ -132,25 +146,28 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
     __syncthreads();
   }
 
-  // every thread takes a run of consecutive requests: local sums, block scan, then the run again
-  const int per = (B + kTabThreads - 1) / kTabThreads;
-  const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
-  auto look = [&](int r, int& code) -> Sums {
-    const int n = p.new_len[r], c = p.cached_len[r];
-    const int row = p.rows != nullptr ? p.rows[r] : r;
-    Sums s{max(n, 0), 0, 0};
+  auto look = [&](int r, const Req& q, int& code) -> Sums {
+    Sums s{max(q.n, 0), 0, 0};
     code = PD_DEV_OK;
-    const long long kv = (long long)n + c;
-    const long long old = ((long long)c + p.page_size - 1) / p.page_size, tot = (kv + p.page_size - 1) / p.page_size;
-    if (n < 0 || c < 0 || kv > 0x7fffffffLL || tot > p.table_cols) {
+    const long long kv = (long long)q.n + q.c;
+    const int P = p.page_size;
+    if (q.n < 0 || q.c < 0 || kv > 0x7fffffffLL) {
       code = PD_DEV_BAD_LENGTH;
       return s;
     }
-    bool row_ok = row >= 0 && row < p.table_rows;
+    // both below 2^31 and rounded up without passing it
+    const int old = q.c / P + (q.c % P != 0), tot = (int)kv / P + ((int)kv % P != 0);
+    if (tot > p.table_cols) {
+      code = PD_DEV_BAD_LENGTH;
+      return s;
+    }
+    bool row_ok = q.row >= 0 && q.row < p.table_rows;
     if (row_ok && p.rows != nullptr) {
-      unsigned h = (unsigned)row * 2654435761u;
-      while (p.rows[hash[h & (unsigned)(p.hash_size - 1)]] != row) ++h;
-      row_ok = hash[h & (unsigned)(p.hash_size - 1)] == r;
+      // the row's entry: other rows on the way there are other requests'
+      unsigned h = (unsigned)q.row * 2654435761u;
+      int at;
+      while ((at = hash[h & (unsigned)(p.hash_size - 1)]) != r && p.rows[at] != q.row) ++h;
+      row_ok = at == r;
     }
     if (!row_ok) {
       code = PD_DEV_BAD_ROW;
@@ -160,18 +177,28 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
     s.need = pops ? tot - old : 0;
     return s;
   };
-  Sums mine{0, 0, 0};
+  Sums mine{0, 0, 0}, first{0, 0, 0};
+  int first_code = PD_DEV_OK;
   for (int r = r0; r < r1; ++r) {
     int code;
-    const Sums s = look(r, code);
+    const Sums s = look(r, r == r0 ? mine0 : read(r), code);
+    if (r == r0) {
+      first = s;
+      first_code = code;
+    }
     mine.rows += s.rows;
     mine.pages += s.pages;
     mine.need += s.need;
   }
   Sums at = block_scan(mine, warp_tot);
   for (int r = r0; r < r1; ++r) {
-    int code;
-    const Sums s = look(r, code);
+    Req q = mine0;
+    Sums s = first;
+    int code = first_code;
+    if (r > r0) {
+      q = read(r);
+      s = look(r, q, code);
+    }
     const Sums end{at.rows + s.rows, at.pages + s.pages, at.need + s.need};
     if (code == PD_DEV_OK && (end.rows > p.total_qo || end.pages > p.max_page_indices)) code = PD_DEV_BAD_INDPTR;
     if (code == PD_DEV_OK && s.need > 0 && end.need > avail) code = PD_DEV_NO_PAGES;
@@ -180,10 +207,10 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
       qo[r] = (int)min(at.rows, (long long)p.total_qo);
       pg[r] = (int)min(at.pages, (long long)p.max_page_indices);
       need[r] = (int)min(at.need, (long long)0x7fffffff);
-      const int c = p.cached_len[r];
       old_pages[r] = code != PD_DEV_OK ? -1 : (int)(s.pages - s.need);
+      table_row[r] = q.row;
       if (blockIdx.x == 0) {
-        p.kv_len[r] = code != PD_DEV_OK ? -1 : c + (int)s.rows;
+        p.kv_len[r] = code != PD_DEV_OK ? -1 : q.c + (int)s.rows;
         p.qo_indptr[r] = qo[r];
         p.page_indptr[r] = pg[r];
         if (code != PD_DEV_OK) report(p.status, code);
@@ -208,40 +235,45 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
     *p.free_count_out = avail - (int)taken;
   if (COMMIT) return;
 
-  // the page lists, then the rows
+  // The page lists, then the rows: a few entries of a thread at a time, their
+  // searches and their reads of the tables side by side.
   const int nnz = pg[B], real_rows = qo[B];
   const int P = p.page_size;
-  auto page_of = [&](int r, int row, int j) -> int {
-    const int old = old_pages[r];
-    return j < old ? p.block_table[(int64_t)row * p.table_cols + j]
-                   : p.free_pages[avail - 1 - (need[r] + j - old)];
-  };
-  const int64_t total = (int64_t)nnz + p.total_qo;
-  for (int64_t e = (int64_t)blockIdx.x * kTabThreads + tid; e < total; e += (int64_t)gridDim.x * kTabThreads) {
-    if (e < nnz) {
-      const int i = (int)e, r = owner(pg, 0, B, i);
-      int page = -1;
-      if (old_pages[r] >= 0) {
-        const int row = p.rows != nullptr ? p.rows[r] : r, j = i - pg[r];
-        page = page_of(r, row, j);
-        if (j >= old_pages[r]) p.block_table[(int64_t)row * p.table_cols + j] = page;
-        if (page < 0 || page >= p.num_pages) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+  const int64_t total = (int64_t)nnz + p.total_qo, stride = (int64_t)gridDim.x * kTabThreads;
+  for (int64_t e0 = (int64_t)blockIdx.x * kTabThreads + tid; e0 < total; e0 += kFill * stride) {
+    int r[kFill], j[kFill], pos[kFill], page[kFill];
+#pragma unroll
+    for (int x = 0; x < kFill; ++x) {
+      const int64_t e = e0 + x * stride;
+      r[x] = -1;
+      j[x] = pos[x] = 0;
+      page[x] = -1;
+      if (e < nnz) {
+        r[x] = owner(pg, 0, B, (int)e);
+        j[x] = (int)e - pg[r[x]];
+      } else if (e < nnz + (int64_t)real_rows) {
+        r[x] = owner(qo, 0, B, (int)(e - nnz));
+        if (old_pages[r[x]] >= 0) pos[x] = p.cached_len[r[x]] + (int)(e - nnz) - qo[r[x]];
+        j[x] = pos[x] / P;
       }
-      p.page_indices[i] = page;
-    } else {
-      const int i = (int)(e - nnz);
-      int pos = 0;
-      int64_t slot = -1;
-      if (i < real_rows) {
-        const int r = owner(qo, 0, B, i);
-        if (old_pages[r] >= 0) {
-          pos = p.cached_len[r] + i - qo[r];
-          const int page = page_of(r, p.rows != nullptr ? p.rows[r] : r, pos / P);
-          if (page >= 0 && page < p.num_pages) slot = (int64_t)page * P + pos % P;
-        }
+      if (r[x] >= 0 && old_pages[r[x]] >= 0)
+        page[x] = j[x] < old_pages[r[x]]
+                      ? p.block_table[(int64_t)table_row[r[x]] * p.table_cols + j[x]]
+                      : p.free_pages[avail - 1 - (need[r[x]] + j[x] - old_pages[r[x]])];
+    }
+#pragma unroll
+    for (int x = 0; x < kFill; ++x) {
+      const int64_t e = e0 + x * stride;
+      if (e >= total) break;
+      const bool served = r[x] >= 0 && old_pages[r[x]] >= 0, known = page[x] >= 0 && page[x] < p.num_pages;
+      if (e < nnz) {
+        if (served && j[x] >= old_pages[r[x]]) p.block_table[(int64_t)table_row[r[x]] * p.table_cols + j[x]] = page[x];
+        if (served && !known) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+        p.page_indices[e] = page[x];
+      } else {
+        p.positions[e - nnz] = pos[x];
+        p.slot_map[e - nnz] = served && known ? (int64_t)page[x] * P + (pos[x] - j[x] * P) : -1;
       }
-      p.positions[i] = pos;
-      p.slot_map[i] = slot;
     }
   }
 }
@@ -249,6 +281,8 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
 // Positions and slots of the rows of a batch whose page table the caller has:
 // one thread per row.
 __global__ void __launch_bounds__(256) slot_map_kernel(const SlotMapParams p) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= p.total_qo) return;
   int pos = 0;
@@ -278,9 +312,10 @@ __global__ void __launch_bounds__(256) slot_map_kernel(const SlotMapParams p) {
 // ------------------------------------------------------------------- host
 int launch_batch_tables(TablesParams& p, cudaStream_t stream) {
   p.hash_size = p.rows != nullptr ? tables_hash_size(p.batch) : 0;
-  const size_t smem = sizeof(int) * ((size_t)4 * p.batch + 2 + p.hash_size);
+  const size_t smem = sizeof(int) * ((size_t)5 * p.batch + 2 + p.hash_size);
+  // an entry a thread, up to a CTA per SM
   const int64_t entries = (int64_t)p.max_page_indices + p.total_qo;
-  int64_t grid = (entries + kEntriesPerCta - 1) / kEntriesPerCta;
+  int64_t grid = (entries + kTabThreads - 1) / kTabThreads;
   if (grid > device_sm_count()) grid = device_sm_count();
   if (grid < 1) grid = 1;
   if (smem > 40 * 1024) {
@@ -292,19 +327,19 @@ int launch_batch_tables(TablesParams& p, cudaStream_t stream) {
   }
   last_kernel() = "batch_tables_kernel";
   profile_begin(stream);
-  batch_tables_kernel<false><<<(unsigned)grid, kTabThreads, smem, stream>>>(p);
+  cudaError_t e = launch_dependent(batch_tables_kernel<false>, dim3((unsigned)grid), kTabThreads, smem, stream, p);
   profile_end(stream);
-  if (p.free_pages != nullptr && p.free_count == p.free_count_out)
-    batch_tables_kernel<true><<<1, kTabThreads, smem, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+  if (e == cudaSuccess && p.free_pages != nullptr && p.free_count == p.free_count_out)
+    e = launch_dependent(batch_tables_kernel<true>, dim3(1), kTabThreads, smem, stream, p);
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 int launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
   last_kernel() = "slot_map_kernel";
   profile_begin(stream);
-  slot_map_kernel<<<(unsigned)((p.total_qo + 255) / 256), 256, 0, stream>>>(p);
+  const cudaError_t e = launch_dependent(slot_map_kernel, dim3((unsigned)((p.total_qo + 255) / 256)), 256, 0, stream, p);
   profile_end(stream);
-  return cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // namespace pd
