@@ -20,92 +20,17 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-__device__ bool chunk_request_ok(const ChunkParams& p, int r) {
-  const int a = p.qo_indptr[r], b = p.qo_indptr[r + 1], n = p.kv_len[r];
-  const int pa = p.page_indptr[r], pb = p.page_indptr[r + 1];
-  int code = PD_DEV_OK;
-  if (a < 0 || b < a || b > p.total_qo || pa < 0 || pb < pa) code = PD_DEV_BAD_INDPTR;
-  else if (n < 0 || n > p.max_kv_len || b - a > p.max_qo_len) code = PD_DEV_BAD_LENGTH;
-  else if ((long long)(pb - pa) * p.page_size < n) code = PD_DEV_BAD_PAGE_TABLE;
-  if (code != PD_DEV_OK) report(p.status, code);
-  return code == PD_DEV_OK;
-}
-
-// Exclusive scan over the CTA, and the total.
-__device__ long long scan_exclusive(long long v, long long* warp_tot, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();  // the totals of an earlier scan have been read
-  if (lane == 31) warp_tot[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = warp_tot[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += y;
-    }
-    warp_tot[lane] = w;
-  }
-  __syncthreads();
-  total = warp_tot[kPlanThreads / 32 - 1];
-  return (warp > 0 ? warp_tot[warp - 1] : 0) + x - v;
-}
-
 }  // namespace
 
 // ------------------------------------------------------------------- plan
-// One CTA: checks the requests, numbers their token blocks and sums the blocks' units.
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p) {
   __shared__ long long warp_tot[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int tid = threadIdx.x;
-  long long carry = 0, total;
-  for (int r0 = 0; r0 < p.batch; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    long long n = 0;
-    if (r < p.batch && chunk_request_ok(p, r))
-      n = (p.qo_indptr[r + 1] - p.qo_indptr[r] + p.item_tokens - 1) / p.item_tokens;
-    const long long at = carry + scan_exclusive(n, warp_tot, total);
-    // rows of different requests do not overlap in a sound batch, so the bound holds there
-    if (r < p.batch) p.req_first[r] = (int)min(at, (long long)p.max_blocks);
-    carry += total;
-  }
-  const int blocks = (int)min(carry, (long long)p.max_blocks);
-  if (tid == 0) p.req_first[p.batch] = blocks;
-  __syncthreads();
-  carry = 0;
-  for (int b0 = 0; b0 < blocks; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    long long units = 0;
-    if (b < blocks) {
-      int lo = 0, hi = p.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.req_first[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      const int qo = p.qo_indptr[lo + 1] - p.qo_indptr[lo], t0 = (b - p.req_first[lo]) * p.item_tokens;
-      units = p.item_cost +
-              chunk_tiles(p, chunk_keys(p, qo, p.kv_len[lo], t0, min(qo, t0 + p.item_tokens)));
-    }
-    const long long at = carry + scan_exclusive(units, warp_tot, total);
-    if (b < blocks) p.pre[b] = at;
-    carry += total;
-  }
-  if (tid == 0) {
-    p.pre[blocks] = carry;
-    const long long units = carry * p.item_heads;
-    long long parts = (units + p.min_units - 1) / p.min_units;  // at least so many units a part
-    if (parts > p.max_parts) parts = p.max_parts;
-    p.hdr[0] = units;
-    p.hdr[1] = parts < 1 ? 1 : parts;
+  const ChunkLine line = plan_line<kPlanThreads>(p, p.req_first, p.pre, warp_tot);
+  if (threadIdx.x == 0) {
+    p.hdr[0] = line.units;
+    p.hdr[1] = line.parts;
   }
 }
 
@@ -122,15 +47,14 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
   if (c + 1 >= parts || units == 0) return;
   const int64_t from = part_start(units, parts, c), cut = part_start(units, parts, c + 1);
   ChunkWalk w;
-  w.seek(p, cut, units);
+  w.seek(p, p.req_first, p.pre, cut, units);
   const int64_t s = w.item_start;
-  const int n = (int)(p.pre[w.b + 1] - p.pre[w.b]) - p.item_cost;
+  const int n = w.tiles(p);
   if (s < from || s >= cut || cut >= s + n) return;  // an earlier part's item, or no tile behind the cut
   int64_t last = c + 1;  // the part that holds the item's last tile
   while (last + 1 < parts && part_start(units, parts, last + 1) < s + n) ++last;
-  const int a = p.qo_indptr[w.r], qo = p.qo_indptr[w.r + 1] - a;
-  const int tok0 = (w.b - w.b0) * p.item_tokens;
-  const int rows = min(p.item_tokens, qo - tok0) * p.tile_heads;
+  const int tok0 = w.b * p.item_tokens;
+  const int rows = min(p.item_tokens, w.q.qo - tok0) * p.tile_heads;
   const int lane = threadIdx.x & 31;
   constexpr int E = D / 32;
   for (int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); m < rows;
@@ -162,7 +86,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int tok = m / p.tile_heads;
-    const int64_t row = (int64_t)(a + tok0 + tok) * p.hq + w.h * p.tile_heads + (m - tok * p.tile_heads);
+    const int64_t row = (int64_t)(w.q.row + tok0 + tok) * p.hq + w.h * p.tile_heads + (m - tok * p.tile_heads);
     if (p.o_dtype == PD_BF16) {
       uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * E);
 #pragma unroll
@@ -199,11 +123,14 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   float* sP = sKV + kSimtKeys * LD;  // [key][row]
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int64_t units = p.hdr[0], parts = p.hdr[1];
-  if (blockIdx.x >= parts) return;
+  const int32_t* line_first;
+  const int64_t* line_pre;
+  const ChunkLine line = take_line<kSimtThreads>(p, simt_smem_raw, line_first, line_pre);
+  if (blockIdx.x >= line.parts) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ChunkWalk walk;
-  walk.seek(p, part_start(units, parts, blockIdx.x), part_start(units, parts, blockIdx.x + 1));
+  walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
+            part_start(line.units, line.parts, blockIdx.x + 1));
   constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
   ChunkItem I;
   while (walk.next(p, I)) {
@@ -425,6 +352,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
   L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);
   L.total = off;
+  p.self_plan = p.batch <= kSelfBatch && p.max_blocks <= kSelfBlocks;
   return L;
 }
 
@@ -445,7 +373,8 @@ cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
 }  // namespace
 
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
-  cudaError_t e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  cudaError_t e = cudaSuccess;
+  if (!p.self_plan) e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return PD_ERR_CUDA;
   const bool d64 = p.head_dim == 64, few = p.rows == 16;
   if (p.tc)

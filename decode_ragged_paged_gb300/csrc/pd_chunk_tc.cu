@@ -55,15 +55,20 @@ struct Shape {
   static constexpr int kRing = D == 128 ? 5 : 8;        // slots of the K ring and of the V ring
   static constexpr int kQ = D == 128 ? 2 : 4;           // slots of the Q ring
   static constexpr uint32_t kOffK = kQ * kQTile, kOffV = kOffK + kRing * kTile, kOffBar = kOffV + kRing * kTile;
-  static constexpr size_t kSmem = kOffBar + 512 + 128 * 2 * sizeof(float) + 1024;
+  static constexpr uint32_t kOffML = kOffBar + 1024;    // group 1's maxima and sums
+  static constexpr size_t kSmem = kOffML + 128 * 2 * sizeof(float) + 1024;
 };
+static_assert(kSelfBytes <= Shape<64>::kOffBar && kSelfBytes <= Shape<128>::kOffBar, "the rings hold the line first");
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
 // Slots of the Q, K and V rings are freed by one arrival of each group. A group
 // waits for every slot's every fill, its own or not, and then frees it, at once
 // if the tile is the other group's: were it to pass over a fill without waiting,
 // it could look at a barrier two phases early, where a parity wait lets it by.
+constexpr int kItems = 4;  // items that the scheduler is ahead
 struct Bars {
+  ChunkItem items[kItems];  // no tokens: the end
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full[4], q_empty[4];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [group][S buffer]
@@ -72,7 +77,7 @@ struct Bars {
   uint32_t tmem_slot;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= 1024, "barrier block");
 
 // TMEM: two S / P buffers of 64 columns a group, then the groups' O accumulators.
 __device__ __forceinline__ uint32_t col_s(int g, uint32_t buf) { return (uint32_t)(2 * g + buf) * kN; }
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base, *sK = base + S::kOffK, *sV = base + S::kOffV;
   Bars* bars = reinterpret_cast<Bars*>(base + S::kOffBar);
-  float2* sML = reinterpret_cast<float2*>(base + S::kOffBar + 512);  // group 1's (m, l) of every row
+  float2* sML = reinterpret_cast<float2*>(base + S::kOffML);  // group 1's (m, l) of every row
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -153,6 +158,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_init(&bars->s_full[i >> 1][i & 1], 1);
       mbar_init(&bars->p_full[i >> 1][i & 1], 4);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], kCtThreads / 32 - 1);  // every warp but the scheduler
     }
     mbar_init(&bars->ml_ready, 4);
     mbar_init(&bars->merged, 4);
@@ -175,12 +184,47 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const uint32_t tmem = bars->tmem_slot;
   pdl_launch_dependents();
   pdl_wait_primary();  // the plan's work line
-  const int64_t units = p.hdr[0], parts = p.hdr[1];
-  ChunkWalk walk;
-  walk.u = walk.u1 = 0;
-  if (blockIdx.x < parts)
-    walk.seek(p, part_start(units, parts, blockIdx.x), part_start(units, parts, blockIdx.x + 1));
+  const int32_t* line_first;
+  const int64_t* line_pre;
+  const ChunkLine line = take_line<kCtThreads>(p, base, line_first, line_pre);
   ChunkItem I{};
+  if (warp == 6) {
+    ChunkWalk walk;
+    if (blockIdx.x < line.parts)
+      walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
+                part_start(line.units, line.parts, blockIdx.x + 1));
+    if (p.self_plan) {
+      fence_proxy_async_smem();
+      __syncthreads();  // the line has been read: its place goes to the rings
+    }
+    // ------------------------------------------------------------ scheduler
+    // Walks the CTA's part of the line ahead of the other warps.
+    uint32_t slot = 0, turn = 0;
+    for (bool more = true; more;) {
+      more = walk.next(p, I);
+      if (!more) I.tokens = 0;
+      if (!warp_mbar_wait(&bars->item_empty[slot], (turn & 1u) ^ 1u, abort, p.status)) break;
+      if (lane == 0) {
+        bars->items[slot] = I;
+        mbar_arrive(&bars->item_full[slot]);
+      }
+      __syncwarp();
+      if (++slot == kItems) slot = 0, ++turn;
+    }
+  } else if (p.self_plan) {
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+  // The next item of the scheduler's, in every other warp.
+  uint32_t item_slot = 0, item_turn = 0;
+  auto next_item = [&]() -> bool {
+    if (!warp_mbar_wait(&bars->item_full[item_slot], item_turn & 1u, abort, p.status)) return false;
+    I = bars->items[item_slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[item_slot]);
+    if (++item_slot == kItems) item_slot = 0, ++item_turn;
+    return I.tokens > 0;
+  };
 
   if (warp == 0 || warp == 2) {
     // ----------------------------------------------------------- K, V loads
@@ -194,7 +238,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const int idx = 32 * w + lane;
       return idx < I.need ? __ldg(p.page_indices + I.pbase + idx) : 0;
     };
-    while (ok && walk.next(p, I)) {
+    while (ok && next_item()) {
       if (I.t1 <= I.t0) continue;
       int win = (I.tile0 + I.t0) * kN / p.page_size >> 5;
       int ids = window(win), ahead = window(win + 1);
@@ -218,7 +262,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // --------------------------------------------------------------- Q loads
     uint32_t q = 0, qturn = 0;
     bool ok = true;
-    while (ok && walk.next(p, I)) {
+    while (ok && next_item()) {
       if (I.t1 <= I.t0) continue;
       const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.item_tokens / 2;
       for (int x = 0; ok && x < tiles; ++x) {
@@ -243,7 +287,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     uint32_t q = 0, qturn = 0, ks = 0, kturn = 0;
     uint32_t own = 0;  // scores issued
     bool ok = true;
-    while (ok && walk.next(p, I)) {
+    while (ok && next_item()) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const bool two = two_tiles(p, I);
@@ -292,7 +336,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
     uint32_t vs = 0, vturn = 0, own = 0;
     bool ok = true;
-    while (ok && walk.next(p, I)) {
+    while (ok && next_item()) {
       const int nt = I.t1 - I.t0;
       const bool two = two_tiles(p, I);
       const int i0 = two ? 0 : g;
@@ -351,7 +395,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     uint32_t own = 0, merges = 0, ks = 0;  // ks: K slot of the next tile (of either group)
     bool ok = true;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    while (ok && walk.next(p, I)) {
+    while (ok && next_item()) {
       const int nt = max(I.t1 - I.t0, 0);
       const bool two = two_tiles(p, I);
       const int half_tok = p.item_tokens / 2;
