@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
             part_start(line.units, line.parts, blockIdx.x + 1));
   constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
+  constexpr int NV = kSimtKeys * VR / kSimtThreads;  // vectors of a tile per thread
   ChunkItem I;
   while (walk.next(p, I)) {
     const int rows = I.tokens * p.tile_heads;
@@ -173,41 +174,55 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       hi[i] = m < rows ? k.hi : 0;
     }
     const int kv_head = I.h / p.group;
-    // rows of tile keys [k0, k0 + 64) of a pool to shared memory; keys that no row of the item sees are zero
-    auto load = [&](const void* pool, int k0) {
-      for (int i = tid; i < kSimtKeys * VR; i += kSimtThreads) {
-        const int key = i / VR, c = i - key * VR, j = k0 + key;
-        float f[VE] = {};
-        if (j >= I.keys.lo && j < I.keys.hi) {
-          const int page = p.page_indices[I.pbase + j / p.page_size], slot = j % p.page_size;
-          if (page >= 0 && page < p.num_pages) {
-            const int64_t row = p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head
-                                      : ((int64_t)page * p.hkv + kv_head) * p.page_size + slot;
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // A thread's vectors of the rows of keys [k0, k0 + 64): fetched into
+    // registers, K's a tile ahead and V's while the scores are computed, then put
+    // into shared memory. Keys that no row of the item sees are zero.
+    auto fetch = [&](const void* pool, int k0, uint4 (&v)[NV]) {
+      int page[NV];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (sizeof(T) == 4) {
-                f[e] = __uint_as_float(w[e]);
-              } else {
-                f[2 * e] = bf16_lo(w[e]);
-                f[2 * e + 1] = bf16_hi(w[e]);
-              }
-            }
-          } else {
-            report(p.status, PD_DEV_BAD_PAGE_TABLE);
-          }
+      for (int x = 0; x < NV; ++x) {
+        const int j = k0 + (tid + x * kSimtThreads) / VR;
+        page[x] = -1;
+        if (j >= I.keys.lo && j < I.keys.hi)
+          page[x] = p.page_indices[I.pbase + (p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size)];
+      }
+#pragma unroll
+      for (int x = 0; x < NV; ++x) {
+        const int i = tid + x * kSimtThreads, c = i % VR, j = k0 + i / VR;
+        v[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < I.keys.lo || j >= I.keys.hi) continue;
+        if (page[x] < 0 || page[x] >= p.num_pages) {
+          report(p.status, PD_DEV_BAD_PAGE_TABLE);
+          continue;
         }
-#pragma unroll
-        for (int e = 0; e < VE; e += 4)
-          *reinterpret_cast<float4*>(sKV + key * LD + c * VE + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        const int slot = p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
+        const int64_t row = p.nhd ? ((int64_t)page[x] * p.page_size + slot) * p.hkv + kv_head
+                                  : ((int64_t)page[x] * p.hkv + kv_head) * p.page_size + slot;
+        v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE));
       }
     };
+    auto put = [&](const uint4 (&v)[NV]) {
+#pragma unroll
+      for (int x = 0; x < NV; ++x) {
+        const int i = tid + x * kSimtThreads;
+        float4* to = reinterpret_cast<float4*>(sKV + (i / VR) * LD + (i % VR) * VE);
+        if constexpr (sizeof(T) == 4) {
+          to[0] = make_float4(__uint_as_float(v[x].x), __uint_as_float(v[x].y), __uint_as_float(v[x].z),
+                              __uint_as_float(v[x].w));
+        } else {
+          to[0] = make_float4(bf16_lo(v[x].x), bf16_hi(v[x].x), bf16_lo(v[x].y), bf16_hi(v[x].y));
+          to[1] = make_float4(bf16_lo(v[x].z), bf16_hi(v[x].z), bf16_lo(v[x].w), bf16_hi(v[x].w));
+        }
+      }
+    };
+    uint4 kv[NV];
+    if (I.t0 < I.t1) fetch(p.k_pool, (I.tile0 + I.t0) * kSimtKeys, kv);
     for (int t = I.t0; t < I.t1; ++t) {
       const int k0 = (I.tile0 + t) * kSimtKeys;
       __syncthreads();
-      load(p.k_pool, k0);
+      put(kv);
       __syncthreads();
+      fetch(p.v_pool, k0, kv);
       float s[RT][4];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -215,19 +230,19 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        float4 qv[RT], kv[4];
+        float4 qv[RT], kf[4];
 #pragma unroll
         for (int i = 0; i < RT; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * LD + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * j) * LD + d);
+        for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * j) * LD + d);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-            s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-            s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+            s[i][j] = fmaf(qv[i].x, kf[j].x, s[i][j]);
+            s[i][j] = fmaf(qv[i].y, kf[j].y, s[i][j]);
+            s[i][j] = fmaf(qv[i].z, kf[j].z, s[i][j]);
+            s[i][j] = fmaf(qv[i].w, kf[j].w, s[i][j]);
           }
       }
 #pragma unroll
@@ -259,8 +274,9 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
         for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
       }
       __syncthreads();  // the scores have read K, and the weights are written
-      load(p.v_pool, k0);
+      put(kv);
       __syncthreads();
+      if (t + 1 < I.t1) fetch(p.k_pool, k0 + kSimtKeys, kv);
 #pragma unroll 4
       for (int key = 0; key < kSimtKeys; ++key) {
         float w[RT];
@@ -335,6 +351,9 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.min_units = 2;
     p.max_parts = device_sm_count() * 2;
   }
+  p.page_shift = -1;
+  if ((p.page_size & (p.page_size - 1)) == 0)
+    for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
   p.item_heads = p.hq / p.tile_heads;
   const int64_t by_len = (int64_t)p.batch * (((int64_t)p.max_qo_len + p.item_tokens - 1) / p.item_tokens);
   const int64_t by_rows = (int64_t)p.total_qo / p.item_tokens + p.batch;

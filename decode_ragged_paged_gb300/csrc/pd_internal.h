@@ -242,8 +242,9 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 struct ChunkParams {
   int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
   int32_t causal, window, o_dtype, nhd;
-  int32_t tc;         // the tensor-core kernel takes the call
-  int32_t self_plan;  // every CTA makes the work line for itself
+  int32_t tc;          // the tensor-core kernel takes the call
+  int32_t page_shift;  // log2 of a page size that is a power of two, else -1
+  int32_t self_plan;   // every CTA makes the work line for itself
   int32_t tile_heads, item_heads, item_tokens, key_tile, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)
   int64_t q_stride;  // elements between query tokens
