@@ -35,40 +35,31 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
 }
 
 // ------------------------------------------------------------------ merge
-// o and lse of the items that the line's cuts fell into: block x looks at the
-// cut behind part x, and works if an item's first cut is there. One warp a row.
+// o and lse of the items that the line's cuts fell into: block x has the item
+// that part x begins and does not end, if there is one. One warp a row.
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int64_t units = p.hdr[0], parts = p.hdr[1];
   const int c = blockIdx.x;
-  if (c + 1 >= parts || units == 0) return;
-  const int64_t from = part_start(units, parts, c), cut = part_start(units, parts, c + 1);
-  ChunkWalk w;
-  w.seek(p, p.req_first, p.pre, cut, units);
-  const int64_t s = w.item_start;
-  const int n = w.tiles(p);
-  if (s < from || s >= cut || cut >= s + n) return;  // an earlier part's item, or no tile behind the cut
-  int64_t last = c + 1;  // the part that holds the item's last tile
-  while (last + 1 < parts && part_start(units, parts, last + 1) < s + n) ++last;
-  const int tok0 = w.b * p.item_tokens;
-  const int rows = min(p.item_tokens, w.q.qo - tok0) * p.tile_heads;
+  const int4 cut = p.cuts[c];  // {row of the first token, rows, query head, last part}
+  const int rows = cut.y, last = cut.w;
+  if (last <= c) return;
   const int lane = threadIdx.x & 31;
   constexpr int E = D / 32;
   for (int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); m < rows;
        m += gridDim.y * (kMergeThreads / 32)) {
     float best = -INFINITY;
-    for (int64_t x = c; x <= last; ++x)
-      best = fmaxf(best, p.part_lse[(2 * x + (x == c ? 1 : 0)) * p.rows + m]);
+    for (int x = c; x <= last; ++x)
+      best = fmaxf(best, p.part_lse[(2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m]);
     if (best == -INFINITY) best = 0.f;  // no part has a key: every factor below is 0
     float sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int64_t x = c; x <= last; ++x) {
-      const int64_t slot = (2 * x + (x == c ? 1 : 0)) * p.rows + m;
+    for (int x = c; x <= last; ++x) {
+      const int64_t slot = (2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m;
       const float f = exp2f(p.part_lse[slot] - best);
       const float* o = p.part_o + slot * D + lane * E;
       sum += f;
@@ -86,7 +77,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int tok = m / p.tile_heads;
-    const int64_t row = (int64_t)(w.q.row + tok0 + tok) * p.hq + w.h * p.tile_heads + (m - tok * p.tile_heads);
+    const int64_t row = (int64_t)(cut.x + tok) * p.hq + cut.z + (m - tok * p.tile_heads);
     if (p.o_dtype == PD_BF16) {
       uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * E);
 #pragma unroll
@@ -126,7 +117,11 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   const int32_t* line_first;
   const int64_t* line_pre;
   const ChunkLine line = take_line<kSimtThreads>(p, simt_smem_raw, line_first, line_pre);
-  if (blockIdx.x >= line.parts) return;
+  if (blockIdx.x >= line.parts) {
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, -1);
+    return;
+  }
+  int4 cut = make_int4(0, 0, 0, -1);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ChunkWalk walk;
   walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
@@ -134,7 +129,8 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
   constexpr int NV = kSimtKeys * VR / kSimtThreads;  // vectors of a tile per thread
   ChunkItem I;
-  while (walk.next(p, I)) {
+  int64_t item_at;
+  while (walk.next(p, I, item_at)) {
     const int rows = I.tokens * p.tile_heads;
     __syncthreads();  // the last item's shared rows have been read
     for (int i = tid; i < R * VR; i += kSimtThreads) {
@@ -215,6 +211,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
         }
       }
     };
+    const bool has_rows = (tid >> 5) * 2 * RT < rows;  // of this warp's; the others only load
     uint4 kv[NV];
     if (I.t0 < I.t1) fetch(p.k_pool, (I.tile0 + I.t0) * kSimtKeys, kv);
     for (int t = I.t0; t < I.t1; ++t) {
@@ -223,6 +220,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       put(kv);
       __syncthreads();
       fetch(p.v_pool, k0, kv);
+      if (has_rows) {
       float s[RT][4];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -273,11 +271,13 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
 #pragma unroll
         for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
       }
+      }
       __syncthreads();  // the scores have read K, and the weights are written
       put(kv);
       __syncthreads();
       if (t + 1 < I.t1) fetch(p.k_pool, k0 + kSimtKeys, kv);
-#pragma unroll 4
+      if (!has_rows) continue;
+#pragma unroll 8
       for (int key = 0; key < kSimtKeys; ++key) {
         float w[RT];
 #pragma unroll
@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       }
     }
     const int64_t slot = part_slot(I, blockIdx.x);
+    if (I.t0 == 0 && I.t1 < I.n) cut = cut_of(p, line, I, item_at, blockIdx.x);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int m = ty * RT + i;
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       }
     }
   }
+  if (tid == 0) p.cuts[blockIdx.x] = cut;
 }
 
 // ------------------------------------------------------------------- host
@@ -348,7 +350,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.item_tokens = p.rows / p.tile_heads;
     p.key_tile = kSimtKeys;
     p.item_cost = 1;
-    p.min_units = 2;
+    p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
     p.max_parts = device_sm_count() * 2;
   }
   p.page_shift = -1;
@@ -368,6 +370,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   L.hdr = take(32 * sizeof(int64_t));
   L.req_first = take(sizeof(int32_t) * ((size_t)p.batch + 1));
   L.pre = take(sizeof(int64_t) * ((size_t)p.max_blocks + 1));
+  L.cuts = take(sizeof(int4) * (size_t)p.max_parts);
   L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
   L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);
   L.total = off;

@@ -142,10 +142,9 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pr
   return line;
 }
 
-// A small batch's line is made by every CTA for itself, in `scratch` (plan_words
-// words of 8 bytes of its shared memory); CTA 0 leaves it for the merge. A large
-// one's has been left in the workspace by the plan kernel. The seek that follows
-// reads it where this returns it.
+// A small batch's line is made by every CTA for itself, in `scratch` (kSelfBytes
+// of its shared memory); a large one's has been left in the workspace by the plan
+// kernel. The seek that follows reads it where this returns it.
 constexpr int kSelfBatch = 256, kSelfBlocks = 1024;
 constexpr size_t kSelfBytes = 32 * 8 + (kSelfBlocks + 2) * 8 + (kSelfBatch + 2) * 4;
 
@@ -160,21 +159,9 @@ __device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scrat
   long long* warp_tot = static_cast<long long*>(scratch);
   int64_t* own_pre = reinterpret_cast<int64_t*>(warp_tot + 32);
   int32_t* own_first = reinterpret_cast<int32_t*>(own_pre + kSelfBlocks + 2);
-  const ChunkLine line = plan_line<NT>(p, own_first, own_pre, warp_tot);
   first = own_first;
   pre = own_pre;
-  if (blockIdx.x == 0) {
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-      p.hdr[0] = line.units;
-      p.hdr[1] = line.parts;
-    }
-    if (line.units > 0) {
-      for (int r = tid; r <= p.batch; r += NT) p.req_first[r] = own_first[r];
-      for (int b = tid; b <= own_first[p.batch]; b += NT) p.pre[b] = own_pre[b];
-    }
-  }
-  return line;
+  return plan_line<NT>(p, own_first, own_pre, warp_tot);
 }
 
 struct ChunkWalk {
@@ -214,13 +201,8 @@ struct ChunkWalk {
     q = chunk_request(p, r, false);
   }
 
-  // Key tiles of the item at hand.
-  __device__ __forceinline__ int tiles(const ChunkParams& p) const {
-    return block_units(p, q.qo, q.kv, b) - p.item_cost;
-  }
-
-  // The next item of the part that has keys here, or none at all to see.
-  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkItem& I) {
+  // The next item of the part that has keys here, or none at all to see; `at`: its first unit.
+  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkItem& I, int64_t& at) {
     while (u < u1) {
       I.first_tok = b * p.item_tokens;
       I.tokens = min(p.item_tokens, q.qo - I.first_tok);
@@ -233,6 +215,7 @@ struct ChunkWalk {
       I.keys = chunk_keys(p, q.qo, q.kv, I.first_tok, I.first_tok + I.tokens);
       I.tile0 = I.keys.lo / p.key_tile;
       I.n = chunk_tiles(p, I.keys);
+      at = item_start;
       I.t0 = (int)(u - item_start);
       I.t1 = (int)min((int64_t)I.n, u1 - item_start);
       const bool some = I.n > 0 ? I.t0 < I.n : I.t0 == 0;
@@ -262,6 +245,15 @@ struct ChunkWalk {
 __device__ __forceinline__ int64_t part_slot(const ChunkItem& I, int c) {
   if (I.t0 == 0 && I.t1 == I.n) return -1;
   return 2 * (int64_t)c + (I.t0 == 0 ? 1 : 0);
+}
+
+// What the merge has to know of an item that part c begins and does not end:
+// {row of its first token, rows, query head, part that holds its last tile}.
+__device__ __forceinline__ int4 cut_of(const ChunkParams& p, const ChunkLine& line, const ChunkItem& I, int64_t at,
+                                       int c) {
+  int last = c + 1;
+  while (last + 1 < line.parts && part_start(line.units, line.parts, last + 1) < at + I.n) ++last;
+  return make_int4(I.q0, I.tokens * p.tile_heads, I.h, last);
 }
 
 }  // namespace pd

@@ -200,9 +200,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // ------------------------------------------------------------ scheduler
     // Walks the CTA's part of the line ahead of the other warps.
     uint32_t slot = 0, turn = 0;
+    int4 cut = make_int4(0, 0, 0, -1);
+    int64_t item_at;
     for (bool more = true; more;) {
-      more = walk.next(p, I);
+      more = walk.next(p, I, item_at);
       if (!more) I.tokens = 0;
+      else if (I.t0 == 0 && I.t1 < I.n) cut = cut_of(p, line, I, item_at, blockIdx.x);
       if (!warp_mbar_wait(&bars->item_empty[slot], (turn & 1u) ^ 1u, abort, p.status)) break;
       if (lane == 0) {
         bars->items[slot] = I;
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       __syncwarp();
       if (++slot == kItems) slot = 0, ++turn;
     }
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
   } else if (p.self_plan) {
     fence_proxy_async_smem();
     __syncthreads();

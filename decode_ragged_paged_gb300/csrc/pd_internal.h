@@ -237,6 +237,7 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 //   hdr        int64[32]        hdr[0] = units in total, hdr[1] = parts
 //   req_first  int32[B + 1]     first block of every request
 //   pre        int64[max_blocks + 1]  units of one head before every block
+//   cuts       int4[parts]      the item that a part begins and does not end
 //   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
 //   part_o     float[2 * parts][rows][D]  its normalised output
 struct ChunkParams {
@@ -260,12 +261,13 @@ struct ChunkParams {
   int64_t* hdr;
   int32_t* req_first;
   int64_t* pre;
+  int4* cuts;
   float* part_lse;
   float* part_o;
   int32_t* status;
 };
 struct ChunkLayout {
-  size_t hdr, req_first, pre, part_lse, part_o, total;
+  size_t hdr, req_first, pre, cuts, part_lse, part_o, total;
 };
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
