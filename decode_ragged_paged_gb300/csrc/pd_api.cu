@@ -728,6 +728,7 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   p.hdr = reinterpret_cast<int64_t*>(ws + L.hdr);
   p.req_first = reinterpret_cast<int32_t*>(ws + L.req_first);
   p.pre = reinterpret_cast<int64_t*>(ws + L.pre);
+  p.pos = reinterpret_cast<int64_t*>(ws + L.pos);
   p.cuts = reinterpret_cast<int4*>(ws + L.cuts);
   p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);

@@ -27,10 +27,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   __shared__ long long warp_tot[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const ChunkLine line = plan_line<kPlanThreads>(p, p.req_first, p.pre, warp_tot);
+  const ChunkLine line = plan_line<kPlanThreads>(p, p.req_first, p.pre, p.pos, warp_tot);
   if (threadIdx.x == 0) {
-    p.hdr[0] = line.units;
-    p.hdr[1] = line.parts;
+    p.hdr[0] = line.rem;
+    p.hdr[1] = line.head;
+    p.hdr[2] = line.base;
+    p.hdr[3] = line.parts;
+    p.hdr[4] = line.whole;
   }
 }
 
@@ -52,13 +55,14 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
        m += gridDim.y * (kMergeThreads / 32)) {
     float best = -INFINITY;
     for (int x = c; x <= last; ++x)
-      best = fmaxf(best, p.part_lse[(2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m]);
+      if (x == c || p.cuts[x].y >= 0) best = fmaxf(best, p.part_lse[(2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m]);
     if (best == -INFINITY) best = 0.f;  // no part has a key: every factor below is 0
     float sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
     for (int x = c; x <= last; ++x) {
+      if (x > c && p.cuts[x].y < 0) continue;  // an empty part
       const int64_t slot = (2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m;
       const float f = exp2f(p.part_lse[slot] - best);
       const float* o = p.part_o + slot * D + lane * E;
@@ -114,23 +118,17 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   float* sP = sKV + kSimtKeys * LD;  // [key][row]
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int32_t* line_first;
-  const int64_t* line_pre;
-  const ChunkLine line = take_line<kSimtThreads>(p, simt_smem_raw, line_first, line_pre);
-  if (blockIdx.x >= line.parts) {
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, -1);
-    return;
-  }
-  int4 cut = make_int4(0, 0, 0, -1);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ChunkWalk walk;
-  walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
-            part_start(line.units, line.parts, blockIdx.x + 1));
+  {
+    const ChunkLine line = take_line<kSimtThreads>(p, simt_smem_raw);
+    const int4 cut = walk.begin(p, line, blockIdx.x);
+    if (tid == 0) p.cuts[blockIdx.x] = cut;
+  }
   constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
   constexpr int NV = kSimtKeys * VR / kSimtThreads;  // vectors of a tile per thread
   ChunkItem I;
-  int64_t item_at;
-  while (walk.next(p, I, item_at)) {
+  while (walk.next(p, I)) {
     const int rows = I.tokens * p.tile_heads;
     __syncthreads();  // the last item's shared rows have been read
     for (int i = tid; i < R * VR; i += kSimtThreads) {
@@ -296,7 +294,6 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       }
     }
     const int64_t slot = part_slot(I, blockIdx.x);
-    if (I.t0 == 0 && I.t1 < I.n) cut = cut_of(p, line, I, item_at, blockIdx.x);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int m = ty * RT + i;
@@ -325,7 +322,6 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       }
     }
   }
-  if (tid == 0) p.cuts[blockIdx.x] = cut;
 }
 
 // ------------------------------------------------------------------- host
@@ -370,11 +366,12 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   L.hdr = take(32 * sizeof(int64_t));
   L.req_first = take(sizeof(int32_t) * ((size_t)p.batch + 1));
   L.pre = take(sizeof(int64_t) * ((size_t)p.max_blocks + 1));
+  L.pos = take(sizeof(int64_t) * ((size_t)p.max_parts + 1));
   L.cuts = take(sizeof(int4) * (size_t)p.max_parts);
   L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
   L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);
   L.total = off;
-  p.self_plan = p.batch <= kSelfBatch && p.max_blocks <= kSelfBlocks;
+  p.self_plan = p.batch <= kSelfBatch && p.max_blocks <= kSelfBlocks && p.max_parts <= kSelfParts;
   return L;
 }
 

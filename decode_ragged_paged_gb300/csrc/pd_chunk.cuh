@@ -1,11 +1,19 @@
-// pd_chunk.cuh -- the work line of the chunk attention: how (request, token
-// block, head) items become units, and how a CTA walks its part of the line.
+// pd_chunk.cuh -- the work of the chunk attention: how (request, token block,
+// head) items are dealt to the CTAs.
 //
-// The blocks of a request follow one another, its heads follow one another
-// around them (all blocks of a head, then the next head), the requests around
-// those. pre[b] holds the units of one head before block b, so request r's
-// units start at item_heads * pre[first(r)], its head h at + h * (pre[first(r +
-// 1)] - pre[first(r)]), and a position is found by two binary searches.
+// An item's work is counted in units, one per key tile and item_cost more; pre[b]
+// holds the units of one head before block b of the batch.
+//   The line. The items in a row, head by head, a head's blocks in batch order,
+// cut into equal parts, one per CTA, anywhere between two key tiles: every CTA
+// has the same work, and an item that a cut falls into is merged afterwards.
+// With the head outermost, CTAs that are at the same place of different heads
+// read the same pages at the same time (two thirds of HBM's rate came to be four
+// fifths by that order alone, for requests of a few tokens).
+//   Whole items. Blocks of one request read the same keys. Where there are
+// several times more items than CTAs, the first `whole` blocks are dealt out
+// item by item, block by block with its heads: the CTAs then stream the same
+// keys at the same time, out of L2. What is left makes the line, cut so that
+// every CTA's whole items and part come to the same.
 #pragma once
 
 #include "pd_common.cuh"
@@ -62,8 +70,6 @@ __device__ __forceinline__ int block_units(const ChunkParams& p, int qo, int kv,
   return p.item_cost + chunk_tiles(p, chunk_keys(p, qo, kv, t0, min(qo, t0 + p.item_tokens)));
 }
 
-__device__ __forceinline__ int64_t part_start(int64_t units, int64_t parts, int64_t c) { return units * c / parts; }
-
 // Exclusive scan over a CTA of NT threads, and the total; warp_tot: NT / 32 words of shared memory.
 template <int NT>
 __device__ __forceinline__ long long scan_exclusive(long long v, long long* warp_tot, long long& total) {
@@ -88,16 +94,25 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long* warp
   return (warp > 0 ? before : 0) + x - v;
 }
 
-// The work line of a batch, by one CTA: checks the requests, numbers their
-// blocks (first [B + 1]) and sums the blocks' units (pre [blocks + 1]), both in
-// global memory or in the CTA's own shared memory. Ends with a barrier.
+// What a CTA has to know of the line.
 struct ChunkLine {
-  int64_t units, parts;
+  int64_t rem, head, base;  // units of the line, of one head of it, and of one head before it
+  int parts, whole;         // parts of the line; blocks dealt out whole before it
+  const int32_t* first;     // first block of every request
+  const int64_t* pre;       // units of one head before every block
+  const int64_t* pos;       // first unit of every part
+
+  __device__ __forceinline__ int64_t start(int c) const { return pos[c]; }
 };
 
+// The line of a batch, by one CTA: checks the requests, numbers their blocks
+// (first [B + 1]), sums the blocks' units (pre [blocks + 1]) and cuts the line
+// (pos [max_parts + 1]), in global memory or in the CTA's own shared memory. Ends
+// with a barrier.
 template <int NT>
-__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pre, long long* warp_tot) {
+__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pre, int64_t* pos, long long* warp_tot) {
   const int tid = threadIdx.x;
+  ChunkLine line{0, 1, 0, 0, 0, first, pre, pos};
   long long carry = 0, total;
   for (int r0 = 0; r0 < p.batch; r0 += NT) {
     const int r = r0 + tid;
@@ -106,11 +121,11 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pr
     if (r < p.batch) first[r] = (int)min(at, (long long)p.max_blocks);
     carry += total;
   }
-  if (carry > p.max_blocks) {
-    // more blocks than rows allow: requests whose rows overlap. None is worked on.
-    if (tid == 0) report(p.status, PD_DEV_BAD_INDPTR);
+  if (carry > p.max_blocks || carry == 0) {
+    // none, or more blocks than rows allow: requests whose rows overlap. None is worked on.
+    if (tid == 0 && carry > 0) report(p.status, PD_DEV_BAD_INDPTR);
     __syncthreads();
-    return ChunkLine{0, 1};
+    return line;
   }
   const int blocks = (int)carry;
   if (tid == 0) first[p.batch] = blocks;
@@ -133,106 +148,178 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pr
     carry += total;
   }
   if (tid == 0) pre[blocks] = carry;
-  ChunkLine line;
-  line.units = carry * p.item_heads;
-  line.parts = (line.units + p.min_units - 1) / p.min_units;  // at least so many units a part
-  if (line.parts > p.max_parts) line.parts = p.max_parts;
-  if (line.parts < 1) line.parts = 1;
+  __syncthreads();
+  const int G = p.max_parts, H = p.item_heads;
+  const int64_t items = (int64_t)blocks * H, units = carry * H;
+  // whole items: all rounds but the last, whose items the line evens out
+  if (blocks >= 2 * p.batch && items >= 3 * (int64_t)G) line.whole = (int)((items / G - 1) * G / H);
+  line.base = pre[line.whole];
+  line.head = carry - line.base;
+  line.rem = line.head * H;
+  if (line.whole == 0) {
+    const int64_t most = (units + p.min_units - 1) / p.min_units;  // at least so many units a part
+    line.parts = (int)min((int64_t)G, most);
+    for (int c = tid; c <= line.parts; c += NT) pos[c] = line.rem * c / line.parts;
+  } else {
+    line.parts = G;
+    carry = 0;
+    for (int c0 = 0; c0 < G; c0 += NT) {
+      const int c = c0 + tid;
+      long long share = 0;
+      if (c < G) {
+        for (int64_t i = c; i < (int64_t)line.whole * H; i += G) share += pre[i / H + 1] - pre[i / H];
+        share = max(units / G - share, 0LL);
+      }
+      const long long at = carry + scan_exclusive<NT>(share, warp_tot, total);
+      if (c < G) pos[c] = at;
+      carry += total;
+    }
+    __syncthreads();
+    // the shares come to the line's units, or (rounding, CTAs with too much already) to nearly that
+    const double scale = carry > 0 ? (double)line.rem / (double)carry : 0.0;
+    for (int c = tid; c < G; c += NT) pos[c] = min((int64_t)((double)pos[c] * scale), line.rem);
+    if (tid == 0) pos[G] = line.rem;
+  }
   __syncthreads();
   return line;
 }
 
 // A small batch's line is made by every CTA for itself, in `scratch` (kSelfBytes
 // of its shared memory); a large one's has been left in the workspace by the plan
-// kernel. The seek that follows reads it where this returns it.
-constexpr int kSelfBatch = 256, kSelfBlocks = 1024;
-constexpr size_t kSelfBytes = 32 * 8 + (kSelfBlocks + 2) * 8 + (kSelfBatch + 2) * 4;
+// kernel.
+constexpr int kSelfBatch = 256, kSelfBlocks = 1024, kSelfParts = 512;
+constexpr size_t kSelfBytes = 32 * 8 + (kSelfBlocks + 2) * 8 + (kSelfParts + 2) * 8 + (kSelfBatch + 2) * 4;
 
 template <int NT>
-__device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scratch, const int32_t*& first,
-                                               const int64_t*& pre) {
-  if (!p.self_plan) {
-    first = p.req_first;
-    pre = p.pre;
-    return ChunkLine{p.hdr[0], p.hdr[1]};
-  }
+__device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scratch) {
+  if (!p.self_plan)
+    return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], (int)p.hdr[3], (int)p.hdr[4], p.req_first, p.pre, p.pos};
   long long* warp_tot = static_cast<long long*>(scratch);
-  int64_t* own_pre = reinterpret_cast<int64_t*>(warp_tot + 32);
-  int32_t* own_first = reinterpret_cast<int32_t*>(own_pre + kSelfBlocks + 2);
-  first = own_first;
-  pre = own_pre;
-  return plan_line<NT>(p, own_first, own_pre, warp_tot);
+  int64_t* pre = reinterpret_cast<int64_t*>(warp_tot + 32);
+  int64_t* pos = pre + kSelfBlocks + 2;
+  return plan_line<NT>(p, reinterpret_cast<int32_t*>(pos + kSelfParts + 2), pre, pos, warp_tot);
 }
 
-struct ChunkWalk {
-  int64_t u = 0, u1 = 0;  // units left: [u, u1)
-  int64_t item_start;
-  int r, b, h;  // request, block of it, item head
+// A place among the items: block b of request r, item head h.
+struct ChunkPlace {
+  int r, b, h;
   ChunkRequest q;
 
-  // To unit `at` of the line; the part ends before unit `end`.
-  __device__ __forceinline__ void seek(const ChunkParams& p, const int32_t* first, const int64_t* pre, int64_t at,
-                                       int64_t end) {
-    u = at;
-    u1 = end;
-    if (u >= u1) return;
-    // last request whose units start at or before `at` (requests without blocks start where the next one does)
+  // `n` blocks on, over requests without any; false past the last request.
+  __device__ __forceinline__ bool skip(const ChunkParams& p, int n) {
+    b += n;
+    while (b >= q.blocks) {
+      b -= q.blocks;
+      if (++r >= p.batch) return false;
+      q = chunk_request(p, r, false);
+    }
+    return true;
+  }
+};
+
+struct ChunkWalk {
+  // whole items: number `item` of `whole_items`, at place w
+  int64_t item = 0, whole_items = 0;
+  ChunkPlace w;
+  // the part of the line: units [u, u1), in the item that starts at item_start, at place l
+  int64_t u = 0, u1 = 0, item_start = 0;
+  ChunkPlace l, line_first;  // line_first: the line's first block
+
+  // Place of block number `block` of the batch.
+  static __device__ __forceinline__ ChunkPlace place(const ChunkParams& p, const ChunkLine& line, int block, int h) {
+    // last request whose blocks start at or before it (requests without blocks start where the next one does)
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pre[first[mid]] * p.item_heads <= at) lo = mid;
+      if (line.first[mid] <= block) lo = mid;
       else hi = mid;
     }
-    r = lo;
-    const int b0 = first[r], b1 = first[r + 1];
-    const int64_t start = pre[b0] * p.item_heads, per_head = pre[b1] - pre[b0];
-    h = (int)((at - start) / per_head);
-    const int64_t head_start = start + h * per_head;
-    const int64_t rest = at - head_start + pre[b0];
-    lo = b0;
-    hi = b1;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= rest) lo = mid;
-      else hi = mid;
-    }
-    b = lo - b0;
-    item_start = head_start + pre[lo] - pre[b0];
-    q = chunk_request(p, r, false);
+    return ChunkPlace{lo, block - line.first[lo], h, chunk_request(p, lo, false)};
   }
 
-  // The next item of the part that has keys here, or none at all to see; `at`: its first unit.
-  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkItem& I, int64_t& at) {
+  // Place of unit `at` of the line, and its item's first unit.
+  static __device__ __forceinline__ ChunkPlace seek(const ChunkParams& p, const ChunkLine& line, int64_t at,
+                                                    int64_t& item_start) {
+    const int h = (int)(at / line.head);
+    const int64_t rest = at - h * line.head + line.base;
+    int lo = line.whole, hi = line.first[p.batch];
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (line.pre[mid] <= rest) lo = mid;
+      else hi = mid;
+    }
+    item_start = h * line.head + line.pre[lo] - line.base;
+    return place(p, line, lo, h);
+  }
+
+  // To CTA c's work. Returns what the merge has to know of the item that its part
+  // begins and does not end: {row of its first token, rows, query head, part that
+  // holds its last tile}, the last -1 if there is none; rows -1: the part is empty.
+  __device__ __forceinline__ int4 begin(const ChunkParams& p, const ChunkLine& line, int c) {
+    int4 cut = make_int4(0, 0, 0, -1);
+    whole_items = (int64_t)line.whole * p.item_heads;
+    item = c;
+    if (item < whole_items) w = place(p, line, c / p.item_heads, c % p.item_heads);
+    if (c >= line.parts) return cut;
+    u = line.pos[c];
+    u1 = line.pos[c + 1];
+    if (u == u1) cut.y = -1;
+    if (u < u1) {
+      l = seek(p, line, u, item_start);
+      line_first = place(p, line, line.whole, 0);
+    }
+    if (u1 < line.rem) {
+      int64_t s;
+      const ChunkPlace at = seek(p, line, u1, s);
+      const int64_t end = s + block_units(p, at.q.qo, at.q.kv, at.b) - p.item_cost;  // of its tiles
+      if (s >= u && s < u1 && u1 < end) {
+        const int t0 = at.b * p.item_tokens;
+        cut = make_int4(at.q.row + t0, min(p.item_tokens, at.q.qo - t0) * p.tile_heads, at.h * p.tile_heads, c + 1);
+        while (cut.w + 1 < line.parts && line.pos[cut.w + 1] < end) ++cut.w;
+      }
+    }
+    return cut;
+  }
+
+  static __device__ __forceinline__ void describe(const ChunkParams& p, const ChunkPlace& at, ChunkItem& I) {
+    I.first_tok = at.b * p.item_tokens;
+    I.tokens = min(p.item_tokens, at.q.qo - I.first_tok);
+    I.q0 = at.q.row + I.first_tok;
+    I.h = at.h * p.tile_heads;
+    I.qo = at.q.qo;
+    I.kv = at.q.kv;
+    I.pbase = at.q.pbase;
+    I.need = (at.q.kv + p.page_size - 1) / p.page_size;
+    I.keys = chunk_keys(p, at.q.qo, at.q.kv, I.first_tok, I.first_tok + I.tokens);
+    I.tile0 = I.keys.lo / p.key_tile;
+    I.n = chunk_tiles(p, I.keys);
+  }
+
+  // The next item that has keys here, or none at all to see.
+  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkItem& I) {
+    if (item < whole_items) {
+      describe(p, w, I);
+      I.t0 = 0;
+      I.t1 = I.n;
+      const int block = (int)(item / p.item_heads);
+      item += gridDim.x;
+      if (item < whole_items) {
+        w.h = (int)(item % p.item_heads);
+        if (!w.skip(p, (int)(item / p.item_heads) - block)) item = whole_items;
+      }
+      return true;
+    }
     while (u < u1) {
-      I.first_tok = b * p.item_tokens;
-      I.tokens = min(p.item_tokens, q.qo - I.first_tok);
-      I.q0 = q.row + I.first_tok;
-      I.h = h * p.tile_heads;
-      I.qo = q.qo;
-      I.kv = q.kv;
-      I.pbase = q.pbase;
-      I.need = (q.kv + p.page_size - 1) / p.page_size;
-      I.keys = chunk_keys(p, q.qo, q.kv, I.first_tok, I.first_tok + I.tokens);
-      I.tile0 = I.keys.lo / p.key_tile;
-      I.n = chunk_tiles(p, I.keys);
-      at = item_start;
+      describe(p, l, I);
       I.t0 = (int)(u - item_start);
       I.t1 = (int)min((int64_t)I.n, u1 - item_start);
       const bool some = I.n > 0 ? I.t0 < I.n : I.t0 == 0;
       item_start += I.n + p.item_cost;
       u = item_start;
-      if (++b == q.blocks) {
-        b = 0;
-        if (++h == p.item_heads) {
-          h = 0;
-          do {
-            if (++r == p.batch) {
-              u = u1;
-              break;
-            }
-            q = chunk_request(p, r, false);
-          } while (q.blocks == 0);
-        }
+      if (u < u1 && !l.skip(p, 1)) {  // the next head, from the line's first block on
+        const int h = l.h + 1;
+        l = line_first;
+        l.h = h;
       }
       if (some) return true;
     }
@@ -245,15 +332,6 @@ struct ChunkWalk {
 __device__ __forceinline__ int64_t part_slot(const ChunkItem& I, int c) {
   if (I.t0 == 0 && I.t1 == I.n) return -1;
   return 2 * (int64_t)c + (I.t0 == 0 ? 1 : 0);
-}
-
-// What the merge has to know of an item that part c begins and does not end:
-// {row of its first token, rows, query head, part that holds its last tile}.
-__device__ __forceinline__ int4 cut_of(const ChunkParams& p, const ChunkLine& line, const ChunkItem& I, int64_t at,
-                                       int c) {
-  int last = c + 1;
-  while (last + 1 < line.parts && part_start(line.units, line.parts, last + 1) < at + I.n) ++last;
-  return make_int4(I.q0, I.tokens * p.tile_heads, I.h, last);
 }
 
 }  // namespace pd

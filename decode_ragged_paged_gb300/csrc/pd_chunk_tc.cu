@@ -184,15 +184,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const uint32_t tmem = bars->tmem_slot;
   pdl_launch_dependents();
   pdl_wait_primary();  // the plan's work line
-  const int32_t* line_first;
-  const int64_t* line_pre;
-  const ChunkLine line = take_line<kCtThreads>(p, base, line_first, line_pre);
+  const ChunkLine line = take_line<kCtThreads>(p, base);
   ChunkItem I{};
   if (warp == 6) {
     ChunkWalk walk;
-    if (blockIdx.x < line.parts)
-      walk.seek(p, line_first, line_pre, part_start(line.units, line.parts, blockIdx.x),
-                part_start(line.units, line.parts, blockIdx.x + 1));
+    const int4 cut = walk.begin(p, line, blockIdx.x);
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
     if (p.self_plan) {
       fence_proxy_async_smem();
       __syncthreads();  // the line has been read: its place goes to the rings
@@ -200,12 +197,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // ------------------------------------------------------------ scheduler
     // Walks the CTA's part of the line ahead of the other warps.
     uint32_t slot = 0, turn = 0;
-    int4 cut = make_int4(0, 0, 0, -1);
-    int64_t item_at;
     for (bool more = true; more;) {
-      more = walk.next(p, I, item_at);
+      more = walk.next(p, I);
       if (!more) I.tokens = 0;
-      else if (I.t0 == 0 && I.t1 < I.n) cut = cut_of(p, line, I, item_at, blockIdx.x);
       if (!warp_mbar_wait(&bars->item_empty[slot], (turn & 1u) ^ 1u, abort, p.status)) break;
       if (lane == 0) {
         bars->items[slot] = I;
@@ -214,7 +208,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       __syncwarp();
       if (++slot == kItems) slot = 0, ++turn;
     }
-    if (lane == 0) p.cuts[blockIdx.x] = cut;
   } else if (p.self_plan) {
     fence_proxy_async_smem();
     __syncthreads();

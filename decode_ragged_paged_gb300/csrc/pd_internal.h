@@ -230,14 +230,14 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 
 // --------------------------------------------------------- chunk attention
 // An item is (request, block of item_tokens query tokens, tile_heads query
-// heads of one KV head); its keys are cut into tiles of key_tile. All items
-// form one line of units, a tile costing one and an item item_cost more; the
-// line is cut into equal parts, one per CTA (see pd_chunk.cuh).
+// heads of one KV head); its keys are cut into tiles of key_tile. How the items
+// are dealt to the CTAs: pd_chunk.cuh.
 // Workspace (offsets 256-byte aligned):
-//   hdr        int64[32]        hdr[0] = units in total, hdr[1] = parts
+//   hdr        int64[32]        the line's {units, units of a head, units before it, parts, whole blocks}
 //   req_first  int32[B + 1]     first block of every request
 //   pre        int64[max_blocks + 1]  units of one head before every block
-//   cuts       int4[parts]      the item that a part begins and does not end
+//   pos        int64[parts + 1]  first unit of every part of the line
+//   cuts       int4[parts]       the item that a part begins and does not end
 //   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
 //   part_o     float[2 * parts][rows][D]  its normalised output
 struct ChunkParams {
@@ -261,13 +261,14 @@ struct ChunkParams {
   int64_t* hdr;
   int32_t* req_first;
   int64_t* pre;
+  int64_t* pos;
   int4* cuts;
   float* part_lse;
   float* part_o;
   int32_t* status;
 };
 struct ChunkLayout {
-  size_t hdr, req_first, pre, cuts, part_lse, part_o, total;
+  size_t hdr, req_first, pre, pos, cuts, part_lse, part_o, total;
 };
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
