@@ -710,6 +710,7 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   const int rc = check_attn(desc, batch, true);
   if (rc != PD_OK) return rc;
   ChunkParams p = chunk_params(desc, batch, window_left, q_stride);
+  if (batch->max_kv_len > kChunkMaxKeys) return PD_ERR_UNSUPPORTED;
   if (p.q_stride < (int64_t)p.hq * p.head_dim || p.q_stride * elem_size(desc->kv_dtype) % 16 != 0)
     return PD_ERR_INVALID_ARG;
   if (batch->batch_size == 0 || batch->total_qo == 0 || batch->max_qo_len == 0) return PD_OK;
@@ -725,10 +726,10 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   p.o = o;
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.hdr = reinterpret_cast<int64_t*>(ws + L.hdr);
+  p.hdr = reinterpret_cast<int32_t*>(ws + L.hdr);
   p.req_first = reinterpret_cast<int32_t*>(ws + L.req_first);
-  p.pre = reinterpret_cast<int64_t*>(ws + L.pre);
-  p.pos = reinterpret_cast<int64_t*>(ws + L.pos);
+  p.pre = reinterpret_cast<int32_t*>(ws + L.pre);
+  p.pos = reinterpret_cast<int32_t*>(ws + L.pos);
   p.cuts = reinterpret_cast<int4*>(ws + L.cuts);
   p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);

@@ -24,7 +24,7 @@ constexpr int kPlanThreads = 1024;
 
 // ------------------------------------------------------------------- plan
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p) {
-  __shared__ long long warp_tot[kPlanThreads / 32];
+  __shared__ int warp_tot[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait_primary();
   const ChunkLine line = plan_line<kPlanThreads>(p, p.req_first, p.pre, p.pos, warp_tot);
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
 // scores, the same rows and D / 16 columns of the output; a row's maximum and
 // sum go over its 16 lanes by shuffles.
 constexpr int kSimtThreads = 256;
-constexpr int kSimtKeys = 64;
+constexpr int kSimtKeys = kChunkKeys;
 
 template <int R, int D>
 constexpr size_t simt_smem() {
@@ -333,7 +333,6 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
     p.item_tokens = 2 * (128 / p.tile_heads);  // two query tiles
     p.rows = p.item_tokens * p.tile_heads;
-    p.key_tile = kChunkTcKeys;
     p.item_cost = 2;
     p.min_units = 4;
     p.max_parts = device_sm_count();
@@ -344,7 +343,6 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.rows = most <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
-    p.key_tile = kSimtKeys;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
     p.max_parts = device_sm_count() * 2;
@@ -363,10 +361,10 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     off = align_up(off + bytes, 256);
     return at;
   };
-  L.hdr = take(32 * sizeof(int64_t));
+  L.hdr = take(32 * sizeof(int32_t));
   L.req_first = take(sizeof(int32_t) * ((size_t)p.batch + 1));
-  L.pre = take(sizeof(int64_t) * ((size_t)p.max_blocks + 1));
-  L.pos = take(sizeof(int64_t) * ((size_t)p.max_parts + 1));
+  L.pre = take(sizeof(int32_t) * ((size_t)p.max_blocks + 1));
+  L.pos = take(sizeof(int32_t) * ((size_t)p.max_parts + 1));
   L.cuts = take(sizeof(int4) * (size_t)p.max_parts);
   L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
   L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);

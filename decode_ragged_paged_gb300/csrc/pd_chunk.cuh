@@ -6,9 +6,6 @@
 //   The line. The items in a row, head by head, a head's blocks in batch order,
 // cut into equal parts, one per CTA, anywhere between two key tiles: every CTA
 // has the same work, and an item that a cut falls into is merged afterwards.
-// With the head outermost, CTAs that are at the same place of different heads
-// read the same pages at the same time (two thirds of HBM's rate came to be four
-// fifths by that order alone, for requests of a few tokens).
 //   Whole items. Blocks of one request read the same keys. Where there are
 // several times more items than CTAs, the first `whole` blocks are dealt out
 // item by item, block by block with its heads: the CTAs then stream the same
@@ -34,7 +31,7 @@ __device__ __forceinline__ KeyRange chunk_keys(const ChunkParams& p, int qo, int
 }
 
 __device__ __forceinline__ int chunk_tiles(const ChunkParams& p, KeyRange k) {
-  return k.hi > k.lo ? (k.hi + p.key_tile - 1) / p.key_tile - k.lo / p.key_tile : 0;
+  return k.hi > k.lo ? (k.hi - 1) / kChunkKeys + 1 - k.lo / kChunkKeys : 0;
 }
 
 // A CTA's share of one item: key tiles [t0, t1) of its n.
@@ -72,37 +69,36 @@ __device__ __forceinline__ int block_units(const ChunkParams& p, int qo, int kv,
 
 // Exclusive scan over a CTA of NT threads, and the total; warp_tot: NT / 32 words of shared memory.
 template <int NT>
-__device__ __forceinline__ long long scan_exclusive(long long v, long long* warp_tot, long long& total) {
+__device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  int x = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
   __syncthreads();  // the totals of an earlier scan have been read
   if (lane == 31) warp_tot[warp] = x;
   __syncthreads();
-  long long w = lane < NT / 32 ? warp_tot[lane] : 0;
+  int w = lane < NT / 32 ? warp_tot[lane] : 0;
 #pragma unroll
   for (int d = 1; d < NT / 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, w, d);
+    const int y = __shfl_up_sync(0xffffffffu, w, d);
     if (lane >= d) w += y;
   }
   total = __shfl_sync(0xffffffffu, w, NT / 32 - 1);
-  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   return (warp > 0 ? before : 0) + x - v;
 }
 
-// What a CTA has to know of the line.
+// What a CTA has to know of the line. Units are counted in 32 bits: 2^31 tiles of
+// 64 keys and 256 rows are hours of work.
 struct ChunkLine {
-  int64_t rem, head, base;  // units of the line, of one head of it, and of one head before it
-  int parts, whole;         // parts of the line; blocks dealt out whole before it
-  const int32_t* first;     // first block of every request
-  const int64_t* pre;       // units of one head before every block
-  const int64_t* pos;       // first unit of every part
-
-  __device__ __forceinline__ int64_t start(int c) const { return pos[c]; }
+  int rem, head, base;  // units of the line, of one head of it, and of one head before it
+  int parts, whole;     // parts of the line; blocks dealt out whole before it
+  const int32_t* first; // first block of every request
+  const int32_t* pre;   // units of one head before every block
+  const int32_t* pos;   // first unit of every part
 };
 
 // The line of a batch, by one CTA: checks the requests, numbers their blocks
@@ -110,30 +106,28 @@ struct ChunkLine {
 // (pos [max_parts + 1]), in global memory or in the CTA's own shared memory. Ends
 // with a barrier.
 template <int NT>
-__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pre, int64_t* pos, long long* warp_tot) {
+__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pre, int32_t* pos, int* warp_tot) {
   const int tid = threadIdx.x;
   ChunkLine line{0, 1, 0, 0, 0, first, pre, pos};
-  long long carry = 0, total;
+  // kChunkMaxKeys and the rows that fit a GPU keep the sums of NT requests or blocks inside 32 bits
+  int carry = 0, total;
+  bool over = false;
   for (int r0 = 0; r0 < p.batch; r0 += NT) {
     const int r = r0 + tid;
-    const long long n = r < p.batch ? chunk_request(p, r, true).blocks : 0;
-    const long long at = carry + scan_exclusive<NT>(n, warp_tot, total);
-    if (r < p.batch) first[r] = (int)min(at, (long long)p.max_blocks);
+    const int n = r < p.batch ? chunk_request(p, r, true).blocks : 0;
+    const int at = carry + scan_exclusive<NT>(n, warp_tot, total);
+    if (r < p.batch) first[r] = min(at, p.max_blocks);
     carry += total;
+    over = over || carry > p.max_blocks;
+    if (over) break;
   }
-  if (carry > p.max_blocks || carry == 0) {
-    // none, or more blocks than rows allow: requests whose rows overlap. None is worked on.
-    if (tid == 0 && carry > 0) report(p.status, PD_DEV_BAD_INDPTR);
-    __syncthreads();
-    return line;
-  }
-  const int blocks = (int)carry;
-  if (tid == 0) first[p.batch] = blocks;
+  const int blocks = carry;
+  if (!over && tid == 0) first[p.batch] = blocks;
   __syncthreads();
-  carry = 0;
-  for (int b0 = 0; b0 < blocks; b0 += NT) {
+  long long sum = 0;
+  for (int b0 = 0; !over && b0 < blocks; b0 += NT) {
     const int b = b0 + tid;
-    long long units = 0;
+    int units = 0;
     if (b < blocks) {
       int lo = 0, hi = p.batch;
       while (hi - lo > 1) {
@@ -143,41 +137,48 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pr
       }
       units = block_units(p, p.qo_indptr[lo + 1] - p.qo_indptr[lo], p.kv_len[lo], b - first[lo]);
     }
-    const long long at = carry + scan_exclusive<NT>(units, warp_tot, total);
-    if (b < blocks) pre[b] = at;
-    carry += total;
+    const int at = scan_exclusive<NT>(units, warp_tot, total);
+    if (b < blocks) pre[b] = (int)sum + at;
+    sum += total;
+    over = sum * p.item_heads > 0x7fffffffLL;
+  }
+  carry = (int)sum;
+  if (over || carry == 0) {
+    // more blocks than rows allow (requests whose rows overlap), or more work than a call takes: none is worked on
+    if (tid == 0 && over) report(p.status, PD_DEV_BAD_INDPTR);
+    __syncthreads();
+    return line;
   }
   if (tid == 0) pre[blocks] = carry;
   __syncthreads();
-  const int G = p.max_parts, H = p.item_heads;
-  const int64_t items = (int64_t)blocks * H, units = carry * H;
+  const int G = p.max_parts, H = p.item_heads, units = carry * H;
   // whole items: all rounds but the last, whose items the line evens out
-  if (blocks >= 2 * p.batch && items >= 3 * (int64_t)G) line.whole = (int)((items / G - 1) * G / H);
+  if (blocks >= 2 * p.batch && (int64_t)blocks * H >= 3 * (int64_t)G)
+    line.whole = (int)(((int64_t)blocks * H / G - 1) * G / H);
   line.base = pre[line.whole];
   line.head = carry - line.base;
   line.rem = line.head * H;
   if (line.whole == 0) {
-    const int64_t most = (units + p.min_units - 1) / p.min_units;  // at least so many units a part
-    line.parts = (int)min((int64_t)G, most);
-    for (int c = tid; c <= line.parts; c += NT) pos[c] = line.rem * c / line.parts;
+    line.parts = min(G, (units + p.min_units - 1) / p.min_units);  // at least so many units a part
+    const int each = line.rem / line.parts, left = line.rem - each * line.parts;
+    for (int c = tid; c <= line.parts; c += NT) pos[c] = each * c + left * c / line.parts;
   } else {
     line.parts = G;
     carry = 0;
     for (int c0 = 0; c0 < G; c0 += NT) {
       const int c = c0 + tid;
-      long long share = 0;
+      int share = 0;
       if (c < G) {
-        for (int64_t i = c; i < (int64_t)line.whole * H; i += G) share += pre[i / H + 1] - pre[i / H];
-        share = max(units / G - share, 0LL);
+        for (int i = c; i < line.whole * H; i += G) share += pre[i / H + 1] - pre[i / H];
+        share = max(units / G - share, 0);
       }
-      const long long at = carry + scan_exclusive<NT>(share, warp_tot, total);
+      const int at = carry + scan_exclusive<NT>(share, warp_tot, total);
       if (c < G) pos[c] = at;
       carry += total;
     }
     __syncthreads();
     // the shares come to the line's units, or (rounding, CTAs with too much already) to nearly that
-    const double scale = carry > 0 ? (double)line.rem / (double)carry : 0.0;
-    for (int c = tid; c < G; c += NT) pos[c] = min((int64_t)((double)pos[c] * scale), line.rem);
+    for (int c = tid; c < G; c += NT) pos[c] = carry > 0 ? (int)((int64_t)pos[c] * line.rem / carry) : 0;
     if (tid == 0) pos[G] = line.rem;
   }
   __syncthreads();
@@ -188,22 +189,27 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int64_t* pr
 // of its shared memory); a large one's has been left in the workspace by the plan
 // kernel.
 constexpr int kSelfBatch = 256, kSelfBlocks = 1024, kSelfParts = 512;
-constexpr size_t kSelfBytes = 32 * 8 + (kSelfBlocks + 2) * 8 + (kSelfParts + 2) * 8 + (kSelfBatch + 2) * 4;
+constexpr size_t kSelfBytes = 4 * (32 + kSelfBlocks + 2 + kSelfParts + 2 + kSelfBatch + 2);
 
 template <int NT>
 __device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scratch) {
-  if (!p.self_plan)
-    return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], (int)p.hdr[3], (int)p.hdr[4], p.req_first, p.pre, p.pos};
-  long long* warp_tot = static_cast<long long*>(scratch);
-  int64_t* pre = reinterpret_cast<int64_t*>(warp_tot + 32);
-  int64_t* pos = pre + kSelfBlocks + 2;
-  return plan_line<NT>(p, reinterpret_cast<int32_t*>(pos + kSelfParts + 2), pre, pos, warp_tot);
+  if (!p.self_plan) return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], p.hdr[3], p.hdr[4], p.req_first, p.pre, p.pos};
+  int32_t* warp_tot = static_cast<int32_t*>(scratch);
+  int32_t* pre = warp_tot + 32;
+  int32_t* pos = pre + kSelfBlocks + 2;
+  return plan_line<NT>(p, pos + kSelfParts + 2, pre, pos, warp_tot);
 }
 
 // A place among the items: block b of request r, item head h.
 struct ChunkPlace {
   int r, b, h;
   ChunkRequest q;
+
+  // The place that lane `x` of the warp has.
+  __device__ __forceinline__ ChunkPlace from(int x) const {
+    auto get = [x](int v) { return __shfl_sync(0xffffffffu, v, x); };
+    return ChunkPlace{get(r), get(b), get(h), {get(q.row), get(q.qo), get(q.kv), get(q.pbase), get(q.blocks)}};
+  }
 
   // `n` blocks on, over requests without any; false past the last request.
   __device__ __forceinline__ bool skip(const ChunkParams& p, int n) {
@@ -219,62 +225,70 @@ struct ChunkPlace {
 
 struct ChunkWalk {
   // whole items: number `item` of `whole_items`, at place w
-  int64_t item = 0, whole_items = 0;
+  int item = 0, whole_items = 0;
   ChunkPlace w;
   // the part of the line: units [u, u1), in the item that starts at item_start, at place l
-  int64_t u = 0, u1 = 0, item_start = 0;
+  int u = 0, u1 = 0, item_start = 0;
   ChunkPlace l, line_first;  // line_first: the line's first block
 
-  // Place of block number `block` of the batch.
-  static __device__ __forceinline__ ChunkPlace place(const ChunkParams& p, const ChunkLine& line, int block, int h) {
-    // last request whose blocks start at or before it (requests without blocks start where the next one does)
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (line.first[mid] <= block) lo = mid;
-      else hi = mid;
-    }
-    return ChunkPlace{lo, block - line.first[lo], h, chunk_request(p, lo, false)};
-  }
-
-  // Place of unit `at` of the line, and its item's first unit.
-  static __device__ __forceinline__ ChunkPlace seek(const ChunkParams& p, const ChunkLine& line, int64_t at,
-                                                    int64_t& item_start) {
-    const int h = (int)(at / line.head);
-    const int64_t rest = at - h * line.head + line.base;
-    int lo = line.whole, hi = line.first[p.batch];
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (line.pre[mid] <= rest) lo = mid;
-      else hi = mid;
-    }
-    item_start = h * line.head + line.pre[lo] - line.base;
-    return place(p, line, lo, h);
-  }
-
-  // To CTA c's work. Returns what the merge has to know of the item that its part
-  // begins and does not end: {row of its first token, rows, query head, part that
-  // holds its last tile}, the last -1 if there is none; rows -1: the part is empty.
+  // To CTA c's work; a whole warp calls it. Returns what the merge has to know of
+  // the item that its part begins and does not end: {row of its first token, rows,
+  // query head, part that holds its last tile}, the last -1 if there is none; rows
+  // -1: the part is empty. The four places that have to be found (the first whole
+  // item, both ends of the part, the line's first block) are found by four lanes,
+  // so that their searches and reads take the time of one.
   __device__ __forceinline__ int4 begin(const ChunkParams& p, const ChunkLine& line, int c) {
     int4 cut = make_int4(0, 0, 0, -1);
-    whole_items = (int64_t)line.whole * p.item_heads;
+    const int lane = threadIdx.x & 31;
+    whole_items = line.whole * p.item_heads;
     item = c;
-    if (item < whole_items) w = place(p, line, c / p.item_heads, c % p.item_heads);
-    if (c >= line.parts) return cut;
-    u = line.pos[c];
-    u1 = line.pos[c + 1];
-    if (u == u1) cut.y = -1;
-    if (u < u1) {
-      l = seek(p, line, u, item_start);
-      line_first = place(p, line, line.whole, 0);
+    const bool has_part = c < line.parts;
+    if (has_part) {
+      u = line.pos[c];
+      u1 = line.pos[c + 1];
     }
-    if (u1 < line.rem) {
-      int64_t s;
-      const ChunkPlace at = seek(p, line, u1, s);
-      const int64_t end = s + block_units(p, at.q.qo, at.q.kv, at.b) - p.item_cost;  // of its tiles
+    if (line.parts == 0 || (!has_part && item >= whole_items)) return cut;
+    // lane 0: unit u of the line; 1: unit u1 (or the last); 2: the line's first block; 3: the first whole item
+    const int at = lane == 1 ? min(u1, line.rem - 1) : min(u, line.rem - 1);
+    ChunkPlace here;
+    here.h = at / line.head;
+    int lo = line.whole, hi = line.first[p.batch], start = 0;
+    if (lane < 2) {
+      const int rest = at - here.h * line.head + line.base;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (line.pre[mid] <= rest) lo = mid;
+        else hi = mid;
+      }
+      start = here.h * line.head + line.pre[lo] - line.base;
+    } else if (lane == 3) {
+      lo = min(c, max(whole_items - 1, 0)) / p.item_heads;
+      here.h = c % p.item_heads;
+    }
+    // last request whose blocks start at or before it (requests without blocks start where the next one does)
+    int r0 = 0, r1 = p.batch;
+    while (r1 - r0 > 1) {
+      const int mid = (r0 + r1) >> 1;
+      if (line.first[mid] <= lo) r0 = mid;
+      else r1 = mid;
+    }
+    here.r = r0;
+    here.b = lo - line.first[r0];
+    here.q = chunk_request(p, r0, false);
+    l = here.from(0);
+    item_start = __shfl_sync(0xffffffffu, start, 0);
+    line_first = here.from(2);
+    line_first.h = 0;
+    w = here.from(3);
+    if (!has_part || u == u1) {
+      cut.y = has_part ? -1 : 0;
+    } else if (u1 < line.rem) {
+      const ChunkPlace e = here.from(1);
+      const int s = __shfl_sync(0xffffffffu, start, 1);
+      const int end = s + block_units(p, e.q.qo, e.q.kv, e.b) - p.item_cost;  // of its tiles
       if (s >= u && s < u1 && u1 < end) {
-        const int t0 = at.b * p.item_tokens;
-        cut = make_int4(at.q.row + t0, min(p.item_tokens, at.q.qo - t0) * p.tile_heads, at.h * p.tile_heads, c + 1);
+        const int t0 = e.b * p.item_tokens;
+        cut = make_int4(e.q.row + t0, min(p.item_tokens, e.q.qo - t0) * p.tile_heads, e.h * p.tile_heads, c + 1);
         while (cut.w + 1 < line.parts && line.pos[cut.w + 1] < end) ++cut.w;
       }
     }
@@ -291,7 +305,7 @@ struct ChunkWalk {
     I.pbase = at.q.pbase;
     I.need = (at.q.kv + p.page_size - 1) / p.page_size;
     I.keys = chunk_keys(p, at.q.qo, at.q.kv, I.first_tok, I.first_tok + I.tokens);
-    I.tile0 = I.keys.lo / p.key_tile;
+    I.tile0 = I.keys.lo / kChunkKeys;
     I.n = chunk_tiles(p, I.keys);
   }
 
@@ -301,18 +315,18 @@ struct ChunkWalk {
       describe(p, w, I);
       I.t0 = 0;
       I.t1 = I.n;
-      const int block = (int)(item / p.item_heads);
-      item += gridDim.x;
+      const int block = item / p.item_heads;
+      item += (int)gridDim.x;
       if (item < whole_items) {
-        w.h = (int)(item % p.item_heads);
-        if (!w.skip(p, (int)(item / p.item_heads) - block)) item = whole_items;
+        w.h = item % p.item_heads;
+        if (!w.skip(p, item / p.item_heads - block)) item = whole_items;
       }
       return true;
     }
     while (u < u1) {
       describe(p, l, I);
-      I.t0 = (int)(u - item_start);
-      I.t1 = (int)min((int64_t)I.n, u1 - item_start);
+      I.t0 = u - item_start;
+      I.t1 = min(I.n, u1 - item_start);
       const bool some = I.n > 0 ? I.t0 < I.n : I.t0 == 0;
       item_start += I.n + p.item_cost;
       u = item_start;

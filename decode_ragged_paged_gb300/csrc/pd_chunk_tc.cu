@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kCtThreads = 512;
 constexpr int kM = 128;  // query rows of a tile
-constexpr int kN = kChunkTcKeys;
+constexpr int kN = kChunkKeys;
 constexpr float kSumLimit = 256.0f;   // 2^8: largest row sum of weights taken with a stale maximum
 constexpr float kRaise = 8.0f;        // log2 of it: a maximum is raised when it grew by more
 

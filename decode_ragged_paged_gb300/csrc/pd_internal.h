@@ -230,23 +230,25 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 
 // --------------------------------------------------------- chunk attention
 // An item is (request, block of item_tokens query tokens, tile_heads query
-// heads of one KV head); its keys are cut into tiles of key_tile. How the items
+// heads of one KV head); its keys are cut into tiles of kChunkKeys. How the items
 // are dealt to the CTAs: pd_chunk.cuh.
 // Workspace (offsets 256-byte aligned):
-//   hdr        int64[32]        the line's {units, units of a head, units before it, parts, whole blocks}
+//   hdr        int32[32]        the line's {units, units of a head, units before it, parts, whole blocks}
 //   req_first  int32[B + 1]     first block of every request
-//   pre        int64[max_blocks + 1]  units of one head before every block
-//   pos        int64[parts + 1]  first unit of every part of the line
+//   pre        int32[max_blocks + 1]  units of one head before every block
+//   pos        int32[parts + 1]  first unit of every part of the line
 //   cuts       int4[parts]       the item that a part begins and does not end
 //   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
 //   part_o     float[2 * parts][rows][D]  its normalised output
+constexpr int kChunkKeys = 64;
+constexpr int kChunkMaxKeys = 1 << 26;  // of a request
 struct ChunkParams {
   int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
   int32_t causal, window, o_dtype, nhd;
   int32_t tc;          // the tensor-core kernel takes the call
   int32_t page_shift;  // log2 of a page size that is a power of two, else -1
   int32_t self_plan;   // every CTA makes the work line for itself
-  int32_t tile_heads, item_heads, item_tokens, key_tile, item_cost, min_units, rows, max_blocks, max_parts;
+  int32_t tile_heads, item_heads, item_tokens, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)
   int64_t q_stride;  // elements between query tokens
   const int32_t* qo_indptr;
@@ -258,10 +260,10 @@ struct ChunkParams {
   const void* v_pool;
   void* o;
   float* lse;
-  int64_t* hdr;
+  int32_t* hdr;
   int32_t* req_first;
-  int64_t* pre;
-  int64_t* pos;
+  int32_t* pre;
+  int32_t* pos;
   int4* cuts;
   float* part_lse;
   float* part_o;
@@ -273,7 +275,7 @@ struct ChunkLayout {
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
-constexpr int kChunkTcKeys = 64;  // keys of a tensor-core tile
+
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
