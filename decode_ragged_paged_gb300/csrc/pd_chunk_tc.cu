@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
               tc_mma_f16(t_s, desc_advance(dq, (kk / 4) * S::kQHalf + (kk % 4) * 32),
                          desc_advance(dk, (kk / 4) * S::kHalf + (kk % 4) * 32), idesc_s, kk > 0);
             tc_commit(&bars->s_full[g][buf]);
+            // (by the softmax warps, who may still be two tiles behind, the K ring would be half held)
+            tc_commit(&bars->k_empty[ks]);
             if (i + step >= nt) tc_commit(&bars->q_empty[q_slot]);  // the group's last of this item
           }
           __syncwarp();
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int g = (warp - 8) >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    uint32_t own = 0, merges = 0, ks = 0;  // ks: K slot of the next tile (of either group)
+    uint32_t own = 0, merges = 0;
     bool ok = true;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     while (ok && next_item()) {
@@ -409,14 +411,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       }
       float m = valid ? -INFINITY : 0.f, l = 0.f;
       for (int i = 0; i < nt; ++i) {
-        const uint32_t slot = ks;
-        if (++ks == S::kRing) ks = 0;
         if (!two && (i & 1) != g) continue;  // the other group's tile
         const uint32_t buf = own & 1u, t_s = tmem + lanes + col_s(g, buf);
         ok = warp_mbar_wait(&bars->s_full[g][buf], (own >> 1) & 1u, abort, p.status);
         if (!ok) break;
         ++own;
-        if (wq == 0 && lane == 0) mbar_arrive(&bars->k_empty[slot]);  // the scores are there: the tile has been read
         if (warp_valid) {
           tc_fence_after();
           const int k0 = (I.tile0 + I.t0 + i) * kN;
