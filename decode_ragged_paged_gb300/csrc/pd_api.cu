@@ -725,6 +725,7 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   p.v_pool = v_pool;
   p.o = o;
   p.lse = lse;
+  p.aligned32 = ((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(workspace)) & 31u) == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hdr = reinterpret_cast<int32_t*>(ws + L.hdr);
   p.req_first = reinterpret_cast<int32_t*>(ws + L.req_first);

@@ -127,6 +127,19 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int l
   }
 }
 
+// 32 bytes, a whole sector where the buffers are aligned to it: rows are a thread
+// each, so narrower stores write sectors in pieces.
+__device__ __forceinline__ void store_sector(void* to, const uint32_t* v, bool aligned32) {
+  if (!aligned32) {
+    static_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 }  // namespace
 
 template <int D>
@@ -428,18 +441,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           const int k0 = (I.tile0 + I.t0 + i) * kN;
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
-          // columns [c_lo, c_hi) of 32-column chunk c as a bit mask
-          auto mask_of = [&](int c) -> uint32_t {
-            const int a = min(max(c_lo - 32 * c, 0), 32), b = min(max(c_hi - 32 * c, 0), 32);
-            const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
-            const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
-            return below_b & ~below_a;
-          };
+          // Scores outside columns [c_lo, c_hi) of chunk c become -inf, 16 at a time
+          // and only where some row of the warp has any to hide: a warp's rows end
+          // within a few columns of one another.
           auto hide = [&](int c, uint32_t (&v)[32]) {
             if (full) return;
-            const uint32_t keep = mask_of(c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (keep >> e) & 1u ? v[e] : 0xff800000u;
+            for (int half = 0; half < 32; half += 16) {
+              const int from = c_lo - 32 * c - half, to = c_hi - 32 * c - half;
+              if (__all_sync(0xffffffffu, from <= 0 && to >= 16)) continue;
+              // bits [from, to) of 16
+              const uint32_t keep = (to <= 0 ? 0u : 0xffffu >> (16 - min(to, 16))) & (from >= 16 ? 0u : 0xffffu << max(from, 0));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[half + e] = (keep >> e) & 1u ? v[half + e] : 0xff800000u;
+            }
           };
           uint32_t w[kN / 2];
           float2 sum[2];
@@ -584,22 +599,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
           if (valid) {
             if (slot < 0 && p.o_dtype == PD_BF16) {
-              uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + 32 * c);
+              uint16_t* o = static_cast<uint16_t*>(p.o) + orow * D + 32 * c;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 u;
-                u.x = pack_bf16x2(__uint_as_float(v[8 * e + 0]), __uint_as_float(v[8 * e + 1]));
-                u.y = pack_bf16x2(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
-                u.z = pack_bf16x2(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
-                u.w = pack_bf16x2(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-                o[e] = u;
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t u[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  u[x] = pack_bf16x2(__uint_as_float(v[e + 2 * x]), __uint_as_float(v[e + 2 * x + 1]));
+                store_sector(o + e, u, p.aligned32);
               }
             } else {
               float* o = (slot < 0 ? static_cast<float*>(p.o) + orow * D : p.part_o + (slot * p.rows + mrow) * D) +
                          32 * c;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(o + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              for (int e = 0; e < 32; e += 8) store_sector(o + e, v + e, p.aligned32);
             }
           }
         }

@@ -247,6 +247,7 @@ struct ChunkParams {
   int32_t causal, window, o_dtype, nhd;
   int32_t tc;          // the tensor-core kernel takes the call
   int32_t page_shift;  // log2 of a page size that is a power of two, else -1
+  int32_t aligned32;   // o and the workspace are 32-byte aligned
   int32_t self_plan;   // every CTA makes the work line for itself
   int32_t tile_heads, item_heads, item_tokens, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)

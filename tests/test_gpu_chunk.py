@@ -256,6 +256,20 @@ def test_workspace_reuse_streams_and_a_graph():
         assert torch.equal(o[m:], behind[m:])  # rows behind the last request's are left alone
 
 
+@pytest.mark.parametrize("dt,d,page", TYPES[:4])
+def test_outputs_and_workspace_aligned_to_16_bytes_only(dt, d, page):
+    b = Batch(18, [3, 100], [5000, 300], 8, 2, d, page, dt)
+    size = b.q.numel()
+    buf = torch.zeros(size + 64, dtype=dt, device="cuda")
+    off = 16 // buf.element_size()
+    o = buf[off:off + size].view(b.q.shape)
+    ws = torch.empty((100 << 20) + 16, dtype=torch.uint8, device="cuda")[16:]
+    for args in (dict(o=o), dict(workspace=ws), dict(o=o, workspace=ws)):
+        got, lse = b.run(**args)
+        ref.check_attention(got, lse, b.ref())
+        assert bool((buf[:off] == 0).all()) and bool((buf[off + size:] == 0).all())
+
+
 def test_cache_past_32_bit_offsets():
     d, hkv, page = 128, 8, 64
     pages = (1 << 32) // (hkv * page * d) + 40
