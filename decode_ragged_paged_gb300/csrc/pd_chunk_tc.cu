@@ -88,31 +88,6 @@ __device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem&
   return I.tokens > p.item_tokens / 2;
 }
 
-// The halves of one key tile of a pool, a box per page and half, all from one
-// thread with the pages in registers that the whole warp has alike: a box issued
-// by a lane of its own took 130 cycles, as the lanes take turns at an instruction
-// that wants uniform operands, and a tile of 16-slot pages has 8.
-template <int D>
-__device__ __forceinline__ void load_tile(const ChunkParams& p, const CUtensorMap* map, int kv_head, int soff, int ids,
-                                          int first, uint8_t* dst, uint64_t* bar) {
-  const int pb = p.page_size < kN ? p.page_size : kN, boxes = kN / pb;
-  int page[8];
-#pragma unroll
-  for (int b = 0; b < 8; ++b) page[b] = b < boxes ? __shfl_sync(0xffffffffu, ids, first + b) : 0;
-  const int c1 = p.nhd ? kv_head : soff, c2 = p.nhd ? soff : kv_head;
-  if (elect_one()) {
-    mbar_arrive_expect_tx(bar, Shape<D>::kTile);
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      if (b == boxes) break;
-#pragma unroll
-      for (int h = 0; h < Shape<D>::kHalves; ++h)
-        tma_load_4d(dst + h * Shape<D>::kHalf + b * pb * 128, map, 64 * h, c1, c2, page[b], bar);
-    }
-  }
-  __syncwarp();
-}
-
 // V rows of keys that no row of the item sees become zeros, so that nothing of
 // what they hold reaches O through a zero weight.
 template <int D>
@@ -237,43 +212,61 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   if (warp == 0 || warp == 2) {
     // ----------------------------------------------------------- K, V loads
-    // Page ids are read 32 at a time, a window ahead: lane l holds the id of the
-    // request's page 32 w + l.
-    const bool is_v = warp == 2;
+    // One thread: a tile is a box per page and 64-column half, up to 16 of them,
+    // and a box issued by a lane of its own takes 130 cycles (the lanes take turns
+    // at an instruction that wants uniform operands) against 30 here. A tile's page
+    // ids are read a tile ahead.
+    const bool is_v = warp == 2, leader = elect_one();
+    const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+    uint8_t* ring = is_v ? sV : sK;
+    uint64_t *full = is_v ? bars->v_full : bars->k_full, *empty = is_v ? bars->v_empty : bars->k_empty;
+    const int pb = p.page_size < kN ? p.page_size : kN, boxes = kN / pb;
     uint32_t slot = 0, turn = 0;
     bool ok = true;
-    auto window = [&](int w) -> int {
-      const int idx = 32 * w + lane;
-      return idx < I.need ? __ldg(p.page_indices + I.pbase + idx) : 0;
-    };
-    // Pages past the request's end, and ids outside the pools, become page num_pages, which TMA reads as zeros.
-    auto sound = [&](int w, int id) -> int {
-      if (32 * w + lane >= I.need) return p.num_pages;
-      if (id >= 0 && id < p.num_pages) return id;
-      report(p.status, PD_DEV_BAD_PAGE_TABLE);
-      return p.num_pages;
-    };
     while (ok && next_item()) {
       if (I.t1 <= I.t0) continue;
-      const int kv_head = I.h / p.group;
-      int win = (I.tile0 + I.t0) * kN / p.page_size >> 5;
-      int raw = window(win), ahead = window(win + 1);
-      int ids = sound(win, raw);
-      for (int t = I.t0; t < I.t1; ++t) {
-        const int tok = (I.tile0 + t) * kN;
-        const int idx = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
-        if ((idx >> 5) != win) {
-          win = idx >> 5;
-          ids = sound(win, ahead);
-          ahead = window(win + 1);
+      if (leader) {
+        const int kv_head = I.h / p.group;
+        const int* list = p.page_indices + I.pbase;
+        int next[8];
+        auto read = [&](int tile) {
+          const int idx = tile * kN >> p.page_shift;
+#pragma unroll
+          for (int b = 0; b < 8; ++b) next[b] = b < boxes && idx + b < I.need ? __ldg(list + idx + b) : 0;
+        };
+        read(I.tile0 + I.t0);
+        for (int t = I.t0; t < I.t1; ++t) {
+          const int tile = I.tile0 + t, idx = tile * kN >> p.page_shift;
+          int page[8];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) page[b] = next[b];
+          if (t + 1 < I.t1) read(tile + 1);
+          ok = mbar_wait(&empty[slot], (turn & 1u) ^ 1u, abort, p.status);
+          if (!ok) break;
+          const int soff = tile * kN & (p.page_size - 1) & ~(kN - 1);
+          const int c1 = p.nhd ? kv_head : soff, c2 = p.nhd ? soff : kv_head;
+          uint8_t* to = ring + slot * S::kTile;
+          mbar_arrive_expect_tx(&full[slot], S::kTile);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            if (b == boxes) break;
+            // pages past the request's end, and ids outside the pools: page num_pages, which TMA reads as zeros
+            int id = page[b];
+            if (idx + b >= I.need) {
+              id = p.num_pages;
+            } else if (id < 0 || id >= p.num_pages) {
+              report(p.status, PD_DEV_BAD_PAGE_TABLE);
+              id = p.num_pages;
+            }
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_4d(to + h * S::kHalf + b * pb * 128, map, 64 * h, c1, c2, id, &full[slot]);
+          }
+          if (++slot == S::kRing) slot = 0, ++turn;
         }
-        // a tile's pages lie in one window: there is one, or a power of two of them up to 8
-        ok = warp_mbar_wait(is_v ? &bars->v_empty[slot] : &bars->k_empty[slot], (turn & 1u) ^ 1u, abort, p.status);
-        if (!ok) break;
-        load_tile<D>(p, is_v ? &tm_v : &tm_k, kv_head, tok & (p.page_size - 1) & ~(kN - 1), ids, idx & 31,
-                     (is_v ? sV : sK) + slot * S::kTile, is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
-        if (++slot == S::kRing) slot = 0, ++turn;
       }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
     }
   } else if (warp == 4) {
     // --------------------------------------------------------------- Q loads
