@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ChunkWalk walk;
   {
-    const ChunkLine line = take_line<kSimtThreads>(p, simt_smem_raw);
+    const ChunkLine line = take_line(p, simt_smem_raw);
     const int4 cut = walk.begin(p, line, blockIdx.x);
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   }

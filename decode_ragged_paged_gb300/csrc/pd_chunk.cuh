@@ -67,7 +67,14 @@ __device__ __forceinline__ int block_units(const ChunkParams& p, int qo, int kv,
   return p.item_cost + chunk_tiles(p, chunk_keys(p, qo, kv, t0, min(qo, t0 + p.item_tokens)));
 }
 
-// Exclusive scan over a CTA of NT threads, and the total; warp_tot: NT / 32 words of shared memory.
+// A CTA of NT threads, or with NT = 32 a warp by itself.
+template <int NT>
+__device__ __forceinline__ void sync_of() {
+  if constexpr (NT == 32) __syncwarp();
+  else __syncthreads();
+}
+
+// Exclusive scan over them, and the total; warp_tot: NT / 32 words of shared memory.
 template <int NT>
 __device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -76,6 +83,10 @@ __device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) 
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
+  }
+  if constexpr (NT == 32) {
+    total = __shfl_sync(0xffffffffu, x, 31);
+    return x - v;
   }
   __syncthreads();  // the totals of an earlier scan have been read
   if (lane == 31) warp_tot[warp] = x;
@@ -101,13 +112,13 @@ struct ChunkLine {
   const int32_t* pos;   // first unit of every part
 };
 
-// The line of a batch, by one CTA: checks the requests, numbers their blocks
+// The line of a batch, by one CTA or one warp: checks the requests, numbers their blocks
 // (first [B + 1]), sums the blocks' units (pre [blocks + 1]) and cuts the line
 // (pos [max_parts + 1]), in global memory or in the CTA's own shared memory. Ends
 // with a barrier.
 template <int NT>
 __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pre, int32_t* pos, int* warp_tot) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x & (NT - 1);
   ChunkLine line{0, 1, 0, 0, 0, first, pre, pos};
   // kChunkMaxKeys and the rows that fit a GPU keep the sums of NT requests or blocks inside 32 bits
   int carry = 0, total;
@@ -123,7 +134,7 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
   }
   const int blocks = carry;
   if (!over && tid == 0) first[p.batch] = blocks;
-  __syncthreads();
+  sync_of<NT>();
   long long sum = 0;
   for (int b0 = 0; !over && b0 < blocks; b0 += NT) {
     const int b = b0 + tid;
@@ -146,11 +157,11 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
   if (over || carry == 0) {
     // more blocks than rows allow (requests whose rows overlap), or more work than a call takes: none is worked on
     if (tid == 0 && over) report(p.status, PD_DEV_BAD_INDPTR);
-    __syncthreads();
+    sync_of<NT>();
     return line;
   }
   if (tid == 0) pre[blocks] = carry;
-  __syncthreads();
+  sync_of<NT>();
   const int G = p.max_parts, H = p.item_heads, units = carry * H;
   // whole items: all rounds but the last, whose items the line evens out
   if (blocks >= 2 * p.batch && (int64_t)blocks * H >= 3 * (int64_t)G)
@@ -176,28 +187,28 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
       if (c < G) pos[c] = at;
       carry += total;
     }
-    __syncthreads();
+    sync_of<NT>();
     // the shares come to the line's units, or (rounding, CTAs with too much already) to nearly that
     for (int c = tid; c < G; c += NT) pos[c] = carry > 0 ? (int)((int64_t)pos[c] * line.rem / carry) : 0;
     if (tid == 0) pos[G] = line.rem;
   }
-  __syncthreads();
+  sync_of<NT>();
   return line;
 }
 
-// A small batch's line is made by every CTA for itself, in `scratch` (kSelfBytes
-// of its shared memory); a large one's has been left in the workspace by the plan
-// kernel.
-constexpr int kSelfBatch = 256, kSelfBlocks = 1024, kSelfParts = 512;
-constexpr size_t kSelfBytes = 4 * (32 + kSelfBlocks + 2 + kSelfParts + 2 + kSelfBatch + 2);
+// A small batch's line is made by every warp that needs it for itself, in
+// `scratch` (kSelfBytes of shared memory; warps that share it write the same): no
+// launch more, and no barrier of the CTA. It takes the warp about 200 cycles per
+// 32 requests and per 32 blocks, so a large batch's (over 4 us that way) is left
+// in the workspace by the plan kernel, which takes that long to launch and run.
+constexpr int kSelfBatch = 128, kSelfBlocks = 512, kSelfParts = 512;
+constexpr size_t kSelfBytes = 4 * (kSelfBlocks + 2 + kSelfParts + 2 + kSelfBatch + 2);
 
-template <int NT>
 __device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scratch) {
   if (!p.self_plan) return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], p.hdr[3], p.hdr[4], p.req_first, p.pre, p.pos};
-  int32_t* warp_tot = static_cast<int32_t*>(scratch);
-  int32_t* pre = warp_tot + 32;
+  int32_t* pre = static_cast<int32_t*>(scratch);
   int32_t* pos = pre + kSelfBlocks + 2;
-  return plan_line<NT>(p, pos + kSelfParts + 2, pre, pos, warp_tot);
+  return plan_line<32>(p, pos + kSelfParts + 2, pre, pos, nullptr);
 }
 
 // A place among the items: block b of request r, item head h.

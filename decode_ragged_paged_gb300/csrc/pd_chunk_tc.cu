@@ -171,18 +171,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const uint32_t tmem = bars->tmem_slot;
   pdl_launch_dependents();
   pdl_wait_primary();  // the plan's work line
-  const ChunkLine line = take_line<kCtThreads>(p, base);
   ChunkItem I{};
   if (warp == 6) {
-    ChunkWalk walk;
-    const int4 cut = walk.begin(p, line, blockIdx.x);
-    if (lane == 0) p.cuts[blockIdx.x] = cut;
-    if (p.self_plan) {
-      fence_proxy_async_smem();
-      __syncthreads();  // the line has been read: its place goes to the rings
-    }
     // ------------------------------------------------------------ scheduler
-    // Walks the CTA's part of the line ahead of the other warps.
+    // Finds the CTA's work and walks through it ahead of the other warps. The
+    // rings hold the line until the first item is out, as nothing else uses them
+    // before that.
+    ChunkWalk walk;
+    const int4 cut = walk.begin(p, take_line(p, base), blockIdx.x);
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
+    fence_proxy_async_smem();
+    __syncwarp();
     uint32_t slot = 0, turn = 0;
     for (bool more = true; more;) {
       more = walk.next(p, I);
@@ -195,9 +194,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       __syncwarp();
       if (++slot == kItems) slot = 0, ++turn;
     }
-  } else if (p.self_plan) {
-    fence_proxy_async_smem();
-    __syncthreads();
   }
   // The next item of the scheduler's, in every other warp.
   uint32_t item_slot = 0, item_turn = 0;
