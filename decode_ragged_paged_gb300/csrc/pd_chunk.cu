@@ -331,7 +331,8 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   p.tc = kv_dtype == PD_BF16 && p.page_size >= 8 && (p.page_size & (p.page_size - 1)) == 0;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
-    p.item_tokens = 2 * (128 / p.tile_heads);  // two query tiles
+    p.tile_tokens = 128 / p.tile_heads;
+    p.item_tokens = 2 * p.tile_tokens;
     p.rows = p.item_tokens * p.tile_heads;
     p.item_cost = 2;
     p.min_units = 4;

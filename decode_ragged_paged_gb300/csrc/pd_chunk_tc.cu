@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t col_o(int g) { return 256u + (uint32_t)g * 1
 
 // Whether the item has a second query tile (else its groups share the first).
 __device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem& I) {
-  return I.tokens > p.item_tokens / 2;
+  return I.tokens > p.tile_tokens;
 }
 
 // V rows of keys that no row of the item sees become zeros, so that nothing of
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     bool ok = true;
     while (ok && next_item()) {
       if (I.t1 <= I.t0) continue;
-      const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.item_tokens / 2;
+      const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.tile_tokens;
       for (int x = 0; ok && x < tiles; ++x) {
         ok = warp_mbar_wait(&bars->q_empty[q], (qturn & 1u) ^ 1u, abort, p.status);
         if (ok && lane == 0) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     while (ok && next_item()) {
       const int nt = max(I.t1 - I.t0, 0);
       const bool two = two_tiles(p, I);
-      const int half_tok = p.item_tokens / 2;
+      const int half_tok = p.tile_tokens;
       const int tokens = two ? (g == 0 ? half_tok : I.tokens - half_tok) : I.tokens;  // of this group's tile
       const int tok0 = two && g == 1 ? half_tok : 0;
       const bool valid = tok_row < tokens;
@@ -656,7 +656,7 @@ cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensor
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   const int pb = p.page_size < kN ? p.page_size : kN;
-  if (!make_rows_map(&tq, p.q, PD_BF16, p.total_qo, p.hq, p.head_dim, 64, p.item_tokens / 2, true, p.tile_heads,
+  if (!make_rows_map(&tq, p.q, PD_BF16, p.total_qo, p.hq, p.head_dim, 64, p.tile_tokens, true, p.tile_heads,
                      p.q_stride) ||
       !make_pool_map(&tk, p.k_pool, PD_BF16, p.num_pages, p.hkv, p.page_size, p.head_dim, 64, pb, true, p.nhd != 0) ||
       !make_pool_map(&tv, p.v_pool, PD_BF16, p.num_pages, p.hkv, p.page_size, p.head_dim, 64, pb, true, p.nhd != 0))
