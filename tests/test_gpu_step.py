@@ -20,7 +20,7 @@ def i32(x):
 @pytest.mark.parametrize("dt,hq,hkv,d,page,layout,window,captured", [
     (torch.float32, 8, 2, 64, 16, "HND", -1, False),
     (torch.bfloat16, 32, 8, 128, 16, "HND", -1, False),
-    (torch.bfloat16, 8, 8, 128, 64, "NHD", 50, False),
+    (torch.bfloat16, 4, 4, 128, 64, "NHD", 50, False),
     (torch.bfloat16, 28, 4, 128, 16, "HND", -1, True),
     (torch.bfloat16, 8, 2, 64, 24, "NHD", -1, True),
 ])
