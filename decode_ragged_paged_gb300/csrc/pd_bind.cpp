@@ -81,6 +81,8 @@ int dtype_code(at::ScalarType t, const char* name) {
 int64_t rows(const at::Tensor& t, const char* name) {
   if (t.dim() != 3 || t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != t.size(2)))
     refuse("%s must be [tokens][heads][dim] with contiguous heads", name);
+  // (a stride of 0 says "contiguous" to the library)
+  if (t.size(0) > 1 && t.stride(0) == 0 && t.numel() > 0) refuse("the tokens of %s are one row", name);
   return t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);
 }
 

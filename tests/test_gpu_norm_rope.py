@@ -222,3 +222,21 @@ def test_refusals():
     for call in bad:
         with pytest.raises(pd.PdError):
             call()
+
+
+def test_tokens_that_are_one_row_are_refused():
+    # a broadcast row's stride of 0 would be read as rows one after another
+    one, q = torch.randn(1, 8, 64, device="cuda").expand(4, 8, 64), torch.randn(4, 8, 64, device="cuda")
+    pos = torch.arange(4, device="cuda", dtype=torch.int32)
+    pool, slot = torch.zeros(2, 8, 16, 64, device="cuda"), torch.arange(4, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for call in (lambda: pd.pd_qk_norm_rope(one, q, None, None, freqs(64), pos),
+                 lambda: pd.pd_qk_norm_rope(q, one, None, None, freqs(64), pos),
+                 lambda: pd.pd_qk_norm_rope(q, q, None, None, freqs(64), pos, q_out=one),
+                 lambda: pd.pd_qk_norm_rope_append(q, q, one, None, None, freqs(64), pos, slot, pool, pool),
+                 lambda: pd.pd_attn_chunk(one, pool, pool, i32([4]), i32([0, 1]), i32([0]), i32([0, 4]), max_qo_len=4,
+                                          max_kv_len=4)):
+        with pytest.raises(pd.PdError):
+            call()
+    got, _ = pd.pd_qk_norm_rope(one[:1], q[:1], None, None, None, None)
+    assert torch.equal(got, one[:1])
