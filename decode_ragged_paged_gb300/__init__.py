@@ -381,6 +381,18 @@ def _vector(t, name, dtype, n=None):
         raise PdError(f"{name} has {t.numel()} entries, {n} are needed")
 
 
+def _empty(stream, shape, dtype, device):
+    """torch.empty for a call on `stream`, allocated there: memory of another stream could still be in
+    use by, or be handed on to, that stream's own work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -409,9 +421,9 @@ def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
     slice of a wider row. Without max_qo_len / max_kv_len they are read from the device (a
     synchronisation). Returns (o, lse)."""
     if o is None:
-        o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
+        o = _empty(stream, q.shape, o_dtype if o_dtype is not None else q.dtype, q.device)
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.shape[:2], torch.float32, q.device)
     elif lse is False:
         lse = None
     if max_qo_len is None:
@@ -422,7 +434,7 @@ def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
     tail = (dev_status, causal, window_left, sm_scale or None, max_qo_len, max_kv_len, _layout_code(layout))
     rc = _bound("attn_chunk", stream, *head, workspace, *tail)
     if rc is not None and rc[1] == PD_ERR_WORKSPACE:  # none, or one too small for this batch
-        workspace = torch.empty(max(rc[0], 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(rc[0], 16), torch.uint8, q.device)
         rc = _bound("attn_chunk", stream, *head, workspace, *tail)
     if rc is not None:
         _check(rc[1], "pd_attn_chunk")
@@ -437,12 +449,12 @@ def pd_batch_tables(new_len, cached_len, block_table, *, page_size, num_pages, t
     one entry) counts the free pages; free_count_out gets what is left (free_count itself: in
     place). `out` may hold the six result tensors. Returns BatchTables."""
     if free_pages is not None and free_count_out is None and free_count is not None:
-        free_count_out = torch.empty_like(free_count)
+        free_count_out = _empty(stream, free_count.shape, free_count.dtype, free_count.device)
     if out is None:
         B, i32 = new_len.numel(), torch.int32
         sizes = ((B + 1, i32), (B, i32), (B + 1, i32), (max_page_indices, i32), (total_qo, i32),
                  (total_qo, torch.int64))
-        out = (torch.empty(n, dtype=t, device=new_len.device) for n, t in sizes)
+        out = (_empty(stream, n, t, new_len.device) for n, t in sizes)
     out = BatchTables(*out)
     rc = _bound("batch_tables", stream, new_len, cached_len, block_table, rows, free_pages, free_count, free_count_out,
                 *out, dev_status, page_size, num_pages, total_qo, max_page_indices)
@@ -463,9 +475,9 @@ def pd_slot_map(qo_indptr, kv_len, page_indptr, page_indices, *, page_size, num_
     _vector(qo_indptr, "qo_indptr", torch.int32, B + 1)
     _vector(page_indptr, "page_indptr", torch.int32, B + 1)
     if positions is None:
-        positions = torch.empty(total_qo, dtype=torch.int32, device=kv_len.device)
+        positions = _empty(stream, total_qo, torch.int32, kv_len.device)
     if slot_map is None:
-        slot_map = torch.empty(total_qo, dtype=torch.int64, device=kv_len.device)
+        slot_map = _empty(stream, total_qo, torch.int64, kv_len.device)
     _vector(positions, "positions", torch.int32, total_qo)
     _vector(slot_map, "slot_map", torch.int64, total_qo)
     batch = make_batch(kv_len, page_indptr, page_indices, num_pages, qo_indptr=qo_indptr, total_qo=total_qo,
@@ -482,9 +494,9 @@ def pd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, 
     [T][Hq][D] and k [T][Hkv][D], which may be slices of a wider row. q_out / k_out may be q / k
     themselves. Returns (q_out, k_out)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _empty(stream, q.shape, q.dtype, q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _empty(stream, k.shape, k.dtype, k.device)
     rc = _bound("norm_rope", stream, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved)
     if rc is not None:
         _check(rc[1], "pd_qk_norm_rope")
@@ -497,7 +509,7 @@ def pd_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, slo
     int64 [T], from pd_batch_tables or pd_slot_map; rows with a negative slot are left alone).
     Returns q_out."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _empty(stream, q.shape, q.dtype, q.device)
     rc = _bound("norm_rope_append", stream, q, k, q_weight, k_weight, inv_freq, positions, v, slot_map, k_pool, v_pool,
                 q_out, dev_status, eps, interleaved, _layout_code(layout))
     if rc is not None:

@@ -99,3 +99,31 @@ def test_steps(dt, hq, hkv, d, page, layout, window, captured):
                              layout=layout)
         ref.check_attention(o[:at], lse[:at], want)
         cached.copy_(out.kv_len)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_results_of_a_call_on_another_stream_are_its_own(handle):
+    """Memory that the current stream has let go of, but will still write, is not taken for them."""
+    q, k = (torch.randn(300, 8, 128, device="cuda").bfloat16() for _ in range(2))
+    pool = torch.randn(20, 8, 16, 128, device="cuda").bfloat16()
+    pp, px, qo, kv = i32([0, 19]), torch.arange(20, device="cuda", dtype=torch.int32), i32([0, 300]), i32([300])
+    new, have, table = i32([300]), i32([0]), px.view(1, 20).clone()
+    stream = torch.cuda.Stream()
+    calls = [
+        lambda **kw: pd.pd_qk_norm_rope(q, k, None, None, None, None, **kw),
+        lambda **kw: pd.pd_attn_chunk(q, pool, pool, kv, pp, px, qo, max_qo_len=300, max_kv_len=300, **kw),
+        lambda **kw: pd.pd_slot_map(qo, kv, pp, px, page_size=16, num_pages=20, total_qo=300, max_kv_len=300, **kw),
+        lambda **kw: pd.pd_batch_tables(new, have, table, page_size=16, num_pages=20, total_qo=300,
+                                        max_page_indices=19, **kw),
+    ]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        spent = [torch.empty_like(t) for t in want] + [torch.empty(1 << 20, dtype=torch.uint8, device="cuda")]
+        torch.cuda._sleep(20_000_000)
+        for t in spent:
+            t.fill_(7)
+        del t, spent
+        got = call(stream=stream.cuda_stream if handle else stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
