@@ -241,7 +241,9 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 //   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
 //   part_o     float[2 * parts][rows][D]  its normalised output
 constexpr int kChunkKeys = 64;
-constexpr int kChunkMaxKeys = 1 << 26;  // of a request
+// Keys of a request: 2^24 are 2^18 tiles of at most about 0.8 us, so that a warp
+// that waits for the item before its own to end stays far below the limit of a wait.
+constexpr int kChunkMaxKeys = 1 << 24;
 struct ChunkParams {
   int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
   int32_t causal, window, o_dtype, nhd;

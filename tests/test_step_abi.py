@@ -44,6 +44,7 @@ def _chunk(lib, d=None, b=None, window=-1, stride=0, q=A, o=A, ws=A, ws_bytes=1 
     ({}, dict(num_pages=0), {}, pd.PD_ERR_INVALID_ARG),
     ({}, dict(total_qo=-1), {}, pd.PD_ERR_INVALID_ARG),
     ({}, dict(max_kv_len=(1 << 26) + 1), {}, pd.PD_ERR_UNSUPPORTED),
+    ({}, dict(max_kv_len=(1 << 24) + 1), {}, pd.PD_ERR_UNSUPPORTED),
     ({}, {}, dict(stride=1016), pd.PD_ERR_INVALID_ARG),       # below the 1024 elements of a row
     ({}, {}, dict(stride=1028), pd.PD_ERR_INVALID_ARG),       # rows not 16-byte aligned
     ({}, {}, dict(q=A + 8), pd.PD_ERR_INVALID_ARG),
