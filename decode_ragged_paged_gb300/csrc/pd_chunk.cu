@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     p.hdr[2] = line.base;
     p.hdr[3] = line.parts;
     p.hdr[4] = line.whole;
+    p.hdr[5] = line.shares;
   }
 }
 

@@ -107,19 +107,28 @@ __device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) 
 struct ChunkLine {
   int rem, head, base;  // units of the line, of one head of it, and of one head before it
   int parts, whole;     // parts of the line; blocks dealt out whole before it
+  int shares;           // what pos counts up to: the sum of the parts' shares, or 0 if pos is in units
   const int32_t* first; // first block of every request
   const int32_t* pre;   // units of one head before every block
-  const int32_t* pos;   // first unit of every part
+  const int32_t* pos;   // where every part starts
+
+  // First unit of part c. The shares come to the line's units, or (rounding, CTAs
+  // with too much already) to nearly that, and are stretched to it here.
+  __device__ __forceinline__ int start(int c) const {
+    if (shares == 0) return pos[c];
+    return c == parts ? rem : (int)((int64_t)pos[c] * rem / shares);
+  }
 };
 
 // The line of a batch, by one CTA or one warp: checks the requests, numbers their blocks
 // (first [B + 1]), sums the blocks' units (pre [blocks + 1]) and cuts the line
-// (pos [max_parts + 1]), in global memory or in the CTA's own shared memory. Ends
-// with a barrier.
+// (pos [max_parts + 1]), in global memory or in the CTA's own shared memory. Every
+// word gets one value only, as several warps may make the same line in the same
+// place, one still writing what another reads. Ends with a barrier.
 template <int NT>
 __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pre, int32_t* pos, int* warp_tot) {
   const int tid = threadIdx.x & (NT - 1);
-  ChunkLine line{0, 1, 0, 0, 0, first, pre, pos};
+  ChunkLine line{0, 1, 0, 0, 0, 0, first, pre, pos};
   // kChunkMaxKeys and the rows that fit a GPU keep the sums of NT requests or blocks inside 32 bits
   int carry = 0, total;
   bool over = false;
@@ -187,10 +196,7 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
       if (c < G) pos[c] = at;
       carry += total;
     }
-    sync_of<NT>();
-    // the shares come to the line's units, or (rounding, CTAs with too much already) to nearly that
-    for (int c = tid; c < G; c += NT) pos[c] = carry > 0 ? (int)((int64_t)pos[c] * line.rem / carry) : 0;
-    if (tid == 0) pos[G] = line.rem;
+    line.shares = max(carry, 1);  // (no shares: every part but the last starts at 0)
   }
   sync_of<NT>();
   return line;
@@ -205,7 +211,7 @@ constexpr int kSelfBatch = 128, kSelfBlocks = 512, kSelfParts = 512;
 constexpr size_t kSelfBytes = 4 * (kSelfBlocks + 2 + kSelfParts + 2 + kSelfBatch + 2);
 
 __device__ __forceinline__ ChunkLine take_line(const ChunkParams& p, void* scratch) {
-  if (!p.self_plan) return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], p.hdr[3], p.hdr[4], p.req_first, p.pre, p.pos};
+  if (!p.self_plan) return ChunkLine{p.hdr[0], p.hdr[1], p.hdr[2], p.hdr[3], p.hdr[4], p.hdr[5], p.req_first, p.pre, p.pos};
   int32_t* pre = static_cast<int32_t*>(scratch);
   int32_t* pos = pre + kSelfBlocks + 2;
   return plan_line<32>(p, pos + kSelfParts + 2, pre, pos, nullptr);
@@ -255,8 +261,8 @@ struct ChunkWalk {
     item = c;
     const bool has_part = c < line.parts;
     if (has_part) {
-      u = line.pos[c];
-      u1 = line.pos[c + 1];
+      u = line.start(c);
+      u1 = line.start(c + 1);
     }
     if (line.parts == 0 || (!has_part && item >= whole_items)) return cut;
     // lane 0: unit u of the line; 1: unit u1 (or the last); 2: the line's first block; 3: the first whole item
@@ -300,7 +306,7 @@ struct ChunkWalk {
       if (s >= u && s < u1 && u1 < end) {
         const int t0 = e.b * p.item_tokens;
         cut = make_int4(e.q.row + t0, min(p.item_tokens, e.q.qo - t0) * p.tile_heads, e.h * p.tile_heads, c + 1);
-        while (cut.w + 1 < line.parts && line.pos[cut.w + 1] < end) ++cut.w;
+        while (cut.w + 1 < line.parts && line.start(cut.w + 1) < end) ++cut.w;
       }
     }
     return cut;

@@ -233,7 +233,7 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 // heads of one KV head); its keys are cut into tiles of kChunkKeys. How the items
 // are dealt to the CTAs: pd_chunk.cuh.
 // Workspace (offsets 256-byte aligned):
-//   hdr        int32[32]        the line's {units, units of a head, units before it, parts, whole blocks}
+//   hdr        int32[32]        the line's {units, units of a head, units before it, parts, whole blocks, shares}
 //   req_first  int32[B + 1]     first block of every request
 //   pre        int32[max_blocks + 1]  units of one head before every block
 //   pos        int32[parts + 1]  first unit of every part of the line

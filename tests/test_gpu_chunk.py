@@ -135,6 +135,26 @@ def test_drawn(dt, d, page, seed):
     b.check(window=rng.choice([-1, -1, 20, 200]), causal=rng.random() < 0.8)
 
 
+@pytest.mark.parametrize("dt,d,page", [TYPES[0], TYPES[2], TYPES[3]])
+@pytest.mark.parametrize("new,kv,window", [
+    ([900, 130, 3], [1200, 130, 500], -1),   # several rounds of whole items and a line
+    ([500, 500], [500, 4000], -1),           # short items first: some parts of the line get no share
+    ([500, 0, 500], [4000, 0, 501], 100),
+    ([700, 300], [600, 300], -1),            # rows without keys among whole items
+])
+def test_whole_items_dealt_by_rounds(dt, d, page, new, kv, window):
+    Batch(19, new, kv, 128, 8, d, page, dt).check(window=window)
+
+
+@pytest.mark.parametrize("dt,d,page", [TYPES[0], TYPES[2], TYPES[3]])
+def test_many_requests_of_several_blocks(dt, d, page):
+    # more requests, and then more blocks, than a warp plans by itself
+    rng = random.Random(20)
+    new = [rng.choice([33, 20, 70, 0, 1]) for _ in range(140)]
+    Batch(20, new, [n + rng.randint(0, 80) for n in new], 64, 4, d, page, dt).check()
+    Batch(21, [1300, 5], [1300, 2000], 128, 1, d, page, dt).check(window=64)
+
+
 @pytest.mark.parametrize("dt,d,page", TYPES[:4])
 def test_strided_queries_and_rows_behind_the_last(dt, d, page):
     b = Batch(8, [20, 150], [20, 300], 8, 2, d, page, dt)
