@@ -469,11 +469,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
               }
             }
           };
-          bool stale = __all_sync(0xffffffffu, m > -INFINITY);
+          bool stale = __all_sync(0xffffffffu, m > -INFINITY), over = false;
           if (stale) {
             weights(-m);
             const float s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            stale = !__any_sync(0xffffffffu, valid && s > kSumLimit);
+            over = __any_sync(0xffffffffu, valid && s > kSumLimit);
+            stale = !over;
           }
           if (!stale) {
             // the tile's own maximum
@@ -492,7 +493,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             if (valid && mx > -INFINITY) {
               if (m == -INFINITY) {
                 m = ms;
-              } else if (ms > m + kRaise) {
+              } else if (ms > (over ? m : m + kRaise)) {
+                // (a maximum left below a row's weights' limit would do every tile twice)
                 alpha = exp2f(m - ms);
                 m = ms;
               }
