@@ -30,6 +30,7 @@
 // Every wait is bounded; on a timeout the CTA records PD_DEV_TIMEOUT, drains
 // and frees its TMEM.
 #include <math.h>
+#include <stddef.h>
 #include <string.h>
 
 #include <atomic>
@@ -88,6 +89,38 @@ __device__ __forceinline__ bool two_tiles(const ChunkParams& p, const ChunkItem&
   return I.tokens > p.tile_tokens;
 }
 
+// The whole warp looks at a barrier and agrees: one uniform branch if the phase is
+// there. (mbar_wait's lanes look one by one and meet again afterwards, which took a
+// warp 100 to 200 cycles at a barrier that was ready: a fifth of a tile's time.)
+__device__ __forceinline__ bool try_all(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred q, p, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// warp_mbar_wait by try_all.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  if (try_all(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (try_all(bar, parity)) return true;
+    const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+    if (late) {
+      report(status, PD_DEV_TIMEOUT);
+      *abort = 1;
+    }
+    if (__any_sync(0xffffffffu, late || *abort != 0)) return false;
+  }
+}
+
 // V rows of keys that no row of the item sees become zeros, so that nothing of
 // what they hold reaches O through a zero weight.
 template <int D>
@@ -128,6 +161,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(base + S::kOffBar);
   float2* sML = reinterpret_cast<float2*>(base + S::kOffML);  // group 1's (m, l) of every row
   volatile int* abort = &bars->abort;
+  const uint32_t bars32 = smem_u32(bars);
+  auto bar = [&](size_t member, uint32_t i = 0) { return bars32 + (uint32_t)member + 8 * i; };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort, p.status); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -186,7 +222,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     for (bool more = true; more;) {
       more = walk.next(p, I);
       if (!more) I.tokens = 0;
-      if (!warp_mbar_wait(&bars->item_empty[slot], (turn & 1u) ^ 1u, abort, p.status)) break;
+      if (!wait(bar(offsetof(Bars, item_empty), slot), (turn & 1u) ^ 1u)) break;
       if (lane == 0) {
         bars->items[slot] = I;
         mbar_arrive(&bars->item_full[slot]);
@@ -198,7 +234,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // The next item of the scheduler's, in every other warp.
   uint32_t item_slot = 0, item_turn = 0;
   auto next_item = [&]() -> bool {
-    if (!warp_mbar_wait(&bars->item_full[item_slot], item_turn & 1u, abort, p.status)) return false;
+    if (!wait(bar(offsetof(Bars, item_full), item_slot), item_turn & 1u)) return false;
     I = bars->items[item_slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->item_empty[item_slot]);
@@ -272,7 +308,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (I.t1 <= I.t0) continue;
       const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.tile_tokens;
       for (int x = 0; ok && x < tiles; ++x) {
-        ok = warp_mbar_wait(&bars->q_empty[q], (qturn & 1u) ^ 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, q_empty), q), (qturn & 1u) ^ 1u);
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&bars->q_full[q], (uint32_t)(S::kHalves * tok * p.tile_heads * 128));
           for (int h = 0; h < S::kHalves; ++h)
@@ -300,7 +336,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const int step = two ? 1 : 2;
       uint32_t q_slot = q;  // of the group's query tile
       for (int x = 0; ok && x < (two ? 2 : 1); ++x) {
-        ok = warp_mbar_wait(&bars->q_full[q], qturn & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, q_full), q), qturn & 1u);
         if (x == g || !two) q_slot = q;
         else if (ok && lane == 0) mbar_arrive(&bars->q_empty[q]);  // the other group's
         if (++q == S::kQ) q = 0, ++qturn;
@@ -308,11 +344,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (!ok) break;
       const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, sQa + q_slot * S::kQTile, 0), 16, 1024);
       for (int i = 0; i < nt; ++i) {
-        ok = warp_mbar_wait(&bars->k_full[ks], kturn & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, k_full), ks), kturn & 1u);
         if (!ok) break;
         if (two || (i & 1) == g) {
           const uint32_t buf = own & 1u;
-          ok = own < 2 || warp_mbar_wait(&bars->pv_done[g][buf], ((own - 2) >> 1) & 1u, abort, p.status);
+          ok = own < 2 || wait(bar(offsetof(Bars, pv_done), 2 * g + buf), ((own - 2) >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, sKa + ks * S::kTile, 0), 16, 1024);
@@ -349,7 +385,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const bool two = two_tiles(p, I);
       const int i0 = two ? 0 : g;
       for (int i = 0; i < nt; ++i) {
-        ok = warp_mbar_wait(&bars->v_full[vs], vturn & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, v_full), vs), vturn & 1u);
         if (!ok) break;
         if (two || (i & 1) == g) {
           const uint32_t buf = own & 1u;
@@ -362,7 +398,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          ok = warp_mbar_wait(&bars->p_full[g][buf], (own >> 1) & 1u, abort, p.status);
+          ok = wait(bar(offsetof(Bars, p_full), 2 * g + buf), (own >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dv = sw128_desc(__shfl_sync(0xffffffffu, sVa + vs * S::kTile, 0), S::kHalf, 1024);
@@ -376,7 +412,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
           __syncwarp();
           // the V slot is free once the product is done: a wait and a plain arrival here cost less than a second commit
-          ok = warp_mbar_wait(&bars->pv_done[g][buf], (own >> 1) & 1u, abort, p.status);
+          ok = wait(bar(offsetof(Bars, pv_done), 2 * g + buf), (own >> 1) & 1u);
           if (!ok) break;
           ++own;
         }
@@ -419,10 +455,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         hi = k.hi;
       }
       float m = valid ? -INFINITY : 0.f, l = 0.f;
-      for (int i = 0; i < nt; ++i) {
-        if (!two && (i & 1) != g) continue;  // the other group's tile
+      for (int i = two ? 0 : g; i < nt; i += two ? 1 : 2) {  // (else the others are the other group's)
         const uint32_t buf = own & 1u, t_s = tmem + lanes + col_s(g, buf);
-        ok = warp_mbar_wait(&bars->s_full[g][buf], (own >> 1) & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, s_full), 2 * g + buf), (own >> 1) & 1u);
         if (!ok) break;
         ++own;
         if (warp_valid) {
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
             if (__any_sync(0xffffffffu, alpha != 1.f)) {
               // the product of the tile before (own counts this one already) is under way
-              ok = warp_mbar_wait(&bars->pv_done[g][(own - 2) & 1u], ((own - 2) >> 1) & 1u, abort, p.status);
+              ok = wait(bar(offsetof(Bars, pv_done), 2 * g + ((own - 2) & 1u)), ((own - 2) >> 1) & 1u);
               if (!ok) break;
               tc_fence_after();
               l *= alpha;
@@ -531,7 +566,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const bool other = !two && nt > 1;  // group 1 has tiles of the same rows
       if (g == 1 && !two) {
         if (nt < 2) continue;
-        ok = warp_mbar_wait(&bars->pv_done[1][(own - 1) & 1u], ((own - 1) >> 1) & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, pv_done), 2 + ((own - 1) & 1u)), ((own - 1) >> 1) & 1u);
         if (!ok) break;
         tc_fence_after();
         sML[row] = make_float2(m, l);
@@ -539,18 +574,18 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->ml_ready);
         // group 0 has read this group's output: its accumulator may be written again
-        ok = warp_mbar_wait(&bars->merged, merges & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, merged)), merges & 1u);
         tc_fence_after();
         ++merges;
         continue;
       }
       float f0 = 1.f, f1 = 0.f;
       if (nt > 0) {
-        ok = warp_mbar_wait(&bars->pv_done[g][(own - 1) & 1u], ((own - 1) >> 1) & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, pv_done), 2 * g + ((own - 1) & 1u)), ((own - 1) >> 1) & 1u);
         if (!ok) break;
       }
       if (other) {
-        ok = warp_mbar_wait(&bars->ml_ready, merges & 1u, abort, p.status);
+        ok = wait(bar(offsetof(Bars, ml_ready)), merges & 1u);
         if (!ok) break;
         const float2 b = sML[row];
         const float top = fmaxf(m, b.x), at = top == -INFINITY ? 0.f : top;
