@@ -34,12 +34,19 @@ __device__ __forceinline__ int chunk_tiles(const ChunkParams& p, KeyRange k) {
   return k.hi > k.lo ? (k.hi - 1) / kChunkKeys + 1 - k.lo / kChunkKeys : 0;
 }
 
-// A CTA's share of one item: key tiles [t0, t1) of its n.
+// A CTA's share of one item: key tiles [t0, t1) of its n, in turn from t0 + rot on and
+// around (tile()).
 struct ChunkItem {
   int q0, tokens, first_tok, h;  // row of its first token, tokens, that token's index in the request, query head
   int qo, kv, pbase, need;       // of its request: new tokens, cached ones, page list
-  int n, t0, t1, tile0;          // tile0: its first key tile
+  int n, t0, t1, rot, tile0;     // tile0: its first key tile
   KeyRange keys;
+
+  // Key tile that comes i-th.
+  __device__ __forceinline__ int tile(int i) const {
+    const int t = t0 + rot + i;
+    return tile0 + (t < t1 ? t : t - (t1 - t0));
+  }
 };
 
 // A request as the work line sees it; no blocks if it is skipped.
@@ -244,8 +251,8 @@ struct ChunkWalk {
   // whole items: number `item` of `whole_items`, at place w
   int item = 0, whole_items = 0;
   ChunkPlace w;
-  // the part of the line: units [u, u1), in the item that starts at item_start, at place l
-  int u = 0, u1 = 0, item_start = 0;
+  // the part of the line: units [u, u1) from u0 on, in the item that starts at item_start, at place l
+  int u = 0, u1 = 0, u0 = 0, item_start = 0;
   ChunkPlace l, line_first;  // line_first: the line's first block
 
   // To CTA c's work; a whole warp calls it. Returns what the merge has to know of
@@ -263,6 +270,7 @@ struct ChunkWalk {
     if (has_part) {
       u = line.start(c);
       u1 = line.start(c + 1);
+      u0 = u;
     }
     if (line.parts == 0 || (!has_part && item >= whole_items)) return cut;
     // lane 0: unit u of the line; 1: unit u1 (or the last); 2: the line's first block; 3: the first whole item
@@ -330,7 +338,7 @@ struct ChunkWalk {
   __device__ __forceinline__ bool next(const ChunkParams& p, ChunkItem& I) {
     if (item < whole_items) {
       describe(p, w, I);
-      I.t0 = 0;
+      I.t0 = I.rot = 0;
       I.t1 = I.n;
       const int block = item / p.item_heads;
       item += (int)gridDim.x;
@@ -345,6 +353,16 @@ struct ChunkWalk {
       I.t0 = u - item_start;
       I.t1 = min(I.n, u1 - item_start);
       const bool some = I.n > 0 ? I.t0 < I.n : I.t0 == 0;
+      // Blocks of one request read the same keys, a part each of them, and parts are
+      // about as long as one another: so a CTA that has worked off x units goes on at
+      // a tile that is x modulo a part's length (where its tiles have one), and the
+      // CTAs read the same keys at about the same time, once from HBM.
+      I.rot = 0;
+      if (I.qo > p.item_tokens) {
+        const int length = u1 - u0, ahead = (u - u0 - (I.tile0 + I.t0)) % length;
+        I.rot = ahead < 0 ? ahead + length : ahead;
+        if (I.rot >= I.t1 - I.t0) I.rot = 0;
+      }
       item_start += I.n + p.item_cost;
       u = item_start;
       if (u < u1 && !l.skip(p, 1)) {  // the next head, from the line's first block on

@@ -266,13 +266,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
           for (int b = 0; b < 8; ++b) next[b] = b < boxes && idx + b < I.need ? __ldg(list + idx + b) : 0;
         };
-        read(I.tile0 + I.t0);
-        for (int t = I.t0; t < I.t1; ++t) {
-          const int tile = I.tile0 + t, idx = tile * kN >> p.page_shift;
+        const int nt = I.t1 - I.t0;
+        read(I.tile(0));
+        for (int i = 0; i < nt; ++i) {
+          const int tile = I.tile(i), idx = tile * kN >> p.page_shift;
           int page[8];
 #pragma unroll
           for (int b = 0; b < 8; ++b) page[b] = next[b];
-          if (t + 1 < I.t1) read(tile + 1);
+          if (i + 1 < nt) read(I.tile(i + 1));
           ok = mbar_wait(&empty[slot], (turn & 1u) ^ 1u, abort, p.status);
           if (!ok) break;
           const int soff = tile * kN & (p.page_size - 1) & ~(kN - 1);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (!ok) break;
         if (two || (i & 1) == g) {
           const uint32_t buf = own & 1u;
-          const int k0 = (I.tile0 + I.t0 + i) * kN;
+          const int k0 = I.tile(i) * kN;
           const int from = max(I.keys.lo - k0, 0), to = min(I.keys.hi - k0, kN);
           if (from > 0 || to < kN) {
             // with two tiles both groups' warps write the same zeros
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         ++own;
         if (warp_valid) {
           tc_fence_after();
-          const int k0 = (I.tile0 + I.t0 + i) * kN;
+          const int k0 = I.tile(i) * kN;
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
           // Scores outside columns [c_lo, c_hi) of chunk c become -inf, 16 at a time
