@@ -456,14 +456,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         hi = k.hi;
       }
       float m = valid ? -INFINITY : 0.f, l = 0.f;
-      for (int i = two ? 0 : g; i < nt; i += two ? 1 : 2) {  // (else the others are the other group's)
+      const int step = two ? 1 : 2, keys_end = (I.tile0 + I.t1) * kN;
+      int k0 = (I.tile0 + I.t0 + I.rot + (two ? 0 : g) - step) * kN;  // first key of the tile before
+      for (int i = two ? 0 : g; i < nt; i += step) {  // (with one query tile the others are the other group's)
+        k0 += step * kN;
+        if (k0 >= keys_end) k0 -= nt * kN;
         const uint32_t buf = own & 1u, t_s = tmem + lanes + col_s(g, buf);
         ok = wait(bar(offsetof(Bars, s_full), 2 * g + buf), (own >> 1) & 1u);
         if (!ok) break;
         ++own;
         if (warp_valid) {
           tc_fence_after();
-          const int k0 = I.tile(i) * kN;
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
           // Scores outside columns [c_lo, c_hi) of chunk c become -inf, 16 at a time
