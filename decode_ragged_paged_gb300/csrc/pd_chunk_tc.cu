@@ -104,9 +104,10 @@ __device__ __forceinline__ bool try_all(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// warp_mbar_wait by try_all.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  if (try_all(bar, parity)) return true;
+// warp_mbar_wait by try_all. The waiting itself is a function of its own: the roles'
+// loops together are more than an instruction cache holds, and 16 copies of it in
+// line cost every case 2 to 4 %.
+__device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
@@ -119,6 +120,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     }
     if (__any_sync(0xffffffffu, late || *abort != 0)) return false;
   }
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  return try_all(bar, parity) || warp_wait_long(bar, parity, abort, status);
 }
 
 // V rows of keys that no row of the item sees become zeros, so that nothing of
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
               if (!ok) break;
               tc_fence_after();
               l *= alpha;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lanes + col_o(g) + 32 * c, o);
