@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
 
 // ------------------------------------------------------------------- host
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
-  // The tensor cores take bf16, in pages whose boxes fill a tile (and whose
-  // rows keep the swizzle's groups of 8 whole); the CUDA cores take the rest.
-  p.tc = kv_dtype == PD_BF16 && p.page_size >= 8 && (p.page_size & (p.page_size - 1)) == 0;
+  // The tensor cores take bf16, in pages of whole groups of the swizzle's 8 rows;
+  // the CUDA cores take the rest.
+  p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
     p.tile_tokens = 128 / p.tile_heads;

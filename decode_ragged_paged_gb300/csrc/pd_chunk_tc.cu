@@ -1,5 +1,5 @@
 // pd_chunk_tc.cu -- the tensor-core kernel of the chunk attention (bf16, pages
-// a power of two of at least 8 slots): tcgen05 products with S, P and O in
+// of a multiple of 8 slots): tcgen05 products with S, P and O in
 // tensor memory, tiles fetched by TMA.
 //
 // One persistent CTA per SM walks its part of the work line (pd_chunk.cuh). Two
@@ -80,6 +80,13 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
+// Rows of a box: the largest power of two, up to a tile, that a page is a multiple of,
+// so that every box lies in one page (and is at least a swizzle's 8 rows high).
+__host__ __device__ __forceinline__ int page_box(int page_size) {
+  const int b = page_size & -page_size;
+  return b < kN ? b : kN;
+}
+
 // TMEM: two S / P buffers of 64 columns a group, then the groups' O accumulators.
 __device__ __forceinline__ uint32_t col_s(int g, uint32_t buf) { return (uint32_t)(2 * g + buf) * kN; }
 __device__ __forceinline__ uint32_t col_o(int g) { return 256u + (uint32_t)g * 128; }
@@ -155,7 +162,9 @@ __device__ __forceinline__ void store_sector(void* to, const uint32_t* v, bool a
 
 }  // namespace
 
-template <int D>
+// POW2: pages of a power of two (others cost the loads of every tile a little more:
+// 8 % of a large chunked prefill, so they have a kernel of their own).
+template <int D, bool POW2>
 __global__ void __launch_bounds__(kCtThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
@@ -257,7 +266,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     uint8_t* ring = is_v ? sV : sK;
     uint64_t *full = is_v ? bars->v_full : bars->k_full, *empty = is_v ? bars->v_empty : bars->k_empty;
-    const int pb = p.page_size < kN ? p.page_size : kN, boxes = kN / pb;
+    const int pb = page_box(p.page_size), boxes = kN / pb;
+    // to the next box: a page of a power of two has one (or the tile has)
+    auto step_box = [&](int& idx, int& off) {
+      if (POW2) {
+        ++idx;
+      } else {
+        off += pb;
+        if (off == p.page_size) off = 0, ++idx;
+      }
+    };
     uint32_t slot = 0, turn = 0;
     bool ok = true;
     while (ok && next_item()) {
@@ -265,24 +283,28 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (leader) {
         const int kv_head = I.h / p.group;
         const int* list = p.page_indices + I.pbase;
-        int next[8];
+        // Pages of the next tile's boxes, the first one's number in the request's list and its first row there.
+        int next[8], next_idx = 0, next_off = 0;
         auto read = [&](int tile) {
-          const int idx = tile * kN >> p.page_shift;
+          const int key = tile * kN;
+          next_idx = POW2 ? key >> p.page_shift : key / p.page_size;
+          next_off = POW2 ? key & (p.page_size - 1) & ~(kN - 1) : key - next_idx * p.page_size;
+          int idx = next_idx, off = next_off;
 #pragma unroll
-          for (int b = 0; b < 8; ++b) next[b] = b < boxes && idx + b < I.need ? __ldg(list + idx + b) : 0;
+          for (int b = 0; b < 8; ++b) {
+            next[b] = b < boxes && idx < I.need ? __ldg(list + idx) : 0;
+            step_box(idx, off);
+          }
         };
         const int nt = I.t1 - I.t0;
         read(I.tile(0));
         for (int i = 0; i < nt; ++i) {
-          const int tile = I.tile(i), idx = tile * kN >> p.page_shift;
-          int page[8];
+          int idx = next_idx, off = next_off, page[8];
 #pragma unroll
           for (int b = 0; b < 8; ++b) page[b] = next[b];
           if (i + 1 < nt) read(I.tile(i + 1));
           ok = mbar_wait(&empty[slot], (turn & 1u) ^ 1u, abort, p.status);
           if (!ok) break;
-          const int soff = tile * kN & (p.page_size - 1) & ~(kN - 1);
-          const int c1 = p.nhd ? kv_head : soff, c2 = p.nhd ? soff : kv_head;
           uint8_t* to = ring + slot * S::kTile;
           mbar_arrive_expect_tx(&full[slot], S::kTile);
 #pragma unroll
@@ -290,7 +312,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             if (b == boxes) break;
             // pages past the request's end, and ids outside the pools: page num_pages, which TMA reads as zeros
             int id = page[b];
-            if (idx + b >= I.need) {
+            if (idx >= I.need) {
               id = p.num_pages;
             } else if (id < 0 || id >= p.num_pages) {
               report(p.status, PD_DEV_BAD_PAGE_TABLE);
@@ -298,7 +320,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
 #pragma unroll
             for (int h = 0; h < S::kHalves; ++h)
-              tma_load_4d(to + h * S::kHalf + b * pb * 128, map, 64 * h, c1, c2, id, &full[slot]);
+              tma_load_4d(to + h * S::kHalf + b * pb * 128, map, 64 * h, p.nhd ? kv_head : off, p.nhd ? off : kv_head, id,
+                          &full[slot]);
+            step_box(idx, off);
           }
           if (++slot == S::kRing) slot = 0, ++turn;
         }
@@ -681,10 +705,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 // ------------------------------------------------------------------- host
 namespace {
 
-template <int D>
+template <int D, bool POW2>
 cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
-  auto kernel = chunk_tc_kernel<D>;
+  auto kernel = chunk_tc_kernel<D, POW2>;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -701,7 +725,7 @@ cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensor
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
-  const int pb = p.page_size < kN ? p.page_size : kN;
+  const int pb = page_box(p.page_size);
   if (!make_rows_map(&tq, p.q, PD_BF16, p.total_qo, p.hq, p.head_dim, 64, p.tile_tokens, true, p.tile_heads,
                      p.q_stride) ||
       !make_pool_map(&tk, p.k_pool, PD_BF16, p.num_pages, p.hkv, p.page_size, p.head_dim, 64, pb, true, p.nhd != 0) ||
@@ -709,7 +733,11 @@ cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   last_kernel() = "chunk_tc_kernel";
   profile_begin(stream);
-  const cudaError_t e = p.head_dim == 64 ? launch_d<64>(p, tq, tk, tv, stream) : launch_d<128>(p, tq, tk, tv, stream);
+  cudaError_t e;
+  if (p.page_shift >= 0)
+    e = p.head_dim == 64 ? launch_d<64, true>(p, tq, tk, tv, stream) : launch_d<128, true>(p, tq, tk, tv, stream);
+  else
+    e = p.head_dim == 64 ? launch_d<64, false>(p, tq, tk, tv, stream) : launch_d<128, false>(p, tq, tk, tv, stream);
   profile_end(stream);
   return e;
 }

@@ -280,7 +280,7 @@ PD_API int pd_attn_mixed_split(const pd_attn_desc *desc, const pd_batch *batch, 
  * batch->qo_indptr is required; rows of q past qo_indptr[B] are not used and
  * their o and lse are left as they were. Supported: fp32 and bf16, D 64 or 128,
  * any page size, any group, max_kv_len up to 2^24 (PD_ERR_UNSUPPORTED). bf16 with
- * pages a power of two of at least 8 runs on the tensor cores (the softmax weights
+ * pages of a multiple of 8 slots runs on the tensor cores (the softmax weights
  * enter the product with V as bf16); other calls run in fp32 on the CUDA cores. A
  * workspace serves one call at a time and carries nothing from one to the next. Keys that no token of the request sees
  * (past kv_len, or before the first token's window) may hold anything, also NaN;

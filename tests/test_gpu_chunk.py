@@ -155,6 +155,14 @@ def test_many_requests_of_several_blocks(dt, d, page):
     Batch(21, [1300, 5], [1300, 2000], 128, 1, d, page, dt).check(window=64)
 
 
+@pytest.mark.parametrize("page", [8, 12, 20, 24, 40, 48, 72, 96, 192, 200])
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_page_sizes(page, layout):
+    # pages that end inside a tile, and tiles that end inside a page, at any offset
+    Batch(22, [1, 70, 200], [777, 70, 1300], 8, 2, 128 if page % 16 else 64, page, BF16, layout).check()
+    Batch(23, [3, 150], [1500, 460], 8, 2, 64, page, BF16, layout).check(window=90)
+
+
 @pytest.mark.parametrize("dt,d,page", TYPES[:4])
 def test_strided_queries_and_rows_behind_the_last(dt, d, page):
     b = Batch(8, [20, 150], [20, 300], 8, 2, d, page, dt)
