@@ -325,6 +325,259 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
   }
 }
 
+// ------------------------------------------------------------ few query rows
+// fp32 arithmetic for at most R query rows an item (single tokens, verification):
+// HBM bound, so every warp streams keys by itself, 8 of a tile's 64, without a
+// barrier of the CTA. A lane has D / 32 columns of q, k, v and o. The products of 4
+// rows and 8 keys are 32 sums over the lanes, halved and exchanged until lane i has
+// the i-th; each warp keeps its own maximum, sum and output, and the eight are
+// joined at an item's end. K of the next keys is on its way during the softmax and
+// the product with V, V during the scores.
+constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
+constexpr int kRowsKeys = kChunkKeys / kRowsWarps;
+static_assert(kRowsKeys == 8, "4 rows x 8 keys are the 32 lanes");
+
+template <int R, int D>
+constexpr size_t rows_smem() {
+  return sizeof(float) * (size_t)(R * D + kRowsWarps * (R * D + 2 * R + kRowsKeys * R));
+}
+
+// E consecutive elements as they are in memory, and as fp32.
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> { using type = uint4; };
+template <>
+struct Raw<8> { using type = uint2; };
+template <>
+struct Raw<4> { using type = uint32_t; };
+
+template <typename T, int E>
+struct Elems {
+  typename Raw<E * sizeof(T)>::type raw;
+  __device__ __forceinline__ void load(const T* p) {
+    raw = __ldg(reinterpret_cast<const typename Raw<E * sizeof(T)>::type*>(p));
+  }
+  __device__ __forceinline__ void load_shared(const T* p) {
+    raw = *reinterpret_cast<const typename Raw<E * sizeof(T)>::type*>(p);
+  }
+  __device__ __forceinline__ void zero() { raw = {}; }
+  __device__ __forceinline__ float get(int e) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+};
+
+// One of a lane's two sums with the lane's across bit `half` added: `high` in the
+// lanes that have the bit, `low` in the others.
+__device__ __forceinline__ float halve(float low, float high, int half, int lane) {
+  const bool up = lane & half;
+  return (up ? high : low) + __shfl_xor_sync(0xffffffffu, up ? low : high, half);
+}
+
+template <typename T, int R, int D>
+__global__ void __launch_bounds__(kRowsThreads, R == 4 ? 2 : 1) chunk_rows_kernel(const ChunkParams p) {
+  constexpr int E = D / 32, SETS = R / 4;
+  extern __shared__ float4 rows_smem_raw[];
+  float* sQ = reinterpret_cast<float*>(rows_smem_raw);    // [row][D], scaled
+  float* sAcc = sQ + R * D;                               // [warp][row][D]
+  float* sM = sAcc + kRowsWarps * R * D;                  // [warp][row] maxima, then sums
+  float* sL = sM + kRowsWarps * R;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, key = lane & 7;
+  float* sP = sL + kRowsWarps * R + warp * kRowsKeys * R;  // [key][row], this warp's
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  ChunkWalk walk;
+  {
+    const ChunkLine line = take_line(p, rows_smem_raw);
+    const int4 cut = walk.begin(p, line, blockIdx.x);
+    if (tid == 0) p.cuts[blockIdx.x] = cut;
+  }
+  ChunkItem I;
+  while (walk.next(p, I)) {
+    __syncthreads();  // the line, or the last item's outputs, have been read
+    const int rows = I.tokens * p.tile_heads;
+    for (int r = warp; r < R; r += kRowsWarps) {
+      Elems<T, E> x;
+      x.zero();
+      if (r < rows) {
+        const int tok = r / p.tile_heads;
+        x.load(static_cast<const T*>(p.q) + (int64_t)(I.q0 + tok) * p.q_stride +
+               (int64_t)(I.h + r - tok * p.tile_heads) * D + lane * E);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) sQ[r * D + lane * E + e] = x.get(e) * p.scale_log2;
+    }
+    float acc[R][E];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+    // this lane's scores are of rows 4 s + lane / 8
+    float m[SETS], l[SETS];
+    int lo[SETS], hi[SETS];
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+      m[s] = -INFINITY;
+      l[s] = 0.f;
+      const int r = 4 * s + lane / 8, tok = I.first_tok + r / p.tile_heads;
+      const KeyRange k = chunk_keys(p, I.qo, I.kv, tok, tok + 1);
+      lo[s] = k.lo;
+      hi[s] = r < rows ? k.hi : 0;
+    }
+    const int kv_head = I.h / p.group;
+    // Element offset of this lane's key of the warp's keys [k0, k0 + 8), or -1 where no row of the item sees it.
+    auto place = [&](int k0) -> int64_t {
+      const int j = k0 + key;
+      if (j < I.keys.lo || j >= I.keys.hi) return -1;
+      const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+      const int page = p.page_indices[I.pbase + idx], slot = j - idx * p.page_size;
+      if (page < 0 || page >= p.num_pages) {
+        report(p.status, PD_DEV_BAD_PAGE_TABLE);
+        return -1;
+      }
+      return (p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head
+                    : ((int64_t)page * p.hkv + kv_head) * p.page_size + slot) * D;
+    };
+    Elems<T, E> k[kRowsKeys], v[kRowsKeys];
+    auto fetch = [&](const void* pool, int64_t at, Elems<T, E> (&x)[kRowsKeys]) {
+#pragma unroll
+      for (int j = 0; j < kRowsKeys; ++j) {
+        const int64_t o = __shfl_sync(0xffffffffu, at, j);
+        x[j].zero();
+        if (o >= 0) x[j].load(static_cast<const T*>(pool) + o + lane * E);
+      }
+    };
+    const int first = (I.tile0 + I.t0) * kChunkKeys + warp * kRowsKeys, last = (I.tile0 + I.t1) * kChunkKeys;
+    int64_t at = first < last ? place(first) : -1;
+    if (first < last) {
+      fetch(p.k_pool, at, k);
+      fetch(p.v_pool, at, v);
+    }
+    __syncthreads();  // q
+    for (int k0 = first; k0 < last; k0 += kChunkKeys) {
+      const bool more = k0 + kChunkKeys < last;
+      if (more) at = place(k0 + kChunkKeys);
+      float s[SETS];
+#pragma unroll
+      for (int x = 0; x < SETS; ++x) {
+        // products with rows 4 x + r and r + 2 at once, so that 16 sums are held and not 32
+        float part[16];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          Elems<float, E> qa, qb;
+          qa.load_shared(sQ + (4 * x + r) * D + lane * E);
+          qb.load_shared(sQ + (4 * x + r + 2) * D + lane * E);
+#pragma unroll
+          for (int j = 0; j < kRowsKeys; ++j) {
+            float a = qa.get(0) * k[j].get(0), b = qb.get(0) * k[j].get(0);
+#pragma unroll
+            for (int e = 1; e < E; ++e) {
+              a = fmaf(qa.get(e), k[j].get(e), a);
+              b = fmaf(qb.get(e), k[j].get(e), b);
+            }
+            part[8 * r + j] = halve(a, b, 16, lane);
+          }
+        }
+#pragma unroll
+        for (int half = 8; half > 0; half >>= 1)
+#pragma unroll
+          for (int i = 0; i < half; ++i) part[i] = halve(part[i], part[i + half], half, lane);
+        s[x] = part[0];
+      }
+      if (more) fetch(p.k_pool, at, k);
+#pragma unroll
+      for (int x = 0; x < SETS; ++x) {
+        const float sc = k0 + key >= lo[x] && k0 + key < hi[x] ? s[x] : -INFINITY;
+        float top = sc;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m[x]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float alpha = exp2f(m[x] - base), w = exp2f(sc - base);
+        l[x] = l[x] * alpha + w;
+        m[x] = top;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float f = __shfl_sync(0xffffffffu, alpha, 8 * r);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[4 * x + r][e] *= f;
+          }
+        }
+        sP[key * R + 4 * x + lane / 8] = w;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kRowsKeys; ++j)
+#pragma unroll
+        for (int x = 0; x < SETS; ++x) {
+          const float4 w = *reinterpret_cast<const float4*>(sP + j * R + 4 * x);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float y = v[j].get(e);
+            acc[4 * x][e] = fmaf(w.x, y, acc[4 * x][e]);
+            acc[4 * x + 1][e] = fmaf(w.y, y, acc[4 * x + 1][e]);
+            acc[4 * x + 2][e] = fmaf(w.z, y, acc[4 * x + 2][e]);
+            acc[4 * x + 3][e] = fmaf(w.w, y, acc[4 * x + 3][e]);
+          }
+        }
+      __syncwarp();  // the weights have been read
+      if (more) fetch(p.v_pool, at, v);
+    }
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) l[s] += __shfl_xor_sync(0xffffffffu, l[s], d);
+      if (key == 0) {
+        sM[warp * R + 4 * s + lane / 8] = m[s];
+        sL[warp * R + 4 * s + lane / 8] = l[s];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sAcc[(warp * R + r) * D + lane * E + e] = acc[r][e];
+    __syncthreads();
+    // the eight warps' outputs of 4 columns of a row
+    const int64_t part = part_slot(I, blockIdx.x);
+    for (int i = tid; i < rows * (D / 4); i += kRowsThreads) {
+      const int r = i / (D / 4), c = 4 * (i - r * (D / 4));
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sM[w * R + r]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) {
+        const float f = exp2f(sM[w * R + r] - base);
+        const float4 a = *reinterpret_cast<const float4*>(sAcc + (w * R + r) * D + c);
+        sum = fmaf(sL[w * R + r], f, sum);
+        o.x = fmaf(a.x, f, o.x);
+        o.y = fmaf(a.y, f, o.y);
+        o.z = fmaf(a.z, f, o.z);
+        o.w = fmaf(a.w, f, o.w);
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const int tok = r / p.tile_heads;
+      const int64_t row = (int64_t)(I.q0 + tok) * p.hq + I.h + r - tok * p.tile_heads;
+      if (part < 0 && p.o_dtype == PD_BF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + c) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      else
+        *reinterpret_cast<float4*>((part < 0 ? static_cast<float*>(p.o) + row * D : p.part_o + (part * p.rows + r) * D) +
+                                   c) = o;
+      if (c == 0) {
+        const float lse2 = sum != 0.f ? top + log2f(sum) : -INFINITY;
+        if (part >= 0) p.part_lse[part * p.rows + r] = lse2;
+        else if (p.lse != nullptr) p.lse[row] = lse2 * kLn2;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------- host
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // The tensor cores take bf16, in pages of whole groups of the swizzle's 8 rows;
@@ -339,15 +592,15 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.min_units = 4;
     p.max_parts = device_sm_count();
   } else {
-    // Rows of an item: 16 where no request has more, else 64 (a 64-row tile with
-    // few rows would spend its time on rows that are not there).
+    // Rows of an item: 4 or 16 where that takes a request's rows in one go or in a
+    // few (the kernel for few rows), else 64.
     const int64_t most = (int64_t)p.max_qo_len * p.group;
-    p.rows = most <= 16 ? 16 : 64;
+    p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * 2;
+    p.max_parts = device_sm_count() * (p.rows == 16 ? 1 : 2);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)
@@ -377,16 +630,25 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
 
 namespace {
 
-template <typename T, int R, int D>
-cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
-  auto kernel = chunk_simt_kernel<T, R, D>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<R, D>());
+template <typename Kernel>
+cudaError_t launch_cores(Kernel kernel, const char* name, int threads, size_t smem, const ChunkParams& p,
+                         cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  last_kernel() = "chunk_simt_kernel";
+  last_kernel() = name;
   profile_begin(stream);
-  e = launch_dependent(kernel, dim3(p.max_parts), kSimtThreads, simt_smem<R, D>(), stream, p);
+  e = launch_dependent(kernel, dim3(p.max_parts), threads, smem, stream, p);
   profile_end(stream);
   return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
+  if (p.rows == 4)
+    return launch_cores(chunk_rows_kernel<T, 4, D>, "chunk_rows_kernel", kRowsThreads, rows_smem<4, D>(), p, stream);
+  if (p.rows == 16)
+    return launch_cores(chunk_rows_kernel<T, 16, D>, "chunk_rows_kernel", kRowsThreads, rows_smem<16, D>(), p, stream);
+  return launch_cores(chunk_simt_kernel<T, 64, D>, "chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
 }
 
 }  // namespace
@@ -395,15 +657,13 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (!p.self_plan) e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return PD_ERR_CUDA;
-  const bool d64 = p.head_dim == 64, few = p.rows == 16;
+  const bool d64 = p.head_dim == 64;
   if (p.tc)
     e = launch_chunk_tc(p, stream);
   else if (kv_dtype == PD_BF16)
-    e = d64 ? (few ? launch_simt<uint16_t, 16, 64>(p, stream) : launch_simt<uint16_t, 64, 64>(p, stream))
-            : (few ? launch_simt<uint16_t, 16, 128>(p, stream) : launch_simt<uint16_t, 64, 128>(p, stream));
+    e = d64 ? launch_simt<uint16_t, 64>(p, stream) : launch_simt<uint16_t, 128>(p, stream);
   else
-    e = d64 ? (few ? launch_simt<float, 16, 64>(p, stream) : launch_simt<float, 64, 64>(p, stream))
-            : (few ? launch_simt<float, 16, 128>(p, stream) : launch_simt<float, 64, 128>(p, stream));
+    e = d64 ? launch_simt<float, 64>(p, stream) : launch_simt<float, 128>(p, stream);
   if (e != cudaSuccess) return PD_ERR_CUDA;
   if (p.max_parts > 1) {
     const dim3 grid(p.max_parts - 1, (p.rows + 31) / 32);
