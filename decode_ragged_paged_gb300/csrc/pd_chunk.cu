@@ -331,16 +331,21 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
 // barrier of the CTA. A lane has D / 32 columns of q, k, v and o. The products of 4
 // rows and 8 keys are 32 sums over the lanes, halved and exchanged until lane i has
 // the i-th; each warp keeps its own maximum, sum and output, and the eight are
-// joined at an item's end. K of the next keys is on its way during the softmax and
-// the product with V, V during the scores.
+// joined at an item's end. The next keys are on their way to shared memory meanwhile.
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
 constexpr int kRowsKeys = kChunkKeys / kRowsWarps;
+constexpr int kRowsStages = 3;  // of a warp's 8 keys, K and V
 static_assert(kRowsKeys == 8, "4 rows x 8 keys are the 32 lanes");
 
-template <int R, int D>
-constexpr size_t rows_smem() {
-  return sizeof(float) * (size_t)(R * D + kRowsWarps * (R * D + 2 * R + kRowsKeys * R));
-}
+template <typename T, int R, int D>
+struct RowsShape {
+  static constexpr size_t kTile = kRowsKeys * D * sizeof(T);          // K or V of a warp's keys
+  static constexpr size_t kWarp = kRowsStages * 2 * kTile;
+  static constexpr size_t kJoin = sizeof(float) * kRowsWarps * R * D;  // the warps' outputs, once their keys are done
+  static constexpr size_t kRing = kRowsWarps * kWarp > kJoin ? kRowsWarps * kWarp : kJoin;
+  static constexpr size_t kSmem = kRing + sizeof(float) * (R * D + kRowsWarps * (2 * R + kRowsKeys * R));
+  static_assert(kSelfBytes <= kRing && kSmem <= 232448, "shared memory of a CTA");
+};
 
 // E consecutive elements as they are in memory, and as fp32.
 template <int BYTES>
@@ -357,6 +362,12 @@ struct Elems {
   typename Raw<E * sizeof(T)>::type raw;
   __device__ __forceinline__ void load(const T* p) {
     raw = __ldg(reinterpret_cast<const typename Raw<E * sizeof(T)>::type*>(p));
+  }
+  // From global to this thread's place in shared memory, asynchronously; zeros where not `there`.
+  static __device__ __forceinline__ void copy_async(T* to, const T* from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(to)), "l"(from),
+                 "n"((int)(E * sizeof(T))), "r"(there ? (int)(E * sizeof(T)) : 0)
+                 : "memory");
   }
   __device__ __forceinline__ void load_shared(const T* p) {
     raw = *reinterpret_cast<const typename Raw<E * sizeof(T)>::type*>(p);
@@ -377,15 +388,18 @@ __device__ __forceinline__ float halve(float low, float high, int half, int lane
 }
 
 template <typename T, int R, int D>
-__global__ void __launch_bounds__(kRowsThreads, R == 4 ? 2 : 1) chunk_rows_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkParams p) {
+  using S = RowsShape<T, R, D>;
   constexpr int E = D / 32, SETS = R / 4;
   extern __shared__ float4 rows_smem_raw[];
-  float* sQ = reinterpret_cast<float*>(rows_smem_raw);    // [row][D], scaled
-  float* sAcc = sQ + R * D;                               // [warp][row][D]
-  float* sM = sAcc + kRowsWarps * R * D;                  // [warp][row] maxima, then sums
-  float* sL = sM + kRowsWarps * R;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(rows_smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, key = lane & 7;
-  float* sP = sL + kRowsWarps * R + warp * kRowsKeys * R;  // [key][row], this warp's
+  T* ring = reinterpret_cast<T*>(smem + warp * S::kWarp) + lane * E;  // [stage][K, V][key][D], from this lane's columns on
+  float* sAcc = reinterpret_cast<float*>(smem);                       // [warp][row][D]
+  float* sQ = reinterpret_cast<float*>(smem + S::kRing);              // [row][D], scaled
+  float* sM = sQ + R * D;                                             // [warp][row] maxima, then sums
+  float* sL = sM + kRowsWarps * R;
+  float* sP = sL + kRowsWarps * R + warp * kRowsKeys * R;             // [key][row], this warp's
   pdl_launch_dependents();
   pdl_wait_primary();
   ChunkWalk walk;
@@ -440,42 +454,56 @@ __global__ void __launch_bounds__(kRowsThreads, R == 4 ? 2 : 1) chunk_rows_kerne
       return (p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head
                     : ((int64_t)page * p.hkv + kv_head) * p.page_size + slot) * D;
     };
-    Elems<T, E> k[kRowsKeys], v[kRowsKeys];
-    auto fetch = [&](const void* pool, int64_t at, Elems<T, E> (&x)[kRowsKeys]) {
+    // Starts the copies of the keys at `at` into a stage; every lane reads only what it copied.
+    auto fetch = [&](int64_t at, int stage) {
+      T* to = ring + stage * (2 * kRowsKeys * D);
 #pragma unroll
       for (int j = 0; j < kRowsKeys; ++j) {
         const int64_t o = __shfl_sync(0xffffffffu, at, j);
-        x[j].zero();
-        if (o >= 0) x[j].load(static_cast<const T*>(pool) + o + lane * E);
+        const int64_t from = (o >= 0 ? o : 0) + lane * E;
+        Elems<T, E>::copy_async(to + j * D, static_cast<const T*>(p.k_pool) + from, o >= 0);
+        Elems<T, E>::copy_async(to + (kRowsKeys + j) * D, static_cast<const T*>(p.v_pool) + from, o >= 0);
       }
     };
     const int first = (I.tile0 + I.t0) * kChunkKeys + warp * kRowsKeys, last = (I.tile0 + I.t1) * kChunkKeys;
     int64_t at = first < last ? place(first) : -1;
-    if (first < last) {
-      fetch(p.k_pool, at, k);
-      fetch(p.v_pool, at, v);
+#pragma unroll
+    for (int i = 0; i < kRowsStages - 1; ++i) {
+      const int k0 = first + i * kChunkKeys;
+      if (k0 < last) fetch(at, i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (k0 + kChunkKeys < last) at = place(k0 + kChunkKeys);
     }
     __syncthreads();  // q
+    int stage = 0;
     for (int k0 = first; k0 < last; k0 += kChunkKeys) {
-      const bool more = k0 + kChunkKeys < last;
-      if (more) at = place(k0 + kChunkKeys);
+      const int ahead = k0 + (kRowsStages - 1) * kChunkKeys;
+      if (ahead < last) fetch(at, stage == 0 ? kRowsStages - 1 : stage - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (ahead + kChunkKeys < last) at = place(ahead + kChunkKeys);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
+      const T* k_at = ring + stage * (2 * kRowsKeys * D);
+      const T* v_at = k_at + kRowsKeys * D;
+      if (++stage == kRowsStages) stage = 0;
       float s[SETS];
 #pragma unroll
       for (int x = 0; x < SETS; ++x) {
         // products with rows 4 x + r and r + 2 at once, so that 16 sums are held and not 32
         float part[16];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          Elems<float, E> qa, qb;
-          qa.load_shared(sQ + (4 * x + r) * D + lane * E);
-          qb.load_shared(sQ + (4 * x + r + 2) * D + lane * E);
+        for (int j = 0; j < kRowsKeys; ++j) {
+          Elems<T, E> k;
+          k.load_shared(k_at + j * D);
 #pragma unroll
-          for (int j = 0; j < kRowsKeys; ++j) {
-            float a = qa.get(0) * k[j].get(0), b = qb.get(0) * k[j].get(0);
+          for (int r = 0; r < 2; ++r) {
+            Elems<float, E> qa, qb;
+            qa.load_shared(sQ + (4 * x + r) * D + lane * E);
+            qb.load_shared(sQ + (4 * x + r + 2) * D + lane * E);
+            float a = qa.get(0) * k.get(0), b = qb.get(0) * k.get(0);
 #pragma unroll
             for (int e = 1; e < E; ++e) {
-              a = fmaf(qa.get(e), k[j].get(e), a);
-              b = fmaf(qb.get(e), k[j].get(e), b);
+              a = fmaf(qa.get(e), k.get(e), a);
+              b = fmaf(qb.get(e), k.get(e), b);
             }
             part[8 * r + j] = halve(a, b, 16, lane);
           }
@@ -486,7 +514,6 @@ __global__ void __launch_bounds__(kRowsThreads, R == 4 ? 2 : 1) chunk_rows_kerne
           for (int i = 0; i < half; ++i) part[i] = halve(part[i], part[i + half], half, lane);
         s[x] = part[0];
       }
-      if (more) fetch(p.k_pool, at, k);
 #pragma unroll
       for (int x = 0; x < SETS; ++x) {
         const float sc = k0 + key >= lo[x] && k0 + key < hi[x] ? s[x] : -INFINITY;
@@ -510,22 +537,26 @@ __global__ void __launch_bounds__(kRowsThreads, R == 4 ? 2 : 1) chunk_rows_kerne
       }
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < kRowsKeys; ++j)
+      for (int j = 0; j < kRowsKeys; ++j) {
+        Elems<T, E> v;
+        v.load_shared(v_at + j * D);
 #pragma unroll
         for (int x = 0; x < SETS; ++x) {
           const float4 w = *reinterpret_cast<const float4*>(sP + j * R + 4 * x);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float y = v[j].get(e);
+            const float y = v.get(e);
             acc[4 * x][e] = fmaf(w.x, y, acc[4 * x][e]);
             acc[4 * x + 1][e] = fmaf(w.y, y, acc[4 * x + 1][e]);
             acc[4 * x + 2][e] = fmaf(w.z, y, acc[4 * x + 2][e]);
             acc[4 * x + 3][e] = fmaf(w.w, y, acc[4 * x + 3][e]);
           }
         }
+      }
       __syncwarp();  // the weights have been read
-      if (more) fetch(p.v_pool, at, v);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the warps' outputs go where their keys were
 #pragma unroll
     for (int s = 0; s < SETS; ++s) {
 #pragma unroll
@@ -600,7 +631,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.item_tokens = p.rows / p.tile_heads;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * (p.rows == 16 ? 1 : 2);  // CTAs that an SM holds
+    p.max_parts = device_sm_count();  // an SM holds one CTA of each of these kernels
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)
@@ -645,9 +676,9 @@ cudaError_t launch_cores(Kernel kernel, const char* name, int threads, size_t sm
 template <typename T, int D>
 cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
   if (p.rows == 4)
-    return launch_cores(chunk_rows_kernel<T, 4, D>, "chunk_rows_kernel", kRowsThreads, rows_smem<4, D>(), p, stream);
+    return launch_cores(chunk_rows_kernel<T, 4, D>, "chunk_rows_kernel", kRowsThreads, RowsShape<T, 4, D>::kSmem, p, stream);
   if (p.rows == 16)
-    return launch_cores(chunk_rows_kernel<T, 16, D>, "chunk_rows_kernel", kRowsThreads, rows_smem<16, D>(), p, stream);
+    return launch_cores(chunk_rows_kernel<T, 16, D>, "chunk_rows_kernel", kRowsThreads, RowsShape<T, 16, D>::kSmem, p, stream);
   return launch_cores(chunk_simt_kernel<T, 64, D>, "chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
 }
 
