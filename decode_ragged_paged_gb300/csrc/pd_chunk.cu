@@ -220,56 +220,56 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkPar
       __syncthreads();
       fetch(p.v_pool, k0, kv);
       if (has_rows) {
-      float s[RT][4];
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 qv[RT], kf[4];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * LD + d);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * j) * LD + d);
+        float s[RT][4];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          float4 qv[RT], kf[4];
+#pragma unroll
+          for (int i = 0; i < RT; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * LD + d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * j) * LD + d);
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[i][j] = fmaf(qv[i].x, kf[j].x, s[i][j]);
+              s[i][j] = fmaf(qv[i].y, kf[j].y, s[i][j]);
+              s[i][j] = fmaf(qv[i].z, kf[j].z, s[i][j]);
+              s[i][j] = fmaf(qv[i].w, kf[j].w, s[i][j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          float mx = -INFINITY;
+#pragma unroll
           for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(qv[i].x, kf[j].x, s[i][j]);
-            s[i][j] = fmaf(qv[i].y, kf[j].y, s[i][j]);
-            s[i][j] = fmaf(qv[i].z, kf[j].z, s[i][j]);
-            s[i][j] = fmaf(qv[i].w, kf[j].w, s[i][j]);
+            const int key = k0 + tx + 16 * j;
+            s[i][j] = key >= lo[i] && key < hi[i] ? s[i][j] * p.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[i][j]);
           }
-      }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float mx = -INFINITY;
+          for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          const float m_new = fmaxf(m_run[i], mx);
+          const float base = m_new == -INFINITY ? 0.f : m_new;
+          const float alpha = exp2f(m_run[i] - base);
+          float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = k0 + tx + 16 * j;
-          s[i][j] = key >= lo[i] && key < hi[i] ? s[i][j] * p.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
+          for (int j = 0; j < 4; ++j) {
+            const float w = exp2f(s[i][j] - base);
+            sum += w;
+            sP[(tx + 16 * j) * LP + ty * RT + i] = w;
+          }
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          l_run[i] = l_run[i] * alpha + sum;
+          m_run[i] = m_new;
+#pragma unroll
+          for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
         }
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float m_new = fmaxf(m_run[i], mx);
-        const float base = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m_run[i] - base);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float w = exp2f(s[i][j] - base);
-          sum += w;
-          sP[(tx + 16 * j) * LP + ty * RT + i] = w;
-        }
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l_run[i] = l_run[i] * alpha + sum;
-        m_run[i] = m_new;
-#pragma unroll
-        for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
-      }
       }
       __syncthreads();  // the scores have read K, and the weights are written
       put(kv);
