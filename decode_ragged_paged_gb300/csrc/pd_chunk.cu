@@ -111,7 +111,7 @@ constexpr size_t simt_smem() {
 }
 
 template <typename T, int R, int D>
-__global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const ChunkParams p) {
   constexpr int RT = R / 16, LD = D + 4, LP = R + 4, CT = D / 64;  // CT: float4 columns of a thread
   extern __shared__ float4 simt_smem_raw[];
   float* sQ = reinterpret_cast<float*>(simt_smem_raw);
@@ -631,7 +631,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.item_tokens = p.rows / p.tile_heads;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count();  // an SM holds one CTA of each of these kernels
+    p.max_parts = device_sm_count() * (p.rows == 64 ? 2 : 1);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)
