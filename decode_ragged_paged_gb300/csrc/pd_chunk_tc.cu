@@ -27,6 +27,15 @@
 // a result is off by the average of its weights' rounding errors, each at most
 // half a bf16 step.
 //
+// Bound and measured (kernel, cold caches): 4 x 2048 tokens over 14000 to 16384
+// keys, 32 / 8 heads, D 128, 995 us, 1829 TFLOP/s: the tensor cores (81 % of their
+// cycles; the clock gives way to power). 500 tokens over 32700: 162 us, 1643
+// TFLOP/s. 32 verifications of 2 to 8 tokens over 512 to 4096 keys: 54 to 65 us for
+// 273 MB, HBM behind 17 us of start and merge. Windowed prefill, D 64: 49 us; there
+// a tile takes 1450 cycles, two softmax warps a sub-partition with 350 instructions
+// each and their latencies (issue 39 to 50 %; the exponentials 23 to 38 %), and an
+// item 7000 more, from its last tile's product over the output to its next first.
+//
 // Every wait is bounded; on a timeout the CTA records PD_DEV_TIMEOUT, drains
 // and frees its TMEM.
 #include <math.h>

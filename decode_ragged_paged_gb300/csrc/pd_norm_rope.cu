@@ -25,6 +25,11 @@
 //     the heads that the warp takes: z_a = (x_a (c w_a) - x_b (s w_b)) / rms;
 //   the lanes of the heads that a warp holds side by side share the cosines out;
 //   the arithmetic is in packed pairs.
+// Measured (bf16, D 128, cold caches): 4096 tokens of 40 + 2 x 40 heads, 252 MB,
+// 46 us in the kernel, 51 us a call back to back (4.9 TB/s, 73 % of HBM's rate);
+// 16384 tokens of 32 + 2 x 8 heads, 403 MB, 79 us (5.1 TB/s); 128 tokens 5.6 us,
+// the launch. What is left: half of the issue slots are taken, at the 16 warps
+// that 128 registers allow, and a launch's ramp is 7 us of either.
 #include "pd_common.cuh"
 #include "pd_internal.h"
 #include "pd_tc.cuh"

@@ -20,7 +20,10 @@
 // 0.15 MB, a server of 1000 long requests 9 MB), so everything is one launch:
 // every CTA makes the prefix sums of the whole batch in shared memory for
 // itself (three loads and one block scan) and then fills its share of the page
-// list and of the rows. No CTA waits on another.
+// list and of the rows. No CTA waits on another. Back to back a step takes 4.7 us
+// (128 requests), 11.3 us for the 1000 (1 million pages: 66 % of the issue slots,
+// the search for each entry's request; one search for a run of entries left the
+// others of a thread waiting for it: 12.1 us, and 6.2 us for the 128).
 #include "pd_common.cuh"
 #include "pd_internal.h"
 
