@@ -31,8 +31,8 @@
 // keys, 32 / 8 heads, D 128, 995 us, 1829 TFLOP/s: the tensor cores (81 % of their
 // cycles; the clock gives way to power). 500 tokens over 32700: 162 us, 1643
 // TFLOP/s. 32 verifications of 2 to 8 tokens over 512 to 4096 keys: 54 to 65 us for
-// 273 MB, HBM behind 17 us of start and merge. Windowed prefill, D 64: 49 us; there
-// a tile takes 1450 cycles, two softmax warps a sub-partition with 350 instructions
+// 273 MB, HBM behind 17 us of start and merge. Windowed prefill, D 64: 48 us; there
+// a tile takes 1380 cycles, two softmax warps a sub-partition with 350 instructions
 // each and their latencies (issue 39 to 50 %; the exponentials 23 to 38 %), and an
 // item 7000 more, from its last tile's product over the output to its next first.
 //
@@ -140,6 +140,26 @@ __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volat
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   return try_all(bar, parity) || warp_wait_long(bar, parity, abort, status);
+}
+
+// Makes the scores of a row outside columns [lo, hi) of the tile -inf, in tensor
+// memory, before a tile of a mask's edge is weighed: in line with the weights, where
+// most tiles jump over it, it made those slower (D 64: 1450 cycles a tile for 1380).
+__device__ __noinline__ void hide_scores(uint32_t t_s, int lo, int hi) {
+#pragma unroll 1
+  for (int c = 0; c < kN; c += 32) {
+    const int from = lo - c, to = hi - c;
+    if (__all_sync(0xffffffffu, from <= 0 && to >= 32)) continue;  // no row of the warp has any to hide
+    // bits [from, to) of 32
+    const uint32_t keep = (to <= 0 ? 0u : 0xffffffffu >> (32 - min(to, 32))) & (from >= 32 ? 0u : 0xffffffffu << max(from, 0));
+    uint32_t v[32];
+    tmem_ld32(t_s + c, v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = (keep >> e) & 1u ? v[e] : 0xff800000u;
+    tmem_st32(t_s + c, v);
+  }
+  tmem_wait_st();
 }
 
 // V rows of keys that no row of the item sees become zeros, so that nothing of
@@ -507,21 +527,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           tc_fence_after();
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
-          // Scores outside columns [c_lo, c_hi) of chunk c become -inf, 16 at a time
-          // and only where some row of the warp has any to hide: a warp's rows end
-          // within a few columns of one another.
-          auto hide = [&](int c, uint32_t (&v)[32]) {
-            if (full) return;
-#pragma unroll
-            for (int half = 0; half < 32; half += 16) {
-              const int from = c_lo - 32 * c - half, to = c_hi - 32 * c - half;
-              if (__all_sync(0xffffffffu, from <= 0 && to >= 16)) continue;
-              // bits [from, to) of 16
-              const uint32_t keep = (to <= 0 ? 0u : 0xffffu >> (16 - min(to, 16))) & (from >= 16 ? 0u : 0xffffu << max(from, 0));
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[half + e] = (keep >> e) & 1u ? v[half + e] : 0xff800000u;
-            }
-          };
+          if (!full) hide_scores(t_s, c_lo, c_hi);
           uint32_t w[kN / 2];
           float2 sum[2];
           // weights of the tile with maximum m, as bf16 pairs, and their sum
@@ -535,7 +541,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             tmem_wait_ld(v[1]);
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-              hide(c, v[c]);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 x =
@@ -556,12 +561,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           if (!stale) {
             // the tile's own maximum
             float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kN / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(t_s + 32 * c, v);
               tmem_wait_ld(v);
-              hide(c, v);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
             }
