@@ -10,9 +10,8 @@
 // and o = 0, lse = -inf where no key is left.
 #include <math.h>
 
-#include <atomic>
-
 #include "pd_chunk.cuh"
+#include "pd_launch.cuh"
 
 namespace pd {
 
@@ -670,14 +669,13 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
 
 namespace {
 
-template <typename Kernel>
-cudaError_t launch_cores(Kernel kernel, const char* name, int threads, size_t smem, const ChunkParams& p,
-                         cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <auto Kernel>
+cudaError_t launch_cores(const char* name, int threads, size_t smem, const ChunkParams& p, cudaStream_t stream) {
+  cudaError_t e = allow_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
   last_kernel() = name;
   profile_begin(stream);
-  e = launch_dependent(kernel, dim3(p.max_parts), threads, smem, stream, p);
+  e = launch_dependent(Kernel, dim3(p.max_parts), threads, smem, stream, p);
   profile_end(stream);
   return e;
 }
@@ -685,10 +683,10 @@ cudaError_t launch_cores(Kernel kernel, const char* name, int threads, size_t sm
 template <typename T, int D>
 cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
   if (p.rows == 4)
-    return launch_cores(chunk_rows_kernel<T, 4, D>, "chunk_rows_kernel", kRowsThreads, RowsShape<T, 4, D>::kSmem, p, stream);
+    return launch_cores<chunk_rows_kernel<T, 4, D>>("chunk_rows_kernel", kRowsThreads, RowsShape<T, 4, D>::kSmem, p, stream);
   if (p.rows == 16)
-    return launch_cores(chunk_rows_kernel<T, 16, D>, "chunk_rows_kernel", kRowsThreads, RowsShape<T, 16, D>::kSmem, p, stream);
-  return launch_cores(chunk_simt_kernel<T, 64, D>, "chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
+    return launch_cores<chunk_rows_kernel<T, 16, D>>("chunk_rows_kernel", kRowsThreads, RowsShape<T, 16, D>::kSmem, p, stream);
+  return launch_cores<chunk_simt_kernel<T, 64, D>>("chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
 }
 
 }  // namespace

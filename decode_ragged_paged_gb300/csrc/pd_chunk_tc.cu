@@ -42,9 +42,8 @@
 #include <stddef.h>
 #include <string.h>
 
-#include <atomic>
-
 #include "pd_chunk.cuh"
+#include "pd_launch.cuh"
 #include "pd_tc.cuh"
 
 namespace pd {
@@ -721,17 +720,9 @@ namespace {
 template <int D, bool POW2>
 cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
-  auto kernel = chunk_tc_kernel<D, POW2>;
-  static std::atomic<bool> configured[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<chunk_tc_kernel<D, POW2>>(Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
-  }
-  return launch_dependent(kernel, dim3((unsigned)p.max_parts), kCtThreads, Shape<D>::kSmem, stream, tq, tk, tv, p);
+  return launch_dependent(chunk_tc_kernel<D, POW2>, dim3((unsigned)p.max_parts), kCtThreads, Shape<D>::kSmem, stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -32,6 +32,7 @@
 // that 128 registers allow, and a launch's ramp is 7 us of either.
 #include "pd_common.cuh"
 #include "pd_internal.h"
+#include "pd_launch.cuh"
 #include "pd_tc.cuh"
 
 namespace pd {
@@ -392,14 +393,18 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
 // ------------------------------------------------------------------- host
 namespace {
 
+template <auto Kernel>
+cudaError_t launch_k(const NormRopeParams& p, unsigned grid, size_t smem, cudaStream_t stream) {
+  const cudaError_t e = smem > 0 ? allow_smem<Kernel>(smem) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  return launch_dependent(Kernel, dim3(grid), kNrThreads, smem, stream, p);
+}
+
 template <typename T, int V, int C, bool STAGED>
 cudaError_t launch_s(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
-  auto kernel = p.interleaved ? norm_rope_kernel<T, V, true, C, STAGED> : norm_rope_kernel<T, V, false, C, STAGED>;
-  if (STAGED) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNrSmem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_dependent(kernel, dim3(grid), kNrThreads, STAGED ? kNrSmem : 0, stream, p);
+  const size_t smem = STAGED ? kNrSmem : 0;
+  return p.interleaved ? launch_k<norm_rope_kernel<T, V, true, C, STAGED>>(p, grid, smem, stream)
+                       : launch_k<norm_rope_kernel<T, V, false, C, STAGED>>(p, grid, smem, stream);
 }
 
 template <typename T, int V, int C>
