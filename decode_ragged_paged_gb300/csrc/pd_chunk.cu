@@ -663,7 +663,22 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   L.part_lse = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows);
   L.part_o = take(sizeof(float) * 2 * (size_t)p.max_parts * p.rows * p.head_dim);
   L.total = off;
-  p.self_plan = p.batch <= kSelfBatch && p.max_blocks <= kSelfBlocks && p.max_parts <= kSelfParts;
+  const int64_t items = (int64_t)p.max_blocks * p.item_heads;
+  // Uncut items. Cutting spreads them over all CTAs, and costs the line, the parts
+  // and the merge, about as much as `spare` tiles on a CTA. Measured, us uncut / cut,
+  // one token a request over 256, 512, 1024 and 2048 keys, D 128, 8 KV heads: on the
+  // tensor cores 4 requests 8.4 / 12.8, 10.6 / 13.8, 15.1 / 15.5, 23.9 / 18.5, 16
+  // requests 9.0 / 15.2, 11.3 / 17.2, 15.9 / 20.7, 27.3 / 34.3; in fp32 4 requests
+  // 10.4 / 11.5, 16.4 / 13.7, 28.0 / 17.1, 16 requests 10.8 / 16.7, 17.5 / 22.4,
+  // 38.9 / 43.0, 69.8 / 70.2; fp32 items of 64 rows are better cut from two tiles
+  // on. `most_tiles` bounds what requests shorter than the longest lose by it.
+  const int64_t span = p.window >= 0 && p.window + (int64_t)p.item_tokens < p.max_kv_len ? p.window + (int64_t)p.item_tokens + kChunkKeys
+                                                                                        : p.max_kv_len;
+  const int64_t tiles = (span + kChunkKeys - 1) / kChunkKeys;
+  const int spare = p.tc ? 13 : p.rows == 64 ? 1 : 4, most_tiles = p.tc ? 16 : p.rows == 64 ? 1 : 8;
+  p.uncut = items <= p.max_parts && tiles <= most_tiles && tiles * (p.max_parts - items) <= (int64_t)spare * p.max_parts;
+  p.grid = p.uncut ? (int32_t)items : p.max_parts;
+  p.self_plan = p.batch <= kSelfBatch && (p.uncut || (p.max_blocks <= kSelfBlocks && p.max_parts <= kSelfParts));
   return L;
 }
 
@@ -675,7 +690,7 @@ cudaError_t launch_cores(const char* name, int threads, size_t smem, const Chunk
   if (e != cudaSuccess) return e;
   last_kernel() = name;
   profile_begin(stream);
-  e = launch_dependent(Kernel, dim3(p.max_parts), threads, smem, stream, p);
+  e = launch_dependent(Kernel, dim3(p.grid), threads, smem, stream, p);
   profile_end(stream);
   return e;
 }
@@ -703,7 +718,7 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   else
     e = d64 ? launch_simt<float, 64>(p, stream) : launch_simt<float, 128>(p, stream);
   if (e != cudaSuccess) return PD_ERR_CUDA;
-  if (p.max_parts > 1) {
+  if (p.max_parts > 1 && !p.uncut) {
     const dim3 grid(p.max_parts - 1, (p.rows + 31) / 32);
     e = d64 ? launch_dependent(chunk_merge_kernel<64>, grid, kMergeThreads, 0, stream, p)
             : launch_dependent(chunk_merge_kernel<128>, grid, kMergeThreads, 0, stream, p);

@@ -6,6 +6,8 @@
 //   The line. The items in a row, head by head, a head's blocks in batch order,
 // cut into equal parts, one per CTA, anywhere between two key tiles: every CTA
 // has the same work, and an item that a cut falls into is merged afterwards.
+//   Short items. Where there is an item a CTA at most, and none of more than a few
+// tiles, they are not cut, and there is no line and no merge.
 //   Whole items. Blocks of one request read the same keys. Where there are
 // several times more items than CTAs, the first `whole` blocks are dealt out
 // item by item, block by block with its heads: the CTAs then stream the same
@@ -151,6 +153,10 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
   const int blocks = carry;
   if (!over && tid == 0) first[p.batch] = blocks;
   sync_of<NT>();
+  if (p.uncut && !over) {
+    line.whole = blocks;
+    return line;
+  }
   long long sum = 0;
   for (int b0 = 0; !over && b0 < blocks; b0 += NT) {
     const int b = b0 + tid;
@@ -272,7 +278,7 @@ struct ChunkWalk {
       u1 = line.start(c + 1);
       u0 = u;
     }
-    if (line.parts == 0 || (!has_part && item >= whole_items)) return cut;
+    if (!has_part && item >= whole_items) return cut;
     // lane 0: unit u of the line; 1: unit u1 (or the last); 2: the line's first block; 3: the first whole item
     const int at = lane == 1 ? min(u1, line.rem - 1) : min(u, line.rem - 1);
     ChunkPlace here;

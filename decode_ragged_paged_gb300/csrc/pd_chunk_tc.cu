@@ -722,7 +722,7 @@ cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& tq, const CUtensor
                      cudaStream_t stream) {
   const cudaError_t e = allow_smem<chunk_tc_kernel<D, POW2>>(Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_tc_kernel<D, POW2>, dim3((unsigned)p.max_parts), kCtThreads, Shape<D>::kSmem, stream, tq, tk, tv, p);
+  return launch_dependent(chunk_tc_kernel<D, POW2>, dim3((unsigned)p.grid), kCtThreads, Shape<D>::kSmem, stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -251,6 +251,8 @@ struct ChunkParams {
   int32_t page_shift;  // log2 of a page size that is a power of two, else -1
   int32_t aligned32;   // o and the workspace are 32-byte aligned
   int32_t self_plan;   // every CTA makes the work line for itself
+  int32_t uncut;       // an item is one CTA's, and a CTA has one at most: no line, no merge
+  int32_t grid;        // CTAs
   int32_t tile_heads, tile_tokens, item_heads, item_tokens, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)
   int64_t q_stride;  // elements between query tokens

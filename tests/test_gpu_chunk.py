@@ -155,6 +155,17 @@ def test_many_requests_of_several_blocks(dt, d, page):
     Batch(21, [1300, 5], [1300, 2000], 128, 1, d, page, dt).check(window=64)
 
 
+@pytest.mark.parametrize("dt,d,page", TYPES[:4])
+def test_short_caches(dt, d, page):
+    # items that are not cut, up to the lengths and batches from which they are, and beyond
+    for B, top in ((1, 64), (3, 65), (4, 256), (9, 512), (16, 513), (19, 1024), (20, 1025), (38, 300), (200, 60)):
+        rng = random.Random(B)
+        new = [rng.choice([0, 1, 1, 2, 9]) if B != 4 else 1 for _ in range(B)]
+        kv = [max(n, rng.randint(0, top)) for n in new]
+        kv[-1], new[-1] = top, 1
+        Batch(24, new, kv, 8, 8 if B != 9 else 2, d, page, dt).check(window=rng.choice([-1, 40]))
+
+
 @pytest.mark.parametrize("page", [8, 12, 20, 24, 40, 48, 72, 96, 192, 200])
 @pytest.mark.parametrize("layout", ["HND", "NHD"])
 def test_page_sizes(page, layout):
