@@ -40,9 +40,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
 
 // ------------------------------------------------------------------ merge
 // o and lse of the items that the line's cuts fell into: block x has the item
-// that part x begins and does not end, if there is one. One warp a row. Bound by
-// its launch and the parts it reads from L2 (500 tokens over 32700, cut in 216
-// pieces of 131 KB: 12 us behind the kernel's 162).
+// that part x begins and does not end, if there is one. One warp a row, its lanes
+// the parts' sums. Bound by its launch, a chain of three reads and the parts it reads
+// from L2 (500 tokens over 32700, cut in 216 pieces of 131 KB: 8 us behind the
+// kernel's 162; 13 with a part's sum and output read one after the other).
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
@@ -56,30 +57,45 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
   constexpr int E = D / 32;
   for (int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); m < rows;
        m += gridDim.y * (kMergeThreads / 32)) {
-    float best = -INFINITY;
-    for (int x = c; x <= last; ++x)
-      if (x == c || p.cuts[x].y >= 0) best = fmaxf(best, p.part_lse[(2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m]);
-    if (best == -INFINITY) best = 0.f;  // no part has a key: every factor below is 0
-    float sum = 0.f, acc[E];
+    float best = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int x0 = c; x0 <= last; x0 += 32) {
+      // 32 parts' sums, a lane each; an empty part has none
+      const int mine = x0 + lane;
+      const bool there = mine == c || (mine <= last && p.cuts[mine].y >= 0);
+      const float lse = there ? p.part_lse[(2 * (int64_t)mine + (mine == c ? 1 : 0)) * p.rows + m] : -INFINITY;
+      float top = lse;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, best);
+      const float base = top == -INFINITY ? 0.f : top;  // (no part has a key yet: every factor is 0)
+      const float old = exp2f(best - base), f = exp2f(lse - base);
+      best = top;
+      float part = f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+      sum = sum * old + part;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= old;
+      const int parts = min(32, last - x0 + 1);
 #pragma unroll 4
-    for (int x = c; x <= last; ++x) {
-      if (x > c && p.cuts[x].y < 0) continue;  // an empty part
-      const int64_t slot = (2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m;
-      const float f = exp2f(p.part_lse[slot] - best);
-      const float* o = p.part_o + slot * D + lane * E;
-      sum += f;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
-        acc[2] += f * v.z;
-        acc[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
+      for (int i = 0; i < parts; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        if (w == 0.f) continue;
+        const int x = x0 + i;
+        const float* o = p.part_o + ((2 * (int64_t)x + (x == c ? 1 : 0)) * p.rows + m) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(o);
+          acc[0] += w * v.x;
+          acc[1] += w * v.y;
+          acc[2] += w * v.z;
+          acc[3] += w * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(o);
+          acc[0] += w * v.x;
+          acc[1] += w * v.y;
+        }
       }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
@@ -672,9 +688,9 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // 10.4 / 11.5, 16.4 / 13.7, 28.0 / 17.1, 16 requests 10.8 / 16.7, 17.5 / 22.4,
   // 38.9 / 43.0, 69.8 / 70.2; fp32 items of 64 rows are better cut from two tiles
   // on. `most_tiles` bounds what requests shorter than the longest lose by it.
-  const int64_t span = p.window >= 0 && p.window + (int64_t)p.item_tokens < p.max_kv_len ? p.window + (int64_t)p.item_tokens + kChunkKeys
-                                                                                        : p.max_kv_len;
-  const int64_t tiles = (span + kChunkKeys - 1) / kChunkKeys;
+  const int64_t all = ((int64_t)p.max_kv_len + kChunkKeys - 1) / kChunkKeys;
+  const int64_t seen = ((int64_t)p.window + p.item_tokens) / kChunkKeys + 2;  // through a window
+  const int64_t tiles = p.causal && p.window >= 0 && seen < all ? seen : all;
   const int spare = p.tc ? 13 : p.rows == 64 ? 1 : 4, most_tiles = p.tc ? 16 : p.rows == 64 ? 1 : 8;
   p.uncut = items <= p.max_parts && tiles <= most_tiles && tiles * (p.max_parts - items) <= (int64_t)spare * p.max_parts;
   p.grid = p.uncut ? (int32_t)items : p.max_parts;
@@ -719,7 +735,7 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
     e = d64 ? launch_simt<float, 64>(p, stream) : launch_simt<float, 128>(p, stream);
   if (e != cudaSuccess) return PD_ERR_CUDA;
   if (p.max_parts > 1 && !p.uncut) {
-    const dim3 grid(p.max_parts - 1, (p.rows + 31) / 32);
+    const dim3 grid(p.max_parts - 1, (p.rows + 15) / 16);  // two rows a warp
     e = d64 ? launch_dependent(chunk_merge_kernel<64>, grid, kMergeThreads, 0, stream, p)
             : launch_dependent(chunk_merge_kernel<128>, grid, kMergeThreads, 0, stream, p);
   }
