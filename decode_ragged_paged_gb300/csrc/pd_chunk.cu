@@ -683,10 +683,10 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // Uncut items. Cutting spreads them over all CTAs, and costs the line, the parts
   // and the merge, about as much as `spare` tiles on a CTA. Measured, us uncut / cut,
   // one token a request over 256, 512, 1024 and 2048 keys, D 128, 8 KV heads: on the
-  // tensor cores 4 requests 8.4 / 12.8, 10.6 / 13.8, 15.1 / 15.5, 23.9 / 18.5, 16
-  // requests 9.0 / 15.2, 11.3 / 17.2, 15.9 / 20.7, 27.3 / 34.3; in fp32 4 requests
-  // 10.4 / 11.5, 16.4 / 13.7, 28.0 / 17.1, 16 requests 10.8 / 16.7, 17.5 / 22.4,
-  // 38.9 / 43.0, 69.8 / 70.2; fp32 items of 64 rows are better cut from two tiles
+  // tensor cores 4 requests 8.3 / 13.0, 10.6 / 13.3, 15.0 / 14.2, 23.9 / 16.9, 16
+  // requests 8.9 / 15.0, 11.2 / 17.2, 15.8 / 20.5, 27.4 / 34.4; in fp32 4 requests
+  // 10.4 / 10.5, 16.3 / 12.3, 27.9 / 15.8, 16 requests 10.8 / 16.7, 17.4 / 22.6,
+  // 38.9 / 43.1, 69.7 / 70.0; fp32 items of 64 rows are better cut from two tiles
   // on. `most_tiles` bounds what requests shorter than the longest lose by it.
   const int64_t all = ((int64_t)p.max_kv_len + kChunkKeys - 1) / kChunkKeys;
   const int64_t seen = ((int64_t)p.window + p.item_tokens) / kChunkKeys + 2;  // through a window

@@ -21,9 +21,9 @@
 // every CTA makes the prefix sums of the whole batch in shared memory for
 // itself (three loads and one block scan) and then fills its share of the page
 // list and of the rows. No CTA waits on another. Back to back a step takes 4.7 us
-// (128 requests), 11.3 us for the 1000 (1 million pages: 66 % of the issue slots,
-// the search for each entry's request; one search for a run of entries left the
-// others of a thread waiting for it: 12.1 us, and 6.2 us for the 128).
+// (128 requests), 9.8 us for the 1000 (1 million pages: the search for each entry's
+// request, 11.4 over all of them; one search for a run of entries left the others of
+// a thread waiting for it, 12.1 us, and 6.2 us for the 128).
 #include "pd_common.cuh"
 #include "pd_internal.h"
 
@@ -34,6 +34,7 @@ namespace {
 constexpr int kTabThreads = 1024;
 constexpr int kTabWarps = kTabThreads / 32;
 constexpr int kFill = 4;  // entries of the page list or rows that a thread works on together
+constexpr int kHints = 512;  // places of the page list whose requests are looked up ahead
 
 // Prefix sums over the batch.
 struct Sums {
@@ -103,6 +104,7 @@ template <bool COMMIT>
 __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const TablesParams p) {
   extern __shared__ int tab_smem[];
   __shared__ Sums warp_tot[kTabWarps];
+  __shared__ int hint[kHints + 1];
   __shared__ unsigned int taken;
   const int B = p.batch, tid = threadIdx.x;
   int* qo = tab_smem;               // [B + 1] rows before request r, at most total_qo
@@ -243,6 +245,16 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
   const int nnz = pg[B], real_rows = qo[B];
   const int P = p.page_size;
   const int64_t total = (int64_t)nnz + p.total_qo, stride = (int64_t)gridDim.x * kTabThreads;
+  // With several entries a thread, the requests of kHints places of the page list are
+  // found first, and an entry's is searched for between two of them.
+  const bool hinted = nnz >= kFill * stride;
+  int shift = 0;
+  if (hinted) {
+    while ((nnz >> shift) >= kHints) ++shift;
+    for (int k = tid; k <= kHints; k += kTabThreads)
+      hint[k] = owner(pg, 0, B, (int)min((int64_t)k << shift, (int64_t)nnz - 1));
+    __syncthreads();
+  }
   for (int64_t e0 = (int64_t)blockIdx.x * kTabThreads + tid; e0 < total; e0 += kFill * stride) {
     int r[kFill], j[kFill], pos[kFill], page[kFill];
 #pragma unroll
@@ -252,7 +264,8 @@ __global__ void __launch_bounds__(kTabThreads, 1) batch_tables_kernel(const Tabl
       j[x] = pos[x] = 0;
       page[x] = -1;
       if (e < nnz) {
-        r[x] = owner(pg, 0, B, (int)e);
+        const int k = (int)e >> shift;
+        r[x] = hinted ? owner(pg, hint[k], hint[k + 1] + 1, (int)e) : owner(pg, 0, B, (int)e);
         j[x] = (int)e - pg[r[x]];
       } else if (e < nnz + (int64_t)real_rows) {
         r[x] = owner(qo, 0, B, (int)(e - nnz));

@@ -88,6 +88,20 @@ def test_long_requests_and_many_entries():
     assert Case(4, [100000, 0, 7], [1, 70000, 30000], 16).run()[0] == 0
 
 
+@pytest.mark.parametrize("shape", ["even", "ragged", "one"])
+def test_page_lists_of_many_entries_a_thread(shape):
+    # long enough that requests are looked up ahead, with empty ones between them
+    rng = random.Random(6)
+    if shape == "one":
+        cached, new = [0, 660000, 0, 3, 0], [0, 5, 2, 0, 0]
+    else:
+        cached = [2300 if shape == "even" else rng.choice([0, 0, 1, 500, 9000]) for _ in range(400)]
+        new = [rng.choice([0, 1, 3]) for _ in cached]
+    c = Case(7, cached, new, 1, rows=shape != "one")
+    assert c.nnz > 4 * 1024 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert c.run()[0] == 0
+
+
 def test_without_a_free_list():
     assert Case(5, [0, 15, 16, 100], [1, 1, 1, 33], 16, pops=False).run()[0] == 0
     assert Case(5, [0, 15, 16, 100], [1, 1, 1, 33], 16, pops=False, rows=False).run()[0] == 0
