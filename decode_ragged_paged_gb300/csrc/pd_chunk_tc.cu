@@ -25,7 +25,10 @@
 // Sums are fp32. The weights enter the product with V as bf16, as the tensor
 // cores want V's own type there; the sum that divides takes them unrounded, so
 // a result is off by the average of its weights' rounding errors, each at most
-// half a bf16 step.
+// half a bf16 step. Over many keys that averages out; where a row of the item sees
+// fewer than 128 the weights' remainders are multiplied with V too, which leaves
+// 2^-16 of a weight (two keys, values 3.5 to 4 and 0 to 1, bf16 output: 1.1e-2
+// off with bf16 weights, 7.8e-3 with the remainders, half a step of the output).
 //
 // Bound and measured (kernel, cold caches): 4 x 2048 tokens over 14000 to 16384
 // keys, 32 / 8 heads, D 128, 995 us, 1829 TFLOP/s: the tensor cores (81 % of their
@@ -159,6 +162,38 @@ __device__ __noinline__ void hide_scores(uint32_t t_s, int lo, int hi) {
     tmem_st32(t_s + c, v);
   }
   tmem_wait_st();
+}
+
+// Whether some row of the item sees fewer keys than average the weights' rounding
+// out. What a row sees grows with its position under the causal mask, and shrinks
+// without it (a window's lower end alone moves), so the first or the last row sees the fewest.
+constexpr int kFewKeys = 128;
+__device__ __forceinline__ bool few_keys(const ChunkParams& p, const ChunkItem& I) {
+  const int last = I.first_tok + I.tokens - 1;
+  const KeyRange a = chunk_keys(p, I.qo, I.kv, I.first_tok, I.first_tok + 1), b = chunk_keys(p, I.qo, I.kv, last, last + 1);
+  return min(a.hi - a.lo, b.hi - b.lo) < kFewKeys;
+}
+
+// What bf16 leaves of a row's weights 2^(s scale - m), nm = -m, as bf16 pairs in columns
+// 32 .. 63 of its scores' buffer, before the weights themselves overwrite columns
+// 0 .. 31; the upper scores first, so that none is overwritten unread. A function
+// of its own, as hide_scores.
+__device__ __noinline__ void write_remainders(uint32_t t_s, float scale, float nm) {
+  const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+#pragma unroll 1
+  for (int c = kN / 32 - 1; c >= 0; --c) {
+    uint32_t v[32], w[16];
+    tmem_ld32(t_s + 32 * c, v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nm2);
+      const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      const uint32_t hi = pack_bf16x2(pe.x, pe.y);
+      w[e / 2] = pack_bf16x2(pe.x - bf16_lo(hi), pe.y - bf16_hi(hi));  // (the differences are exact)
+    }
+    tmem_st16(t_s + kN / 2 + 16 * c, w);
+  }
 }
 
 // V rows of keys that no row of the item sees become zeros, so that nothing of
@@ -440,7 +475,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     bool ok = true;
     while (ok && next_item()) {
       const int nt = I.t1 - I.t0;
-      const bool two = two_tiles(p, I);
+      const bool two = two_tiles(p, I), few = few_keys(p, I);
       const int i0 = two ? 0 : g;
       for (int i = 0; i < nt; ++i) {
         ok = wait(bar(offsetof(Bars, v_full), vs), vturn & 1u);
@@ -466,6 +501,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk)
               tc_mma_f16_tmem_a(t_o, t_p + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
+            if (few) {  // and their remainders
+#pragma unroll
+              for (int kk = 0; kk < kN / 16; ++kk)
+                tc_mma_f16_tmem_a(t_o, t_p + kN / 2 + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, 1u);
+            }
             tc_commit(&bars->pv_done[g][buf]);
           }
           __syncwarp();
@@ -499,7 +539,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     while (ok && next_item()) {
       const int nt = max(I.t1 - I.t0, 0);
-      const bool two = two_tiles(p, I);
+      const bool two = two_tiles(p, I), few = few_keys(p, I);
       const int half_tok = p.tile_tokens;
       const int tokens = two ? (g == 0 ? half_tok : I.tokens - half_tok) : I.tokens;  // of this group's tile
       const int tok0 = two && g == 1 ? half_tok : 0;
@@ -599,6 +639,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             weights(m == -INFINITY ? 0.f : -m);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (few) write_remainders(t_s, p.scale_log2, m == -INFINITY ? 0.f : -m);
           tmem_st32(t_s, w);
           tmem_wait_st();
           tc_fence_before();

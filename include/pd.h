@@ -280,11 +280,12 @@ PD_API int pd_attn_mixed_split(const pd_attn_desc *desc, const pd_batch *batch, 
  * batch->qo_indptr is required; rows of q past qo_indptr[B] are not used and
  * their o and lse are left as they were. Supported: fp32 and bf16, D 64 or 128,
  * any page size, any group, max_kv_len up to 2^24 (PD_ERR_UNSUPPORTED). bf16 with
- * pages of a multiple of 8 slots runs on the tensor cores (the softmax weights
- * enter the product with V as bf16); other calls run in fp32 on the CUDA cores. A
- * workspace serves one call at a time and carries nothing from one to the next. Keys that no token of the request sees
- * (past kv_len, or before the first token's window) may hold anything, also NaN;
- * V rows that some token of the request sees must be finite for all its tokens.
+ * pages of a multiple of 8 slots runs on the tensor cores: the softmax weights enter
+ * the product with V as bf16, for tokens that see fewer than 128 keys together with
+ * what that leaves of them. Other calls run in fp32 on the CUDA cores. A workspace
+ * serves one call at a time and carries nothing from one to the next. Keys that no
+ * token of the request sees (past kv_len, or before the first token's window) may
+ * hold anything, also NaN; V rows that some token of the request sees must be finite for all its tokens.
  * The call can be captured into a CUDA graph; lengths may change between replays
  * within the host bounds max_qo_len and max_kv_len.
  */

@@ -325,6 +325,60 @@ def test_cache_past_32_bit_offsets():
         ref.check_attention(o, lse, ref.attention(q, kk, vv, [0, 9], [300], [0, 5], px, layout=layout))
 
 
+def few_keys(b, causal, window):
+    """Which rows see fewer than 128 keys."""
+    n = torch.cat([torch.full((x,), y) for x, y in zip(b.new, b.kv)])
+    t = torch.cat([torch.arange(y - x, y) for x, y in zip(b.new, b.kv)])
+    lo = (t - window).clamp(min=0) if window >= 0 else torch.zeros_like(t)
+    return (((t + 1 if causal else n) - lo) < 128).cuda()
+
+
+@pytest.mark.parametrize("d,page,layout", [(64, 16, "HND"), (128, 24, "NHD"), (128, 16, "HND")])
+@pytest.mark.parametrize("new,kv,causal,window", [
+    ([128], [128], True, -1),                            # a prompt's first chunk
+    ([1, 1, 1, 2, 5, 1], [1, 2, 60, 64, 127, 126], True, -1),
+    ([7, 200, 300], [3, 140, 300], True, -1),            # rows without keys; a second block that sees more
+    ([300, 1], [1000, 3000], True, 20),                  # a narrow window over a long cache
+    ([40, 90], [100, 90], False, -1),
+    ([200], [260], False, 30),                           # its last rows see the fewest
+    ([1] * 300, [1 + i % 126 for i in range(300)], True, -1),
+])
+def test_rows_that_see_few_keys_have_exact_weights(d, page, layout, new, kv, causal, window):
+    """Weights of rows with fewer than 128 keys enter the product with V as two bf16 terms: the second
+    is the first's remainder, at most 2^-8 of the weight, and off by at most 2^-8 of that: 2^-16 in all.
+    (step_ref.attention of fp32 queries allows for everything but that.)"""
+    b = Batch(25, new, kv, 8, 2, d, page, BF16, layout)
+    o, lse = b.run(causal=causal, window_left=window, o_dtype=F32, sm_scale=0.05)
+    kw = dict(causal=causal, window=window, scale=0.05, layout=layout)
+    lists = (b.qo, b.kv, b.pp, b.px)
+    ro, rl, ob, lb = ref.attention(b.q.float(), b.k, b.v, *lists, **kw)
+    sizes = ref.attention(b.q.float(), b.k, b.v.abs(), *lists, **kw)[0]
+    few = few_keys(b, causal, window)
+    assert bool(few.any())
+    ref.check_attention(o, lse, (ro, rl, ob + torch.where(few, 2.0 ** -16, 2.0 ** -8)[:, None, None] * sizes, lb))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_keys_stay_within_the_library_bound(d):
+    # outputs of 2 to 4, whose own rounding takes 2^-7 of the 1e-2, from values that lie far apart
+    b = Batch(26, [1] * 200, [2] * 200, 32, 8, d, 16, BF16)
+    g = torch.Generator(device="cuda").manual_seed(27)
+    b.v[:, :, 0] = 3.5 + 0.5 * torch.rand(b.v[:, :, 0].shape, device="cuda", generator=g).to(BF16)
+    b.v[:, :, 1] = torch.rand(b.v[:, :, 1].shape, device="cuda", generator=g).to(BF16)
+    o, lse = b.run()
+    assert float((o.double() - b.ref()[0]).abs().max()) <= 1e-2
+
+
+@pytest.mark.parametrize("dt,d,page", TYPES[:4])
+@pytest.mark.parametrize("new,kv", [([1, 7, 130], [2000, 60, 700]), ([900], [4000]), ([1] * 40, [300] * 40)])
+def test_a_call_repeats_itself(dt, d, page, new, kv):
+    b = Batch(28, new, kv, 16, 4, d, page, dt)
+    first = b.run()
+    for _ in range(4):
+        again = b.run()
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 def test_refusals():
     b = Batch(17, [4], [40], 8, 2, 64, 16, F32)
     args = (b.k, b.v, i32(b.kv), i32(b.pp), b.px, i32(b.qo))
