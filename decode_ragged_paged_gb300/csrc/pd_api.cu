@@ -701,7 +701,8 @@ ChunkParams chunk_params(const pd_attn_desc* d, const pd_batch* b, int32_t windo
 size_t pd_attn_chunk_workspace_size(const pd_attn_desc* desc, const pd_batch* batch) {
   if (check_attn(desc, batch, false) != PD_OK) return 0;
   ChunkParams p = chunk_params(desc, batch, -1, 0);
-  return chunk_layout(p, desc->kv_dtype).total;
+  const size_t total = chunk_layout(p, desc->kv_dtype).total;
+  return chunk_fits(p) ? total : 0;
 }
 
 int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t window_left, int64_t q_stride,
@@ -719,6 +720,7 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(workspace))
     return PD_ERR_INVALID_ARG;
   const ChunkLayout L = chunk_layout(p, desc->kv_dtype);
+  if (!chunk_fits(p)) return PD_ERR_UNSUPPORTED;
   if (workspace_bytes < L.total) return PD_ERR_WORKSPACE;
   p.q = q;
   p.k_pool = k_pool;

@@ -663,7 +663,8 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   p.item_heads = p.hq / p.tile_heads;
   const int64_t by_len = (int64_t)p.batch * (((int64_t)p.max_qo_len + p.item_tokens - 1) / p.item_tokens);
   const int64_t by_rows = (int64_t)p.total_qo / p.item_tokens + p.batch;
-  p.max_blocks = (int32_t)(by_len < by_rows ? by_len : by_rows);
+  const int64_t blocks = by_len < by_rows ? by_len : by_rows;
+  p.max_blocks = (int32_t)(blocks < 0x7fffffff ? blocks : 0x7fffffff);  // (chunk_fits refuses the bound)
   ChunkLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -696,6 +697,15 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   p.grid = p.uncut ? (int32_t)items : p.max_parts;
   p.self_plan = p.batch <= kSelfBatch && (p.uncut || (p.max_blocks <= kSelfBlocks && p.max_parts <= kSelfParts));
   return L;
+}
+
+// Where whole items are dealt out, all rounds of G but the last are: what they leave the
+// line is less than 2 G items and one block's heads. Where they are not, the line has
+// less than 2^31 units, or they would be.
+bool chunk_fits(const ChunkParams& p) {
+  const int64_t most = ((int64_t)p.max_kv_len + kChunkKeys - 1) / kChunkKeys + p.item_cost;  // units of an item
+  return (2 * (int64_t)p.max_parts + p.item_heads) * most <= 0x7fffffffLL &&
+         (int64_t)p.max_blocks * p.item_heads <= 0x7fffffffLL - p.max_parts;
 }
 
 namespace {

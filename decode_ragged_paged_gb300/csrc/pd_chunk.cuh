@@ -12,7 +12,8 @@
 // several times more items than CTAs, the first `whole` blocks are dealt out
 // item by item, block by block with its heads: the CTAs then stream the same
 // keys at the same time, out of L2. What is left makes the line, cut so that
-// every CTA's whole items and part come to the same.
+// every CTA's whole items and part come to the same. More work than 32 bits of
+// units is dealt out like that too, so that the line stays inside them.
 #pragma once
 
 #include "pd_common.cuh"
@@ -111,8 +112,8 @@ __device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) 
   return (warp > 0 ? before : 0) + x - v;
 }
 
-// What a CTA has to know of the line. Units are counted in 32 bits: 2^31 tiles of
-// 64 keys and 256 rows are hours of work.
+// What a CTA has to know of the line. Its units are counted in 32 bits (chunk_fits), those of
+// all blocks before one (pre) modulo 2^32: only differences inside the line are used.
 struct ChunkLine {
   int rem, head, base;  // units of the line, of one head of it, and of one head before it
   int parts, whole;     // parts of the line; blocks dealt out whole before it
@@ -120,6 +121,9 @@ struct ChunkLine {
   const int32_t* first; // first block of every request
   const int32_t* pre;   // units of one head before every block
   const int32_t* pos;   // where every part starts
+
+  // Units of one head of the line before its block b.
+  __device__ __forceinline__ int before(int b) const { return (int)((uint32_t)pre[b] - (uint32_t)base); }
 
   // First unit of part c. The shares come to the line's units, or (rounding, CTAs
   // with too much already) to nearly that, and are stretched to it here.
@@ -171,28 +175,27 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
       units = block_units(p, p.qo_indptr[lo + 1] - p.qo_indptr[lo], p.kv_len[lo], b - first[lo]);
     }
     const int at = scan_exclusive<NT>(units, warp_tot, total);
-    if (b < blocks) pre[b] = (int)sum + at;
+    if (b < blocks) pre[b] = (int)((uint32_t)sum + (uint32_t)at);
     sum += total;
-    over = sum * p.item_heads > 0x7fffffffLL;
   }
-  carry = (int)sum;
-  if (over || carry == 0) {
-    // more blocks than rows allow (requests whose rows overlap), or more work than a call takes: none is worked on
+  if (over || sum == 0) {
+    // more blocks than rows allow (requests whose rows overlap): none is worked on
     if (tid == 0 && over) report(p.status, PD_DEV_BAD_INDPTR);
     sync_of<NT>();
     return line;
   }
-  if (tid == 0) pre[blocks] = carry;
+  if (tid == 0) pre[blocks] = (int)(uint32_t)sum;
   sync_of<NT>();
-  const int G = p.max_parts, H = p.item_heads, units = carry * H;
+  const int G = p.max_parts, H = p.item_heads;
+  const long long units = sum * H;
   // whole items: all rounds but the last, whose items the line evens out
-  if (blocks >= 2 * p.batch && (int64_t)blocks * H >= 3 * (int64_t)G)
+  if ((blocks >= 2 * p.batch && (int64_t)blocks * H >= 3 * (int64_t)G) || units > 0x7fffffffLL)
     line.whole = (int)(((int64_t)blocks * H / G - 1) * G / H);
   line.base = pre[line.whole];
-  line.head = carry - line.base;
+  line.head = line.before(blocks);
   line.rem = line.head * H;
   if (line.whole == 0) {
-    line.parts = min(G, (units + p.min_units - 1) / p.min_units);  // at least so many units a part
+    line.parts = (int)min((long long)G, (units + p.min_units - 1) / p.min_units);  // at least so many units a part
     const int each = line.rem / line.parts, left = line.rem - each * line.parts;
     for (int c = tid; c <= line.parts; c += NT) pos[c] = each * c + left * c / line.parts;
   } else {
@@ -202,8 +205,9 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
       const int c = c0 + tid;
       int share = 0;
       if (c < G) {
-        for (int i = c; i < line.whole * H; i += G) share += pre[i / H + 1] - pre[i / H];
-        share = max(units / G - share, 0);
+        long long has = 0;  // units of this CTA's whole items
+        for (int i = c; i < line.whole * H; i += G) has += (uint32_t)pre[i / H + 1] - (uint32_t)pre[i / H];
+        share = (int)min(max(units / G - has, 0LL), (long long)(0x7fffffff / G));  // (a sum of 32 bits)
       }
       const int at = carry + scan_exclusive<NT>(share, warp_tot, total);
       if (c < G) pos[c] = at;
@@ -285,13 +289,13 @@ struct ChunkWalk {
     here.h = at / line.head;
     int lo = line.whole, hi = line.first[p.batch], start = 0;
     if (lane < 2) {
-      const int rest = at - here.h * line.head + line.base;
+      const int rest = at - here.h * line.head;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (line.pre[mid] <= rest) lo = mid;
+        if (line.before(mid) <= rest) lo = mid;
         else hi = mid;
       }
-      start = here.h * line.head + line.pre[lo] - line.base;
+      start = here.h * line.head + line.before(lo);
     } else if (lane == 3) {
       lo = min(c, max(whole_items - 1, 0)) / p.item_heads;
       here.h = c % p.item_heads;

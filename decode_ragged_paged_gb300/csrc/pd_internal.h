@@ -235,8 +235,9 @@ int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStre
 // Workspace (offsets 256-byte aligned):
 //   hdr        int32[32]        the line's {units, units of a head, units before it, parts, whole blocks, shares}
 //   req_first  int32[B + 1]     first block of every request
-//   pre        int32[max_blocks + 1]  units of one head before every block
-//   pos        int32[parts + 1]  first unit of every part of the line
+//   pre        int32[max_blocks + 1]  units of one head before every block, modulo 2^32
+//   pos        int32[parts + 1]  where every part of the line starts: its first unit, or
+//              with whole items before the line, the shares of the parts before it
 //   cuts       int4[parts]       the item that a part begins and does not end
 //   part_lse   float[2 * parts][rows]     log2-sum-exp2 of a cut item's part
 //   part_o     float[2 * parts][rows][D]  its normalised output
@@ -279,6 +280,8 @@ struct ChunkLayout {
 };
 // Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
+// Whether 32 bits number the items and count the line's units, whatever the lengths are.
+bool chunk_fits(const ChunkParams& p);
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);

@@ -279,7 +279,8 @@ PD_API int pd_attn_mixed_split(const pd_attn_desc *desc, const pd_batch *batch, 
  *   workspace: pd_attn_chunk_workspace_size(desc, batch) bytes
  * batch->qo_indptr is required; rows of q past qo_indptr[B] are not used and
  * their o and lse are left as they were. Supported: fp32 and bf16, D 64 or 128,
- * any page size, any group, max_kv_len up to 2^24 (PD_ERR_UNSUPPORTED). bf16 with
+ * any page size, any group, max_kv_len up to 2^24 (fewer with more than 4096 query
+ * heads), fewer than 2^31 pairs of a token block and a head (PD_ERR_UNSUPPORTED). bf16 with
  * pages of a multiple of 8 slots runs on the tensor cores: the softmax weights enter
  * the product with V as bf16, for tokens that see fewer than 128 keys together with
  * what that leaves of them. Other calls run in fp32 on the CUDA cores. A workspace

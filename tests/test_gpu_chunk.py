@@ -325,6 +325,40 @@ def test_cache_past_32_bit_offsets():
         ref.check_attention(o, lse, ref.attention(q, kk, vv, [0, 9], [300], [0, 5], px, layout=layout))
 
 
+def test_more_work_than_32_bits_of_units():
+    """16384 single tokens over 2^20 keys each, 8 heads: 2^31 units and 262144 more. All requests share one list of pages. Keys count by their position (V is a ramp), so that any that
+    are left out show. Bounds: a row's sum takes 2^14 additions of a tile's weights in fp32, its
+    output 2^16 of 16 keys each in the tensor cores (a truncating adder, 2^-23 each)."""
+    requests, hq, d, page, n = 16384, 8, 64, 4096, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(29)
+    k = torch.randn(n // page, hq, page, d, device="cuda", generator=g).to(BF16)
+    ramp = torch.arange(n, device="cuda", dtype=torch.float32).view(-1, 1, page, 1) / n
+    v = (ramp * (1 + torch.arange(d, device="cuda") / d)).expand(-1, hq, -1, -1).to(BF16).contiguous()
+    q = torch.randn(requests, hq, d, device="cuda", generator=g).to(BF16)
+    px = torch.arange(n // page, device="cuda", dtype=torch.int32).repeat(requests)
+    pp = torch.arange(requests + 1, device="cuda", dtype=torch.int32) * (n // page)
+    qo, kv = torch.arange(requests + 1, device="cuda", dtype=torch.int32), i32([n] * requests)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full_like(q, float("nan"))
+    lse = torch.full((requests, hq), float("nan"), device="cuda")
+    pd.pd_attn_chunk(q, k, v, kv, pp, px, qo, max_qo_len=1, max_kv_len=n, o=o, lse=lse, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
+    scale = d ** -0.5
+    at = torch.cat([torch.tensor([0, 1, requests - 1]), torch.randint(requests, (5,))]).cuda()
+    for h in (0, 3, hq - 1):
+        kh, vh, qh = k[:, h].reshape(n, d).double(), v[:, h].reshape(n, d).double(), q[at, h].double()
+        s = qh @ kh.T * scale
+        es = 4 * d * 2.0 ** -24 * scale * (qh.abs() @ kh.abs().T).amax(-1)
+        want = torch.logsumexp(s, -1)
+        out = torch.softmax(s, -1) @ vh  # (and of |V|, as no value is negative)
+        rel = 2 * es + 2.0 ** -20 + 2.0 ** -10
+        assert bool(((lse[at, h].double() - want).abs() <= rel + 2.0 ** -21 * (1 + want.abs())).all())
+        lim = ((rel + 2.0 ** -8 + 2.0 ** -7)[:, None] + 2.0 ** -8) * out
+        assert bool(((o[at, h].double() - out).abs() <= lim).all())
+
+
 def few_keys(b, causal, window):
     """Which rows see fewer than 128 keys."""
     n = torch.cat([torch.full((x,), y) for x, y in zip(b.new, b.kv)])

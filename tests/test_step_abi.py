@@ -67,6 +67,21 @@ def test_chunk_empty_and_workspace(lib):
     assert size(_attn(), _batch(max_kv_len=1 << 20)) == n
 
 
+def test_chunk_refuses_more_work_than_it_counts(lib):
+    # the line holds up to about two items a CTA and a block's heads, of all their key tiles, in 32 bits
+    many = dict(num_qo_heads=1 << 15, num_kv_heads=1 << 15)
+    assert _chunk(lib, _attn(**many), _batch(max_kv_len=1 << 24), ws_bytes=64) == pd.PD_ERR_UNSUPPORTED
+    assert _chunk(lib, _attn(**many), _batch(max_kv_len=1 << 20), ws_bytes=64) == pd.PD_ERR_WORKSPACE
+    # more items than 32 bits number
+    assert _chunk(lib, b=_batch(batch_size=2 ** 31 - 1, total_qo=2 ** 31 - 1, max_qo_len=2 ** 20),
+                  ws_bytes=64) == pd.PD_ERR_UNSUPPORTED
+    big = _batch(batch_size=2 ** 31 - 1, total_qo=2 ** 31 - 1, max_qo_len=2 ** 20)
+    assert lib.pd_attn_chunk_workspace_size(ctypes.byref(_attn()), ctypes.byref(big)) == 0
+    # a decode of 2^16 requests of any length is within both
+    assert _chunk(lib, b=_batch(batch_size=1 << 16, total_qo=1 << 16, max_qo_len=1, max_kv_len=1 << 24),
+                  ws_bytes=64) == pd.PD_ERR_WORKSPACE
+
+
 def _tables(lib, rows=None, **kw):
     d = dict(batch_size=4, page_size=16, num_pages=64, table_rows=8, table_cols=8, total_qo=16, max_page_indices=32,
              free_capacity=10)
