@@ -24,7 +24,7 @@ constexpr int kPlanThreads = 1024;
 // ------------------------------------------------------------------- plan
 // One CTA makes the line of a batch that is too large for every CTA to make its own.
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p) {
-  __shared__ int warp_tot[kPlanThreads / 32];
+  __shared__ long long warp_tot[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait_primary();
   const ChunkLine line = plan_line<kPlanThreads>(p, p.req_first, p.pre, p.pos, warp_tot);

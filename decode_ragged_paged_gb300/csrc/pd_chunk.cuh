@@ -16,6 +16,8 @@
 // units is dealt out like that too, so that the line stays inside them.
 #pragma once
 
+#include <type_traits>
+
 #include "pd_common.cuh"
 #include "pd_internal.h"
 
@@ -85,13 +87,13 @@ __device__ __forceinline__ void sync_of() {
 }
 
 // Exclusive scan over them, and the total; warp_tot: NT / 32 words of shared memory.
-template <int NT>
-__device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) {
+template <int NT, typename V>
+__device__ __forceinline__ V scan_exclusive(V v, V* warp_tot, V& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  V x = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    const V y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
   if constexpr (NT == 32) {
@@ -101,14 +103,14 @@ __device__ __forceinline__ int scan_exclusive(int v, int* warp_tot, int& total) 
   __syncthreads();  // the totals of an earlier scan have been read
   if (lane == 31) warp_tot[warp] = x;
   __syncthreads();
-  int w = lane < NT / 32 ? warp_tot[lane] : 0;
+  V w = lane < NT / 32 ? warp_tot[lane] : 0;
 #pragma unroll
   for (int d = 1; d < NT / 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, d);
+    const V y = __shfl_up_sync(0xffffffffu, w, d);
     if (lane >= d) w += y;
   }
   total = __shfl_sync(0xffffffffu, w, NT / 32 - 1);
-  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  const V before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   return (warp > 0 ? before : 0) + x - v;
 }
 
@@ -139,22 +141,24 @@ struct ChunkLine {
 // word gets one value only, as several warps may make the same line in the same
 // place, one still writing what another reads. Ends with a barrier.
 template <int NT>
-__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pre, int32_t* pos, int* warp_tot) {
+__device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pre, int32_t* pos, long long* warp_tot) {
   const int tid = threadIdx.x & (NT - 1);
   ChunkLine line{0, 1, 0, 0, 0, 0, first, pre, pos};
-  // kChunkMaxKeys and the rows that fit a GPU keep the sums of NT requests or blocks inside 32 bits
-  int carry = 0, total;
+  // Blocks are summed in 64 bits: 1024 requests with the same rows (an indptr that falls in between) may have
+  // more than 2^31. (The 32 requests of a warp have no more than kSelfBlocks or max_parts each.)
+  using Count = std::conditional_t<NT == 32, int, long long>;
+  Count carry = 0, total;
   bool over = false;
   for (int r0 = 0; r0 < p.batch; r0 += NT) {
     const int r = r0 + tid;
-    const int n = r < p.batch ? chunk_request(p, r, true).blocks : 0;
-    const int at = carry + scan_exclusive<NT>(n, warp_tot, total);
-    if (r < p.batch) first[r] = min(at, p.max_blocks);
+    const Count n = r < p.batch ? chunk_request(p, r, true).blocks : 0;
+    const Count at = carry + scan_exclusive<NT>(n, reinterpret_cast<Count*>(warp_tot), total);
+    if (r < p.batch) first[r] = (int)min(at, (Count)p.max_blocks);
     carry += total;
     over = over || carry > p.max_blocks;
     if (over) break;
   }
-  const int blocks = carry;
+  const int blocks = (int)carry;  // (unless over)
   if (!over && tid == 0) first[p.batch] = blocks;
   sync_of<NT>();
   if (p.uncut && !over) {
@@ -174,9 +178,10 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
       }
       units = block_units(p, p.qo_indptr[lo + 1] - p.qo_indptr[lo], p.kv_len[lo], b - first[lo]);
     }
-    const int at = scan_exclusive<NT>(units, warp_tot, total);
+    int tiles;  // kChunkMaxKeys keeps the sum of NT blocks inside 32 bits
+    const int at = scan_exclusive<NT>(units, reinterpret_cast<int*>(warp_tot), tiles);
     if (b < blocks) pre[b] = (int)((uint32_t)sum + (uint32_t)at);
-    sum += total;
+    sum += tiles;
   }
   if (over || sum == 0) {
     // more blocks than rows allow (requests whose rows overlap): none is worked on
@@ -200,7 +205,7 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
     for (int c = tid; c <= line.parts; c += NT) pos[c] = each * c + left * c / line.parts;
   } else {
     line.parts = G;
-    carry = 0;
+    int shares = 0;
     for (int c0 = 0; c0 < G; c0 += NT) {
       const int c = c0 + tid;
       int share = 0;
@@ -209,11 +214,12 @@ __device__ ChunkLine plan_line(const ChunkParams& p, int32_t* first, int32_t* pr
         for (int i = c; i < line.whole * H; i += G) has += (uint32_t)pre[i / H + 1] - (uint32_t)pre[i / H];
         share = (int)min(max(units / G - has, 0LL), (long long)(0x7fffffff / G));  // (a sum of 32 bits)
       }
-      const int at = carry + scan_exclusive<NT>(share, warp_tot, total);
+      int some;
+      const int at = shares + scan_exclusive<NT>(share, reinterpret_cast<int*>(warp_tot), some);
       if (c < G) pos[c] = at;
-      carry += total;
+      shares += some;
     }
-    line.shares = max(carry, 1);  // (no shares: every part but the last starts at 0)
+    line.shares = max(shares, 1);  // (no shares: every part but the last starts at 0)
   }
   sync_of<NT>();
   return line;

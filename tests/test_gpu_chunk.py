@@ -1,5 +1,6 @@
 """pd_attn_chunk against fp64 attention: every output within its own bound (step_ref.attention), over
 chunk lengths, cache lengths, groups, pages, layouts, windows and types."""
+import ctypes
 import random
 
 import pytest
@@ -326,9 +327,10 @@ def test_cache_past_32_bit_offsets():
 
 
 def test_more_work_than_32_bits_of_units():
-    """16384 single tokens over 2^20 keys each, 8 heads: 2^31 units and 262144 more. All requests share one list of pages. Keys count by their position (V is a ramp), so that any that
-    are left out show. Bounds: a row's sum takes 2^14 additions of a tile's weights in fp32, its
-    output 2^16 of 16 keys each in the tensor cores (a truncating adder, 2^-23 each)."""
+    """16384 single tokens over 2^20 keys each, 8 heads: 2^31 units and 262144 more. All requests share
+    one list of pages. Keys count by their position (V is a ramp), so that any that are left out show.
+    Bounds: a row's sum takes 2^14 additions of a tile's weights in fp32, its output 2^16 of 16 keys
+    each in the tensor cores (a truncating adder, 2^-23 each)."""
     requests, hq, d, page, n = 16384, 8, 64, 4096, 1 << 20
     g = torch.Generator(device="cuda").manual_seed(29)
     k = torch.randn(n // page, hq, page, d, device="cuda", generator=g).to(BF16)
@@ -357,6 +359,29 @@ def test_more_work_than_32_bits_of_units():
         assert bool(((lse[at, h].double() - want).abs() <= rel + 2.0 ** -21 * (1 + want.abs())).all())
         lim = ((rel + 2.0 ** -8 + 2.0 ** -7)[:, None] + 2.0 ** -8) * out
         assert bool(((o[at, h].double() - out).abs() <= lim).all())
+
+
+def test_requests_on_the_same_rows_are_refused():
+    """512 requests that all claim the same 2^23 rows (the indptr falls back to 0 in between), of a
+    block each, and one of 5 rows: 2^32 + 5 blocks. The plan refuses the batch before any row is
+    read, so q need not have them."""
+    rows, B = 1 << 23, 1025
+    q = torch.zeros(8, 64, 64, device="cuda")
+    k = torch.zeros(1, 1, 16, 64, device="cuda")
+    o = torch.full_like(q, 3.0)
+    qo = i32([0, rows] * 512 + [0, 5])
+    kv, pp = i32([1] * B), torch.arange(B + 1, device="cuda", dtype=torch.int32)
+    px = torch.zeros(B, device="cuda", dtype=torch.int32)
+    lib = pd.load_library()
+    desc = pd.make_attn_desc(q, k)
+    batch = pd.make_batch(kv, pp, px, 1, qo_indptr=qo, total_qo=rows, max_qo_len=rows, max_kv_len=1)
+    size = lib.pd_attn_chunk_workspace_size(ctypes.byref(desc), ctypes.byref(batch))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    status = i32([0])
+    assert lib.pd_attn_chunk(ctypes.byref(desc), ctypes.byref(batch), -1, 0, q.data_ptr(), k.data_ptr(), k.data_ptr(),
+                             o.data_ptr(), None, ws.data_ptr(), size, status.data_ptr(), None) == 0
+    torch.cuda.synchronize()
+    assert int(status.item()) == 1 and bool((o == 3).all())
 
 
 def few_keys(b, causal, window):
