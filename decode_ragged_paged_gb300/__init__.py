@@ -21,6 +21,7 @@ Tensor layouts (see ``include/pd.h``):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -237,12 +238,33 @@ def make_attn_desc(q, k_pool, *, causal=True, sm_scale=None, o_dtype=None, layou
                     int(bool(causal)), float(sm_scale) if sm_scale else 0.0)
 
 
+def _on_stream(stream, device):
+    """Makes a call's stream the current one (None: it is)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _longest(stream, *, kv_len=None, indptr=None) -> int:
+    """A call's longest request, read back on the call's stream, behind what writes the lengths there."""
+    t = kv_len if indptr is None else indptr
+    if t is None or t.numel() < (1 if indptr is None else 2):
+        return 0
+    if not t.is_cuda:
+        raise PdError("lengths must be CUDA tensors")
+    with _on_stream(stream, t.device):
+        return int((t if indptr is None else t[1:] - t[:-1]).max().item())
+
+
 def make_batch(kv_len, page_indptr, page_indices, num_pages, *, qo_indptr=None, total_qo=0,
-               max_qo_len=1, max_kv_len=None) -> Batch:
+               max_qo_len=1, max_kv_len=None, stream=None) -> Batch:
     _i32(kv_len, "kv_len"), _i32(page_indptr, "page_indptr"), _i32(page_indices, "page_indices")
     _i32(qo_indptr, "qo_indptr")
     if max_kv_len is None:  # convenience path: reads the lengths back (synchronises)
-        max_kv_len = int(kv_len.max().item()) if kv_len.numel() else 0
+        max_kv_len = _longest(stream, kv_len=kv_len)
     return Batch(kv_len.numel(), _ptr(qo_indptr), _ptr(kv_len), _ptr(page_indptr), _ptr(page_indices),
                  int(num_pages), int(total_qo), int(max_qo_len), int(max_kv_len))
 
@@ -259,7 +281,7 @@ def _attn(name, kind, q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_i
             raise PdError(f"{n} must be a contiguous CUDA tensor")
     desc = make_attn_desc(q, k_pool, causal=causal, sm_scale=sm_scale, o_dtype=o_dtype, layout=layout)
     batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr,
-                       total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len)
+                       total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len, stream=stream)
     if o is None:
         o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
     if lse is True:
@@ -296,7 +318,7 @@ def pd_attn_prefill(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_ind
                     workspace=None, dev_status=None, stream=None, layout="HND"):
     """Prefill attention over ragged query rows (qo_len <= kv_len). Returns (o, lse)."""
     if max_qo_len is None:
-        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if qo_indptr.numel() > 1 else 0
+        max_qo_len = _longest(stream, indptr=qo_indptr)
     return _attn("pd_attn_prefill", PD_KIND_PREFILL, q, k_pool, v_pool, kv_len, page_indptr, page_indices,
                  qo_indptr, causal=causal, sm_scale=sm_scale, max_qo_len=max_qo_len, max_kv_len=max_kv_len,
                  o=o, lse=lse, o_dtype=o_dtype, workspace=workspace, dev_status=dev_status, stream=stream,
@@ -308,7 +330,7 @@ def pd_attn_mixed(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
                   workspace=None, dev_status=None, stream=None, layout="HND"):
     """Mixed prefill + decode batch in one launch. Returns (o, lse)."""
     if max_qo_len is None:
-        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if qo_indptr.numel() > 1 else 0
+        max_qo_len = _longest(stream, indptr=qo_indptr)
     return _attn("pd_attn_mixed", PD_KIND_MIXED, q, k_pool, v_pool, kv_len, page_indptr, page_indices,
                  qo_indptr, causal=causal, sm_scale=sm_scale, max_qo_len=max_qo_len, max_kv_len=max_kv_len,
                  o=o, lse=lse, o_dtype=o_dtype, workspace=workspace, dev_status=dev_status, stream=stream,
@@ -325,10 +347,10 @@ def pd_attn_mixed_split(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo
         if not t.is_cuda or not t.is_contiguous():
             raise PdError(f"{n} must be a contiguous CUDA tensor")
     if max_qo_len is None:
-        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if qo_indptr.numel() > 1 else 0
+        max_qo_len = _longest(stream, indptr=qo_indptr)
     desc = make_attn_desc(q, k_pool, causal=causal, sm_scale=sm_scale, o_dtype=o_dtype, layout=layout)
     batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr,
-                       total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len)
+                       total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len, stream=stream)
     if o is None:
         o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
     if lse is True:
@@ -386,10 +408,7 @@ def _empty(stream, shape, dtype, device):
     use by, or be handed on to, that stream's own work."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)
-        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -427,9 +446,9 @@ def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
     elif lse is False:
         lse = None
     if max_qo_len is None:
-        max_qo_len = int((qo_indptr[1:] - qo_indptr[:-1]).max().item()) if qo_indptr.numel() > 1 else 0
+        max_qo_len = _longest(stream, indptr=qo_indptr)
     if max_kv_len is None:
-        max_kv_len = int(kv_len.max().item()) if kv_len.numel() else 0
+        max_kv_len = _longest(stream, kv_len=kv_len)
     head = (q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, o, lse)
     tail = (dev_status, causal, window_left, sm_scale or None, max_qo_len, max_kv_len, _layout_code(layout))
     rc = _bound("attn_chunk", stream, *head, workspace, *tail)
@@ -481,7 +500,7 @@ def pd_slot_map(qo_indptr, kv_len, page_indptr, page_indices, *, page_size, num_
     _vector(positions, "positions", torch.int32, total_qo)
     _vector(slot_map, "slot_map", torch.int64, total_qo)
     batch = make_batch(kv_len, page_indptr, page_indices, num_pages, qo_indptr=qo_indptr, total_qo=total_qo,
-                       max_kv_len=max_kv_len)
+                       max_kv_len=max_kv_len, stream=stream)
     _launch(device, "pd_slot_map", lib.pd_slot_map, ctypes.byref(batch), int(page_size), positions.data_ptr(),
             slot_map.data_ptr(), _ptr(dev_status), _stream(stream, device))
     return positions, slot_map
@@ -532,7 +551,7 @@ def pd_mla_decode(q, kv_pool, kv_len, page_indptr, page_indices, *, kv_lora_rank
         raise PdError("q and kv_pool rows differ in width")
     desc = MlaDesc(hq, int(kv_lora_rank), w - int(kv_lora_rank), page, _dtype_code(q.dtype),
                    _dtype_code(o_dtype if o_dtype is not None else q.dtype), float(sm_scale) if sm_scale else 0.0)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, total_qo=B, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, total_qo=B, max_kv_len=max_kv_len, stream=stream)
     if o is None:
         o = torch.empty((B, hq, int(kv_lora_rank)), dtype=o_dtype if o_dtype is not None else q.dtype,
                         device=q.device)
@@ -568,7 +587,7 @@ def pd_kv_append(k_new, v_new, k_pool, v_pool, new_indptr, kv_len, page_indptr, 
     lib = load_library()
     desc = _kv_desc(k_pool, layout=layout)
     batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=_i32(new_indptr, "new_indptr"),
-                       total_qo=k_new.shape[0], max_kv_len=max_kv_len)
+                       total_qo=k_new.shape[0], max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_append(ctypes.byref(desc), ctypes.byref(batch), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
                           _ptr(v_pool), _ptr(dev_status), _stream(stream))
     _check(rc, "pd_kv_append")
@@ -586,7 +605,7 @@ def pd_kv_pack(k_pools, v_pools, kv_len, page_indptr, page_indices, dst, dst_off
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_pack(ctypes.byref(desc), ctypes.byref(batch), _ptr(k_pools), _ptr(v_pools), _ptr(dst),
                         dst.numel() * dst.element_size(), _ptr(dst_offsets), _ptr(dev_status), _stream(stream))
     _check(rc, "pd_kv_pack")
@@ -598,7 +617,7 @@ def pd_kv_unpack(src, src_offsets, k_pools, v_pools, kv_len, page_indptr, page_i
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_unpack(ctypes.byref(desc), ctypes.byref(batch), _ptr(src), src.numel() * src.element_size(),
                           _ptr(src_offsets), _ptr(k_pools), _ptr(v_pools), _ptr(dev_status), _stream(stream))
     _check(rc, "pd_kv_unpack")
@@ -610,7 +629,7 @@ def pd_kv_pack_heads(k_pools, v_pools, kv_len, page_indptr, page_indices, dst, d
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_pack_heads(ctypes.byref(desc), ctypes.byref(batch), int(head_begin), int(head_count),
                               _ptr(k_pools), _ptr(v_pools), _ptr(dst), dst.numel() * dst.element_size(),
                               _ptr(dst_offsets), _ptr(dev_status), _stream(stream))
@@ -623,7 +642,7 @@ def pd_kv_unpack_heads(src, src_offsets, k_pools, v_pools, kv_len, page_indptr, 
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_unpack_heads(ctypes.byref(desc), ctypes.byref(batch), int(head_begin), int(head_count),
                                 _ptr(src), src.numel() * src.element_size(), _ptr(src_offsets), _ptr(k_pools),
                                 _ptr(v_pools), _ptr(dev_status), _stream(stream))
@@ -636,7 +655,7 @@ def pd_kv_pack_layers(k_pools, v_pools, kv_len, page_indptr, page_indices, dst, 
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     rc = lib.pd_kv_pack_layers(ctypes.byref(desc), ctypes.byref(batch), int(layer_begin), int(layer_count),
                                _ptr(k_pools), _ptr(v_pools), _ptr(dst), dst.numel() * dst.element_size(),
                                _ptr(dst_offsets), _ptr(dev_status), _stream(stream))
@@ -671,7 +690,7 @@ def pd_messenger_start_pack(host_word, k_pools, v_pools, kv_len, page_indptr, pa
     lib = load_library()
     L, stride, num_pages = _layers(k_pools)
     desc = _kv_desc(k_pools, L, stride, layout)
-    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len)
+    batch = make_batch(kv_len, page_indptr, page_indices, num_pages, max_kv_len=max_kv_len, stream=stream)
     handle = ctypes.c_void_p()
     rc = lib.pd_messenger_start_pack(ctypes.byref(handle), host_word, ctypes.byref(desc), ctypes.byref(batch),
                                      _ptr(k_pools), _ptr(v_pools), _ptr(dst), dst.numel() * dst.element_size(),

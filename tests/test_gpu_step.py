@@ -127,3 +127,45 @@ def test_results_of_a_call_on_another_stream_are_its_own(handle):
         got = call(stream=stream.cuda_stream if handle else stream)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_lengths_are_read_on_the_stream_of_the_call(handle):
+    """Without bounds a call reads the lengths back, and waits for what writes them on its own stream:
+    here they become 60 new tokens of 300 behind a delay, and are one of one before."""
+    q, k, v = (torch.randn(60, 8, 128, device="cuda").bfloat16() for _ in range(3))
+    pool = torch.randn(20, 8, 16, 128, device="cuda").bfloat16()
+    pp, px = i32([0, 19]), torch.arange(20, device="cuda", dtype=torch.int32)
+    kv, qo, late_kv, late_qo = i32([1]), i32([0, 1]), i32([300]), i32([0, 60])
+    mla_q, mla_pool = torch.randn(1, 4, 576, device="cuda").bfloat16(), torch.randn(20, 16, 576, device="cuda").bfloat16()
+    stream = torch.cuda.Stream()
+
+    def append(**kw):
+        pools = [pool.clone(), pool.clone()]
+        pd.pd_kv_append(k, v, *pools, qo, kv, pp, px, **kw)
+        return pools
+
+    calls = [
+        (lambda **kw: pd.pd_attn_chunk(q, pool, pool, kv, pp, px, qo, **kw), True),
+        (lambda **kw: pd.pd_slot_map(qo, kv, pp, px, page_size=16, num_pages=20, total_qo=60, **kw), False),
+        (lambda **kw: pd.pd_attn_prefill(q, pool, pool, kv, pp, px, qo, **kw), True),
+        (lambda **kw: pd.pd_attn_mixed(q, pool, pool, kv, pp, px, qo, **kw), True),
+        (lambda **kw: pd.pd_attn_decode(q[:1], pool, pool, kv, pp, px, **kw), False),
+        (lambda **kw: pd.pd_mla_decode(mla_q, mla_pool, kv, pp, px, **kw), False),
+        (append, False),
+    ]
+    for call, new in calls:
+        status = i32([0])
+        kv.copy_(late_kv), qo.copy_(late_qo)
+        want = call(max_kv_len=300, **(dict(max_qo_len=60) if new else {}))
+        torch.cuda.synchronize()
+        want = [t.clone() for t in want]
+        kv.fill_(1), qo.copy_(i32([0, 1]))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(40_000_000)
+            kv.copy_(late_kv), qo.copy_(late_qo)
+        got = call(stream=stream.cuda_stream if handle else stream, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
