@@ -249,14 +249,15 @@ def _on_stream(stream, device):
 
 
 def _longest(stream, *, kv_len=None, indptr=None) -> int:
-    """A call's longest request, read back on the call's stream, behind what writes the lengths there."""
+    """A call's longest request, read back on the call's stream, behind what writes the lengths there.
+    (Refused requests have a length of -1, and a batch of them a longest of 0.)"""
     t = kv_len if indptr is None else indptr
     if t is None or t.numel() < (1 if indptr is None else 2):
         return 0
     if not t.is_cuda:
         raise PdError("lengths must be CUDA tensors")
     with _on_stream(stream, t.device):
-        return int((t if indptr is None else t[1:] - t[:-1]).max().item())
+        return max(0, int((t if indptr is None else t[1:] - t[:-1]).max().item()))
 
 
 def make_batch(kv_len, page_indptr, page_indices, num_pages, *, qo_indptr=None, total_qo=0,

@@ -169,3 +169,31 @@ def test_lengths_are_read_on_the_stream_of_the_call(handle):
         torch.cuda.synchronize()
         assert int(status.item()) == 0
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_batch_of_refused_requests_is_skipped_without_bounds():
+    """Lengths of -1 (pd_batch_tables: no request could be served) are no bound of -1: the calls skip
+    and report them as they do beside others."""
+    status = i32([0])
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    t = pd.pd_batch_tables(i32([3, 2]), i32([0, 0]), table, page_size=16, num_pages=8, total_qo=5, max_page_indices=8,
+                           free_pages=i32([5, 6]), free_count=i32([0]), free_count_out=i32([0]), dev_status=status)
+    torch.cuda.synchronize()
+    assert t.kv_len.tolist() == [-1, -1] and int(status.item()) == 7
+    q, pool = torch.randn(5, 4, 64, device="cuda"), torch.randn(8, 2, 16, 64, device="cuda")
+    o, lse = torch.full_like(q, 3.0), torch.full((5, 4), 3.0, device="cuda")
+    status.zero_()
+    pd.pd_attn_chunk(q, pool, pool, t.kv_len, t.page_indptr, t.page_indices, t.qo_indptr, o=o, lse=lse,
+                     dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 2 and bool((o == 3).all()) and bool((lse == 3).all())
+    status.zero_()
+    pos, slot = pd.pd_slot_map(t.qo_indptr, t.kv_len, t.page_indptr, t.page_indices, page_size=16, num_pages=8,
+                               total_qo=5, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 2 and pos.tolist() == [0] * 5 and slot.tolist() == [-1] * 5
+    dec = torch.full((2, 4, 64), 3.0, device="cuda")
+    status.zero_()
+    pd.pd_attn_decode(q[:2], pool, pool, t.kv_len, t.page_indptr, t.page_indices, o=dec, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 2 and bool((dec == 3).all())
