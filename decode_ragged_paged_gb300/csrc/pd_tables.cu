@@ -26,6 +26,7 @@
 // a thread waiting for it, 12.1 us, and 6.2 us for the 128).
 #include "pd_common.cuh"
 #include "pd_internal.h"
+#include "pd_launch.cuh"
 
 namespace pd {
 
@@ -89,11 +90,19 @@ __device__ __forceinline__ int owner(const int* pre, int lo, int hi, int at) {
   return lo;
 }
 
-int32_t tables_hash_size(int32_t batch) {
+constexpr int32_t tables_hash_size(int32_t batch) {
   int32_t n = 64;
   while (n < 2 * batch) n <<= 1;
   return n;
 }
+
+constexpr size_t tables_smem(int32_t batch, int32_t hash_size) {
+  return sizeof(int) * ((size_t)5 * batch + 2 + hash_size);
+}
+// What the kernel is allowed, whatever a call's batch takes: a limit of its own for
+// each call would be another thread's as well.
+constexpr size_t kTabSmem = tables_smem(kTablesMaxBatch, tables_hash_size(kTablesMaxBatch));
+static_assert(kTabSmem + kTabWarps * sizeof(Sums) + (kHints + 2) * sizeof(int) <= 232448, "shared memory of a CTA");
 
 }  // namespace
 
@@ -328,19 +337,15 @@ __global__ void __launch_bounds__(256) slot_map_kernel(const SlotMapParams p) {
 // ------------------------------------------------------------------- host
 int launch_batch_tables(TablesParams& p, cudaStream_t stream) {
   p.hash_size = p.rows != nullptr ? tables_hash_size(p.batch) : 0;
-  const size_t smem = sizeof(int) * ((size_t)5 * p.batch + 2 + p.hash_size);
+  const size_t smem = tables_smem(p.batch, p.hash_size);
   // an entry a thread, up to a CTA per SM
   const int64_t entries = (int64_t)p.max_page_indices + p.total_qo;
   int64_t grid = (entries + kTabThreads - 1) / kTabThreads;
   if (grid > device_sm_count()) grid = device_sm_count();
   if (grid < 1) grid = 1;
-  if (smem > 40 * 1024) {
-    if (cudaFuncSetAttribute(batch_tables_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(batch_tables_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess)
-      return PD_ERR_CUDA;
-  }
+  if (allow_smem<batch_tables_kernel<false>>(kTabSmem) != cudaSuccess ||
+      allow_smem<batch_tables_kernel<true>>(kTabSmem) != cudaSuccess)
+    return PD_ERR_CUDA;
   last_kernel() = "batch_tables_kernel";
   profile_begin(stream);
   cudaError_t e = launch_dependent(batch_tables_kernel<false>, dim3((unsigned)grid), kTabThreads, smem, stream, p);

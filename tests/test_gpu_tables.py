@@ -1,5 +1,7 @@
 """pd_batch_tables and pd_slot_map against plain integers: every result equal, entry for entry."""
+import ctypes
 import random
+import threading
 
 import pytest
 import torch
@@ -232,3 +234,45 @@ def test_slot_map_reports_bad_batches():
     assert call([0, 2, 4], [20, 3], [0, 1, 2], [1, 0]) == (3, [-1, -1, 1, 2])          # a page short
     assert call([0, 2, 4], [20, 3], [0, 2, 3], [1, 4, 0]) == (3, [-1, -1, 1, 2])       # id out of range
     assert call([0, 2, 4], [20, 3], [3, 2, 3], [1, 2, 0])[0] == 1
+
+
+def test_threads_with_large_batches_of_different_sizes():
+    """Calls of 8192 and of 2500 requests with a row list from two threads, on a stream each: neither
+    call's shared memory is taken from the other's."""
+    lib = pd.load_library()
+    failed, ran, start = [], [0, 0], threading.Barrier(2)
+
+    def worker(which, B):
+        g = torch.Generator().manual_seed(which)
+        rows = torch.randperm(B, generator=g).int()
+        cached, new = (torch.randint(0, 40, (B,), generator=g, dtype=torch.int32) for _ in range(2))
+        page, cols = 16, 8
+        total, nnz = int(new.sum()), int(((cached + new + page - 1) // page).sum())
+        table = torch.randint(0, 100, (B, cols), generator=g, dtype=torch.int32)
+        dev = [t.cuda() for t in (rows, cached, new, table)]
+        out = [torch.zeros(n, dtype=t, device="cuda") for n, t in ((B + 1, torch.int32), (B, torch.int32),
+               (B + 1, torch.int32), (nnz, torch.int32), (total, torch.int32), (total, torch.int64))]
+        stream = torch.cuda.Stream()
+        desc = pd.TablesDesc(B, page, 100, B, cols, total, nnz, 0)
+        ptrs = [t.data_ptr() for t in dev] + [None] * 3 + [t.data_ptr() for t in out]
+        torch.cuda.synchronize()
+        start.wait()
+        for i in range(3000):
+            rc = lib.pd_batch_tables(ctypes.byref(desc), *ptrs, None, stream.cuda_stream)
+            if rc != 0:
+                failed.append((B, i, rc))
+                break
+            ran[which] += 1
+        stream.synchronize()
+        want = ref.tables(rows.tolist(), cached.tolist(), new.tolist(), table.tolist(), [], 0, page=page, num_pages=100,
+                          total_qo=total, max_page_indices=nnz, pops=False)
+        for name, t in zip(NAMES, out):
+            if t.tolist() != want[name]:
+                failed.append((B, name))
+
+    threads = [threading.Thread(target=worker, args=x) for x in ((0, 8192), (1, 2500))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and ran == [3000, 3000]
