@@ -749,7 +749,7 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
     e = d64 ? launch_dependent(chunk_merge_kernel<64>, grid, kMergeThreads, 0, stream, p)
             : launch_dependent(chunk_merge_kernel<128>, grid, kMergeThreads, 0, stream, p);
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // namespace pd

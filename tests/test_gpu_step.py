@@ -1,5 +1,6 @@
 """A serving step as it is used: tables from lengths, norm + rotation + append into the pages, attention
 of the new tokens, over several steps of a ragged batch; against fp64 attention over a dense cache."""
+import ctypes
 import random
 
 import pytest
@@ -197,3 +198,34 @@ def test_a_batch_of_refused_requests_is_skipped_without_bounds():
     pd.pd_attn_decode(q[:2], pool, pool, t.kv_len, t.page_indptr, t.page_indices, o=dec, dev_status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 2 and bool((dec == 3).all())
+
+
+def _runtime():
+    lib = ctypes.CDLL("libcudart.so.13")  # the one that is loaded
+    lib.cudaStreamCreate.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
+    lib.cudaStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    lib.cudaStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)]
+    lib.cudaStreamDestroy.argtypes = [ctypes.c_void_p]
+    return lib
+
+
+def test_an_error_of_another_call_is_not_the_step_calls():
+    """The thread's last error of something else (here: a device that is not there) is not returned by
+    calls that were launched."""
+    q, pool = torch.randn(5, 4, 64, device="cuda"), torch.randn(8, 2, 16, 64, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(5, 4, device="cuda")
+    ws = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    kv, pp, px, qo = i32([60]), i32([0, 4]), i32([0, 1, 2, 3]), i32([0, 5])
+    pos, slot = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, dtype=torch.int64, device="cuda")
+    want = pd.pd_attn_chunk(q, pool, pool, kv, pp, px, qo, max_qo_len=5, max_kv_len=60)[0].clone()
+    torch.cuda.synchronize()
+    rt = _runtime()
+    try:
+        assert rt.cudaSetDevice(99) != 0 and rt.cudaPeekAtLastError() != 0
+        pd.pd_attn_chunk(q, pool, pool, kv, pp, px, qo, max_qo_len=5, max_kv_len=60, o=o, lse=lse, workspace=ws)
+        pd.pd_slot_map(qo, kv, pp, px, page_size=16, num_pages=8, total_qo=5, max_kv_len=60, positions=pos,
+                       slot_map=slot)
+    finally:
+        rt.cudaGetLastError()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
