@@ -320,7 +320,8 @@ inline void profile_end(cudaStream_t s) {
 // Launches a kernel as a programmatic dependent of the one before it on the
 // stream: its CTAs are placed while that one drains, and wait for it (with
 // pdl_wait_primary(), before they touch global memory). Not while launches are
-// timed alone through the profiling events.
+// timed alone through the profiling events. An error is the caller's to return and is
+// not left behind as the thread's last one, where a later call would find it.
 template <typename... P, typename... A>
 inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                     const A&... args) {
@@ -334,7 +335,9 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = profile_events().start != nullptr ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -19,6 +19,7 @@ inline cudaError_t allow_smem(size_t bytes) {
   if (known && allowed[dev].load(std::memory_order_acquire)) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess && known) allowed[dev].store(true, std::memory_order_release);
+  if (e != cudaSuccess) cudaGetLastError();  // (the caller returns it)
   return e;
 }
 

@@ -229,3 +229,27 @@ def test_an_error_of_another_call_is_not_the_step_calls():
         rt.cudaGetLastError()
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    """A launch on the default stream while another stream is captured is refused by the runtime: the
+    call says so, and the thread's next call starts clean."""
+    lib, rt = pd.load_library(), _runtime()
+    kv, pp, px, qo = i32([60]), i32([0, 4]), i32([0, 1, 2, 3]), i32([0, 5])
+    pos, slot = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, dtype=torch.int64, device="cuda")
+    batch = pd.make_batch(kv, pp, px, 8, qo_indptr=qo, total_qo=5, max_kv_len=60)
+    call = lambda: lib.pd_slot_map(ctypes.byref(batch), 16, pos.data_ptr(), slot.data_ptr(), None, None)  # noqa: E731
+    assert call() == pd.PD_OK
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    try:
+        assert rt.cudaStreamBeginCapture(stream, 0) == 0
+        rc, left = call(), rt.cudaPeekAtLastError()
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+    finally:
+        rt.cudaGetLastError()
+        rt.cudaStreamDestroy(stream)
+    assert rc == pd.PD_ERR_CUDA and left == 0
+    assert call() == pd.PD_OK
+    torch.cuda.synchronize()
