@@ -114,7 +114,7 @@ _lock = threading.Lock()
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libpd.so (raises if it has not been built)."""
-    global _lib, _bind
+    global _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -172,13 +172,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.pd_last_kernel.restype = ctypes.c_char_p
             lib.pd_profile_events.argtypes = [P, P]
             lib.pd_profile_events.restype = ctypes.c_int
-            from . import _pd_bind
-            _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), P).value for n in (
+            _lib = lib
+        return _lib
+
+
+def _load_bind():
+    """The binding module of the step calls (raises if it has not been built)."""
+    global _bind
+    lib = load_library()
+    with _lock:
+        if _bind is None:
+            try:
+                from . import _pd_bind
+            except ImportError as e:
+                raise PdError(f"the binding module _pd_bind cannot be loaded ({e}); run "
+                              "`python -m decode_ragged_paged_gb300.build`") from e
+            _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
                 "pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
                 "pd_attn_chunk_workspace_size")))
             _bind = _pd_bind
-            _lib = lib
-        return _lib
+        return _bind
 
 
 def _check(rc: int, what: str) -> None:
@@ -418,9 +431,7 @@ _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 def _bound(name, stream, *args):
     """Calls a function of the binding module on the tensors' device: None, or (value, pd_status)."""
-    if _lib is None:
-        load_library()
-    fn = getattr(_bind, name)
+    fn = getattr(_bind or _load_bind(), name)
     handle = None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     try:
         device = _current()

@@ -1,6 +1,7 @@
 """CPU checks of the chunk-step entry points (tables, norm and rotation, chunk
 attention): what their host-side checks refuse, before anything touches a GPU."""
 import ctypes
+import sys
 
 import pytest
 
@@ -183,4 +184,22 @@ def test_binding_refuses_host_tensors():
         pd.pd_batch_tables(t, t, t.view(2, 2), page_size=16, num_pages=1, total_qo=4, max_page_indices=4)
     x = torch.zeros(2, 4, 64)
     with pytest.raises(pd.PdError):
+        pd.pd_qk_norm_rope(x, x, None, None, None, None)
+
+
+@pytest.fixture
+def unloaded(lib, monkeypatch):
+    """The package as it is before its first call."""
+    monkeypatch.setattr(pd, "_lib", None)
+    monkeypatch.setattr(pd, "_bind", None)
+    return monkeypatch
+
+
+def test_calls_that_do_not_use_the_binding_module_do_without_it(unloaded):
+    import torch
+    unloaded.setitem(sys.modules, "decode_ragged_paged_gb300._pd_bind", None)  # as if it had not been built
+    unloaded.delattr(pd, "_pd_bind", raising=False)
+    assert pd.load_library().pd_version() >= 100
+    x = torch.zeros(2, 4, 64)
+    with pytest.raises(pd.PdError, match="_pd_bind"):
         pd.pd_qk_norm_rope(x, x, None, None, None, None)
