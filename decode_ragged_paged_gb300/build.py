@@ -2,11 +2,15 @@
 Python binding's extension module with g++.
 
 Each .cu translation unit is compiled in parallel, then linked into
-``decode_ragged_paged_gb300/libpd.so``; ``csrc/pd_bind.cpp`` becomes
-``decode_ragged_paged_gb300/_pd_bind.so``. Re-running is cheap: objects newer
-than their sources and headers are reused.
+``decode_ragged_paged_gb300/libpd.so``; ``csrc/pd_bind.cpp`` becomes the
+package's extension module ``_pd_bind``, named and stamped with the Python and
+the torch that it was compiled against. Re-running is cheap: objects newer than
+their sources and headers are reused.
 
-    python -m decode_ragged_paged_gb300.build [--force] [--verbose-ptxas]
+    python -m decode_ragged_paged_gb300.build [--force] [--verbose-ptxas] [--no-bind]
+
+--no-bind leaves the module out (for programs that call libpd.so from C: it takes
+nvcc alone, and neither Python's nor torch's headers).
 """
 from __future__ import annotations
 
@@ -17,13 +21,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpd.so")
-BIND = os.path.join(HERE, "_pd_bind.so")
+BIND = os.path.join(HERE, "_pd_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -66,12 +71,11 @@ def _host_stamp() -> str:
 
 def _bind() -> None:
     """Compiles the binding module (csrc/pd_bind.cpp) with g++ against torch's headers."""
-    import sysconfig
     import torch
     home = os.path.dirname(torch.__file__)
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DPD_TORCH="{torch.__version__}"',
            "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pd_bind.cpp"), "-o", tmp,
@@ -81,10 +85,30 @@ def _bind() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on pd_bind.cpp:\n{r.stderr}")
     os.replace(tmp, BIND)
+    plain = os.path.join(HERE, "_pd_bind.so")  # (an untagged module, which any Python would load)
+    if os.path.exists(plain):
+        os.remove(plain)
+    with open(BIND_STAMP, "w") as f:
+        f.write(_bind_stamp())
 
 
-def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    """Compile every kernel and the C ABI into libpd.so; returns its path."""
+BIND_STAMP = os.path.join(OBJ, "bind.txt")
+
+
+def _bind_stamp() -> str:
+    """What the module's code takes for granted: it reads torch's and Python's objects in place."""
+    import torch
+    return f"{torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}"
+
+
+def _bind_stale() -> bool:
+    if not os.path.exists(BIND_STAMP) or open(BIND_STAMP).read() != _bind_stamp():
+        return True
+    return _stale(BIND, [os.path.join(CSRC, "pd_bind.cpp"), *_deps()])
+
+
+def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None, bind: bool = True) -> str:
+    """Compile every kernel and the C ABI into libpd.so, and (`bind`) the binding module; returns the library's path."""
     os.makedirs(OBJ, exist_ok=True)
     stamp = os.path.join(OBJ, "host.txt")
     # objects and the library built on another host (another CPU architecture) are never reused
@@ -94,15 +118,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     deps = _deps()
     todo = [s for s in sources
             if force or verbose_ptxas or _stale(os.path.join(OBJ, os.path.basename(s) + ".o"), [s, *deps])]
-    bind = force or _stale(BIND, [os.path.join(CSRC, "pd_bind.cpp"), *deps])
+    bind = bind and (force or _bind_stale())
     logs = []
     if todo or bind:
         with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo) + 1, os.cpu_count() or 4)) as ex:
-            bound = ex.submit(_bind) if bind else None
+            if bind:
+                bound = ex.submit(_bind)
             for obj, log in ex.map(lambda s: _compile(s, verbose_ptxas), todo):
                 logs.append(log)
-            if bound is not None:
-                bound.result()
     objs = [os.path.join(OBJ, os.path.basename(s) + ".o") for s in sources]
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -113,6 +136,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         os.replace(tmp, LIB)
     with open(stamp, "w") as f:
         f.write(_host_stamp())
+    if bind:
+        bound.result()  # after the library, which does not need it
     if verbose_ptxas:
         sys.stderr.write("".join(logs))
     return LIB
@@ -122,8 +147,9 @@ def main() -> None:
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose-ptxas", action="store_true")
+    ap.add_argument("--no-bind", action="store_true")
     a = ap.parse_args()
-    print(build(force=a.force, verbose_ptxas=a.verbose_ptxas))
+    print(build(force=a.force, verbose_ptxas=a.verbose_ptxas, bind=not a.no_bind))
 
 
 if __name__ == "__main__":

@@ -338,4 +338,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pd_bind", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pd_bind() { return PyModule_Create(&g_module); }
+// PD_TORCH: the version of the torch whose headers this was compiled with.
+PyMODINIT_FUNC PyInit__pd_bind() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", PD_TORCH) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -203,3 +203,15 @@ def test_calls_that_do_not_use_the_binding_module_do_without_it(unloaded):
     x = torch.zeros(2, 4, 64)
     with pytest.raises(pd.PdError, match="_pd_bind"):
         pd.pd_qk_norm_rope(x, x, None, None, None, None)
+
+
+def test_the_binding_module_belongs_to_one_torch_and_one_python(unloaded):
+    import sysconfig
+    import torch
+    assert pdbuild.BIND.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and not pdbuild._bind_stale()
+    assert pd._load_bind().__file__ == pdbuild.BIND
+    unloaded.setattr(torch, "__version__", "0.1")
+    assert pdbuild._bind_stale()               # rebuilt by the next build()
+    unloaded.setattr(pd, "_bind", None)
+    with pytest.raises(pd.PdError, match="built for torch"):  # and not used before
+        pd._load_bind()
