@@ -138,6 +138,16 @@ PyObject* done(int device, int status) {
 }
 constexpr int kOtherDevice = 1;  // not a pd_status
 
+// Calls the library without the interpreter's lock, as ctypes does: a launch on a full
+// queue blocks, and no other thread of the program has to wait with it.
+template <typename... P, typename... A>
+int unlocked(int (*call)(P...), A... args) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = call(args...);
+  PyEval_RestoreThread(state);
+  return rc;
+}
+
 // batch_tables(current device, stream or None, new_len, cached_len, block_table, rows, free_pages, free_count,
 //   free_count_out, qo_indptr, kv_len, page_indptr, page_indices, positions, slot_map, dev_status, page_size, num_pages,
 //   total_qo, max_page_indices)
@@ -172,8 +182,8 @@ PyObject* batch_tables(PyObject* const* o) {
   auto* pos = a.vector<int32_t>(o[13], "positions", kI32, d.total_qo);
   auto* slot = a.vector<int64_t>(o[14], "slot_map", kI64, d.total_qo);
   auto* status = a.vector<int32_t>(o[15], "dev_status", kI32, 1, true);
-  return done(a.device, g_batch_tables(&d, row, cached, new_len, block_table, free_pages, count, left, qo, kv, pp, px,
-                                       pos, slot, status, stream_of(o[1])));
+  return done(a.device, unlocked(g_batch_tables, &d, row, cached, new_len, block_table, free_pages, count, left, qo, kv,
+                                 pp, px, pos, slot, status, stream_of(o[1])));
 }
 
 // What both forms of the norm and rotation share: q, k, weights, frequencies and positions at o[2..7].
@@ -218,8 +228,8 @@ PyObject* norm_rope(PyObject* const* o) {
   const at::Tensor *qo = a.tensor(o[8], "q_out"), *ko = a.tensor(o[9], "k_out");
   n.d.q_out_stride = same_rows(*qo, *n.q, "q_out");
   n.d.k_out_stride = same_rows(*ko, *n.k, "k_out");
-  return done(a.device, g_norm_rope(&n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), n.qw, n.kw, n.freq, n.pos,
-                                    qo->data_ptr(), ko->data_ptr(), stream_of(o[1])));
+  return done(a.device, unlocked(g_norm_rope, &n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), n.qw, n.kw, n.freq,
+                                 n.pos, qo->data_ptr(), ko->data_ptr(), stream_of(o[1])));
 }
 
 // norm_rope_append(current device, stream, q, k, q_weight, k_weight, inv_freq, positions, v, slot_map, k_pool, v_pool,
@@ -241,9 +251,9 @@ PyObject* norm_rope_append(PyObject* const* o) {
   const at::Tensor* qo = a.tensor(o[12], "q_out");
   n.d.q_out_stride = same_rows(*qo, *n.q, "q_out");
   auto* status = a.vector<int32_t>(o[13], "dev_status", kI32, 1, true);
-  return done(a.device, g_norm_rope_append(&n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), v->data_ptr(), n.qw, n.kw,
-                                           n.freq, n.pos, slot, qo->data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
-                                           status, stream_of(o[1])));
+  return done(a.device, unlocked(g_norm_rope_append, &n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), v->data_ptr(),
+                                 n.qw, n.kw, n.freq, n.pos, slot, qo->data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
+                                 status, stream_of(o[1])));
 }
 
 // attn_chunk(current device, stream, q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, o, lse, workspace,
@@ -288,8 +298,8 @@ PyObject* attn_chunk(PyObject* const* o) {
   const int32_t window = o[14] == Py_None ? -1 : int32(o[14], "window_left");
   int rc = PD_ERR_WORKSPACE;
   if (ws != nullptr)
-    rc = g_attn_chunk(&d, &b, window, stride, q->data_ptr(), p.k->data_ptr(), p.v->data_ptr(), out->data_ptr(), lse,
-                      ws->data_ptr(), ws->numel() * ws->element_size(), status, stream_of(o[1]));
+    rc = unlocked(g_attn_chunk, &d, &b, window, stride, q->data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
+                  out->data_ptr(), lse, ws->data_ptr(), ws->numel() * ws->element_size(), status, stream_of(o[1]));
   if (rc != PD_ERR_WORKSPACE) return done(a.device, rc);
   return Py_BuildValue("(Ki)", (unsigned long long)g_chunk_workspace(&d, &b), rc);
 }

@@ -2,6 +2,8 @@
 of the new tokens, over several steps of a ragged batch; against fp64 attention over a dense cache."""
 import ctypes
 import random
+import subprocess
+import threading
 
 import pytest
 import torch
@@ -253,3 +255,45 @@ def test_a_refused_launch_leaves_no_error_behind():
     assert rc == pd.PD_ERR_CUDA and left == 0
     assert call() == pd.PD_OK
     torch.cuda.synchronize()
+
+
+def test_other_threads_run_during_a_call(tmp_path):
+    """A call that takes long on the host (here: entry points that sleep, in the library's place) does
+    not keep the interpreter's lock."""
+    src = tmp_path / "slow.c"
+    src.write_text("#include <unistd.h>\nint slow(void) { usleep(300000); return 0; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", tmp_path / "slow.so", src], check=True)
+    slow = ctypes.cast(ctypes.CDLL(str(tmp_path / "slow.so")).slow, ctypes.c_void_p).value
+    x, pool = torch.zeros(4, 8, 64, device="cuda"), torch.zeros(4, 8, 16, 64, device="cuda")
+    n, ids, pos = i32([4]), i32([0, 4]), i32([0, 1, 2, 3])
+    slot, ws = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(64, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(x), torch.empty(4, 8, device="cuda")
+    out = pd.BatchTables(ids.clone(), n.clone(), ids.clone(), pos.clone(), pos.clone(), slot)
+    calls = [
+        lambda: pd.pd_batch_tables(n, n, pos.view(1, 4), page_size=16, num_pages=4, total_qo=4, max_page_indices=4, out=out),
+        lambda: pd.pd_qk_norm_rope(x, x, None, None, None, None, q_out=x, k_out=x),
+        lambda: pd.pd_qk_norm_rope_append(x, x, x, None, None, None, None, slot, pool, pool, q_out=x),
+        lambda: pd.pd_attn_chunk(x, pool, pool, n, ids, pos, ids, max_qo_len=4, max_kv_len=4, o=o, lse=lse, workspace=ws),
+    ]
+    ticks, stop = [0], threading.Event()
+
+    def count():
+        while not stop.wait(0.002):
+            ticks[0] += 1
+
+    thread = threading.Thread(target=count)
+    thread.start()
+    bind = pd._load_bind()
+    try:
+        bind.init(pd.PdError, *[slow] * 5)
+        during = []
+        for call in calls:
+            before = ticks[0]
+            call()
+            during.append(ticks[0] - before)
+    finally:
+        pd._bind = None
+        pd._load_bind()  # the library's own again
+        stop.set()
+        thread.join()
+    assert min(during) >= 20, during  # of about 150; two at most with the lock held
