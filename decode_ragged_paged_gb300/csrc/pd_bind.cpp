@@ -110,6 +110,12 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{};
+  return v == 1;
+}
+
 void* stream_of(PyObject* o) { return reinterpret_cast<void*>(integer(o)); }
 
 struct Pools {
@@ -215,7 +221,7 @@ struct NormRope {
     pos = a.vector<int32_t>(o[7], "positions", kI32, freq != nullptr ? tokens : 0, freq == nullptr);
     d.rope_dim = freq != nullptr ? 2 * (int32_t)THPVariable_Unpack(o[6]).numel() : 0;
     d.eps = (float)real(eps);
-    d.interleaved = PyObject_IsTrue(interleaved) == 1;
+    d.interleaved = truth(interleaved);
   }
 };
 
@@ -293,7 +299,7 @@ PyObject* attn_chunk(PyObject* const* o) {
   d.page_size = p.page;
   d.kv_dtype = dtype_code(q->scalar_type(), "q");
   d.o_dtype = dtype_code(out->scalar_type(), "o");
-  d.causal = PyObject_IsTrue(o[13]) == 1;
+  d.causal = truth(o[13]);
   d.sm_scale = o[15] == Py_None ? 0.f : (float)real(o[15]);
   const int32_t window = o[14] == Py_None ? -1 : int32(o[14], "window_left");
   int rc = PD_ERR_WORKSPACE;

@@ -297,3 +297,12 @@ def test_other_threads_run_during_a_call(tmp_path):
         stop.set()
         thread.join()
     assert min(during) >= 20, during  # of about 150; two at most with the lock held
+
+
+def test_flags_without_a_truth_value_are_refused():
+    x, pool = torch.zeros(4, 8, 64, device="cuda"), torch.zeros(4, 8, 16, 64, device="cuda")
+    flag = torch.tensor([True, False])
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        pd.pd_attn_chunk(x, pool, pool, i32([4]), i32([0, 1]), i32([0]), i32([0, 4]), causal=flag)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        pd.pd_qk_norm_rope(x, x, None, None, None, None, interleaved=flag)
