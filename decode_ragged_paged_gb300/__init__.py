@@ -42,7 +42,8 @@ DEVICE_STATUS = {0: "ok", 1: "bad indptr", 2: "bad length", 3: "bad page table",
 # Every symbol include/pd.h declares.
 EXPORTS = ("pd_attn_workspace_size", "pd_attn_decode", "pd_attn_decode_static", "pd_attn_prefill",
            "pd_attn_mixed", "pd_attn_mixed_split", "pd_attn_chunk_workspace_size", "pd_attn_chunk",
-           "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_mla_workspace_size", "pd_mla_decode",
+           "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope", "pd_qk_norm_rope_append",
+           "pd_mla_workspace_size", "pd_mla_decode",
            "pd_kv_append", "pd_kv_pack", "pd_kv_unpack", "pd_kv_pack_heads", "pd_kv_unpack_heads",
            "pd_kv_pack_layers", "pd_counter_alloc", "pd_counter_free", "pd_layer_signal",
            "pd_messenger_start_pack", "pd_messenger_join",
@@ -300,21 +301,19 @@ def _attn(name, kind, q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_i
     batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr,
                        total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len, stream=stream)
     if o is None:
-        o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
+        o = _empty(stream, q.shape, o_dtype if o_dtype is not None else q.dtype, q.device)
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.shape[:2], torch.float32, q.device)
     elif lse is False:
         lse = None
     fn, dref, bref = getattr(lib, name), ctypes.byref(desc), ctypes.byref(batch)
     ptrs = (_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(o), _ptr(lse))
     status, strm = _ptr(dev_status), _stream(stream, q.get_device())
     if workspace is None:
-        workspace = torch.empty(max(pd_attn_workspace_size(desc, batch, kind), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(pd_attn_workspace_size(desc, batch, kind), 16), torch.uint8, q.device)
     rc = fn(dref, bref, *ptrs, _ptr(workspace), workspace.numel(), status, strm)
     if rc == PD_ERR_WORKSPACE:  # the caller's workspace is too small for this batch: use one that fits
-        workspace = torch.empty(max(pd_attn_workspace_size(desc, batch, kind), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(pd_attn_workspace_size(desc, batch, kind), 16), torch.uint8, q.device)
         rc = fn(dref, bref, *ptrs, _ptr(workspace), workspace.numel(), status, strm)
     _check(rc, name)
     return o, lse
@@ -369,15 +368,15 @@ def pd_attn_mixed_split(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo
     batch = make_batch(kv_len, page_indptr, page_indices, k_pool.shape[0], qo_indptr=qo_indptr,
                        total_qo=q.shape[0], max_qo_len=max_qo_len, max_kv_len=max_kv_len, stream=stream)
     if o is None:
-        o = torch.empty(q.shape, dtype=o_dtype if o_dtype is not None else q.dtype, device=q.device)
+        o = _empty(stream, q.shape, o_dtype if o_dtype is not None else q.dtype, q.device)
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.shape[:2], torch.float32, q.device)
     elif lse is False:
         lse = None
     dref, bref = ctypes.byref(desc), ctypes.byref(batch)
     if workspace is None or workspace.numel() < pd_attn_workspace_size(desc, batch, PD_KIND_MIXED_SPLIT):
-        workspace = torch.empty(max(pd_attn_workspace_size(desc, batch, PD_KIND_MIXED_SPLIT), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(pd_attn_workspace_size(desc, batch, PD_KIND_MIXED_SPLIT), 16), torch.uint8,
+                           q.device)
     rc = lib.pd_attn_mixed_split(dref, bref, int(num_prefill), int(prefill_sms), _ptr(q), _ptr(k_pool),
                                  _ptr(v_pool), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(),
                                  _ptr(dev_status), _stream(stream, q.get_device()))
@@ -568,22 +567,19 @@ def pd_mla_decode(q, kv_pool, kv_len, page_indptr, page_indices, *, kv_lora_rank
                    _dtype_code(o_dtype if o_dtype is not None else q.dtype), float(sm_scale) if sm_scale else 0.0)
     batch = make_batch(kv_len, page_indptr, page_indices, num_pages, total_qo=B, max_kv_len=max_kv_len, stream=stream)
     if o is None:
-        o = torch.empty((B, hq, int(kv_lora_rank)), dtype=o_dtype if o_dtype is not None else q.dtype,
-                        device=q.device)
+        o = _empty(stream, (B, hq, int(kv_lora_rank)), o_dtype if o_dtype is not None else q.dtype, q.device)
     if lse is True:
-        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, hq), torch.float32, q.device)
     elif lse is False:
         lse = None
     dref, bref = ctypes.byref(desc), ctypes.byref(batch)
     args = (_ptr(q), _ptr(kv_pool), _ptr(o), _ptr(lse))
     status, strm = _ptr(dev_status), _stream(stream, q.get_device())
     if workspace is None:
-        workspace = torch.empty(max(int(lib.pd_mla_workspace_size(dref, bref)), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(int(lib.pd_mla_workspace_size(dref, bref)), 16), torch.uint8, q.device)
     rc = lib.pd_mla_decode(dref, bref, *args, _ptr(workspace), workspace.numel(), status, strm)
     if rc == PD_ERR_WORKSPACE:  # the caller's workspace is too small for this batch: use one that fits
-        workspace = torch.empty(max(int(lib.pd_mla_workspace_size(dref, bref)), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(int(lib.pd_mla_workspace_size(dref, bref)), 16), torch.uint8, q.device)
         rc = lib.pd_mla_decode(dref, bref, *args, _ptr(workspace), workspace.numel(), status, strm)
     _check(rc, "pd_mla_decode")
     return o, lse

@@ -306,3 +306,37 @@ def test_flags_without_a_truth_value_are_refused():
         pd.pd_attn_chunk(x, pool, pool, i32([4]), i32([0, 1]), i32([0]), i32([0, 4]), causal=flag)
     with pytest.raises(RuntimeError, match="ambiguous"):
         pd.pd_qk_norm_rope(x, x, None, None, None, None, interleaved=flag)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_results_of_an_attention_call_on_another_stream_are_its_own(handle):
+    """As above, for the calls beside the step's: results and workspace are allocated on the call's stream."""
+    q, pool = torch.randn(300, 8, 128, device="cuda").bfloat16(), torch.randn(20, 8, 16, 128, device="cuda").bfloat16()
+    pp, px, qo, kv = i32([0, 19]), torch.arange(20, device="cuda", dtype=torch.int32), i32([0, 300]), i32([300])
+    B = 40
+    many = dict(kv_len=i32([300] * B), page_indptr=torch.arange(B + 1, device="cuda", dtype=torch.int32) * 19,
+                page_indices=px[:19].repeat(B))
+    mla_q, mla_pool = torch.randn(B, 4, 576, device="cuda").bfloat16(), torch.randn(20, 16, 576, device="cuda").bfloat16()
+    two = dict(kv_len=i32([299, 300]), page_indptr=i32([0, 19, 38]), page_indices=px[:19].repeat(2), max_kv_len=300,
+               qo_indptr=i32([0, 299, 300]))
+    stream = torch.cuda.Stream()
+    calls = [
+        lambda **kw: pd.pd_attn_prefill(q, pool, pool, kv, pp, px, qo, max_qo_len=300, max_kv_len=300, **kw),
+        lambda **kw: pd.pd_attn_mixed(q, pool, pool, kv, pp, px, qo, max_qo_len=300, max_kv_len=300, **kw),
+        lambda **kw: pd.pd_attn_mixed_split(q, pool, pool, num_prefill=1, max_qo_len=299, **two, **kw),
+        lambda **kw: pd.pd_attn_decode(q[:B], pool, pool, max_kv_len=300, **many, **kw),
+        lambda **kw: pd.pd_mla_decode(mla_q, mla_pool, max_kv_len=300, **many, **kw),
+    ]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        # what the call takes from a pool of memory is in use there until the delay is over
+        spent = [torch.empty_like(t) for t in want] + [torch.empty(1 << 20, dtype=torch.uint8, device="cuda")]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for t in spent:
+            t.fill_(7)
+        del t, spent
+        got = call(stream=stream.cuda_stream if handle else stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
