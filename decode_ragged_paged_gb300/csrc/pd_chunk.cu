@@ -354,8 +354,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
 // the i-th; each warp keeps its own maximum, sum and output, and the eight are
 // joined at an item's end. The next keys are on their way to shared memory meanwhile
 // (in registers instead, 2 x 8 keys a warp: 90 us for 82). 16 decodes of 1000 to
-// 4096 keys, 32 / 8 heads, D 128, 265 MB, take 68 us in the kernel, 3.9 TB/s: the
-// latency of 8 warps an SM, whose stages fill its shared memory (issue 32 %).
+// 4096 keys, 32 / 8 heads, D 128, 265 MB, take 68 us in the kernel, 3.9 TB/s. Neither
+// the bytes in flight hold it (two stages of three, 128 KB an SM, where HBM's rate
+// takes about 45 at a latency of 1 us) nor the issue slots (32 %): each warp's 8 keys
+// go through one chain, 31 exchanges, the maximum's three, the exponential and a trip
+// of the weights through shared memory, before its next 8, and 8 warps do not cover it.
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
 constexpr int kRowsKeys = kChunkKeys / kRowsWarps;
 constexpr int kRowsStages = 3;  // of a warp's 8 keys, K and V

@@ -12,9 +12,12 @@
 //
 // Angle. t in turns is position * (inv_freq / 2 pi) mod 1: the frequency is
 // held as a 64-bit fraction of a turn and multiplied by the position in
-// 64-bit integers, whose overflow is the reduction modulo one turn; fp32
+// 64-bit integers, whose overflow is the reduction modulo one turn, exactly; fp32
 // products of far positions would be off by whole turns. The fraction comes from
-// a double, so an angle is off by at most position * 2^-53 of its frequency.
+// a double: 1 / 2 pi and its product with the frequency are each rounded (2^-52 of
+// it together), and the product is cut to 2^-64 of a turn, so an angle is off by at
+// most position * (inv_freq * 2^-52 + 2 pi * 2^-64) before fp32's cosine. (A frequency
+// below zero is off by 2 pi * 2^-54 more: 1 - x is rounded too.)
 //
 // Bound: HBM; every element is read once and written once. What stands in the
 // way is the instructions (at one warp a head group, a first form with scalar

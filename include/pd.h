@@ -399,8 +399,9 @@ PD_API int pd_slot_map(const pd_batch *batch, int32_t page_size, int32_t *positi
  *   (z_a, z_b) = (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
  *   t = positions[token] * inv_freq[i], i < rope_dim / 2,
  *   (a, b) = (i, rope_dim / 2 + i), or (2i, 2i + 1) if interleaved
- * and values past rope_dim stay y. Computed in fp32 (angles exactly modulo a
- * turn) and rounded once.
+ * and values past rope_dim stay y. Computed in fp32 and rounded once; angles are
+ * reduced modulo a turn exactly, in 64 bits, and off by at most positions * inv_freq
+ * * 2^-52 before that.
  *   q, k, v   device, token t at + t * stride elements, [heads][head_dim]; stride 0 means
  *             contiguous (heads * head_dim); slices of one projection's rows have its width
  *   q_weight, k_weight  device [head_dim] (dtype) or NULL
