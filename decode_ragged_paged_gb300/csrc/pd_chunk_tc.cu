@@ -30,11 +30,14 @@
 // 2^-16 of a weight (two keys, values 3.5 to 4 and 0 to 1, bf16 output: 1.1e-2
 // off with bf16 weights, 7.8e-3 with the remainders, half a step of the output).
 //
-// Bound and measured (kernel, cold caches): 4 x 2048 tokens over 14000 to 16384
-// keys, 32 / 8 heads, D 128, 995 us, 1829 TFLOP/s: the tensor cores (81 % of their
-// cycles; the clock gives way to power). 500 tokens over 32700: 162 us, 1643
-// TFLOP/s. 32 verifications of 2 to 8 tokens over 512 to 4096 keys: 54 to 65 us for
-// 273 MB, HBM behind 17 us of start and merge. Windowed prefill, D 64: 48 us; there
+// Bound and measured: 4 x 2048 tokens over 14000 to 16384 keys, 32 / 8 heads, D 128:
+// the tensor cores (81 % of their cycles), 1025 us for one launch after a pause (1775
+// TFLOP/s); calls one after another take 1140 to 1177 (1546 to 1597 TFLOP/s), as the
+// power limit takes the clock down. 500 tokens over 32700: 163 us, and 186 a call one
+// after another (1430 TFLOP/s, with the merge). 32 verifications of 2 to 8 tokens over
+// 512 to 4096 keys: 55 us for 273 MB, HBM behind 17 us of start and merge. Prompts of
+// 128 tokens, all with remainders: 64 of them 64.7 us, 58.6 without; a window of 64
+// keys: 8 x 2000 tokens 112 us, 97 without. Windowed prefill, D 64: 47 us; there
 // a tile takes 1380 cycles, two softmax warps a sub-partition with 350 instructions
 // each and their latencies (issue 39 to 50 %; the exponentials 23 to 38 %), and an
 // item 7000 more, from its last tile's product over the output to its next first.

@@ -286,9 +286,12 @@ PD_API int pd_attn_mixed_split(const pd_attn_desc *desc, const pd_batch *batch, 
  * what that leaves of them. Other calls run in fp32 on the CUDA cores. A workspace
  * serves one call at a time and carries nothing from one to the next. Keys that no
  * token of the request sees (past kv_len, or before the first token's window) may
- * hold anything, also NaN; V rows that some token of the request sees must be finite for all its tokens.
- * The call can be captured into a CUDA graph; lengths may change between replays
- * within the host bounds max_qo_len and max_kv_len.
+ * hold anything, also NaN; V rows that some token of the request sees must be
+ * finite for all its tokens. The call can be captured into a CUDA graph; lengths may
+ * change between replays within the host bounds max_qo_len and max_kv_len.
+ * Which call to take: where pd_attn_decode or pd_attn_prefill would do the same, this
+ * one is as fast (large batches of decodes) or faster (small ones, prefills); a long
+ * prefill among many decodes is better run by pd_attn_mixed or pd_attn_mixed_split.
  */
 PD_API size_t pd_attn_chunk_workspace_size(const pd_attn_desc *desc, const pd_batch *batch);
 PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_t window_left, int64_t q_stride,
