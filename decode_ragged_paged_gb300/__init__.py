@@ -188,8 +188,9 @@ def _load_bind():
             except ImportError as e:
                 raise PdError(f"the binding module _pd_bind cannot be loaded ({e}); run "
                               "`python -m decode_ragged_paged_gb300.build`") from e
-            if _pd_bind.torch_version != torch.__version__:  # it reads torch's objects in place
-                raise PdError(f"_pd_bind was built for torch {_pd_bind.torch_version}, not {torch.__version__}; run "
+            built_for = getattr(_pd_bind, "torch_version", "another version")
+            if built_for != torch.__version__:  # it reads torch's objects in place
+                raise PdError(f"_pd_bind was built for torch {built_for}, not {torch.__version__}; run "
                               "`python -m decode_ragged_paged_gb300.build`")
             _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
                 "pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
