@@ -42,7 +42,9 @@ DEVICE_STATUS = {0: "ok", 1: "bad indptr", 2: "bad length", 3: "bad page table",
 # Every symbol include/pd.h declares.
 EXPORTS = ("pd_attn_workspace_size", "pd_attn_decode", "pd_attn_decode_static", "pd_attn_prefill",
            "pd_attn_mixed", "pd_attn_mixed_split", "pd_attn_chunk_workspace_size", "pd_attn_chunk",
+           "pd_attn_chunk_quant_workspace_size", "pd_attn_chunk_quant", "pd_kv_append_quant",
            "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope", "pd_qk_norm_rope_append",
+           "pd_qk_norm_rope_axes", "pd_qk_norm_rope_axes_append",
            "pd_mla_workspace_size", "pd_mla_decode",
            "pd_kv_append", "pd_kv_pack", "pd_kv_unpack", "pd_kv_pack_heads", "pd_kv_unpack_heads",
            "pd_kv_pack_layers", "pd_counter_alloc", "pd_counter_free", "pd_layer_signal",
@@ -98,6 +100,12 @@ class NormRopeDesc(ctypes.Structure):
                 ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
+class KvQuantDesc(ctypes.Structure):
+    _fields_ = [("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("scale_block", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
 class BatchTables(NamedTuple):
     """What pd_batch_tables writes: the batch of the attention calls, and each new token's place."""
     qo_indptr: torch.Tensor     # int32 [B+1]
@@ -137,8 +145,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.pd_slot_map.argtypes = [ctypes.POINTER(Batch), I32, P, P, P, P]
             lib.pd_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + [P] * 9
             lib.pd_qk_norm_rope_append.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + [P] * 13
+            axes = [I32, ctypes.c_int64, P]
+            lib.pd_qk_norm_rope_axes.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + axes + [P] * 9
+            lib.pd_qk_norm_rope_axes_append.argtypes = [ctypes.POINTER(NormRopeDesc), I32] + axes + [P] * 13
+            lib.pd_kv_append_quant.argtypes = [ctypes.POINTER(KvQuantDesc), ctypes.POINTER(Batch)] + [P] * 8
+            lib.pd_attn_chunk_quant_workspace_size.argtypes = attn[:2] + [I32]
+            lib.pd_attn_chunk_quant_workspace_size.restype = S
+            lib.pd_attn_chunk_quant.argtypes = attn[:2] + [I32, I32, ctypes.c_int64] + [P] * 5 + attn[5:]
             for name in ("pd_attn_chunk", "pd_batch_tables", "pd_slot_map", "pd_qk_norm_rope",
-                         "pd_qk_norm_rope_append"):
+                         "pd_qk_norm_rope_append", "pd_qk_norm_rope_axes", "pd_qk_norm_rope_axes_append",
+                         "pd_kv_append_quant", "pd_attn_chunk_quant"):
                 getattr(lib, name).restype = ctypes.c_int
             lib.pd_mla_workspace_size.argtypes = [ctypes.POINTER(MlaDesc), ctypes.POINTER(Batch)]
             lib.pd_mla_workspace_size.restype = S
@@ -194,7 +210,8 @@ def _load_bind():
                               "`python -m decode_ragged_paged_gb300.build`")
             _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
                 "pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
-                "pd_attn_chunk_workspace_size")))
+                "pd_attn_chunk_workspace_size", "pd_qk_norm_rope_axes", "pd_qk_norm_rope_axes_append",
+                "pd_kv_append_quant", "pd_attn_chunk_quant", "pd_attn_chunk_quant_workspace_size")))
             _bind = _pd_bind
         return _bind
 
@@ -447,13 +464,9 @@ def _bound(name, stream, *args):
     return rc
 
 
-def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, *, causal=True, window_left=-1,
-                  sm_scale=None, max_qo_len=None, max_kv_len=None, o=None, lse=True, o_dtype=None, workspace=None,
-                  dev_status=None, stream=None, layout="HND"):
-    """Attention of each request's new tokens (one or many) over its pages, causal by default, with
-    an optional sliding window of window_left keys before each token. q [total_qo][Hq][D] may be a
-    slice of a wider row. Without max_qo_len / max_kv_len they are read from the device (a
-    synchronisation). Returns (o, lse)."""
+def _attn_chunk(what, q, pools, scales, kv_len, page_indptr, page_indices, qo_indptr, causal, window_left, sm_scale,
+                max_qo_len, max_kv_len, o, lse, o_dtype, workspace, dev_status, stream, layout):
+    """pd_attn_chunk, and with `scales` pd_attn_chunk_quant."""
     if o is None:
         o = _empty(stream, q.shape, o_dtype if o_dtype is not None else q.dtype, q.device)
     if lse is True:
@@ -464,15 +477,39 @@ def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indpt
         max_qo_len = _longest(stream, indptr=qo_indptr)
     if max_kv_len is None:
         max_kv_len = _longest(stream, kv_len=kv_len)
-    head = (q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, o, lse)
-    tail = (dev_status, causal, window_left, sm_scale or None, max_qo_len, max_kv_len, _layout_code(layout))
-    rc = _bound("attn_chunk", stream, *head, workspace, *tail)
+    head = (q, *pools, kv_len, page_indptr, page_indices, qo_indptr, o, lse)
+    tail = (dev_status, causal, window_left, sm_scale or None, max_qo_len, max_kv_len, _layout_code(layout), *scales)
+    name = what[3:]
+    rc = _bound(name, stream, *head, workspace, *tail)
     if rc is not None and rc[1] == PD_ERR_WORKSPACE:  # none, or one too small for this batch
         workspace = _empty(stream, max(rc[0], 16), torch.uint8, q.device)
-        rc = _bound("attn_chunk", stream, *head, workspace, *tail)
+        rc = _bound(name, stream, *head, workspace, *tail)
     if rc is not None:
-        _check(rc[1], "pd_attn_chunk")
+        _check(rc[1], what)
     return o, lse
+
+
+def pd_attn_chunk(q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, *, causal=True, window_left=-1,
+                  sm_scale=None, max_qo_len=None, max_kv_len=None, o=None, lse=True, o_dtype=None, workspace=None,
+                  dev_status=None, stream=None, layout="HND"):
+    """Attention of each request's new tokens (one or many) over its pages, causal by default, with
+    an optional sliding window of window_left keys before each token. q [total_qo][Hq][D] may be a
+    slice of a wider row. Without max_qo_len / max_kv_len they are read from the device (a
+    synchronisation). Returns (o, lse)."""
+    return _attn_chunk("pd_attn_chunk", q, (k_pool, v_pool), (), kv_len, page_indptr, page_indices, qo_indptr, causal,
+                       window_left, sm_scale, max_qo_len, max_kv_len, o, lse, o_dtype, workspace, dev_status, stream,
+                       layout)
+
+
+def pd_attn_chunk_quant(q, k_pool, v_pool, k_scale, v_scale, kv_len, page_indptr, page_indices, qo_indptr, *,
+                        causal=True, window_left=-1, sm_scale=None, max_qo_len=None, max_kv_len=None, o=None, lse=True,
+                        o_dtype=None, workspace=None, dev_status=None, stream=None, layout="HND"):
+    """pd_attn_chunk over pools of 8-bit values (torch.float8_e4m3fn, or their bytes as uint8) with a scale for
+    each block of tokens of a page and each head: k_scale, v_scale fp32 [num_pages][Hkv][page_size / block], as
+    pd_kv_append_quant leaves them. Returns (o, lse)."""
+    return _attn_chunk("pd_attn_chunk_quant", q, (k_pool, v_pool), (k_scale, v_scale), kv_len, page_indptr,
+                       page_indices, qo_indptr, causal, window_left, sm_scale, max_qo_len, max_kv_len, o, lse, o_dtype,
+                       workspace, dev_status, stream, layout)
 
 
 def pd_batch_tables(new_len, cached_len, block_table, *, page_size, num_pages, total_qo, max_page_indices, rows=None,
@@ -551,6 +588,44 @@ def pd_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, slo
     return q_out
 
 
+def _freq_axis(axes) -> bytes:
+    """The axis of every frequency, a byte each."""
+    if isinstance(axes, bytes):
+        return axes
+    try:
+        return bytes([int(a) for a in axes])
+    except (TypeError, ValueError) as e:
+        raise PdError(f"freq_axis must name an axis for each frequency ({e})") from e
+
+
+def pd_qk_norm_rope_axes(q, k, q_weight, k_weight, inv_freq, freq_axis, positions, *, eps=1e-6, interleaved=False,
+                         q_out=None, k_out=None, stream=None):
+    """pd_qk_norm_rope for positions with several axes (time, height, width): positions [axes][T], and
+    freq_axis says by which axis each frequency turns (bytes, or a sequence of small integers on the host:
+    bytes([0] * 16 + [1] * 24 + [2] * 24)). Returns (q_out, k_out)."""
+    if q_out is None:
+        q_out = _empty(stream, q.shape, q.dtype, q.device)
+    if k_out is None:
+        k_out = _empty(stream, k.shape, k.dtype, k.device)
+    rc = _bound("norm_rope_axes", stream, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved,
+                _freq_axis(freq_axis))
+    if rc is not None:
+        _check(rc[1], "pd_qk_norm_rope_axes")
+    return q_out, k_out
+
+
+def pd_qk_norm_rope_axes_append(q, k, v, q_weight, k_weight, inv_freq, freq_axis, positions, slot_map, k_pool, v_pool, *,
+                                eps=1e-6, interleaved=False, q_out=None, dev_status=None, stream=None, layout="HND"):
+    """pd_qk_norm_rope_append for positions with several axes (as pd_qk_norm_rope_axes). Returns q_out."""
+    if q_out is None:
+        q_out = _empty(stream, q.shape, q.dtype, q.device)
+    rc = _bound("norm_rope_axes_append", stream, q, k, q_weight, k_weight, inv_freq, positions, v, slot_map, k_pool,
+                v_pool, q_out, dev_status, eps, interleaved, _layout_code(layout), _freq_axis(freq_axis))
+    if rc is not None:
+        _check(rc[1], "pd_qk_norm_rope_axes_append")
+    return q_out
+
+
 def pd_mla_decode(q, kv_pool, kv_len, page_indptr, page_indices, *, kv_lora_rank=512, sm_scale=None,
                   max_kv_len=None, o=None, lse=True, o_dtype=None, workspace=None, dev_status=None, stream=None):
     """MLA decode over a paged latent cache: q [B][Hq][kv_lora_rank + rope_dim], kv_pool
@@ -603,6 +678,20 @@ def pd_kv_append(k_new, v_new, k_pool, v_pool, new_indptr, kv_len, page_indptr, 
     rc = lib.pd_kv_append(ctypes.byref(desc), ctypes.byref(batch), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
                           _ptr(v_pool), _ptr(dev_status), _stream(stream))
     _check(rc, "pd_kv_append")
+
+
+def pd_kv_append_quant(k_new, v_new, k_pool, v_pool, k_scale, v_scale, new_indptr, kv_len, page_indptr, page_indices, *,
+                       max_kv_len=None, dev_status=None, stream=None, layout="HND"):
+    """pd_kv_append into pools of 8-bit values, in place: k_new, v_new ([total_new][Hkv][D], slices of a wider
+    row will do) are rounded to e4m3 (pools torch.float8_e4m3fn, or uint8) with a power of two as the scale of each
+    block of tokens and head (k_scale, v_scale fp32 [num_pages][Hkv][page_size / block]). A block that grows
+    gets a larger scale when its new values need one, and its earlier values are rounded again."""
+    if max_kv_len is None:
+        max_kv_len = _longest(stream, kv_len=kv_len)
+    rc = _bound("kv_append_quant", stream, k_new, v_new, k_pool, v_pool, k_scale, v_scale, new_indptr, kv_len,
+                page_indptr, page_indices, dev_status, max_kv_len, _layout_code(layout))
+    if rc is not None:
+        _check(rc[1], "pd_kv_append_quant")
 
 
 def _layers(pools):

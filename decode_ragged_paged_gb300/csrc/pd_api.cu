@@ -415,6 +415,56 @@ int pd_kv_append(const pd_kv_desc* desc, const pd_batch* batch, const void* k_ne
   return launch_kv_append(p, static_cast<cudaStream_t>(stream));
 }
 
+int pd_kv_append_quant(const pd_kv_quant_desc* d, const pd_batch* b, const void* k_new, const void* v_new,
+                       void* k_pool, void* v_pool, float* k_scale, float* v_scale, int32_t* dev_status,
+                       void* stream) {
+  if (d == nullptr || b == nullptr) return PD_ERR_INVALID_ARG;
+  const int es = elem_size(d->dtype);
+  if (es == 0 || d->num_kv_heads <= 0 || d->head_dim <= 0 || d->page_size <= 0 || d->scale_block <= 0 ||
+      d->page_size % d->scale_block != 0)
+    return PD_ERR_INVALID_ARG;
+  if (d->layout != PD_LAYOUT_HND && d->layout != PD_LAYOUT_NHD) return PD_ERR_INVALID_ARG;
+  if (b->batch_size < 0 || b->total_qo < 0 || b->max_kv_len < 0) return PD_ERR_INVALID_ARG;
+  if (d->head_dim % 8 != 0 || d->head_dim > 1024 || d->num_kv_heads > (1 << 14)) return PD_ERR_UNSUPPORTED;
+  if (b->batch_size == 0 || b->total_qo == 0) return PD_OK;
+  if (b->num_pages <= 0 || b->qo_indptr == nullptr || b->kv_len == nullptr || b->page_indptr == nullptr ||
+      b->page_indices == nullptr)
+    return PD_ERR_INVALID_ARG;
+  if (k_new == nullptr || v_new == nullptr || k_pool == nullptr || v_pool == nullptr || k_scale == nullptr ||
+      v_scale == nullptr)
+    return PD_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
+      ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u) != 0)
+    return PD_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)d->num_kv_heads * d->head_dim;
+  KvQuantParams p{};
+  p.k_stride = d->k_stride != 0 ? d->k_stride : row;
+  p.v_stride = d->v_stride != 0 ? d->v_stride : row;
+  if (p.k_stride < 0 || p.v_stride < 0 || p.k_stride * es % 16 != 0 || p.v_stride * es % 16 != 0)
+    return PD_ERR_INVALID_ARG;
+  p.batch = b->batch_size;
+  p.hkv = d->num_kv_heads;
+  p.head_dim = d->head_dim;
+  p.page_size = d->page_size;
+  p.scale_block = d->scale_block;
+  p.num_pages = b->num_pages;
+  p.total = b->total_qo;
+  p.max_kv_len = b->max_kv_len;
+  p.nhd = d->layout == PD_LAYOUT_NHD;
+  p.new_indptr = b->qo_indptr;
+  p.kv_len = b->kv_len;
+  p.page_indptr = b->page_indptr;
+  p.page_indices = b->page_indices;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = dev_status;
+  return launch_kv_append_quant(p, es, static_cast<cudaStream_t>(stream));
+}
+
 int pd_kv_pack_heads(const pd_kv_desc* desc, const pd_batch* batch, int32_t head_begin, int32_t head_count,
                      const void* k_pool, const void* v_pool, void* dst, size_t dst_bytes,
                      const int64_t* dst_offsets, int32_t* dev_status, void* stream) {
@@ -591,10 +641,16 @@ int pd_slot_map(const pd_batch* b, int32_t page_size, int32_t* positions, int64_
 namespace {
 
 // Checks and launches either form of the norm and rotation; with a slot map, k and v go to pools.
+// axes: those of a call whose positions have several, else null.
+struct Axes {
+  int32_t count;
+  int64_t stride;
+  const uint8_t* of_freq;
+};
 int run_norm_rope(const pd_norm_rope_desc* d, int32_t num_tokens, const void* q, const void* k, const void* v,
                   const void* q_weight, const void* k_weight, const float* inv_freq, const int32_t* positions,
                   const int64_t* slot_map, void* q_out, void* k_out, void* v_out, bool paged, int32_t* dev_status,
-                  void* stream) {
+                  void* stream, const Axes* axes = nullptr) {
   if (d == nullptr || num_tokens < 0) return PD_ERR_INVALID_ARG;
   const int es = elem_size(d->dtype);
   if (es == 0 || d->num_qo_heads < 0 || d->num_kv_heads < 0 || d->num_qo_heads + (int64_t)d->num_kv_heads == 0 ||
@@ -648,6 +704,11 @@ int run_norm_rope(const pd_norm_rope_desc* d, int32_t num_tokens, const void* q,
     low |= reinterpret_cast<uintptr_t>(a);
   const int vec = norm_rope_vec(p, es, low);
   if (vec == 0) return PD_ERR_UNSUPPORTED;
+  if (axes != nullptr) {
+    p.num_axes = axes->count;
+    p.axis_stride = axes->stride;
+    for (int i = 0; i < d->rope_dim / 2; ++i) p.axis_bits[i >> 4] |= (uint32_t)axes->of_freq[i] << (2 * (i & 15));
+  }
   return launch_norm_rope(p, es, vec, static_cast<cudaStream_t>(stream));
 }
 
@@ -666,6 +727,44 @@ int pd_qk_norm_rope_append(const pd_norm_rope_desc* desc, int32_t num_tokens, co
                            void* v_pool, int32_t* dev_status, void* stream) {
   return run_norm_rope(desc, num_tokens, q, k, v, q_weight, k_weight, inv_freq, positions, slot_map, q_out, k_pool,
                        v_pool, true, dev_status, stream);
+}
+
+namespace {
+
+// What the forms with several axes refuse beyond what run_norm_rope does.
+int check_axes(const pd_norm_rope_desc* d, const Axes& axes) {
+  if (d == nullptr || axes.of_freq == nullptr || axes.count < 1 || axes.stride < 0) return PD_ERR_INVALID_ARG;
+  if (axes.count > 4) return PD_ERR_UNSUPPORTED;
+  if (d->rope_dim <= 0 || d->rope_dim > d->head_dim) return PD_ERR_INVALID_ARG;
+  if (d->rope_dim > 512) return PD_ERR_UNSUPPORTED;  // (no head is wider)
+  for (int i = 0; i < d->rope_dim / 2; ++i)
+    if (axes.of_freq[i] >= axes.count) return PD_ERR_INVALID_ARG;
+  return PD_OK;
+}
+
+}  // namespace
+
+int pd_qk_norm_rope_axes(const pd_norm_rope_desc* desc, int32_t num_tokens, int32_t num_axes, int64_t axis_stride,
+                         const uint8_t* freq_axis, const void* q, const void* k, const void* q_weight,
+                         const void* k_weight, const float* inv_freq, const int32_t* positions, void* q_out,
+                         void* k_out, void* stream) {
+  const Axes axes{num_axes, axis_stride, freq_axis};
+  const int rc = check_axes(desc, axes);
+  if (rc != PD_OK) return rc;
+  return run_norm_rope(desc, num_tokens, q, k, nullptr, q_weight, k_weight, inv_freq, positions, nullptr, q_out,
+                       k_out, nullptr, false, nullptr, stream, &axes);
+}
+
+int pd_qk_norm_rope_axes_append(const pd_norm_rope_desc* desc, int32_t num_tokens, int32_t num_axes,
+                                int64_t axis_stride, const uint8_t* freq_axis, const void* q, const void* k,
+                                const void* v, const void* q_weight, const void* k_weight, const float* inv_freq,
+                                const int32_t* positions, const int64_t* slot_map, void* q_out, void* k_pool,
+                                void* v_pool, int32_t* dev_status, void* stream) {
+  const Axes axes{num_axes, axis_stride, freq_axis};
+  const int rc = check_axes(desc, axes);
+  if (rc != PD_OK) return rc;
+  return run_norm_rope(desc, num_tokens, q, k, v, q_weight, k_weight, inv_freq, positions, slot_map, q_out, k_pool,
+                       v_pool, true, dev_status, stream, &axes);
 }
 
 namespace {
@@ -705,19 +804,21 @@ size_t pd_attn_chunk_workspace_size(const pd_attn_desc* desc, const pd_batch* ba
   return chunk_fits(p) ? total : 0;
 }
 
-int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t window_left, int64_t q_stride,
-                  const void* q, const void* k_pool, const void* v_pool, void* o, float* lse, void* workspace,
-                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  const int rc = check_attn(desc, batch, true);
-  if (rc != PD_OK) return rc;
-  ChunkParams p = chunk_params(desc, batch, window_left, q_stride);
+namespace {
+
+// The rest of pd_attn_chunk and pd_attn_chunk_quant: p has the descriptor's and the batch's part.
+int run_chunk(ChunkParams& p, const pd_attn_desc* desc, const pd_batch* batch, const void* q, const void* k_pool,
+              const void* v_pool, void* o, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+              void* stream) {
   if (batch->max_kv_len > kChunkMaxKeys) return PD_ERR_UNSUPPORTED;
   if (p.q_stride < (int64_t)p.hq * p.head_dim || p.q_stride * elem_size(desc->kv_dtype) % 16 != 0)
     return PD_ERR_INVALID_ARG;
   if (batch->batch_size == 0 || batch->total_qo == 0 || batch->max_qo_len == 0) return PD_OK;
   if (q == nullptr || k_pool == nullptr || v_pool == nullptr || o == nullptr || workspace == nullptr)
     return PD_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(workspace))
+  if (p.scale_block > 0 && (p.k_scale == nullptr || p.v_scale == nullptr)) return PD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) & 3u) != 0)
     return PD_ERR_INVALID_ARG;
   const ChunkLayout L = chunk_layout(p, desc->kv_dtype);
   if (!chunk_fits(p)) return PD_ERR_UNSUPPORTED;
@@ -738,6 +839,45 @@ int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t windo
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);
   p.status = dev_status;
   return launch_chunk(p, desc->kv_dtype, static_cast<cudaStream_t>(stream));
+}
+
+// What 8-bit pools need of a call beyond check_attn.
+int check_chunk_quant(const pd_attn_desc* desc, const pd_batch* batch, int32_t scale_block, bool need_qo_indptr) {
+  const int rc = check_attn(desc, batch, need_qo_indptr);
+  if (rc != PD_OK) return rc;
+  return scale_block > 0 && desc->page_size % scale_block == 0 ? PD_OK : PD_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+int pd_attn_chunk(const pd_attn_desc* desc, const pd_batch* batch, int32_t window_left, int64_t q_stride,
+                  const void* q, const void* k_pool, const void* v_pool, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_attn(desc, batch, true);
+  if (rc != PD_OK) return rc;
+  ChunkParams p = chunk_params(desc, batch, window_left, q_stride);
+  return run_chunk(p, desc, batch, q, k_pool, v_pool, o, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t pd_attn_chunk_quant_workspace_size(const pd_attn_desc* desc, const pd_batch* batch, int32_t scale_block) {
+  if (check_chunk_quant(desc, batch, scale_block, false) != PD_OK) return 0;
+  ChunkParams p = chunk_params(desc, batch, -1, 0);
+  p.scale_block = scale_block;
+  const size_t total = chunk_layout(p, desc->kv_dtype).total;
+  return chunk_fits(p) ? total : 0;
+}
+
+int pd_attn_chunk_quant(const pd_attn_desc* desc, const pd_batch* batch, int32_t scale_block, int32_t window_left,
+                        int64_t q_stride, const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                        const float* v_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                        int32_t* dev_status, void* stream) {
+  const int rc = check_chunk_quant(desc, batch, scale_block, true);
+  if (rc != PD_OK) return rc;
+  ChunkParams p = chunk_params(desc, batch, window_left, q_stride);
+  p.scale_block = scale_block;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return run_chunk(p, desc, batch, q, k_pool, v_pool, o, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

@@ -23,8 +23,13 @@ PyObject* g_error = nullptr;  // the package's PdError
 decltype(&pd_batch_tables) g_batch_tables = nullptr;
 decltype(&pd_qk_norm_rope) g_norm_rope = nullptr;
 decltype(&pd_qk_norm_rope_append) g_norm_rope_append = nullptr;
+decltype(&pd_qk_norm_rope_axes) g_norm_rope_axes = nullptr;
+decltype(&pd_qk_norm_rope_axes_append) g_norm_rope_axes_append = nullptr;
 decltype(&pd_attn_chunk) g_attn_chunk = nullptr;
 decltype(&pd_attn_chunk_workspace_size) g_chunk_workspace = nullptr;
+decltype(&pd_kv_append_quant) g_kv_append_quant = nullptr;
+decltype(&pd_attn_chunk_quant) g_chunk_quant = nullptr;
+decltype(&pd_attn_chunk_quant_workspace_size) g_chunk_quant_workspace = nullptr;
 
 struct Refused {};  // a Python exception is set
 
@@ -201,7 +206,12 @@ struct NormRope {
   pd_norm_rope_desc d{};
   int32_t tokens;
 
-  NormRope(Args& a, PyObject* const* o, PyObject* eps, PyObject* interleaved) {
+  // freq_axis (bytes, an axis for each frequency): positions are [axes][tokens].
+  int32_t num_axes = 0;
+  int64_t axis_stride = 0;
+  const uint8_t* freq_axis = nullptr;
+
+  NormRope(Args& a, PyObject* const* o, PyObject* eps, PyObject* interleaved, PyObject* axes = nullptr) {
     q = a.tensor(o[2], "q");
     k = a.tensor(o[3], "k");
     d.q_stride = rows(*q, "q");
@@ -218,7 +228,23 @@ struct NormRope {
     qw = a.vector<void>(o[4], "q_weight", dt, d.head_dim, true);
     kw = a.vector<void>(o[5], "k_weight", dt, d.head_dim, true);
     freq = a.vector<float>(o[6], "inv_freq", kF32, 0, true);
-    pos = a.vector<int32_t>(o[7], "positions", kI32, freq != nullptr ? tokens : 0, freq == nullptr);
+    if (axes == nullptr) {
+      pos = a.vector<int32_t>(o[7], "positions", kI32, freq != nullptr ? tokens : 0, freq == nullptr);
+    } else {
+      if (freq == nullptr) refuse("inv_freq is missing");
+      const at::Tensor* at = a.tensor(o[7], "positions");
+      if (at->scalar_type() != kI32 || at->dim() != 2 || at->size(1) < tokens || (at->size(1) > 1 && at->stride(1) != 1))
+        refuse("positions must be an Int tensor [axes][tokens] whose tokens lie side by side");
+      if (at->size(0) < 1 || at->size(0) > 4) refuse("positions must have 1 to 4 axes");
+      if (!PyBytes_Check(axes) || PyBytes_GET_SIZE(axes) != THPVariable_Unpack(o[6]).numel())
+        refuse("freq_axis must have an axis for each frequency");
+      pos = static_cast<const int32_t*>(at->data_ptr());
+      num_axes = (int32_t)at->size(0);
+      axis_stride = at->stride(0);
+      freq_axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(axes));
+      for (Py_ssize_t i = 0; i < PyBytes_GET_SIZE(axes); ++i)
+        if (freq_axis[i] >= num_axes) refuse("freq_axis names axis %d of %d", (int)freq_axis[i], (int)num_axes);
+    }
     d.rope_dim = freq != nullptr ? 2 * (int32_t)THPVariable_Unpack(o[6]).numel() : 0;
     d.eps = (float)real(eps);
     d.interleaved = truth(interleaved);
@@ -226,25 +252,33 @@ struct NormRope {
 };
 
 // norm_rope(current device, stream, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved)
+// norm_rope_axes: the same, and freq_axis at the end
+template <bool AXES>
 PyObject* norm_rope(PyObject* const* o) {
   Args a;
   a.tensor(o[2], "q");
   if (a.device != integer(o[0])) return done(a.device, kOtherDevice);
-  NormRope n(a, o, o[10], o[11]);
+  NormRope n(a, o, o[10], o[11], AXES ? o[12] : nullptr);
   const at::Tensor *qo = a.tensor(o[8], "q_out"), *ko = a.tensor(o[9], "k_out");
   n.d.q_out_stride = same_rows(*qo, *n.q, "q_out");
   n.d.k_out_stride = same_rows(*ko, *n.k, "k_out");
+  if (AXES)
+    return done(a.device, unlocked(g_norm_rope_axes, &n.d, n.tokens, n.num_axes, n.axis_stride, n.freq_axis,
+                                   n.q->data_ptr(), n.k->data_ptr(), n.qw, n.kw, n.freq, n.pos, qo->data_ptr(),
+                                   ko->data_ptr(), stream_of(o[1])));
   return done(a.device, unlocked(g_norm_rope, &n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), n.qw, n.kw, n.freq,
                                  n.pos, qo->data_ptr(), ko->data_ptr(), stream_of(o[1])));
 }
 
 // norm_rope_append(current device, stream, q, k, q_weight, k_weight, inv_freq, positions, v, slot_map, k_pool, v_pool,
 //   q_out, dev_status, eps, interleaved, layout)
+// norm_rope_axes_append: the same, and freq_axis at the end
+template <bool AXES>
 PyObject* norm_rope_append(PyObject* const* o) {
   Args a;
   a.tensor(o[2], "q");
   if (a.device != integer(o[0])) return done(a.device, kOtherDevice);
-  NormRope n(a, o, o[14], o[15]);
+  NormRope n(a, o, o[14], o[15], AXES ? o[17] : nullptr);
   const at::Tensor* v = a.tensor(o[8], "v");
   n.d.v_stride = same_rows(*v, *n.k, "v");
   const auto* slot = a.vector<int64_t>(o[9], "slot_map", kI64, n.tokens);
@@ -257,22 +291,85 @@ PyObject* norm_rope_append(PyObject* const* o) {
   const at::Tensor* qo = a.tensor(o[12], "q_out");
   n.d.q_out_stride = same_rows(*qo, *n.q, "q_out");
   auto* status = a.vector<int32_t>(o[13], "dev_status", kI32, 1, true);
+  if (AXES)
+    return done(a.device, unlocked(g_norm_rope_axes_append, &n.d, n.tokens, n.num_axes, n.axis_stride, n.freq_axis,
+                                   n.q->data_ptr(), n.k->data_ptr(), v->data_ptr(), n.qw, n.kw, n.freq, n.pos, slot,
+                                   qo->data_ptr(), p.k->data_ptr(), p.v->data_ptr(), status, stream_of(o[1])));
   return done(a.device, unlocked(g_norm_rope_append, &n.d, n.tokens, n.q->data_ptr(), n.k->data_ptr(), v->data_ptr(),
                                  n.qw, n.kw, n.freq, n.pos, slot, qo->data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
                                  status, stream_of(o[1])));
 }
 
+// Scales [pages][heads][blocks of a page] of an 8-bit pool: their address, and the tokens of a block.
+float* scales(Args& a, PyObject* o, const Pools& p, const char* name, int32_t& block) {
+  const at::Tensor* t = a.tensor(o, name);
+  if (t->scalar_type() != kF32 || t->dim() != 3 || !t->is_contiguous() || t->size(0) != p.num_pages ||
+      t->size(1) != p.heads || t->size(2) < 1 || p.page % t->size(2) != 0)
+    refuse("%s must be a contiguous Float tensor [pages][heads][blocks of a page]", name);
+  const int32_t tokens = p.page / (int32_t)t->size(2);
+  if (block != 0 && block != tokens) refuse("k_scale and v_scale have blocks of another size");
+  block = tokens;
+  return static_cast<float*>(t->data_ptr());
+}
+
+Pools quant_pools(Args& a, PyObject* k, PyObject* v, int layout) {
+  const Pools p = pools(a, k, v, layout);
+  if (p.k->scalar_type() != at::ScalarType::Float8_e4m3fn && p.k->scalar_type() != at::ScalarType::Byte)
+    refuse("the pools must be of e4m3 values (Float8_e4m3fn, or Byte)");
+  return p;
+}
+
+// kv_append_quant(current device, stream, k_new, v_new, k_pool, v_pool, k_scale, v_scale, new_indptr, kv_len,
+//   page_indptr, page_indices, dev_status, max_kv_len, layout)
+PyObject* kv_append_quant(PyObject* const* o) {
+  Args a;
+  const at::Tensor* k = a.tensor(o[2], "k_new");
+  if (a.device != integer(o[0])) return done(a.device, kOtherDevice);
+  const at::Tensor* v = a.tensor(o[3], "v_new");
+  pd_kv_quant_desc d{};
+  d.k_stride = rows(*k, "k_new");
+  d.v_stride = same_rows(*v, *k, "v_new");
+  d.layout = int32(o[14], "layout");
+  const Pools p = quant_pools(a, o[4], o[5], d.layout);
+  if (p.heads != k->size(1) || p.dim != k->size(2)) refuse("the pools' heads or head_dim are not those of k_new");
+  float* ks = scales(a, o[6], p, "k_scale", d.scale_block);
+  float* vs = scales(a, o[7], p, "v_scale", d.scale_block);
+  if (k->size(0) > INT32_MAX) refuse("too many rows");
+  pd_batch b{};
+  b.kv_len = a.vector<int32_t>(o[9], "kv_len", kI32);
+  const int64_t B = THPVariable_Unpack(o[9]).numel();
+  b.batch_size = (int32_t)B;
+  b.qo_indptr = a.vector<int32_t>(o[8], "new_indptr", kI32, B + 1);
+  b.page_indptr = a.vector<int32_t>(o[10], "page_indptr", kI32, B + 1);
+  b.page_indices = a.vector<int32_t>(o[11], "page_indices", kI32);
+  auto* status = a.vector<int32_t>(o[12], "dev_status", kI32, 1, true);
+  b.num_pages = p.num_pages;
+  b.total_qo = (int32_t)k->size(0);
+  b.max_kv_len = int32(o[13], "max_kv_len");
+  d.num_kv_heads = p.heads;
+  d.head_dim = p.dim;
+  d.page_size = p.page;
+  d.dtype = dtype_code(k->scalar_type(), "k_new");
+  return done(a.device, unlocked(g_kv_append_quant, &d, &b, k->data_ptr(), v->data_ptr(), p.k->data_ptr(),
+                                 p.v->data_ptr(), ks, vs, status, stream_of(o[1])));
+}
+
 // attn_chunk(current device, stream, q, k_pool, v_pool, kv_len, page_indptr, page_indices, qo_indptr, o, lse, workspace,
 //   dev_status, causal, window_left, sm_scale, max_qo_len, max_kv_len, layout); a workspace that is missing or too small
 //   gives (the bytes needed, PD_ERR_WORKSPACE)
+// attn_chunk_quant: the same over 8-bit pools, and k_scale and v_scale at the end
+template <bool QUANT>
 PyObject* attn_chunk(PyObject* const* o) {
   Args a;
   const at::Tensor* q = a.tensor(o[2], "q");
   if (a.device != integer(o[0])) return done(a.device, kOtherDevice);
   pd_attn_desc d{};
   d.layout = int32(o[18], "layout");
-  const Pools p = pools(a, o[3], o[4], d.layout);
-  if (p.k->scalar_type() != q->scalar_type()) refuse("q and the pools differ in dtype");
+  const Pools p = QUANT ? quant_pools(a, o[3], o[4], d.layout) : pools(a, o[3], o[4], d.layout);
+  if (!QUANT && p.k->scalar_type() != q->scalar_type()) refuse("q and the pools differ in dtype");
+  int32_t block = 0;
+  const float* ks = QUANT ? scales(a, o[19], p, "k_scale", block) : nullptr;
+  const float* vs = QUANT ? scales(a, o[20], p, "v_scale", block) : nullptr;
   const int64_t stride = rows(*q, "q");
   if (q->size(2) != p.dim) refuse("q and the pools differ in head_dim");
   if (q->size(0) > INT32_MAX) refuse("too many rows");
@@ -303,11 +400,15 @@ PyObject* attn_chunk(PyObject* const* o) {
   d.sm_scale = o[15] == Py_None ? 0.f : (float)real(o[15]);
   const int32_t window = o[14] == Py_None ? -1 : int32(o[14], "window_left");
   int rc = PD_ERR_WORKSPACE;
-  if (ws != nullptr)
+  if (ws != nullptr && QUANT)
+    rc = unlocked(g_chunk_quant, &d, &b, block, window, stride, q->data_ptr(), p.k->data_ptr(), p.v->data_ptr(), ks, vs,
+                  out->data_ptr(), lse, ws->data_ptr(), ws->numel() * ws->element_size(), status, stream_of(o[1]));
+  else if (ws != nullptr)
     rc = unlocked(g_attn_chunk, &d, &b, window, stride, q->data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
                   out->data_ptr(), lse, ws->data_ptr(), ws->numel() * ws->element_size(), status, stream_of(o[1]));
   if (rc != PD_ERR_WORKSPACE) return done(a.device, rc);
-  return Py_BuildValue("(Ki)", (unsigned long long)g_chunk_workspace(&d, &b), rc);
+  const size_t need = QUANT ? g_chunk_quant_workspace(&d, &b, block) : g_chunk_workspace(&d, &b);
+  return Py_BuildValue("(Ki)", (unsigned long long)need, rc);
 }
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -336,6 +437,11 @@ PyObject* init(PyObject* const* o) {
   g_norm_rope_append = reinterpret_cast<decltype(g_norm_rope_append)>(integer(o[3]));
   g_attn_chunk = reinterpret_cast<decltype(g_attn_chunk)>(integer(o[4]));
   g_chunk_workspace = reinterpret_cast<decltype(g_chunk_workspace)>(integer(o[5]));
+  g_norm_rope_axes = reinterpret_cast<decltype(g_norm_rope_axes)>(integer(o[6]));
+  g_norm_rope_axes_append = reinterpret_cast<decltype(g_norm_rope_axes_append)>(integer(o[7]));
+  g_kv_append_quant = reinterpret_cast<decltype(g_kv_append_quant)>(integer(o[8]));
+  g_chunk_quant = reinterpret_cast<decltype(g_chunk_quant)>(integer(o[9]));
+  g_chunk_quant_workspace = reinterpret_cast<decltype(g_chunk_quant_workspace)>(integer(o[10]));
   Py_RETURN_NONE;
 }
 
@@ -344,11 +450,15 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<init, 6>("init"),
+PyMethodDef g_methods[] = {method<init, 11>("init"),
                            method<batch_tables, 20>("batch_tables"),
-                           method<norm_rope, 12>("norm_rope"),
-                           method<norm_rope_append, 17>("norm_rope_append"),
-                           method<attn_chunk, 19>("attn_chunk"),
+                           method<norm_rope<false>, 12>("norm_rope"),
+                           method<norm_rope<true>, 13>("norm_rope_axes"),
+                           method<norm_rope_append<false>, 17>("norm_rope_append"),
+                           method<norm_rope_append<true>, 18>("norm_rope_axes_append"),
+                           method<kv_append_quant, 15>("kv_append_quant"),
+                           method<attn_chunk<false>, 19>("attn_chunk"),
+                           method<attn_chunk<true>, 21>("attn_chunk_quant"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pd_bind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -12,6 +12,7 @@
 
 #include "pd_chunk.cuh"
 #include "pd_launch.cuh"
+#include "pd_quant.cuh"
 
 namespace pd {
 
@@ -131,7 +132,8 @@ constexpr size_t simt_smem() {
   return sizeof(float) * (size_t)(R * (D + 4) + kSimtKeys * (D + 4) + kSimtKeys * (R + 4));
 }
 
-template <typename T, int R, int D>
+// QUANT: pools of 8-bit values with block scales (the value enters the tile as fp32, times its scale).
+template <typename T, int R, int D, bool QUANT>
 __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const ChunkParams p) {
   constexpr int RT = R / 16, LD = D + 4, LP = R + 4, CT = D / 64;  // CT: float4 columns of a thread
   extern __shared__ float4 simt_smem_raw[];
@@ -148,7 +150,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   }
   constexpr int VE = 16 / sizeof(T), VR = D / VE;  // elements of a 16-byte vector, vectors of a row
-  constexpr int NV = kSimtKeys * VR / kSimtThreads;  // vectors of a tile per thread
+  constexpr int KE = QUANT ? 16 : VE, KR = D / KE;     // the same of the pools' rows
+  constexpr int NV = kSimtKeys * KR / kSimtThreads;  // vectors of a tile per thread
   ChunkItem I;
   while (walk.next(p, I)) {
     const int rows = I.tokens * p.tile_heads;
@@ -193,19 +196,21 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
     // A thread's vectors of the rows of keys [k0, k0 + 64): fetched into
     // registers, K's a tile ahead and V's while the scores are computed, then put
     // into shared memory. Keys that no row of the item sees are zero.
-    auto fetch = [&](const void* pool, int k0, uint4 (&v)[NV]) {
+    float factor[NV];  // of a thread's vectors (QUANT)
+    auto fetch = [&](const void* pool, const float* scale, int k0, uint4 (&v)[NV]) {
       int page[NV];
 #pragma unroll
       for (int x = 0; x < NV; ++x) {
-        const int j = k0 + (tid + x * kSimtThreads) / VR;
+        const int j = k0 + (tid + x * kSimtThreads) / KR;
         page[x] = -1;
         if (j >= I.keys.lo && j < I.keys.hi)
           page[x] = p.page_indices[I.pbase + (p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size)];
       }
 #pragma unroll
       for (int x = 0; x < NV; ++x) {
-        const int i = tid + x * kSimtThreads, c = i % VR, j = k0 + i / VR;
+        const int i = tid + x * kSimtThreads, c = i % KR, j = k0 + i / KR;
         v[x] = make_uint4(0u, 0u, 0u, 0u);
+        factor[x] = 0.f;
         if (j < I.keys.lo || j >= I.keys.hi) continue;
         if (page[x] < 0 || page[x] >= p.num_pages) {
           report(p.status, PD_DEV_BAD_PAGE_TABLE);
@@ -214,15 +219,28 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
         const int slot = p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
         const int64_t row = p.nhd ? ((int64_t)page[x] * p.page_size + slot) * p.hkv + kv_head
                                   : ((int64_t)page[x] * p.hkv + kv_head) * p.page_size + slot;
-        v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE));
+        if constexpr (QUANT) {
+          v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) + row * D + c * KE));
+          factor[x] = __ldg(scale + ((int64_t)page[x] * p.hkv + kv_head) * (p.page_size / p.scale_block) +
+                            slot / p.scale_block);
+        } else {
+          v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE));
+        }
       }
     };
     auto put = [&](const uint4 (&v)[NV]) {
 #pragma unroll
       for (int x = 0; x < NV; ++x) {
         const int i = tid + x * kSimtThreads;
-        float4* to = reinterpret_cast<float4*>(sKV + (i / VR) * LD + (i % VR) * VE);
-        if constexpr (sizeof(T) == 4) {
+        float4* to = reinterpret_cast<float4*>(sKV + (i / KR) * LD + (i % KR) * KE);
+        if constexpr (QUANT) {
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = unpack_e4m3x2(w[e] & 0xffffu), b = unpack_e4m3x2(w[e] >> 16);
+            to[e] = make_float4(a.x * factor[x], a.y * factor[x], b.x * factor[x], b.y * factor[x]);
+          }
+        } else if constexpr (sizeof(T) == 4) {
           to[0] = make_float4(__uint_as_float(v[x].x), __uint_as_float(v[x].y), __uint_as_float(v[x].z),
                               __uint_as_float(v[x].w));
         } else {
@@ -233,13 +251,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
     };
     const bool has_rows = (tid >> 5) * 2 * RT < rows;  // of this warp's; the others only load
     uint4 kv[NV];
-    if (I.t0 < I.t1) fetch(p.k_pool, (I.tile0 + I.t0) * kSimtKeys, kv);
+    if (I.t0 < I.t1) fetch(p.k_pool, p.k_scale, (I.tile0 + I.t0) * kSimtKeys, kv);
     for (int t = I.t0; t < I.t1; ++t) {
       const int k0 = (I.tile0 + t) * kSimtKeys;
       __syncthreads();
       put(kv);
       __syncthreads();
-      fetch(p.v_pool, k0, kv);
+      fetch(p.v_pool, p.v_scale, k0, kv);
       if (has_rows) {
         float s[RT][4];
 #pragma unroll
@@ -295,7 +313,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
       __syncthreads();  // the scores have read K, and the weights are written
       put(kv);
       __syncthreads();
-      if (t + 1 < I.t1) fetch(p.k_pool, k0 + kSimtKeys, kv);
+      if (t + 1 < I.t1) fetch(p.k_pool, p.k_scale, k0 + kSimtKeys, kv);
       if (!has_rows) continue;
 #pragma unroll 8
       for (int key = 0; key < kSimtKeys; ++key) {
@@ -640,7 +658,8 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkPar
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // The tensor cores take bf16, in pages of whole groups of the swizzle's 8 rows;
   // the CUDA cores take the rest.
-  p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0;
+  const bool quant = p.scale_block > 0;
+  p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && !quant;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
     p.tile_tokens = 128 / p.tile_heads;
@@ -653,12 +672,14 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     // Rows of an item: 4 or 16 where that takes a request's rows in one go or in a
     // few (the kernel for few rows), else 64.
     const int64_t most = (int64_t)p.max_qo_len * p.group;
-    p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
+    // 8-bit pools have the tiled kernel alone, in which 16 rows cost a fourth of 64.
+    if (quant) p.rows = most <= 16 && p.group <= 16 ? 16 : 64;
+    else p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * (p.rows == 64 ? 2 : 1);  // CTAs that an SM holds
+    p.max_parts = device_sm_count() * (p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)
@@ -730,7 +751,14 @@ cudaError_t launch_simt(const ChunkParams& p, cudaStream_t stream) {
     return launch_cores<chunk_rows_kernel<T, 4, D>>("chunk_rows_kernel", kRowsThreads, RowsShape<T, 4, D>::kSmem, p, stream);
   if (p.rows == 16)
     return launch_cores<chunk_rows_kernel<T, 16, D>>("chunk_rows_kernel", kRowsThreads, RowsShape<T, 16, D>::kSmem, p, stream);
-  return launch_cores<chunk_simt_kernel<T, 64, D>>("chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
+  return launch_cores<chunk_simt_kernel<T, 64, D, false>>("chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_quant_simt(const ChunkParams& p, cudaStream_t stream) {
+  if (p.rows == 16)
+    return launch_cores<chunk_simt_kernel<T, 16, D, true>>("chunk_simt_kernel", kSimtThreads, simt_smem<16, D>(), p, stream);
+  return launch_cores<chunk_simt_kernel<T, 64, D, true>>("chunk_simt_kernel", kSimtThreads, simt_smem<64, D>(), p, stream);
 }
 
 }  // namespace
@@ -742,6 +770,10 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   const bool d64 = p.head_dim == 64;
   if (p.tc)
     e = launch_chunk_tc(p, stream);
+  else if (p.scale_block > 0 && kv_dtype == PD_BF16)
+    e = d64 ? launch_quant_simt<uint16_t, 64>(p, stream) : launch_quant_simt<uint16_t, 128>(p, stream);
+  else if (p.scale_block > 0)
+    e = d64 ? launch_quant_simt<float, 64>(p, stream) : launch_quant_simt<float, 128>(p, stream);
   else if (kv_dtype == PD_BF16)
     e = d64 ? launch_simt<uint16_t, 64>(p, stream) : launch_simt<uint16_t, 128>(p, stream);
   else

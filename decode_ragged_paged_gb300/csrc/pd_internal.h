@@ -132,6 +132,27 @@ int launch_kv_append(const KvCopyParams& p, cudaStream_t stream);
 int launch_kv_pack(const KvCopyParams& p, cudaStream_t stream);
 int launch_kv_unpack(const KvCopyParams& p, cudaStream_t stream);
 
+// -------------------------------------------------------- 8-bit KV append
+struct KvQuantParams {
+  int32_t batch, hkv, head_dim, page_size, scale_block, num_pages, total, max_kv_len, nhd;
+  // set by the launcher: rows and (K or V, head) pairs of a CTA, warps that take a block's head together,
+  // log2 of a row's vectors (-1: no power of two)
+  int32_t rows, per_slice, team_warps, vpr_shift;
+  int64_t k_stride, v_stride;  // elements between tokens
+  const int32_t* new_indptr;
+  const int32_t* kv_len;
+  const int32_t* page_indptr;
+  const int32_t* page_indices;
+  const void* k_new;
+  const void* v_new;
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int32_t* status;
+};
+int launch_kv_append_quant(KvQuantParams& p, int32_t elem_size, cudaStream_t stream);
+
 // -------------------------------------------------------------- MLA decode
 // Workspace (offsets 256-byte aligned):
 //   hdr        int32[64]   hdr[0] = chunks listed, hdr[1] = chunk length
@@ -219,6 +240,9 @@ struct NormRopeParams {
   const void* k_weight;
   const float* inv_freq;
   const int32_t* positions;
+  int32_t num_axes;        // 0: one position a token
+  int64_t axis_stride;     // positions between one axis and the next
+  uint32_t axis_bits[16];  // the axis of every frequency, two bits each
   const int64_t* slot_map;  // null: k goes to rows of k_out
   void* q_out;
   void* k_out;  // rows or pool
@@ -227,6 +251,8 @@ struct NormRopeParams {
 };
 int32_t norm_rope_vec(const NormRopeParams& p, int32_t elem_size, uintptr_t addresses);
 int launch_norm_rope(NormRopeParams& p, int32_t elem_size, int32_t vec, cudaStream_t stream);
+cudaError_t launch_norm_rope_axes(const NormRopeParams& p, int32_t elem_size, int32_t vec, unsigned grid,
+                                  cudaStream_t stream);
 
 // --------------------------------------------------------- chunk attention
 // An item is (request, block of item_tokens query tokens, tile_heads query
@@ -256,6 +282,7 @@ struct ChunkParams {
   int32_t grid;        // CTAs
   int32_t tile_heads, tile_tokens, item_heads, item_tokens, item_cost, min_units, rows, max_blocks, max_parts;
   float scale_log2;  // softmax scale times log2(e)
+  int32_t scale_block;  // tokens of a block of 8-bit pools; 0: pools of q's own type
   int64_t q_stride;  // elements between query tokens
   const int32_t* qo_indptr;
   const int32_t* kv_len;
@@ -264,6 +291,8 @@ struct ChunkParams {
   const void* q;
   const void* k_pool;
   const void* v_pool;
+  const float* k_scale;  // [page][head][block] of 8-bit pools
+  const float* v_scale;
   void* o;
   float* lse;
   int32_t* hdr;
@@ -278,18 +307,22 @@ struct ChunkParams {
 struct ChunkLayout {
   size_t hdr, req_first, pre, pos, cuts, part_lse, part_o, total;
 };
-// Fills the tiling of p (its sizes and types are set) and returns the workspace layout.
+// Fills the tiling of p (its sizes and types are set; kv_dtype: q's and, unless they are 8-bit, the
+// pools') and returns the workspace layout.
 ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype);
 // Whether 32 bits number the items and count the line's units, whatever the lengths are.
 bool chunk_fits(const ChunkParams& p);
 int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_quant_tc(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
 bool make_pool_map(CUtensorMap* map, const void* pool, int32_t dtype, int32_t num_pages, int32_t hkv,
                    int32_t page_size, int32_t head_dim, int32_t box_cols, int32_t box_rows, bool swizzle128,
                    bool nhd = false);
+bool make_code_map(CUtensorMap* map, const void* pool, int32_t num_pages, int32_t hkv, int32_t page_size,
+                   int32_t head_dim, int32_t box_rows, bool swizzle, bool nhd);
 bool make_rows_map(CUtensorMap* map, const void* base, int32_t dtype, int32_t total, int32_t hq, int32_t head_dim,
                    int32_t box_cols, int32_t box_rows, bool swizzle128, int32_t box_heads = 1,
                    int64_t row_stride = 0);

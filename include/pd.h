@@ -299,6 +299,25 @@ PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_
                          void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * pd_attn_chunk over a cache held in 8 bits (pools and scales as pd_kv_append_quant
+ * leaves them; any scales that are finite and not negative will do). desc->kv_dtype is q's
+ * type. Rows, masks, empty rows, lengths, limits and capture as pd_attn_chunk; keys that no
+ * token of the request sees may hold anything, their blocks' scales too.
+ *   k_scale, v_scale  device fp32 [num_pages][num_kv_heads][page_size / scale_block]
+ *   workspace         pd_attn_chunk_quant_workspace_size(desc, batch, scale_block) bytes
+ * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores: a
+ * query enters the products with K as two e4m3 terms of its row's scale, which leaves at
+ * most 2^-17 of the row's largest value, V as bf16 of value times scale, and
+ * the softmax weights as in pd_attn_chunk. Other calls run in fp32 on the CUDA cores.
+ */
+PD_API size_t pd_attn_chunk_quant_workspace_size(const pd_attn_desc *desc, const pd_batch *batch,
+                                                 int32_t scale_block);
+PD_API int pd_attn_chunk_quant(const pd_attn_desc *desc, const pd_batch *batch, int32_t scale_block,
+                               int32_t window_left, int64_t q_stride, const void *q, const void *k_pool,
+                               const void *v_pool, const float *k_scale, const float *v_scale, void *o, float *lse,
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * MLA decode (section "Disaggregated Deployments", "DeepSeek-R1": multi-head
  * latent attention compresses the KV heads of a token into one latent vector
  * that every query head reads, so the cache holds one row per token and is
@@ -442,6 +461,26 @@ PD_API int pd_qk_norm_rope_append(const pd_norm_rope_desc *desc, int32_t num_tok
                                   void *q_out, void *k_pool, void *v_pool, int32_t *dev_status, void *stream);
 
 /*
+ * The same for positions with several axes: a token of an image or a video has a time, a
+ * height and a width, and each frequency turns by one of them:
+ *   t = positions[axis * axis_stride + token] * inv_freq[i], axis = freq_axis[i]
+ *   num_axes    1 .. 4 (more: PD_ERR_UNSUPPORTED)
+ *   axis_stride entries of positions from one axis to the next; 0: all axes read the same
+ *   freq_axis   host [rope_dim / 2], read during the call: the axis of every frequency, in
+ *               any order (runs of one axis after another, or axes that take turns)
+ * rope_dim must not be 0. Everything else is as in the forms with one position a token.
+ */
+PD_API int pd_qk_norm_rope_axes(const pd_norm_rope_desc *desc, int32_t num_tokens, int32_t num_axes,
+                                int64_t axis_stride, const uint8_t *freq_axis, const void *q, const void *k,
+                                const void *q_weight, const void *k_weight, const float *inv_freq,
+                                const int32_t *positions, void *q_out, void *k_out, void *stream);
+PD_API int pd_qk_norm_rope_axes_append(const pd_norm_rope_desc *desc, int32_t num_tokens, int32_t num_axes,
+                                       int64_t axis_stride, const uint8_t *freq_axis, const void *q, const void *k,
+                                       const void *v, const void *q_weight, const void *k_weight,
+                                       const float *inv_freq, const int32_t *positions, const int64_t *slot_map,
+                                       void *q_out, void *k_pool, void *v_pool, int32_t *dev_status, void *stream);
+
+/*
  * KV append (section "KV Messenger": page copies of a layer start once the
  * model has appended that layer's KV entries). The batch's qo_indptr counts
  * the new tokens: request r brings n_r = qo_indptr[r+1] - qo_indptr[r] rows of
@@ -452,6 +491,38 @@ PD_API int pd_qk_norm_rope_append(const pd_norm_rope_desc *desc, int32_t num_tok
 PD_API int pd_kv_append(const pd_kv_desc *desc, const pd_batch *batch, const void *k_new,
                  const void *v_new, void *k_pool, void *v_pool, int32_t *dev_status,
                  void *stream);
+
+/*
+ * KV append to a cache held in 8 bits: pools of e4m3 values (a sign, 4 bits of exponent, 3
+ * of mantissa) with an fp32 scale for each block of scale_block tokens of a page and each
+ * head, in arrays k_scale, v_scale [num_pages][num_kv_heads][page_size / scale_block] for
+ * either pool layout; a value is its e4m3 value times its block's scale. Tokens, rows and
+ * places as pd_kv_append. For the new tokens x of a block:
+ *   s = the smallest power of two >= max(max |x| / 448, 2^-100)
+ *   a block that holds earlier tokens of the request takes the larger of s and the scale it
+ *   has; where that grew, its earlier values are rounded again, v = rn(v s_old / s)
+ *   v = rn(x / s)   (to the nearest, ties to even)
+ * A block without earlier tokens is begun anew, whatever its scale was. What is not finite
+ * becomes NaN and does not count in max |x|. Slots and scales of blocks without new tokens
+ * stay as they are. A block that takes new tokens must belong to one request.
+ *   k_new, v_new  device, row i at + i * stride elements, [num_kv_heads][head_dim] (dtype);
+ *                 stride 0: contiguous; times the element size a multiple of 16 bytes
+ * The same call again gives the same cache. Requests with a bad indptr or length are skipped
+ * and reported, tokens whose page id is out of range dropped and reported. Supported: head_dim a multiple of 8 up to 1024, at most 16384
+ * heads (PD_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* D */
+  int32_t page_size;    /* P >= 1 */
+  int32_t scale_block;  /* tokens of a block: divides page_size */
+  int32_t dtype;        /* pd_dtype of k_new and v_new */
+  int32_t layout;       /* pd_layout of the pools */
+  int64_t k_stride, v_stride; /* elements; 0: contiguous */
+} pd_kv_quant_desc;
+PD_API int pd_kv_append_quant(const pd_kv_quant_desc *desc, const pd_batch *batch, const void *k_new,
+                              const void *v_new, void *k_pool, void *v_pool, float *k_scale, float *v_scale,
+                              int32_t *dev_status, void *stream);
 
 /*
  * KV pack (sections "KV Messenger" and "Sharded KV cache transfers": a
