@@ -659,7 +659,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // The tensor cores take bf16, in pages of whole groups of the swizzle's 8 rows;
   // the CUDA cores take the rest.
   const bool quant = p.scale_block > 0;
-  p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && !quant;
+  p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && p.scale_block % 8 == 0;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
     p.tile_tokens = 128 / p.tile_heads;
@@ -769,7 +769,7 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   if (e != cudaSuccess) return PD_ERR_CUDA;
   const bool d64 = p.head_dim == 64;
   if (p.tc)
-    e = launch_chunk_tc(p, stream);
+    e = p.scale_block > 0 ? launch_chunk_quant_tc(p, stream) : launch_chunk_tc(p, stream);
   else if (p.scale_block > 0 && kv_dtype == PD_BF16)
     e = d64 ? launch_quant_simt<uint16_t, 64>(p, stream) : launch_quant_simt<uint16_t, 128>(p, stream);
   else if (p.scale_block > 0)

@@ -64,6 +64,32 @@ bool make_pool_map(CUtensorMap* map, const void* pool, int32_t dtype, int32_t nu
   return r == CUDA_SUCCESS;
 }
 
+// The same of a pool of 8-bit values, a box whole rows wide: swizzled for a K-major operand of
+// the tensor cores (128 bytes or, of rows of 64, 64), or as they are.
+bool make_code_map(CUtensorMap* map, const void* pool, int32_t num_pages, int32_t hkv, int32_t page_size,
+                   int32_t head_dim, int32_t box_rows, bool swizzle, bool nhd) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = (cuuint64_t)head_dim;
+  cuuint64_t dims[4] = {row, (cuuint64_t)page_size, (cuuint64_t)hkv, (cuuint64_t)num_pages};
+  cuuint64_t strides[3] = {row, (cuuint64_t)page_size * row, (cuuint64_t)hkv * page_size * row};
+  cuuint32_t box[4] = {(cuuint32_t)head_dim, (cuuint32_t)box_rows, 1, 1};
+  if (nhd) {
+    dims[1] = (cuuint64_t)hkv;
+    dims[2] = (cuuint64_t)page_size;
+    strides[1] = (cuuint64_t)hkv * row;
+    box[1] = 1;
+    box[2] = (cuuint32_t)box_rows;
+  }
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle sw = !swizzle          ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                  : CU_TENSOR_MAP_SWIZZLE_64B;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // q / o rows [total][hq][head_dim] as a 3-D tensor {head_dim, hq, total}; one box
 // = box_rows consecutive rows of box_heads consecutive heads, box_cols elements
 // wide, laid out (row, head)-major in shared memory. Rows lie row_stride elements
