@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
                                   : ((int64_t)page[x] * p.hkv + kv_head) * p.page_size + slot;
         if constexpr (QUANT) {
           v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) + row * D + c * KE));
-          factor[x] = __ldg(scale + ((int64_t)page[x] * p.hkv + kv_head) * (p.page_size / p.scale_block) +
-                            slot / p.scale_block);
+          factor[x] = fmaxf(__ldg(scale + ((int64_t)page[x] * p.hkv + kv_head) * (p.page_size / p.scale_block) +
+                                  slot / p.scale_block), kScaleMin);
         } else {
           v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + row * D + c * VE));
         }

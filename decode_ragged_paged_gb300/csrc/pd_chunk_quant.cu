@@ -38,9 +38,8 @@ constexpr int kCqThreads = 640;
 constexpr int kScaleTiles = 32;  // tiles whose K scales are kept
 constexpr int kGroups = kN / 8;  // 8-token groups of a tile
 constexpr int kCqItems = 4;      // items that the scheduler is ahead
-// Registers of a thread: 96 at launch (640 x 96 of the SM's 65536); the loaders and issuers give
-// what the softmax warps take, and the converters keep theirs: 2 x 72 + 2 x 120 + 96 = 5 x 96.
-constexpr int kRegsFew = 72, kRegsSoftmax = 128, kRegsConvert = 80;
+constexpr float kShift = 7.0f;              // log2 of the weight that a row's largest key gets
+constexpr float kWeightLimit = 32768.0f;   // 2^15: largest row sum of weights, kSumLimit 2^kShift
 
 template <int D>
 struct QuantShape {
@@ -54,9 +53,9 @@ struct QuantShape {
   static constexpr uint32_t kOffK = kQ * kQTile, kOffC = kOffK + kK * kCodes, kOffV = kOffC + kC * kCodes;
   static constexpr uint32_t kOffBar = kOffV + kV * kVTile;
   static constexpr uint32_t kOffML = kOffBar + 1024;                       // group 1's maxima and sums
-  static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // K's scales [tile][group]
-  static constexpr uint32_t kOffVS = kOffKS + kScaleTiles * kGroups * 4;   // V's [slot][group]
-  static constexpr uint32_t kOffQS = kOffVS + kC * kGroups * 4;            // the rows' scales of q [slot][row]
+  static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // scales [tile][K, V][group]
+  static constexpr uint32_t kOffLog = kOffKS + kScaleTiles * 2 * kGroups * 4;  // a softmax warp's logarithms of them
+  static constexpr uint32_t kOffQS = kOffLog + 8 * 2 * kGroups * 4;            // the rows' scales of q [slot][row]
   static constexpr size_t kSmem = kOffQS + kQ * kM * 4 + 1024;
   static_assert(kSelfBytes <= kOffBar, "the rings hold the line first");
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -90,15 +89,6 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 }
 __device__ __forceinline__ void st_shared(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-template <int REGS>
-__device__ __forceinline__ void give_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void take_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 // Two bf16 values (times f) as two e4m3 terms each: h in the low 16 bits, l in the high ones.
@@ -152,41 +142,27 @@ __device__ __forceinline__ float split_row(uint32_t tile, int row) {
   return m <= 3.4e38f ? power_of_two(e) : 1.f;
 }
 
-// 16 e4m3 values times a scale, as bf16.
-__device__ __forceinline__ void to_bf16(const uint4& v, float scale, uint32_t (&out)[8]) {
+// 16 e4m3 values as fp16, exactly.
+__device__ __forceinline__ void to_f16(const uint4& v, uint32_t (&out)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  const float2 s2 = make_float2(scale, scale);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = fmul2(unpack_e4m3x2(w[i] & 0xffffu), s2), b = fmul2(unpack_e4m3x2(w[i] >> 16), s2);
-    out[2 * i] = pack_bf16x2(a.x, a.y);
-    out[2 * i + 1] = pack_bf16x2(b.x, b.y);
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
+        : "r"(w[i]));
 }
 
-// What a score of group `i` of a tile is multiplied by for the softmax's base-2 exponents. Not 0 or
-// less than a normal number, whatever the scales: a masked score is -inf, and times 0 it would be NaN.
+// Two fp32 values -> one fp16x2 word, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What a score of a group is multiplied by for the softmax's base-2 exponents. Not 0 or less than a
+// normal number, whatever the scales: a masked score is -inf, and times 0 it would be NaN.
 __device__ __forceinline__ float group_factor(float scale, float row) { return fmaxf(scale * row, 1e-37f); }
-
-// write_remainders with a factor for each group.
-__device__ __forceinline__ void write_remainders_by_group(uint32_t t_s, const float* scales, float row, float nm) {
-  const float2 nm2 = make_float2(nm, nm);
-#pragma unroll 1
-  for (int c = kN / 32 - 1; c >= 0; --c) {
-    uint32_t v[32], w[16];
-    tmem_ld32(t_s + 32 * c, v);
-    tmem_wait_ld(v);
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float f = group_factor(scales[4 * c + e / 8], row);
-      const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), make_float2(f, f), nm2);
-      const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      const uint32_t hi = pack_bf16x2(pe.x, pe.y);
-      w[e / 2] = pack_bf16x2(pe.x - bf16_lo(hi), pe.y - bf16_hi(hi));
-    }
-    tmem_st16(t_s + kN / 2 + 16 * c, w);
-  }
-}
 
 }  // namespace
 
@@ -201,15 +177,12 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   const uint32_t base32 = smem_u32(base);
   QuantBars* bars = reinterpret_cast<QuantBars*>(base + S::kOffBar);
   float2* sML = reinterpret_cast<float2*>(base + S::kOffML);
-  const float* sKS = reinterpret_cast<const float*>(base + S::kOffKS);
-  const float* sVS = reinterpret_cast<const float*>(base + S::kOffVS);
+  const float* sScales = reinterpret_cast<const float*>(base + S::kOffKS);
   float* sQS = reinterpret_cast<float*>(base + S::kOffQS);
   volatile int* abort = &bars->abort;
   const uint32_t bars32 = smem_u32(bars);
   auto bar = [&](size_t member, uint32_t i = 0) { return bars32 + (uint32_t)member + 8 * i; };
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    return try_all(bar, parity) || warp_wait_loop(bar, parity, abort, p.status);
-  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort, p.status); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -219,11 +192,11 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       mbar_init(&bars->q_empty[i], 2 + 8);  // the groups' last scores, and every softmax warp has its rows' scales
     }
     for (int i = 0; i < S::kK; ++i) {
-      mbar_init(&bars->k_full[i], 1 + kGroups);  // the tile, and its groups' scales
+      mbar_init(&bars->k_full[i], 1 + 2 * kGroups);  // the tile, and the scales of its groups of K and V
       mbar_init(&bars->k_empty[i], 2);
     }
     for (int i = 0; i < S::kC; ++i) {
-      mbar_init(&bars->c_full[i], 1 + kGroups);
+      mbar_init(&bars->c_full[i], 1);
       mbar_init(&bars->c_empty[i], 4);
     }
     for (int i = 0; i < S::kV; ++i) {
@@ -272,7 +245,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     return I.tokens > 0;
   };
   if (warp < 8) {
-  give_registers<kRegsFew>();
   if (warp == 6) {
     // ------------------------------------------------------------ scheduler
     ChunkWalk walk;
@@ -296,13 +268,14 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     // ----------------------------------------------------------- K, V loads
     // A lane has one of the tile's 8-token groups (in turn): its page, read a tile ahead, and its
     // scale. One thread issues the boxes, a page's each.
-    const bool is_v = warp == 2, leader = elect_one();
+    const bool is_v = warp == 2;
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-    const uint32_t ring = base32 + (is_v ? S::kOffC : S::kOffK), scales = base32 + (is_v ? S::kOffVS : S::kOffKS);
+    uint8_t* ring = base + (is_v ? S::kOffC : S::kOffK);
+    const uint32_t scales = base32 + S::kOffKS;
     const size_t full = is_v ? offsetof(QuantBars, c_full) : offsetof(QuantBars, k_full);
     const size_t empty = is_v ? offsetof(QuantBars, c_empty) : offsetof(QuantBars, k_empty);
     const uint32_t slots = is_v ? S::kC : S::kK;
-    const float* scale = is_v ? p.v_scale : p.k_scale;
+    const float* scale = lane < kGroups ? p.k_scale : p.v_scale;
     const int pb = page_box(p.page_size), boxes = kN / pb, per_box = pb / 8, blocks = p.page_size / p.scale_block;
     uint32_t slot = 0, turn = 0, count = 0;
     bool ok = true;
@@ -333,23 +306,29 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         }
         ok = wait(bar(empty, slot), (turn & 1u) ^ 1u);
         if (!ok) break;
-        const uint32_t f = bar(full, slot);
-        if (lane < kGroups) {
+        if (!is_v && lane < 2 * kGroups) {
           // (a group that no row of the item sees may have anything as its scale: it gets 0)
           const bool there = id < p.num_pages && key < I.keys.hi && key + 8 > I.keys.lo;
           const int64_t from = there ? ((int64_t)id * p.hkv + kv_head) * blocks + off / p.scale_block : 0;
-          copy_word_async(scales + ((is_v ? slot : count & (kScaleTiles - 1)) * kGroups + lane) * 4, scale + from, there);
-          copy_async_arrive(f);
+          copy_word_async(scales + ((count & (kScaleTiles - 1)) * 2 * kGroups + lane) * 4, scale + from, there);
+          copy_async_arrive(bar(full, slot));
         }
-        const uint32_t to = ring + slot * S::kCodes;
-        if (leader) mbar_arrive_expect_tx(is_v ? &bars->c_full[slot] : &bars->k_full[slot], S::kCodes);
+        int bid[8], boff[8];
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
           if (b == boxes) break;
-          const int bid = __shfl_sync(0xffffffffu, id, b * per_box), boff = __shfl_sync(0xffffffffu, off, b * per_box);
-          if (leader)
-            tma_load_4d(base + (to - base32) + b * pb * D, map, 0, p.nhd ? kv_head : boff, p.nhd ? boff : kv_head, bid,
-                        is_v ? &bars->c_full[slot] : &bars->k_full[slot]);
+          bid[b] = __shfl_sync(0xffffffffu, id, b * per_box);
+          boff[b] = __shfl_sync(0xffffffffu, off, b * per_box);
+        }
+        if (elect_one()) {
+          uint64_t* full_at = is_v ? &bars->c_full[slot] : &bars->k_full[slot];
+          uint8_t* to = ring + slot * S::kCodes;
+          mbar_arrive_expect_tx(full_at, S::kCodes);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            if (b == boxes) break;
+            tma_load_4d(to + b * pb * D, map, 0, p.nhd ? kv_head : boff[b], p.nhd ? boff[b] : kv_head, bid[b], full_at);
+          }
         }
         __syncwarp();
         ++count;
@@ -428,13 +407,13 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   } else if (warp == 3 || warp == 7) {
     // --------------------------------------------------------------- O += P V
     const int g = warp >> 2;
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(kM, D, 1);
+    constexpr uint32_t idesc_pv = idesc_f16_f32(kM, D, 1);
     const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
     uint32_t vs = 0, vturn = 0, own = 0;
     bool ok = true;
     while (ok && next_item()) {
       const int nt = I.t1 - I.t0;
-      const bool two = two_tiles(p, I), few = few_keys(p, I);
+      const bool two = two_tiles(p, I);
       const int i0 = two ? 0 : g;
       for (int i = 0; i < nt; ++i) {
         ok = wait(bar(offsetof(QuantBars, v_full), vs), vturn & 1u);
@@ -452,11 +431,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk)
               tc_mma_f16_tmem_a(t_o, t_p + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, kk > 0 ? 1u : more);
-            if (few) {  // and their remainders
-#pragma unroll
-              for (int kk = 0; kk < kN / 16; ++kk)
-                tc_mma_f16_tmem_a(t_o, t_p + kN / 2 + 8 * kk, desc_advance(dv, kk * 2048), idesc_pv, 1u);
-            }
             tc_commit(&bars->pv_done[g][buf]);
           }
           __syncwarp();
@@ -480,16 +454,16 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     __syncwarp();
   }
   } else if (warp < 16) {
-    take_registers<kRegsSoftmax>();
     // ----------------------------------------------------- softmax, epilogue
     const int g = (warp - 8) >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    float* logs = reinterpret_cast<float*>(base + S::kOffLog) + (warp - 8) * 2 * kGroups;
     uint32_t own = 0, merges = 0, q = 0, qturn = 0, count = 0;
     bool ok = true;
     while (ok && next_item()) {
       const int nt = max(I.t1 - I.t0, 0);
-      const bool two = two_tiles(p, I), few = few_keys(p, I);
+      const bool two = two_tiles(p, I);
       const int half_tok = p.tile_tokens;
       const int tokens = two ? (g == 0 ? half_tok : I.tokens - half_tok) : I.tokens;  // of this group's tile
       const int tok0 = two && g == 1 ? half_tok : 0;
@@ -526,42 +500,56 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           tc_fence_after();
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
-          if (!full) hide_scores_inline(t_s, c_lo, c_hi);
-          const float* scales = sKS + ((count + i) & (kScaleTiles - 1)) * kGroups;
+          if (!full) hide_scores(t_s, c_lo, c_hi);
+          const float* scales = sScales + ((count + i) & (kScaleTiles - 1)) * 2 * kGroups;
+          if (lane < kGroups) {
+            const float b = log2f(fmaxf(scales[kGroups + lane], kScaleMin));
+            logs[lane] = b;
+            logs[kGroups + lane] = exp2f(-b);
+          }
+          __syncwarp();
           uint32_t w[kN / 2];
-          float2 sum[2];
-          // weights of the tile with maximum m, as bf16 pairs, and their sum
+          float total, part;  // of the tile's weights, and of them over V's scales
+          // weights of the tile, as fp16 pairs
           auto weights = [&](float nm) {
-            const float2 nm2 = make_float2(nm, nm);
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
-            uint32_t v[2][32];
-            tmem_ld32(t_s, v[0]);
-            tmem_ld32(t_s + 32, v[1]);
+            total = part = 0.f;
+            uint32_t v[2][16];
+            tmem_ld16(t_s, v[0]);
             tmem_wait_ld(v[0]);
-            tmem_wait_ld(v[1]);
 #pragma unroll
-            for (int c = 0; c < kN / 32; ++c) {
-              const float4 a = *reinterpret_cast<const float4*>(scales + 4 * c);
-              const float f[4] = {group_factor(a.x, rs), group_factor(a.y, rs), group_factor(a.z, rs),
-                                  group_factor(a.w, rs)};
+            for (int c = 0; c < kN / 16; ++c) {
+              if (c + 1 < kN / 16) tmem_ld16(t_s + 16 * (c + 1), v[(c + 1) & 1]);
+              const float2 a = *reinterpret_cast<const float2*>(scales + 2 * c);
+              const float2 b = *reinterpret_cast<const float2*>(logs + 2 * c);
+              const float2 r = *reinterpret_cast<const float2*>(logs + kGroups + 2 * c);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 x = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
-                                       make_float2(f[e / 8], f[e / 8]), nm2);
-                const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                w[16 * c + e / 2] = pack_bf16x2(pe.x, pe.y);
-                sum[(e / 2) & 1] = fadd2(sum[(e / 2) & 1], pe);
+              for (int h = 0; h < 2; ++h) {
+                const float f = group_factor(h ? a.y : a.x, rs), x0 = (h ? b.y : b.x) + nm;
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 8 * h; e < 8 * h + 8; e += 2) {
+                  const float2 x = ffma2(make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])),
+                                         make_float2(f, f), make_float2(x0, x0));
+                  const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                  w[8 * c + e / 2] = pack_f16x2(pe.x, pe.y);
+                  sum = fadd2(sum, pe);
+                }
+                const float s = sum.x + sum.y;
+                total += s;
+                part = fmaf(s, h ? r.y : r.x, part);
               }
+              if (c + 1 < kN / 16) tmem_wait_ld(v[(c + 1) & 1]);
             }
           };
           bool stale = __all_sync(0xffffffffu, m > -INFINITY), over = false;
-          if (stale) {
-            weights(-m);
-            const float s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            over = __any_sync(0xffffffffu, valid && s > kSumLimit);
-            stale = !over;
-          }
-          if (!stale) {
+#pragma unroll 1
+          while (true) {
+            if (stale) {
+              weights(m == -INFINITY ? 0.f : -m);
+              if (over) break;  // with the tile's own maximum
+              over = __any_sync(0xffffffffu, valid && total > kWeightLimit);
+              if (!over) break;
+            }
             // the tile's own maximum
             float ms = -INFINITY;
 #pragma unroll 1
@@ -575,14 +563,15 @@ __global__ void __launch_bounds__(kCqThreads, 1)
 #pragma unroll
                 for (int x = 1; x < 7; x += 2) mx = fmax3(mx, __uint_as_float(v[e + x]), __uint_as_float(v[e + x + 1]));
                 mx = fmaxf(mx, __uint_as_float(v[e + 7]));
-                ms = fmaxf(ms, mx * group_factor(scales[4 * c + e / 8], rs));  // (the factor is positive)
+                // (the factor is positive)
+                ms = fmaxf(ms, fmaf(mx, group_factor(scales[4 * c + e / 8], rs), logs[4 * c + e / 8]) - kShift);
               }
             }
             float alpha = 1.f;
             if (valid && ms > -INFINITY) {
               if (m == -INFINITY) {
                 m = ms;
-              } else if (ms > (over ? m : m + kRaise)) {
+              } else if (ms > (stale ? m : m + kRaise)) {
                 // (a maximum left below a row's weights' limit would do every tile twice)
                 alpha = exp2f(m - ms);
                 m = ms;
@@ -605,10 +594,10 @@ __global__ void __launch_bounds__(kCqThreads, 1)
               }
               tmem_wait_st();
             }
-            weights(m == -INFINITY ? 0.f : -m);
+            stale = over = true;
           }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (few) write_remainders_by_group(t_s, scales, rs, m == -INFINITY ? 0.f : -m);
+          if (!ok) break;
+          l += part;
           tmem_st32(t_s, w);
           tmem_wait_st();
           tc_fence_before();
@@ -711,7 +700,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       }
     }
   } else {
-    give_registers<kRegsConvert>();
     // ------------------------------------------- q to two e4m3 terms, V to bf16
     const int t = threadIdx.x - 512;
     constexpr int kRow = D / 16, kUnits = kN * kRow / 128;  // 16-value chunks of a row, and of a thread
@@ -735,20 +723,15 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (!ok) break;
         const int k0 = I.tile(i) * kN;
         uint4 v[kUnits];
-        float s[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int c = u * 128 + t;
-          v[u] = ld_shared(base32 + S::kOffC + cs * S::kCodes + c * 16);
-          s[u] = sVS[cs * kGroups + c / kRow / 8];
-        }
+        for (int u = 0; u < kUnits; ++u) v[u] = ld_shared(base32 + S::kOffC + cs * S::kCodes + (u * 128 + t) * 16);
         ok = wait(bar(offsetof(QuantBars, v_empty), vs), (vturn & 1u) ^ 1u);
         if (!ok) break;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
           const int c = u * 128 + t, row = c / kRow, j = c % kRow;
           uint32_t w[8];
-          to_bf16(v[u], s[u], w);
+          to_f16(v[u], w);
           const int key = k0 + row;
           if (key < I.keys.lo || key >= I.keys.hi) {  // may be NaN, which a weight of 0 would not hide
 #pragma unroll

@@ -50,8 +50,7 @@ __device__ __forceinline__ bool try_all(uint32_t bar, uint32_t parity) {
 // warp_mbar_wait by try_all. The waiting itself is a function of its own: the roles'
 // loops together are more than an instruction cache holds, and 16 copies of it in
 // line cost every case 2 to 4 %.
-// (A kernel that moves registers between its warps cannot call functions: it has the loop in line.)
-__device__ __forceinline__ bool warp_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+__device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
@@ -66,10 +65,6 @@ __device__ __forceinline__ bool warp_wait_loop(uint32_t bar, uint32_t parity, vo
   }
 }
 
-__device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  return warp_wait_loop(bar, parity, abort, status);
-}
-
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   return try_all(bar, parity) || warp_wait_long(bar, parity, abort, status);
 }
@@ -77,7 +72,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // Makes the scores of a row outside columns [lo, hi) of the tile -inf, in tensor
 // memory, before a tile of a mask's edge is weighed: in line with the weights, where
 // most tiles jump over it, it made those slower (D 64: 1450 cycles a tile for 1380).
-__device__ __forceinline__ void hide_scores_inline(uint32_t t_s, int lo, int hi) {
+__device__ __noinline__ void hide_scores(uint32_t t_s, int lo, int hi) {
 #pragma unroll 1
   for (int c = 0; c < kN; c += 32) {
     const int from = lo - c, to = hi - c;
@@ -93,7 +88,6 @@ __device__ __forceinline__ void hide_scores_inline(uint32_t t_s, int lo, int hi)
   }
   tmem_wait_st();
 }
-__device__ __noinline__ void hide_scores(uint32_t t_s, int lo, int hi) { hide_scores_inline(t_s, lo, hi); }
 
 // Whether some row of the item sees fewer keys than average the weights' rounding
 // out. What a row sees grows with its position under the causal mask, and shrinks

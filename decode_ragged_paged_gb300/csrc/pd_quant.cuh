@@ -36,6 +36,8 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return max(e, -100);
 }
 
+constexpr float kScaleMin = 0x1p-100f;  // the smallest scale
+
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 

@@ -300,15 +300,15 @@ PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_
 
 /*
  * pd_attn_chunk over a cache held in 8 bits (pools and scales as pd_kv_append_quant
- * leaves them; any scales that are finite and not negative will do). desc->kv_dtype is q's
+ * leaves them; any finite scales will do, and below 2^-100 they count as that). desc->kv_dtype is q's
  * type. Rows, masks, empty rows, lengths, limits and capture as pd_attn_chunk; keys that no
  * token of the request sees may hold anything, their blocks' scales too.
  *   k_scale, v_scale  device fp32 [num_pages][num_kv_heads][page_size / scale_block]
  *   workspace         pd_attn_chunk_quant_workspace_size(desc, batch, scale_block) bytes
  * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores: a
  * query enters the products with K as two e4m3 terms of its row's scale, which leaves at
- * most 2^-17 of the row's largest value, V as bf16 of value times scale, and
- * the softmax weights as in pd_attn_chunk. Other calls run in fp32 on the CUDA cores.
+ * most 2^-17 of the row's largest value, and the softmax weights, times their keys' scales of
+ * V, enter the product with V as fp16. Other calls run in fp32 on the CUDA cores.
  */
 PD_API size_t pd_attn_chunk_quant_workspace_size(const pd_attn_desc *desc, const pd_batch *batch,
                                                  int32_t scale_block);

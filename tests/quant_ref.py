@@ -55,10 +55,10 @@ def append(x_new, pool, scale, qo, kv, pp, px, page, block, layout):
 
 
 def dequant(pool, scale, layout):
-    """[pages][...] fp64 values of an 8-bit pool, in its layout."""
+    """[pages][...] fp64 values of an 8-bit pool, in its layout (scales below 2^-100 count as that)."""
     x = heads_first(pool.view(torch.uint8).view(E4M3).double(), layout)
     block = x.shape[2] // scale.shape[2]
-    x = x * scale.double().repeat_interleave(block, 2)[..., None]
+    x = x * scale.double().clamp(min=2.0 ** -100).repeat_interleave(block, 2)[..., None]
     return heads_first(x, layout).contiguous()
 
 
