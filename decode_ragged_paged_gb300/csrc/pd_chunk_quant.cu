@@ -41,6 +41,12 @@ constexpr int kCqItems = 4;      // items that the scheduler is ahead
 constexpr float kShift = 7.0f;              // log2 of the weight that a row's largest key gets
 constexpr float kWeightLimit = 32768.0f;   // 2^15: largest row sum of weights, kSumLimit 2^kShift
 
+// A tile's scales as the softmax takes them, each twice for its packed arithmetic.
+struct Factors {
+  float4 of[kGroups];      // K's scale twice, log2 of V's scale twice
+  float inverse[kGroups];  // 1 / V's scale
+};
+
 template <int D>
 struct QuantShape {
   static constexpr uint32_t kQHalf = kM * 128, kQTile = D / 64 * kQHalf;  // query tiles: bf16, then [h | l]
@@ -54,8 +60,8 @@ struct QuantShape {
   static constexpr uint32_t kOffBar = kOffV + kV * kVTile;
   static constexpr uint32_t kOffML = kOffBar + 1024;                       // group 1's maxima and sums
   static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // scales [tile][K, V][group]
-  static constexpr uint32_t kOffLog = kOffKS + kScaleTiles * 2 * kGroups * 4;  // a softmax warp's logarithms of them
-  static constexpr uint32_t kOffQS = kOffLog + 8 * 2 * kGroups * 4;            // the rows' scales of q [slot][row]
+  static constexpr uint32_t kOffFactors = kOffKS + kScaleTiles * 2 * kGroups * 4;  // what the softmax makes of them
+  static constexpr uint32_t kOffQS = kOffFactors + kScaleTiles * sizeof(Factors);  // the rows' scales of q [slot][row]
   static constexpr size_t kSmem = kOffQS + kQ * kM * 4 + 1024;
   static_assert(kSelfBytes <= kOffBar, "the rings hold the line first");
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -160,9 +166,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// What a score of a group is multiplied by for the softmax's base-2 exponents. Not 0 or less than a
-// normal number, whatever the scales: a masked score is -inf, and times 0 it would be NaN.
-__device__ __forceinline__ float group_factor(float scale, float row) { return fmaxf(scale * row, 1e-37f); }
+// What a score of a group is multiplied by for the softmax's base-2 exponents, K's scale times the row's.
+// Never 0: a masked score is -inf, and times 0 it would be NaN.
+constexpr float kFactorMin = 1e-37f;
 
 }  // namespace
 
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   QuantBars* bars = reinterpret_cast<QuantBars*>(base + S::kOffBar);
   float2* sML = reinterpret_cast<float2*>(base + S::kOffML);
   const float* sScales = reinterpret_cast<const float*>(base + S::kOffKS);
+  Factors* sFactors = reinterpret_cast<Factors*>(base + S::kOffFactors);
   float* sQS = reinterpret_cast<float*>(base + S::kOffQS);
   volatile int* abort = &bars->abort;
   const uint32_t bars32 = smem_u32(bars);
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       mbar_init(&bars->v_empty[i], 2);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
+      mbar_init(&bars->s_full[i >> 1][i & 1], 2);  // the product, and the tile's factors
       mbar_init(&bars->p_full[i >> 1][i & 1], 4);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
@@ -276,7 +283,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const size_t empty = is_v ? offsetof(QuantBars, c_empty) : offsetof(QuantBars, k_empty);
     const uint32_t slots = is_v ? S::kC : S::kK;
     const float* scale = lane < kGroups ? p.k_scale : p.v_scale;
-    const int pb = page_box(p.page_size), boxes = kN / pb, per_box = pb / 8, blocks = p.page_size / p.scale_block;
+    const int pb = page_box(p.page_size), boxes = kN / pb, per_box = pb / 8, blocks = p.page_size / p.scale_block,
+              block_shift = 31 - __clz(p.scale_block);
     uint32_t slot = 0, turn = 0, count = 0;
     bool ok = true;
     while (ok && next_item()) {
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (!is_v && lane < 2 * kGroups) {
           // (a group that no row of the item sees may have anything as its scale: it gets 0)
           const bool there = id < p.num_pages && key < I.keys.hi && key + 8 > I.keys.lo;
-          const int64_t from = there ? ((int64_t)id * p.hkv + kv_head) * blocks + off / p.scale_block : 0;
+          const int64_t from = there ? ((int64_t)id * p.hkv + kv_head) * blocks + (POW2 ? off >> block_shift : off / p.scale_block) : 0;
           copy_word_async(scales + ((count & (kScaleTiles - 1)) * 2 * kGroups + lane) * 4, scale + from, there);
           copy_async_arrive(bar(full, slot));
         }
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const int g = warp >> 2;
     constexpr uint32_t idesc_s = idesc_e4m3_f32(kM, kN);
     uint32_t q = 0, qturn = 0, ks = 0, kturn = 0;
-    uint32_t own = 0;  // scores issued
+    uint32_t own = 0, count = 0;  // scores issued, tiles
     bool ok = true;
     while (ok && next_item()) {
       const int nt = I.t1 - I.t0;
@@ -382,6 +390,16 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           ok = own < 2 || wait(bar(offsetof(QuantBars, pv_done), 2 * g + buf), ((own - 2) >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
+          if (lane < kGroups) {
+            // (with two query tiles both groups' issuers write the same)
+            const float* at = sScales + ((count + i) & (kScaleTiles - 1)) * 2 * kGroups + lane;
+            Factors& f = sFactors[(count + i) & (kScaleTiles - 1)];
+            const float a = at[0], b = log2f(fmaxf(at[kGroups], kScaleMin));
+            f.of[lane] = make_float4(a, a, b, b);
+            f.inverse[lane] = exp2f(-b);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->s_full[g][buf]);
           const uint32_t at = __shfl_sync(0xffffffffu, base32 + S::kOffK + ks * S::kCodes, 0);
           const uint64_t dk = D == 128 ? sw128_desc(at, 16, 1024) : sw64_desc(at, 512);
           const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + col_s(g, buf), 0);
@@ -403,6 +421,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (++ks == S::kK) ks = 0, ++kturn;
       }
       if (ok && !two && g >= nt && lane == 0) mbar_arrive(&bars->q_empty[q_slot]);  // no tile of the item is its own
+      count += nt;
     }
   } else if (warp == 3 || warp == 7) {
     // --------------------------------------------------------------- O += P V
@@ -458,7 +477,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const int g = (warp - 8) >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok_row = row / p.tile_heads, head = row - tok_row * p.tile_heads;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    float* logs = reinterpret_cast<float*>(base + S::kOffLog) + (warp - 8) * 2 * kGroups;
     uint32_t own = 0, merges = 0, q = 0, qturn = 0, count = 0;
     bool ok = true;
     while (ok && next_item()) {
@@ -501,38 +519,32 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           const int c_lo = lo - k0, c_hi = hi - k0;
           const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kN);
           if (!full) hide_scores(t_s, c_lo, c_hi);
-          const float* scales = sScales + ((count + i) & (kScaleTiles - 1)) * 2 * kGroups;
-          if (lane < kGroups) {
-            const float b = log2f(fmaxf(scales[kGroups + lane], kScaleMin));
-            logs[lane] = b;
-            logs[kGroups + lane] = exp2f(-b);
-          }
-          __syncwarp();
+          const Factors& factors = sFactors[(count + i) & (kScaleTiles - 1)];
           uint32_t w[kN / 2];
           float total, part;  // of the tile's weights, and of them over V's scales
           // weights of the tile, as fp16 pairs
           auto weights = [&](float nm) {
             total = part = 0.f;
+            const float2 nm2 = make_float2(nm, nm), rs2 = make_float2(rs, rs);
             uint32_t v[2][16];
             tmem_ld16(t_s, v[0]);
             tmem_wait_ld(v[0]);
 #pragma unroll
             for (int c = 0; c < kN / 16; ++c) {
               if (c + 1 < kN / 16) tmem_ld16(t_s + 16 * (c + 1), v[(c + 1) & 1]);
-              const float2 a = *reinterpret_cast<const float2*>(scales + 2 * c);
-              const float2 b = *reinterpret_cast<const float2*>(logs + 2 * c);
-              const float2 r = *reinterpret_cast<const float2*>(logs + kGroups + 2 * c);
+              const float2 r = *reinterpret_cast<const float2*>(factors.inverse + 2 * c);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float f = group_factor(h ? a.y : a.x, rs), x0 = (h ? b.y : b.x) + nm;
+                const float4 of = factors.of[2 * c + h];
+                const float2 f = ffma2(make_float2(of.x, of.y), rs2, make_float2(kFactorMin, kFactorMin));
+                const float2 x0 = fadd2(make_float2(of.z, of.w), nm2);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int e = 8 * h; e < 8 * h + 8; e += 2) {
-                  const float2 x = ffma2(make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])),
-                                         make_float2(f, f), make_float2(x0, x0));
+                  const float2 x = ffma2(make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])), f, x0);
                   const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                   w[8 * c + e / 2] = pack_f16x2(pe.x, pe.y);
-                  sum = fadd2(sum, pe);
+                  sum = e == 8 * h ? pe : fadd2(sum, pe);
                 }
                 const float s = sum.x + sum.y;
                 total += s;
@@ -564,7 +576,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
                 for (int x = 1; x < 7; x += 2) mx = fmax3(mx, __uint_as_float(v[e + x]), __uint_as_float(v[e + x + 1]));
                 mx = fmaxf(mx, __uint_as_float(v[e + 7]));
                 // (the factor is positive)
-                ms = fmaxf(ms, fmaf(mx, group_factor(scales[4 * c + e / 8], rs), logs[4 * c + e / 8]) - kShift);
+                const float4 of = factors.of[4 * c + e / 8];
+                ms = fmaxf(ms, fmaf(mx, fmaf(of.x, rs, kFactorMin), of.z) - kShift);
               }
             }
             float alpha = 1.f;
