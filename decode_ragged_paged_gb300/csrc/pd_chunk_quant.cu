@@ -35,16 +35,17 @@ namespace pd {
 namespace {
 
 constexpr int kCqThreads = 640;
-constexpr int kScaleTiles = 32;  // tiles whose K scales are kept
+constexpr int kScaleTiles = 32;  // tiles whose factors are kept
 constexpr int kGroups = kN / 8;  // 8-token groups of a tile
-constexpr int kCqItems = 4;      // items that the scheduler is ahead
-constexpr float kShift = 7.0f;              // log2 of the weight that a row's largest key gets
-constexpr float kWeightLimit = 32768.0f;   // 2^15: largest row sum of weights, kSumLimit 2^kShift
+constexpr int kCqItems = 6;      // items that the scheduler is ahead
+constexpr float kShift = 3.0f;             // log2 of the weight of a row's largest key
+constexpr float kSumShift = kShift + 6;   // and of the sum of 64 alike
+constexpr float kWeightLimit = 32768.0f;  // 2^15: largest row sum of weights taken with a stale maximum
 
 // A tile's scales as the softmax takes them, each twice for its packed arithmetic.
 struct Factors {
-  float4 of[kGroups];      // K's scale twice, log2 of V's scale twice
-  float inverse[kGroups];  // 1 / V's scale
+  float4 of[kGroups];        // K's scale twice, log2 of V's scale twice
+  float inverse[kGroups];    // 1 / V's scale
 };
 
 template <int D>
@@ -59,8 +60,8 @@ struct QuantShape {
   static constexpr uint32_t kOffK = kQ * kQTile, kOffC = kOffK + kK * kCodes, kOffV = kOffC + kC * kCodes;
   static constexpr uint32_t kOffBar = kOffV + kV * kVTile;
   static constexpr uint32_t kOffML = kOffBar + 1024;                       // group 1's maxima and sums
-  static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // scales [tile][K, V][group]
-  static constexpr uint32_t kOffFactors = kOffKS + kScaleTiles * 2 * kGroups * 4;  // what the softmax makes of them
+  static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // scales [K's slot][K, V][group]
+  static constexpr uint32_t kOffFactors = kOffKS + kK * 2 * kGroups * 4;  // what the softmax makes of them
   static constexpr uint32_t kOffQS = kOffFactors + kScaleTiles * sizeof(Factors);  // the rows' scales of q [slot][row]
   static constexpr size_t kSmem = kOffQS + kQ * kM * 4 + 1024;
   static_assert(kSelfBytes <= kOffBar, "the rings hold the line first");
@@ -159,6 +160,13 @@ __device__ __forceinline__ void to_f16(const uint4& v, uint32_t (&out)[8]) {
         : "r"(w[i]));
 }
 
+// log2 of a normal positive number with the hardware approximation.
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two fp32 values -> one fp16x2 word, `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -240,25 +248,31 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   const uint32_t tmem = bars->tmem_slot;
   pdl_launch_dependents();
   pdl_wait_primary();  // the plan's work line, and what the cache was appended by
-  ChunkItem I{};
-  // The next item of the scheduler's, in every other warp.
+  // The next item of the scheduler's, in every other warp; and that the warp is done with it.
   uint32_t item_slot = 0, item_turn = 0;
-  auto next_item = [&]() -> bool {
-    if (!wait(bar(offsetof(QuantBars, item_full), item_slot), item_turn & 1u)) return false;
-    I = bars->items[item_slot];
+  auto await_item = [&]() -> bool {
+    return wait(bar(offsetof(QuantBars, item_full), item_slot), item_turn & 1u) && bars->items[item_slot].tokens > 0;
+  };
+  auto leave_item = [&] {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->item_empty[item_slot]);
     if (++item_slot == kCqItems) item_slot = 0, ++item_turn;
-    return I.tokens > 0;
+  };
+  auto next_item = [&](ChunkItem& I) -> bool {
+    if (!await_item()) return false;
+    I = bars->items[item_slot];
+    leave_item();
+    return true;
   };
   if (warp < 8) {
-  if (warp == 6) {
+  if (warp == 0) {
     // ------------------------------------------------------------ scheduler
     ChunkWalk walk;
     const int4 cut = walk.begin(p, take_line(p, base), blockIdx.x);
     if (lane == 0) p.cuts[blockIdx.x] = cut;
     fence_proxy_async_smem();
     __syncwarp();
+    ChunkItem I{};
     uint32_t slot = 0, turn = 0;
     for (bool more = true; more;) {
       more = walk.next(p, I);
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       __syncwarp();
       if (++slot == kCqItems) slot = 0, ++turn;
     }
-  } else if (warp == 0 || warp == 2) {
+  } else if (warp == 6 || warp == 2) {
     // ----------------------------------------------------------- K, V loads
     // A lane has one of the tile's 8-token groups (in turn): its page, read a tile ahead, and its
     // scale. One thread issues the boxes, a page's each.
@@ -285,20 +299,21 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const float* scale = lane < kGroups ? p.k_scale : p.v_scale;
     const int pb = page_box(p.page_size), boxes = kN / pb, per_box = pb / 8, blocks = p.page_size / p.scale_block,
               block_shift = 31 - __clz(p.scale_block);
-    uint32_t slot = 0, turn = 0, count = 0;
+    uint32_t slot = 0, turn = 0;
     bool ok = true;
-    while (ok && next_item()) {
+    ChunkItem I;
+    while (ok && next_item(I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const int kv_head = I.h / p.group;
       const int* list = p.page_indices + I.pbase;
-      auto place = [&](int tile) {  // of the lane's group in the request's page list
-        const int key = tile * kN + 8 * (lane & 7);
-        return POW2 ? key >> p.page_shift : key / p.page_size;
-      };
-      int next_idx = place(I.tile(0)), next = next_idx < I.need ? __ldg(list + next_idx) : 0;
+      // the lane's group of a tile: its first key, and that key's place in the request's page list
+      const int end = (I.tile0 + I.t1) * kN, rounds = nt * kN;
+      int next_key = I.tile(0) * kN + 8 * (lane & 7);
+      int next_idx = POW2 ? next_key >> p.page_shift : next_key / p.page_size;
+      int next = next_idx < I.need ? __ldg(list + next_idx) : 0;
       for (int i = 0; i < nt; ++i) {
-        const int key = I.tile(i) * kN + 8 * (lane & 7), idx = next_idx;
+        const int key = next_key, idx = next_idx;
         const int off = key - idx * p.page_size;
         // pages past the request's end, and ids outside the pools: page num_pages, which TMA reads as zeros
         int id = next;
@@ -308,17 +323,18 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           report(p.status, PD_DEV_BAD_PAGE_TABLE);
           id = p.num_pages;
         }
-        if (i + 1 < nt) {
-          next_idx = place(I.tile(i + 1));
-          next = next_idx < I.need ? __ldg(list + next_idx) : 0;
-        }
+        next_key += kN;
+        if (next_key >= end) next_key -= rounds;
+        next_idx = POW2 ? next_key >> p.page_shift : next_key / p.page_size;
+        if (i + 1 < nt) next = next_idx < I.need ? __ldg(list + next_idx) : 0;
         ok = wait(bar(empty, slot), (turn & 1u) ^ 1u);
         if (!ok) break;
         if (!is_v && lane < 2 * kGroups) {
           // (a group that no row of the item sees may have anything as its scale: it gets 0)
           const bool there = id < p.num_pages && key < I.keys.hi && key + 8 > I.keys.lo;
-          const int64_t from = there ? ((int64_t)id * p.hkv + kv_head) * blocks + (POW2 ? off >> block_shift : off / p.scale_block) : 0;
-          copy_word_async(scales + ((count & (kScaleTiles - 1)) * 2 * kGroups + lane) * 4, scale + from, there);
+          const int64_t from =
+              there ? ((int64_t)id * p.hkv + kv_head) * blocks + (POW2 ? off >> block_shift : off / p.scale_block) : 0;
+          copy_word_async(scales + (slot * 2 * kGroups + lane) * 4, scale + from, there);
           copy_async_arrive(bar(full, slot));
         }
         int bid[8], boff[8];
@@ -339,7 +355,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           }
         }
         __syncwarp();
-        ++count;
         if (++slot == slots) slot = 0, ++turn;
       }
     }
@@ -347,7 +362,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     // --------------------------------------------------------------- Q loads
     uint32_t q = 0, qturn = 0;
     bool ok = true;
-    while (ok && next_item()) {
+    ChunkItem I;
+    while (ok && next_item(I)) {
       if (I.t1 <= I.t0) continue;
       const int tiles = two_tiles(p, I) ? 2 : 1, tok = p.tile_tokens;
       for (int x = 0; ok && x < tiles; ++x) {
@@ -368,7 +384,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     uint32_t q = 0, qturn = 0, ks = 0, kturn = 0;
     uint32_t own = 0, count = 0;  // scores issued, tiles
     bool ok = true;
-    while (ok && next_item()) {
+    ChunkItem I;
+    while (ok && next_item(I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const bool two = two_tiles(p, I);
@@ -392,11 +409,11 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           tc_fence_after();
           if (lane < kGroups) {
             // (with two query tiles both groups' issuers write the same)
-            const float* at = sScales + ((count + i) & (kScaleTiles - 1)) * 2 * kGroups + lane;
+            const float* at = sScales + ks * 2 * kGroups + lane;
             Factors& f = sFactors[(count + i) & (kScaleTiles - 1)];
-            const float a = at[0], b = log2f(fmaxf(at[kGroups], kScaleMin));
+            const float a = at[0], b = fast_log2(fmaxf(at[kGroups], kScaleMin)), r = fast_exp2(-b);
             f.of[lane] = make_float4(a, a, b, b);
-            f.inverse[lane] = exp2f(-b);
+            f.inverse[lane] = r;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->s_full[g][buf]);
@@ -430,7 +447,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const uint32_t t_o = __shfl_sync(0xffffffffu, tmem + col_o(g), 0);
     uint32_t vs = 0, vturn = 0, own = 0;
     bool ok = true;
-    while (ok && next_item()) {
+    ChunkItem I;
+    while (ok && next_item(I)) {
       const int nt = I.t1 - I.t0;
       const bool two = two_tiles(p, I);
       const int i0 = two ? 0 : g;
@@ -479,7 +497,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     uint32_t own = 0, merges = 0, q = 0, qturn = 0, count = 0;
     bool ok = true;
-    while (ok && next_item()) {
+    while (ok && await_item()) {
+      const ChunkItem& I = bars->items[item_slot];  // (where it is: registers are short)
       const int nt = max(I.t1 - I.t0, 0);
       const bool two = two_tiles(p, I);
       const int half_tok = p.tile_tokens;
@@ -562,10 +581,13 @@ __global__ void __launch_bounds__(kCqThreads, 1)
               over = __any_sync(0xffffffffu, valid && total > kWeightLimit);
               if (!over) break;
             }
-            // the tile's own maximum
+            // the tile's own maximum: where weights were over the limit, out of their sum, which is between the
+            // largest and 2^6 times that; else out of the scores
             float ms = -INFINITY;
+            const bool summed = stale && __all_sync(0xffffffffu, !valid || total < 0x1p120f);
+            if (summed) ms = m + fast_log2(total) - kSumShift;
 #pragma unroll 1
-            for (int c = 0; c < kN / 32; ++c) {
+            for (int c = 0; !summed && c < kN / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(t_s + 32 * c, v);
               tmem_wait_ld(v);
@@ -623,7 +645,10 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       count += nt;
       const bool other = !two && nt > 1;  // group 1 has tiles of the same rows
       if (g == 1 && !two) {
-        if (nt < 2) continue;
+        if (nt < 2) {
+          leave_item();
+          continue;
+        }
         ok = wait(bar(offsetof(QuantBars, pv_done), 2 + ((own - 1) & 1u)), ((own - 1) >> 1) & 1u);
         if (!ok) break;
         tc_fence_after();
@@ -635,6 +660,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         ok = wait(bar(offsetof(QuantBars, merged)), merges & 1u);
         tc_fence_after();
         ++merges;
+        leave_item();
         continue;
       }
       float f0 = 1.f, f1 = 0.f;
@@ -706,19 +732,27 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
       }
       tc_fence_before();
-      __syncwarp();
+      leave_item();
       if (other) {
         if (lane == 0) mbar_arrive(&bars->merged);
         ++merges;
       }
     }
   } else {
-    // ------------------------------------------- q to two e4m3 terms, V to bf16
+    // ------------------------------------------- q to two e4m3 terms, V to fp16
+    // A thread takes 16 values of a row, and of every kStep-th row on: chunks c and c + 1 of the
+    // row's 8-value chunks, at the same place of the swizzle each time.
     const int t = threadIdx.x - 512;
-    constexpr int kRow = D / 16, kUnits = kN * kRow / 128;  // 16-value chunks of a row, and of a thread
+    constexpr int kRow = D / 16, kStep = 128 / kRow, kUnits = kN / kStep;
+    static_assert(kStep % 8 == 0, "whole swizzles");
+    const int row0 = t / kRow, j = t % kRow, c = 2 * (j % 4);
+    const uint32_t from0 = base32 + S::kOffC + t * 16;
+    const uint32_t to0 = base32 + S::kOffV + (j / 4) * S::kVHalf + row0 * 128;
+    const uint32_t to_a = to0 + ((c ^ (row0 & 7)) << 4), to_b = to0 + (((c + 1) ^ (row0 & 7)) << 4);
     uint32_t q = 0, qturn = 0, cs = 0, cturn = 0, vs = 0, vturn = 0;
     bool ok = true;
-    while (ok && next_item()) {
+    ChunkItem I;
+    while (ok && next_item(I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
       const int tiles = two_tiles(p, I) ? 2 : 1;
@@ -731,35 +765,33 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (lane == 0) mbar_arrive(&bars->q_ready[q]);
         if (++q == S::kQ) q = 0, ++qturn;
       }
+      int tile = I.tile(0);
+      const int end = I.tile0 + I.t1;
       for (int i = 0; ok && i < nt; ++i) {
         ok = wait(bar(offsetof(QuantBars, c_full), cs), cturn & 1u);
         if (!ok) break;
-        const int k0 = I.tile(i) * kN;
         uint4 v[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) v[u] = ld_shared(base32 + S::kOffC + cs * S::kCodes + (u * 128 + t) * 16);
+        for (int u = 0; u < kUnits; ++u) v[u] = ld_shared(from0 + cs * S::kCodes + u * (kStep * D));
+        const int k0 = tile * kN;
+        if (++tile == end) tile = I.tile0 + I.t0;
+        if (k0 < I.keys.lo || k0 + kN > I.keys.hi) {
+          // keys that no row sees: may be NaN, which a weight of 0 would not hide
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            const int key = k0 + u * kStep + row0;
+            if (key < I.keys.lo || key >= I.keys.hi) v[u] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
         ok = wait(bar(offsetof(QuantBars, v_empty), vs), (vturn & 1u) ^ 1u);
         if (!ok) break;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          const int c = u * 128 + t, row = c / kRow, j = c % kRow;
           uint32_t w[8];
           to_f16(v[u], w);
-          const int key = k0 + row;
-          if (key < I.keys.lo || key >= I.keys.hi) {  // may be NaN, which a weight of 0 would not hide
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 0u;
-          }
-          // chunks 2 j and 2 j + 1 of the row's 8-value chunks, 8 of them in a half; the lanes of the second half
-          // write them in the other order, so that no two of a quarter of a warp meet in a bank
-          const uint32_t at = base32 + S::kOffV + vs * S::kVTile + (j / 4) * S::kVHalf + row * 128;
-          const int first = j / 4, c0 = 2 * (j % 4);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = e ^ first;
-            st_shared(at + (((c0 + x) ^ (row & 7)) << 4),
-                      x == 0 ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(w[4], w[5], w[6], w[7]));
-          }
+          const uint32_t at = vs * S::kVTile + u * (kStep * 128);
+          st_shared(to_a + at, make_uint4(w[0], w[1], w[2], w[3]));
+          st_shared(to_b + at, make_uint4(w[4], w[5], w[6], w[7]));
         }
         fence_proxy_async_smem();
         __syncwarp();

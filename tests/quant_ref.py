@@ -62,14 +62,13 @@ def dequant(pool, scale, layout):
     return heads_first(x, layout).contiguous()
 
 
-def attention(q, k_pool, v_pool, k_scale, v_scale, qo, kv, pp, px, *, causal=True, window=-1, scale=None, layout="HND",
-              odd_scales=False):
+def attention(q, k_pool, v_pool, k_scale, v_scale, qo, kv, pp, px, *, causal=True, window=-1, scale=None, layout="HND"):
     """step_ref.attention over the values that the cache holds, its bounds widened by what the 8-bit cache's
     tensor-core form adds (bf16 queries):
       a query value is two e4m3 terms, off by at most half of e4m3's smallest step, 2^-10, where the row's
         largest value is over 224: 2^-17 of that, times sum |k| in a score, and twice in a weight;
-      a value of V is its e4m3 value times its scale, rounded to bf16: exact where scales are powers of two, half a
-        step (2^-8) where they are not."""
+      weights times their keys' scales of V are fp16 whose largest is at least 2^3 (2^2 to allow for its own
+        errors): half of fp16's smallest step, 2^-25, is 2^-27 of the largest, times the sum of the e4m3 sizes."""
     k, v = dequant(k_pool, k_scale, layout), dequant(v_pool, v_scale, layout)
     kw = dict(causal=causal, window=window, scale=scale, layout=layout)
     o, lse, ob, lb = ref.attention(q, k, v, qo, kv, pp, px, **kw)
@@ -78,12 +77,25 @@ def attention(q, k_pool, v_pool, k_scale, v_scale, qo, kv, pp, px, *, causal=Tru
     sizes = ref.attention(q, k, torch.nan_to_num(v).abs(), qo, kv, pp, px, **kw)[0]
     sm = 1 / math.sqrt(q.shape[2]) if scale is None else scale
     extra = torch.zeros(q.shape[:2], dtype=torch.float64, device=q.device)
+    floor = torch.zeros_like(o)
+    codes = dequant(v_pool, torch.ones_like(v_scale), layout)
+    spread = dequant(torch.ones_like(v_pool, dtype=torch.float32).to(E4M3), v_scale, layout)  # every slot's scale
     g = q.shape[1] // k_scale.shape[1]
     for r, n in enumerate(kv):
         a, b = qo[r], qo[r + 1]
-        if b > a and n > 0:
-            kk = torch.nan_to_num(ref.gather(k, px[pp[r]:pp[r + 1]], n, layout))
-            most = kk.abs().sum(-1).amax(0).repeat_interleave(g)  # [query head]
-            extra[a:b] = sm * 2.0 ** -17 * q[a:b].double().abs().amax(-1) * most
-    rel = 2 * extra + (2.0 ** -8 if odd_scales else 0.0)
-    return o, lse, ob + rel[..., None] * sizes, lb + extra
+        if b == a or n == 0:
+            continue
+        ids = px[pp[r]:pp[r + 1]]
+        kk, cc, bb = (torch.nan_to_num(ref.gather(x, ids, n, layout)) for x in (k, codes, spread))
+        extra[a:b] = sm * 2.0 ** -17 * q[a:b].double().abs().amax(-1) * kk.abs().sum(-1).amax(0).repeat_interleave(g)
+        pos = torch.arange(n - (b - a), n, device=q.device)[:, None]
+        j = torch.arange(n, device=q.device)[None]
+        keep = (j <= pos) if causal else torch.ones(b - a, n, dtype=torch.bool, device=q.device)
+        if window >= 0:
+            keep = keep & (j >= pos - window)
+        for h in range(q.shape[1]):
+            s = torch.nan_to_num(q[a:b, h].double() @ kk[:, h // g].T * sm).masked_fill(~keep, -math.inf)
+            top = (torch.softmax(s, -1).nan_to_num() * bb[:, h // g, 0]).amax(-1)  # the largest weight times its scale
+            floor[a:b, h] = 2.0 ** -27 * top[:, None] * (keep.double() @ cc[:, h // g].abs())
+    rel = 2 * extra
+    return o, lse, ob + rel[..., None] * sizes + floor, lb + extra

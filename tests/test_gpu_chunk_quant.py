@@ -27,7 +27,7 @@ class Batch:
 
     def __init__(self, seed, new, kv, hq, hkv, d, page, block, dt, layout="HND", spare=2, odd=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
-        self.new, self.kv, self.layout, self.d, self.page, self.block, self.odd = new, kv, layout, d, page, block, odd
+        self.new, self.kv, self.layout, self.d, self.page, self.block = new, kv, layout, d, page, block
         pages = [ref.ceil_div(n, page) for n in kv]
         self.qo = [sum(new[:i]) for i in range(len(new) + 1)]
         self.pp = [sum(pages[:i]) for i in range(len(new) + 1)]
@@ -67,7 +67,7 @@ class Batch:
 
     def ref(self, causal=True, window=-1, scale=None):
         return qref.attention(self.q, self.k, self.v, self.ks, self.vs, self.qo, self.kv, self.pp, self.px, causal=causal,
-                              window=window, scale=scale, layout=self.layout, odd_scales=self.odd)
+                              window=window, scale=scale, layout=self.layout)
 
     def check(self, causal=True, window=-1, **kw):
         o, lse = self.run(causal=causal, window_left=window, **kw)
