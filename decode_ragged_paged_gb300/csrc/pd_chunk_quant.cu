@@ -60,8 +60,7 @@ struct QuantShape {
   static constexpr uint32_t kOffK = kQ * kQTile, kOffC = kOffK + kK * kCodes, kOffV = kOffC + kC * kCodes;
   static constexpr uint32_t kOffBar = kOffV + kV * kVTile;
   static constexpr uint32_t kOffML = kOffBar + 1024;                       // group 1's maxima and sums
-  static constexpr uint32_t kOffKS = kOffML + kM * 8;                      // scales [K's slot][K, V][group]
-  static constexpr uint32_t kOffFactors = kOffKS + kK * 2 * kGroups * 4;  // what the softmax makes of them
+  static constexpr uint32_t kOffFactors = kOffML + kM * 8;                 // of the last tiles
   static constexpr uint32_t kOffQS = kOffFactors + kScaleTiles * sizeof(Factors);  // the rows' scales of q [slot][row]
   static constexpr size_t kSmem = kOffQS + kQ * kM * 4 + 1024;
   static_assert(kSelfBytes <= kOffBar, "the rings hold the line first");
@@ -79,15 +78,6 @@ struct QuantBars {
   int abort;
 };
 static_assert(sizeof(QuantBars) <= 1024, "barrier block");
-
-// 4 bytes from global to shared memory, asynchronously; zeros where not `there`.
-__device__ __forceinline__ void copy_word_async(uint32_t to, const float* from, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
-}
-// Arrives on a barrier (one of its counted arrivals) once this thread's copies so far are there.
-__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
   uint4 v;
@@ -191,7 +181,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   const uint32_t base32 = smem_u32(base);
   QuantBars* bars = reinterpret_cast<QuantBars*>(base + S::kOffBar);
   float2* sML = reinterpret_cast<float2*>(base + S::kOffML);
-  const float* sScales = reinterpret_cast<const float*>(base + S::kOffKS);
   Factors* sFactors = reinterpret_cast<Factors*>(base + S::kOffFactors);
   float* sQS = reinterpret_cast<float*>(base + S::kOffQS);
   volatile int* abort = &bars->abort;
@@ -207,7 +196,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       mbar_init(&bars->q_empty[i], 2 + 8);  // the groups' last scores, and every softmax warp has its rows' scales
     }
     for (int i = 0; i < S::kK; ++i) {
-      mbar_init(&bars->k_full[i], 1 + 2 * kGroups);  // the tile, and the scales of its groups of K and V
+      mbar_init(&bars->k_full[i], 1);
       mbar_init(&bars->k_empty[i], 2);
     }
     for (int i = 0; i < S::kC; ++i) {
@@ -219,7 +208,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       mbar_init(&bars->v_empty[i], 2);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->s_full[i >> 1][i & 1], 2);  // the product, and the tile's factors
+      mbar_init(&bars->s_full[i >> 1][i & 1], 2);  // the product, and the issuer, who has seen the tile's factors
       mbar_init(&bars->p_full[i >> 1][i & 1], 4);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
@@ -287,76 +276,101 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     }
   } else if (warp == 6 || warp == 2) {
     // ----------------------------------------------------------- K, V loads
-    // A lane has one of the tile's 8-token groups (in turn): its page, read a tile ahead, and its
-    // scale. One thread issues the boxes, a page's each.
+    // Four tiles at a time: a lane has one 8-token group of one of them. Their pages are read two
+    // such batches ahead, and K's loader reads their scales one ahead and makes the factors of four tiles
+    // in one go; read a tile ahead, either kept a tile waiting for about 1000 cycles. The boxes, a page's
+    // each, are issued by one thread. A tile's bytes may arrive before they are expected: the
+    // barrier waits for the arrival that expects them.
     const bool is_v = warp == 2;
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     uint8_t* ring = base + (is_v ? S::kOffC : S::kOffK);
-    const uint32_t scales = base32 + S::kOffKS;
-    const size_t full = is_v ? offsetof(QuantBars, c_full) : offsetof(QuantBars, k_full);
-    const size_t empty = is_v ? offsetof(QuantBars, c_empty) : offsetof(QuantBars, k_empty);
+    uint64_t* full_bars = is_v ? bars->c_full : bars->k_full;
+    const uint32_t empty = bar(is_v ? offsetof(QuantBars, c_empty) : offsetof(QuantBars, k_empty));
     const uint32_t slots = is_v ? S::kC : S::kK;
-    const float* scale = lane < kGroups ? p.k_scale : p.v_scale;
     const int pb = page_box(p.page_size), boxes = kN / pb, per_box = pb / 8, blocks = p.page_size / p.scale_block,
               block_shift = 31 - __clz(p.scale_block);
-    uint32_t slot = 0, turn = 0;
+    uint32_t slot = 0, turn = 0, count = 0;
     bool ok = true;
     ChunkItem I;
     while (ok && next_item(I)) {
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
-      const int kv_head = I.h / p.group;
+      const int kv_head = I.h / p.group, start = I.tile(0), end = I.tile0 + I.t1;
       const int* list = p.page_indices + I.pbase;
-      // the lane's group of a tile: its first key, and that key's place in the request's page list
-      const int end = (I.tile0 + I.t1) * kN, rounds = nt * kN;
-      int next_key = I.tile(0) * kN + 8 * (lane & 7);
-      int next_idx = POW2 ? next_key >> p.page_shift : next_key / p.page_size;
-      int next = next_idx < I.need ? __ldg(list + next_idx) : 0;
-      for (int i = 0; i < nt; ++i) {
-        const int key = next_key, idx = next_idx;
-        const int off = key - idx * p.page_size;
-        // pages past the request's end, and ids outside the pools: page num_pages, which TMA reads as zeros
-        int id = next;
-        if (idx >= I.need) {
-          id = p.num_pages;
-        } else if (id < 0 || id >= p.num_pages) {
-          report(p.status, PD_DEV_BAD_PAGE_TABLE);
-          id = p.num_pages;
+      // the lane's group in the batch from tile i on: its first key, and that key's place in the list (-1: none)
+      auto group_key = [&](int i) {
+        const int tile = start + i + lane / 8;
+        return (tile < end ? tile : tile - nt) * kN + 8 * (lane & 7);
+      };
+      auto group_idx = [&](int key, int i) {
+        const int idx = POW2 ? key >> p.page_shift : key / p.page_size;
+        return i + lane / 8 < nt && idx < I.need ? idx : -1;
+      };
+      auto read_page = [&](int i) {
+        const int idx = group_idx(group_key(i), i);
+        return idx >= 0 ? __ldg(list + idx) : p.num_pages;
+      };
+      // pages past the request's end, and ids outside the pools: page num_pages, which TMA reads as zeros
+      auto checked = [&](int id, int i) {
+        if (id >= 0 && id < p.num_pages) return id;
+        if (group_idx(group_key(i), i) >= 0) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+        return p.num_pages;
+      };
+      float scale_k = 0.f, scale_v = 0.f;  // of the next batch
+      auto read_scales = [&](int id, int i) {
+        const int key = group_key(i), off = key - (POW2 ? key >> p.page_shift : key / p.page_size) * p.page_size;
+        scale_k = scale_v = 0.f;
+        // (a group that no row of the item sees may have anything as its scale)
+        if (id < p.num_pages && key < I.keys.hi && key + 8 > I.keys.lo) {
+          const int64_t at = ((int64_t)id * p.hkv + kv_head) * blocks + (POW2 ? off >> block_shift : off / p.scale_block);
+          scale_k = __ldg(p.k_scale + at);
+          scale_v = __ldg(p.v_scale + at);
         }
-        next_key += kN;
-        if (next_key >= end) next_key -= rounds;
-        next_idx = POW2 ? next_key >> p.page_shift : next_key / p.page_size;
-        if (i + 1 < nt) next = next_idx < I.need ? __ldg(list + next_idx) : 0;
-        ok = wait(bar(empty, slot), (turn & 1u) ^ 1u);
-        if (!ok) break;
-        if (!is_v && lane < 2 * kGroups) {
-          // (a group that no row of the item sees may have anything as its scale: it gets 0)
-          const bool there = id < p.num_pages && key < I.keys.hi && key + 8 > I.keys.lo;
-          const int64_t from =
-              there ? ((int64_t)id * p.hkv + kv_head) * blocks + (POW2 ? off >> block_shift : off / p.scale_block) : 0;
-          copy_word_async(scales + (slot * 2 * kGroups + lane) * 4, scale + from, there);
-          copy_async_arrive(bar(full, slot));
-        }
-        int bid[8], boff[8];
+      };
+      int id = checked(read_page(0), 0), ahead = read_page(4);
+      if (!is_v) read_scales(id, 0);
+      for (int i0 = 0; ok && i0 < nt; i0 += 4) {
+        const int key = group_key(i0), off = key - (POW2 ? key >> p.page_shift : key / p.page_size) * p.page_size;
+        const int next = checked(ahead, i0 + 4);
+        ahead = read_page(i0 + 8);
+        const float a = scale_k, b = scale_v;
+        if (!is_v) read_scales(next, i0 + 4);
+        const int tiles = min(4, nt - i0);
+        for (int x = 0; x < tiles; ++x) {
+          ok = wait(empty + 8 * slot, (turn & 1u) ^ 1u);
+          if (!ok) break;
+          int bid[8], boff[8];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          if (b == boxes) break;
-          bid[b] = __shfl_sync(0xffffffffu, id, b * per_box);
-          boff[b] = __shfl_sync(0xffffffffu, off, b * per_box);
-        }
-        if (elect_one()) {
-          uint64_t* full_at = is_v ? &bars->c_full[slot] : &bars->k_full[slot];
-          uint8_t* to = ring + slot * S::kCodes;
-          mbar_arrive_expect_tx(full_at, S::kCodes);
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            if (b == boxes) break;
-            tma_load_4d(to + b * pb * D, map, 0, p.nhd ? kv_head : boff[b], p.nhd ? boff[b] : kv_head, bid[b], full_at);
+          for (int n = 0; n < 8; ++n) {
+            if (n == boxes) break;
+            bid[n] = __shfl_sync(0xffffffffu, id, 8 * x + n * per_box);
+            boff[n] = __shfl_sync(0xffffffffu, off, 8 * x + n * per_box);
           }
+          if (elect_one()) {
+            uint8_t* to = ring + slot * S::kCodes;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              if (n == boxes) break;
+              tma_load_4d(to + n * pb * D, map, 0, p.nhd ? kv_head : boff[n], p.nhd ? boff[n] : kv_head, bid[n],
+                          &full_bars[slot]);
+            }
+          }
+          __syncwarp();
+          if (!is_v && x == 0) {
+            Factors& f = sFactors[(count + i0 + lane / 8) & (kScaleTiles - 1)];
+            const float lb = fast_log2(fmaxf(b, kScaleMin));
+            if (lane / 8 < tiles) {
+              f.of[lane & 7] = make_float4(a, a, lb, lb);
+              f.inverse[lane & 7] = fast_exp2(-lb);
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full_bars[slot], S::kCodes);
+          if (++slot == slots) slot = 0, ++turn;
         }
-        __syncwarp();
-        if (++slot == slots) slot = 0, ++turn;
+        id = next;
       }
+      count += nt;
     }
   } else if (warp == 4) {
     // --------------------------------------------------------------- Q loads
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const int g = warp >> 2;
     constexpr uint32_t idesc_s = idesc_e4m3_f32(kM, kN);
     uint32_t q = 0, qturn = 0, ks = 0, kturn = 0;
-    uint32_t own = 0, count = 0;  // scores issued, tiles
+    uint32_t own = 0;  // scores issued
     bool ok = true;
     ChunkItem I;
     while (ok && next_item(I)) {
@@ -407,15 +421,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           ok = own < 2 || wait(bar(offsetof(QuantBars, pv_done), 2 * g + buf), ((own - 2) >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
-          if (lane < kGroups) {
-            // (with two query tiles both groups' issuers write the same)
-            const float* at = sScales + ks * 2 * kGroups + lane;
-            Factors& f = sFactors[(count + i) & (kScaleTiles - 1)];
-            const float a = at[0], b = fast_log2(fmaxf(at[kGroups], kScaleMin)), r = fast_exp2(-b);
-            f.of[lane] = make_float4(a, a, b, b);
-            f.inverse[lane] = r;
-          }
-          __syncwarp();
           if (lane == 0) mbar_arrive(&bars->s_full[g][buf]);
           const uint32_t at = __shfl_sync(0xffffffffu, base32 + S::kOffK + ks * S::kCodes, 0);
           const uint64_t dk = D == 128 ? sw128_desc(at, 16, 1024) : sw64_desc(at, 512);
@@ -438,7 +443,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (++ks == S::kK) ks = 0, ++kturn;
       }
       if (ok && !two && g >= nt && lane == 0) mbar_arrive(&bars->q_empty[q_slot]);  // no tile of the item is its own
-      count += nt;
     }
   } else if (warp == 3 || warp == 7) {
     // --------------------------------------------------------------- O += P V
