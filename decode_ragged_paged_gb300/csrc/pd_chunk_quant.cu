@@ -777,6 +777,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         uint4 v[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) v[u] = ld_shared(from0 + cs * S::kCodes + u * (kStep * D));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->c_empty[cs]);
         const int k0 = tile * kN;
         if (++tile == end) tile = I.tile0 + I.t0;
         if (k0 < I.keys.lo || k0 + kN > I.keys.hi) {
@@ -799,10 +801,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->c_empty[cs]);
-          mbar_arrive(&bars->v_full[vs]);
-        }
+        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
         if (++cs == S::kC) cs = 0, ++cturn;
         if (++vs == S::kV) vs = 0, ++vturn;
       }
