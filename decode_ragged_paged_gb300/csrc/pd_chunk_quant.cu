@@ -42,10 +42,11 @@ constexpr float kShift = 3.0f;             // log2 of the weight of a row's larg
 constexpr float kSumShift = kShift + 6;   // and of the sum of 64 alike
 constexpr float kWeightLimit = 32768.0f;  // 2^15: largest row sum of weights taken with a stale maximum
 
-// A tile's scales as the softmax takes them, each twice for its packed arithmetic.
+// A tile's scales as the softmax takes them.
 struct Factors {
-  float4 of[kGroups];        // K's scale twice, log2 of V's scale twice
-  float inverse[kGroups];    // 1 / V's scale
+  float4 k[kGroups / 4];        // K's
+  float4 log_v[kGroups / 4];    // log2 of V's
+  float4 inverse[kGroups / 4];  // 1 / V's
 };
 
 template <int D>
@@ -360,8 +361,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
             Factors& f = sFactors[(count + i0 + lane / 8) & (kScaleTiles - 1)];
             const float lb = fast_log2(fmaxf(b, kScaleMin));
             if (lane / 8 < tiles) {
-              f.of[lane & 7] = make_float4(a, a, lb, lb);
-              f.inverse[lane & 7] = fast_exp2(-lb);
+              reinterpret_cast<float*>(f.k)[lane & 7] = a;
+              reinterpret_cast<float*>(f.log_v)[lane & 7] = lb;
+              reinterpret_cast<float*>(f.inverse)[lane & 7] = fast_exp2(-lb);
             }
             __syncwarp();
           }
@@ -548,32 +550,44 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           // weights of the tile, as fp16 pairs
           auto weights = [&](float nm) {
             total = part = 0.f;
-            const float2 nm2 = make_float2(nm, nm), rs2 = make_float2(rs, rs);
             uint32_t v[2][16];
             tmem_ld16(t_s, v[0]);
+            // all of the tile's at once, while the scores are on their way
+            float f[kGroups], x0[kGroups];
+#pragma unroll
+            for (int n = 0; n < kGroups / 4; ++n) {
+              const float4 a = factors.k[n], b = factors.log_v[n];
+              f[4 * n] = fmaf(a.x, rs, kFactorMin), f[4 * n + 1] = fmaf(a.y, rs, kFactorMin);
+              f[4 * n + 2] = fmaf(a.z, rs, kFactorMin), f[4 * n + 3] = fmaf(a.w, rs, kFactorMin);
+              x0[4 * n] = b.x + nm, x0[4 * n + 1] = b.y + nm, x0[4 * n + 2] = b.z + nm, x0[4 * n + 3] = b.w + nm;
+            }
             tmem_wait_ld(v[0]);
+            float sums[kGroups];
 #pragma unroll
             for (int c = 0; c < kN / 16; ++c) {
               if (c + 1 < kN / 16) tmem_ld16(t_s + 16 * (c + 1), v[(c + 1) & 1]);
-              const float2 r = *reinterpret_cast<const float2*>(factors.inverse + 2 * c);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float4 of = factors.of[2 * c + h];
-                const float2 f = ffma2(make_float2(of.x, of.y), rs2, make_float2(kFactorMin, kFactorMin));
-                const float2 x0 = fadd2(make_float2(of.z, of.w), nm2);
+                const int n = 2 * c + h;
+                const float2 f2 = make_float2(f[n], f[n]), x2 = make_float2(x0[n], x0[n]);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int e = 8 * h; e < 8 * h + 8; e += 2) {
-                  const float2 x = ffma2(make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])), f, x0);
+                  const float2 x = ffma2(make_float2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1])), f2, x2);
                   const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                   w[8 * c + e / 2] = pack_f16x2(pe.x, pe.y);
                   sum = e == 8 * h ? pe : fadd2(sum, pe);
                 }
-                const float s = sum.x + sum.y;
-                total += s;
-                part = fmaf(s, h ? r.y : r.x, part);
+                sums[n] = sum.x + sum.y;
               }
               if (c + 1 < kN / 16) tmem_wait_ld(v[(c + 1) & 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < kGroups / 4; ++n) {
+              const float4 r = factors.inverse[n];
+              const float* x = sums + 4 * n;
+              total += (x[0] + x[1]) + (x[2] + x[3]);
+              part += fmaf(x[0], r.x, x[1] * r.y) + fmaf(x[2], r.z, x[3] * r.w);
             }
           };
           bool stale = __all_sync(0xffffffffu, m > -INFINITY), over = false;
@@ -602,8 +616,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
                 for (int x = 1; x < 7; x += 2) mx = fmax3(mx, __uint_as_float(v[e + x]), __uint_as_float(v[e + x + 1]));
                 mx = fmaxf(mx, __uint_as_float(v[e + 7]));
                 // (the factor is positive)
-                const float4 of = factors.of[4 * c + e / 8];
-                ms = fmaxf(ms, fmaf(mx, fmaf(of.x, rs, kFactorMin), of.z) - kShift);
+                const int n = 4 * c + e / 8;
+                ms = fmaxf(ms, fmaf(mx, fmaf(reinterpret_cast<const float*>(factors.k)[n], rs, kFactorMin),
+                                    reinterpret_cast<const float*>(factors.log_v)[n]) - kShift);
               }
             }
             float alpha = 1.f;
