@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
                 m = ms;
               } else if (ms > (stale ? m : m + kRaise)) {
                 // (a maximum left below a row's weights' limit would do every tile twice)
-                alpha = exp2f(m - ms);
+                alpha = fast_exp2(m - ms);
                 m = ms;
               }
             }
