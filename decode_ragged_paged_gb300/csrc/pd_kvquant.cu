@@ -17,10 +17,14 @@
 // its rows begin: a request's row is looked for with 32 probes at a time, as one
 // after another they would cost a decode more than everything else.
 #include <cfloat>
+#include <type_traits>
+
+#include <cuda_bf16.h>
 
 #include "pd_common.cuh"
 #include "pd_internal.h"
 #include "pd_quant.cuh"
+#include "pd_tc.cuh"
 
 namespace pd {
 
@@ -51,11 +55,70 @@ struct Vec8 {
     if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     else return make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
   }
+  // The largest |x| of them and of m (an infinity among them; a NaN is passed over), in T's own arithmetic.
+  using Max = std::conditional_t<sizeof(T) == 4, float, __nv_bfloat162>;
+  __device__ __forceinline__ void largest(Max& m) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+#pragma unroll
+    for (int e = 0; e < 4 * N; ++e) {
+      if constexpr (sizeof(T) == 4) m = fmaxf(m, fabsf(__uint_as_float(w[e])));
+      else m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+    }
+  }
+  static __device__ __forceinline__ Max none() {
+    if constexpr (sizeof(T) == 4) return 0.f;
+    else return __float2bfloat162_rn(0.f);
+  }
+  static __device__ __forceinline__ float of(Max m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else return fmaxf(__low2float(m), __high2float(m));
+  }
+  // Times a power of two, as e4m3.
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    uint32_t v[4];
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = fmul2(get(e), inv2);
+      v[e] = pack_e4m3x2(f.x, f.y);
+    }
+    return make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+  }
 };
 
-// What a CTA's rows begin: `count` new tokens from row `row` on, at places i0 and on of a block.
+// The largest finite |x| of a lane's share of a block's new values, one by one: only where some are not finite.
+template <typename T>
+__device__ __noinline__ float largest_finite(const T* src, int64_t stride, int count, int D, int at, int step) {
+  float m = 0.f;
+  for (int i = at; i < count * D; i += step) {
+    const T x = src[(i / D) * stride + i % D];
+    float a;
+    if constexpr (sizeof(T) == 4) a = fabsf(x);
+    else a = fabsf(bf16_lo(x));
+    if (a <= FLT_MAX) m = fmaxf(m, a);
+  }
+  return m;
+}
+
+// Stores a lane's share of a block's new values one by one, with a division: where some are not finite (what is
+// not becomes NaN), or the caller's own scale is no power of two, whose inverse would not be exact.
+template <typename T>
+__device__ __noinline__ void store_slowly(const T* src, int64_t stride, int count, int D, float s, uint8_t* to, int64_t to_step,
+                                          int at, int step) {
+  for (int i = at; i < count * D; i += step) {
+    const int tok = i / D, d = i - tok * D;
+    float x;
+    if constexpr (sizeof(T) == 4) x = src[tok * stride + d];
+    else x = bf16_lo(src[tok * stride + d]);
+    x = fabsf(x) <= FLT_MAX ? x / s : __uint_as_float(0x7fffffffu);
+    to[tok * to_step + d] = (uint8_t)pack_e4m3x2(x, 0.f);
+  }
+}
+
+// What a CTA's rows begin: `count` new tokens from row `row` on, at places i0 and on of a block of the page that
+// is number `entry` of the page lists.
 struct Begun {
-  int row, count, i0, page, block;
+  int row, count, i0, entry, block;
 };
 
 // The last request whose rows begin at or before `row`, by a whole warp (0 if the indptr starts behind it).
@@ -74,7 +137,7 @@ __device__ __forceinline__ int request_of(const int32_t* indptr, int batch, int 
 }  // namespace
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(kQaThreads) kv_append_quant_kernel(const KvQuantParams p) {
+__global__ void __launch_bounds__(kQaThreads, 3) kv_append_quant_kernel(const KvQuantParams p) {
   __shared__ Begun begun[kQaRows];
   __shared__ int num_begun;
   __shared__ uint32_t red[kQaWarps];
@@ -109,9 +172,8 @@ __global__ void __launch_bounds__(kQaThreads) kv_append_quant_kernel(const KvQua
         } else if ((int64_t)(pb - pa) * P < n) {
           report(p.status, PD_DEV_BAD_PAGE_TABLE);
         } else if (row == a || t % S == 0) {
-          w.page = __ldg(p.page_indices + pa + t / P);
-          leads = w.page >= 0 && w.page < p.num_pages;
-          if (!leads) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+          leads = true;
+          w.entry = pa + t / P;
           w.row = row;
           w.i0 = t % S;
           w.block = t % P / S;
@@ -140,34 +202,22 @@ __global__ void __launch_bounds__(kQaThreads) kv_append_quant_kernel(const KvQua
     const int h = is_v ? c - p.hkv : c;
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) + w.row * stride + (int64_t)h * D;
-    float* scale = (is_v ? p.v_scale : p.k_scale) + ((int64_t)w.page * p.hkv + h) * (P / S) + w.block;
-    const float was = w.i0 > 0 ? *scale : 0.f;
+    const int page = __ldg(p.page_indices + w.entry);  // (on its way with the new values)
     const int vecs = w.count * vpr;
     Vec8<T> x[NV];
+    // vector i of the block: its row and its first element there (where a row's vectors divide a team's lanes, a lane
+    // stays in its column)
     auto row_of = [&](int i) { return p.vpr_shift >= 0 ? i >> p.vpr_shift : i / vpr; };
     auto load = [&](int i0) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
+        if (i0 + u * tw >= vecs) break;  // (none of the team's)
         const int i = i0 + tl + u * tw, tok = row_of(i);
         if (i < vecs) x[u].load(src + tok * stride + (i - tok * vpr) * 8);
         else x[u].zero();
       }
     };
-    // The largest |x| of the team's; `finite`: of what is finite (fmaxf passes over NaN by itself).
-    auto largest = [&](bool finite) {
-      float m = 0.f;
-      for (int i0 = 0; i0 < vecs; i0 += NV * tw) {
-        if (vecs > NV * tw || !finite) load(i0);
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = x[u].get(e);
-            const float ax = fabsf(f.x), ay = fabsf(f.y);
-            m = fmaxf(m, !finite || ax <= FLT_MAX ? ax : 0.f);
-            m = fmaxf(m, !finite || ay <= FLT_MAX ? ay : 0.f);
-          }
-      }
+    auto whole_team = [&](float m) {  // the largest of the team's
       uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
       if (team_warps > 1) {
         if (lane == 0) red[warp] = bits;
@@ -177,15 +227,35 @@ __global__ void __launch_bounds__(kQaThreads) kv_append_quant_kernel(const KvQua
       }
       return __uint_as_float(bits);
     };
-    float amax = largest(false);
-    const bool infinite = amax > FLT_MAX;
-    if (infinite) amax = largest(true);
+    auto m = Vec8<T>::none();
+    float was = 0.f;
+    float* scale = nullptr;
+    for (int i0 = 0; i0 < vecs; i0 += NV * tw) {
+      load(i0);
+      if (i0 == 0) {
+        if (page < 0 || page >= p.num_pages) {
+          if (tl == 0) report(p.status, PD_DEV_BAD_PAGE_TABLE);
+          break;
+        }
+        scale = (is_v ? p.v_scale : p.k_scale) + ((int64_t)page * p.hkv + h) * (P / S) + w.block;
+        if (w.i0 > 0) was = *scale;
+      }
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (i0 + u * tw >= vecs) break;
+        x[u].largest(m);
+      }
+    }
+    if (scale == nullptr) continue;  // (the whole team's)
+    float amax = whole_team(Vec8<T>::of(m));
+    const bool finite = amax <= FLT_MAX;
+    if (!finite) amax = whole_team(largest_finite(src, stride, w.count, D, tl, tw));
     float s = power_of_two(scale_exponent(amax));
     if (w.i0 > 0) s = fmaxf(s, was);
     uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
     const int slot0 = w.block * S;
-    const int64_t at = p.nhd ? (((int64_t)w.page * P + slot0) * p.hkv + h) * D
-                             : (((int64_t)w.page * p.hkv + h) * P + slot0) * D;
+    const int64_t at = p.nhd ? (((int64_t)page * P + slot0) * p.hkv + h) * D
+                             : (((int64_t)page * p.hkv + h) * P + slot0) * D;
     const int64_t step = p.nhd ? (int64_t)p.hkv * D : D;  // from one slot to the next
     if (w.i0 > 0 && s != was) {
       const float f = was / s;
@@ -202,28 +272,20 @@ __global__ void __launch_bounds__(kQaThreads) kv_append_quant_kernel(const KvQua
         *to = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
       }
     }
-    // (a scale that the caller put there need not be a power of two, whose inverse is exact)
-    const bool power = (__float_as_uint(s) & 0x7fffffu) == 0;
-    const float inv = 1.f / s;
-    for (int i0 = 0; i0 < vecs; i0 += NV * tw) {
-      if (vecs > NV * tw) load(i0);
+    uint8_t* to = pool + at + w.i0 * step;
+    if (finite && (__float_as_uint(s) & 0x7fffffu) == 0) {
+      const float inv = 1.f / s;
+      for (int i0 = 0; i0 < vecs; i0 += NV * tw) {
+        if (vecs > NV * tw) load(i0);
 #pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int i = i0 + tl + u * tw, tok = row_of(i);
-        uint32_t v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float2 f = x[u].get(e);
-          if (infinite) {  // infinity times zero is NaN, and so is what it is added to
-            f.x = fmaf(f.x, 0.f, f.x);
-            f.y = fmaf(f.y, 0.f, f.y);
-          }
-          v[e] = power ? pack_e4m3x2(f.x * inv, f.y * inv) : pack_e4m3x2(f.x / s, f.y / s);
+        for (int u = 0; u < NV; ++u) {
+          if (i0 + u * tw >= vecs) break;
+          const int i = i0 + tl + u * tw, tok = row_of(i);
+          if (i < vecs) *reinterpret_cast<uint2*>(to + tok * step + (i - tok * vpr) * 8) = x[u].encode(inv);
         }
-        if (i < vecs)
-          *reinterpret_cast<uint2*>(pool + at + (w.i0 + tok) * step + (i - tok * vpr) * 8) =
-              make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
       }
+    } else {
+      store_slowly(src, stride, w.count, D, s, to, step, tl, tw);
     }
     if (tl == 0) *scale = s;
   }
