@@ -659,7 +659,11 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // The tensor cores take bf16, in pages of whole groups of the swizzle's 8 rows;
   // the CUDA cores take the rest.
   const bool quant = p.scale_block > 0;
+  const int64_t most = (int64_t)p.max_qo_len * p.group;  // rows of a request's KV head
   p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && p.scale_block % 8 == 0;
+  // Few rows of an 8-bit cache have a kernel of their own.
+  p.few = quant && p.tc && most <= 16;
+  p.tc = p.tc && !p.few;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
     p.tile_tokens = 128 / p.tile_heads;
@@ -670,16 +674,16 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.max_parts = device_sm_count();
   } else {
     // Rows of an item: 4 or 16 where that takes a request's rows in one go or in a
-    // few (the kernel for few rows), else 64.
-    const int64_t most = (int64_t)p.max_qo_len * p.group;
-    // 8-bit pools have the tiled kernel alone, in which 16 rows cost a fourth of 64.
-    if (quant) p.rows = most <= 16 && p.group <= 16 ? 16 : 64;
+    // few (the kernel for few rows), else 64. Of 8-bit pools the tiled kernel takes any
+    // number of rows that theirs does not; in it 16 cost a fourth of 64.
+    if (p.few) p.rows = 16;
+    else if (quant) p.rows = most <= 16 && p.group <= 16 ? 16 : 64;
     else p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
     p.item_cost = 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * (p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
+    p.max_parts = device_sm_count() * (p.rows == 64 || (quant && !p.few) ? 2 : 1);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)
@@ -770,6 +774,8 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream) {
   const bool d64 = p.head_dim == 64;
   if (p.tc)
     e = p.scale_block > 0 ? launch_chunk_quant_tc(p, stream) : launch_chunk_tc(p, stream);
+  else if (p.few)
+    e = launch_chunk_quant_rows(p, stream);
   else if (p.scale_block > 0 && kv_dtype == PD_BF16)
     e = d64 ? launch_quant_simt<uint16_t, 64>(p, stream) : launch_quant_simt<uint16_t, 128>(p, stream);
   else if (p.scale_block > 0)

@@ -140,24 +140,6 @@ __device__ __forceinline__ float split_row(uint32_t tile, int row) {
   return m <= 3.4e38f ? power_of_two(e) : 1.f;
 }
 
-// 16 e4m3 values as fp16, exactly.
-__device__ __forceinline__ void to_f16(const uint4& v, uint32_t (&out)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
-        : "r"(w[i]));
-}
-
-// log2 of a normal positive number with the hardware approximation.
-__device__ __forceinline__ float fast_log2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 values -> one fp16x2 word, `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;

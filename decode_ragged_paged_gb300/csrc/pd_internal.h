@@ -275,6 +275,7 @@ struct ChunkParams {
   int32_t batch, hq, hkv, group, head_dim, page_size, num_pages, total_qo, max_qo_len, max_kv_len;
   int32_t causal, window, o_dtype, nhd;
   int32_t tc;          // the tensor-core kernel takes the call
+  int32_t few;         // the kernel for few rows of 8-bit pools does
   int32_t page_shift;  // log2 of a page size that is a power of two, else -1
   int32_t aligned32;   // o and the workspace are 32-byte aligned
   int32_t self_plan;   // every CTA makes the work line for itself
@@ -316,6 +317,7 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_quant_tc(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_quant_rows(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
 bool make_pool_map(CUtensorMap* map, const void* pool, int32_t dtype, int32_t num_pages, int32_t hkv,

@@ -25,6 +25,34 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
   return f;
 }
 
+// Two times two e4m3 values, as two and two fp16 pairs, exactly: of a's low and high half, then b's.
+__device__ __forceinline__ void pairs_to_f16(uint32_t a, uint32_t b, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(out[0]), "=r"(out[1])
+      : "r"(a));
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(out[2]), "=r"(out[3])
+      : "r"(b));
+}
+
+// 16 e4m3 values as fp16, exactly.
+__device__ __forceinline__ void to_f16(const uint4& v, uint32_t (&out)[8]) {
+  uint32_t lo[4], hi[4];
+  pairs_to_f16(v.x, v.y, lo);
+  pairs_to_f16(v.z, v.w, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = lo[i], out[4 + i] = hi[i];
+}
+
+// log2 of a normal positive number with the hardware approximation.
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The exponent of the scale of values up to amax (finite, not negative): the smallest power of two,
 // at least 2^-100, times 448 is not below amax. 448 = 1.75 * 2^8. A power of two, because values
 // are then scaled without rounding, and what a block holds already keeps its value when the scale grows
