@@ -676,7 +676,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     // Rows of an item: 4 or 16 where that takes a request's rows in one go or in a
     // few (the kernel for few rows), else 64. Of 8-bit pools the tiled kernel takes any
     // number of rows that theirs does not; in it 16 cost a fourth of 64.
-    if (p.few) p.rows = 16;
+    if (p.few) p.rows = most <= 8 ? 8 : 16;
     else if (quant) p.rows = most <= 16 && p.group <= 16 ? 16 : 64;
     else p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;

@@ -1,21 +1,24 @@
 // pd_chunk_quant_rows.cu -- chunk attention over a cache held in 8 bits, for few query
 // rows (single tokens, a few drafted ones; bf16 queries, pages and blocks of a multiple of 8 tokens).
 //
-// HBM bound: an item has at most 16 query rows (tokens x heads of a KV head), and its keys
-// pass once. Tiles of 128 rows through tensor memory would keep 4 of them busy, a
+// HBM bound: an item has at most 8 or 16 query rows (tokens x heads of a KV head), and its
+// keys pass once. Tiles of 128 rows through tensor memory would keep 4 of them busy, a
 // softmax warp of 4 and every wait between the roles for them (128 decodes of 512 to 4096 keys:
 // 160 us); so here a warp does all of it by itself, as the fp32 kernel for few rows does, with
-// products of 16 rows (mma.m16n8k16, fp16 in, fp32 out), and the CTA's eight warps meet at an
-// item's end only:
-//   16 keys of 128 a warp: their 8-bit rows come through a ring of its own in shared memory by
+// products of 8 columns (mma.m16n8k16, fp16 in, fp32 out) that are the query rows, and the
+// CTA's warps meet at an item's end only:
+//   16 keys a warp in turn: their 8-bit rows come through a ring of its own in shared memory by
 //     cp.async, the scales of their two 8-key groups with them;
-//   scores: q as fp16 (scaled by a power of two a row, exact), k as fp16 by one conversion a pair.
-//     The products' inner index may be any order of the head's values, so a lane takes 16
+//   scores, K q^T: q as fp16 (scaled by a power of two a row, exact), k as fp16 by one conversion a
+//     pair. The products' inner index may be any order of the head's values, so a lane takes 16
 //     neighbouring bytes of a key and not 2 here and there;
-//   weights W = 2^(s + log2 b - m), b the key's scale of V and m the row's running maximum of s + log2 b
-//     (raised where it grew by more than 2^8), fp16 with the largest from 2^4 to 2^12;
-//     their sum over b is the softmax's;
-//   o += W v: a lane takes 16 neighbouring values of 4 keys, and a byte of two keys is one pair.
+//   weights W = 2^(s + log2 b - m), b the key's scale of V and m the row's running maximum of s + log2 b, fp16 with
+//     the largest from 2^4 to 2^12: only a score over that raises m, and has the lanes' maxima
+//     exchanged. Their sum over b is the softmax's;
+//   o, V^T W: the weights' 8 x 8 blocks turned by movmatrix; a lane takes 16 neighbouring values of 4 keys, and a byte
+//     of two keys is one pair.
+// (With the rows as the 16 of the products, 8 of them empty, a turn took twice the products and registers,
+// and 8 warps an SM: 210 us.)
 #include <math.h>
 
 #include "pd_chunk.cuh"
@@ -27,29 +30,39 @@ namespace pd {
 
 namespace {
 
-constexpr int kRqThreads = 256, kRqWarps = kRqThreads / 32;
-constexpr int kRqRows = 16, kRqKeys = 16;       // of an item, and of a warp's turn
-constexpr int kRqSpan = kRqWarps * kRqKeys;     // keys of the CTA's turn
-constexpr int kRqStages = 6;
-constexpr float kRqShift = 4.0f, kRqRaise = 8.0f;
+constexpr int kRqKeys = 16;  // of a warp's turn
+constexpr float kRqShift = 4.0f, kRqRaise = 12.0f;
 
-template <int D>
+// NT: 8 query rows each.
+template <int D, int NT>
 struct RowsQuantShape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kWarps = NT == 1 ? 16 : 8, kThreads = 32 * kWarps;
+  static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
+  static constexpr int kStages = NT == 1 ? 3 : 6;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
   static constexpr int kStage = 2 * kCodes + 16;                  // and four scales
-  static constexpr int kWarp = kRqStages * kStage;
-  static constexpr int kJoin = kRqRows * D * 4;                   // a warp's output
-  static constexpr int kRing = kRqWarps * (kWarp > kJoin ? kWarp : kJoin);
-  static constexpr size_t kSmem = kRing + 2 * kRqWarps * kRqRows * sizeof(float);
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kJoin = kRows * D * 4;                     // a warp's output
+  static constexpr int kRing = kWarps * (kWarp > kJoin ? kWarp : kJoin);
+  static constexpr size_t kSmem = kRing + 2 * kWarps * kRows * sizeof(float);
   static_assert(kSelfBytes <= kRing && kSmem <= 232448, "shared memory of a CTA");
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// An 8 x 8 block of 16-bit values, two of a row a lane, turned.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // A lane's bytes from global to shared memory, asynchronously; zeros where not `there`.
@@ -71,20 +84,19 @@ __device__ __forceinline__ int v_chunk(int key, int c) { return D == 128 ? c ^ (
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kRqThreads, 1) chunk_quant_rows_kernel(const ChunkParams p) {
-  using S = RowsQuantShape<D>;
-  constexpr int kSteps = D / 16;       // products of 16 values of a head
-  constexpr int kTiles = D / 8;        // of 8 columns of the output
+template <int D, int NT>
+__global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quant_rows_kernel(const ChunkParams p) {
+  using S = RowsQuantShape<D, NT>;
+  constexpr int kTiles = D / 16;       // of 16 values of the output
   constexpr int kChunks = D / 16;      // 16-byte chunks of a row
   constexpr int kPer = kRqKeys * kChunks / 32;  // chunks of K (or V) that a lane copies
   extern __shared__ __align__(128) uint8_t rq_smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;  // the lane's rows g and g + 8, and its place among the four that share them
+  const int g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(rq_smem) + warp * S::kWarp;
   float* sAcc = reinterpret_cast<float*>(rq_smem);                // [warp][row][D]
   float* sM = reinterpret_cast<float*>(rq_smem + S::kRing);       // [warp][row] maxima, then sums
-  float* sL = sM + kRqWarps * kRqRows;
+  float* sL = sM + S::kWarps * S::kRows;
   pdl_launch_dependents();
   pdl_wait_primary();
   ChunkWalk walk;
@@ -93,66 +105,71 @@ __global__ void __launch_bounds__(kRqThreads, 1) chunk_quant_rows_kernel(const C
     const int4 cut = walk.begin(p, line, blockIdx.x);
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   }
-  const int blocks = p.page_size / p.scale_block;
+  const int blocks = p.page_size / p.scale_block, block_shift = 31 - __clz(p.scale_block);
+  // what a lane copies: 16-byte chunk `chunk` of key key0 and of every (32 / chunks of a row)th from there on
+  const int key0 = lane / kChunks, chunk = lane % kChunks, row_step = p.nhd ? p.hkv : 1;
   ChunkItem I;
   while (walk.next(p, I)) {
     __syncthreads();  // the line, or the last item's outputs, have been read
     const int rows = I.tokens * p.tile_heads;
     const int kv_head = I.h / p.group;
-    // A lane's key of the warp's 16 from k0 on (lanes 16 to 31 as lanes 0 to 15): its row of the pools and its block of
-    // the scales, -1 where no row of the item sees it.
-    auto place = [&](int k0, int64_t& block) -> int64_t {
-      const int j = k0 + (lane & 15);
-      block = -1;
-      if (j < I.keys.lo || j >= I.keys.hi) return -1;
+    // A warp's 16 keys from k0 on are two groups of 8, a run of slots of one page each. An odd lane has the second, an
+    // even one the first: its first row in the pools, and its block of the scales; -1 where no row of the item sees it.
+    struct Group {
+      int64_t row, block;
+    };
+    auto place = [&](int k0) -> Group {
+      const int j = k0 + 8 * (lane & 1);
+      if (j + 8 <= I.keys.lo || j >= I.keys.hi) return Group{-1, -1};
       const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
       const int page = p.page_indices[I.pbase + idx], slot = j - idx * p.page_size;
       if (page < 0 || page >= p.num_pages) {
         report(p.status, PD_DEV_BAD_PAGE_TABLE);
-        return -1;
+        return Group{-1, -1};
       }
       const int64_t head = (int64_t)page * p.hkv + kv_head;
-      block = head * blocks + slot / p.scale_block;
-      return p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head : head * p.page_size + slot;
+      return Group{p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head : head * p.page_size + slot,
+                   head * blocks + (p.page_shift >= 0 ? slot >> block_shift : slot / p.scale_block)};
     };
-    // Starts the copies of the keys at `at` into a stage.
-    auto fetch = [&](int64_t at, int64_t block, int stage) {
+    // Starts the copies of the keys from k0 on into a stage; those that no row of the item sees become zeros.
+    auto fetch = [&](const Group& at, int k0, int stage) {
       const uint32_t to = ring + stage * S::kStage;
+      const int64_t r0 = __shfl_sync(0xffffffffu, at.row, 0), r1 = __shfl_sync(0xffffffffu, at.row, 1);
+      const bool whole = k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int key = (lane + 32 * i) / kChunks, ch = lane % kChunks;
-        const int64_t row = __shfl_sync(0xffffffffu, at, key);
-        const int64_t from = (row >= 0 ? row : 0) * D + ch * 16;
-        copy_async<16>(to + key * D + k_chunk<D>(key, ch) * 16, static_cast<const uint8_t*>(p.k_pool) + from, row >= 0);
-        copy_async<16>(to + S::kCodes + key * D + v_chunk<D>(key, ch) * 16, static_cast<const uint8_t*>(p.v_pool) + from,
-                       row >= 0);
+        constexpr int kStep = 32 / kChunks;  // keys of 32 lanes
+        const int key = key0 + i * kStep;    // (of a group: i * kStep / 8)
+        const int64_t base = i * kStep < 8 ? r0 : r1;
+        bool there = true;
+        if (!whole) there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
+        const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
+        copy_async<16>(to + key * D + k_chunk<D>(key, chunk) * 16, static_cast<const uint8_t*>(p.k_pool) + from, there);
+        copy_async<16>(to + S::kCodes + key * D + v_chunk<D>(key, chunk) * 16,
+                       static_cast<const uint8_t*>(p.v_pool) + from, there);
       }
-      // lanes 0 to 3: K's scales of the two groups, and V's. A group's block is that of any key of it that is seen.
-      int64_t seen = block;
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) {
-        const int64_t o = __shfl_xor_sync(0xffffffffu, seen, d);
-        seen = o > seen ? o : seen;
-      }
-      const int64_t mine = __shfl_sync(0xffffffffu, seen, 8 * (lane & 1));
-      if (lane < 4)
-        copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (mine >= 0 ? mine : 0), mine >= 0);
+      if (lane < 4)  // K's scales of the two groups, and V's
+        copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
+                      at.block >= 0);
     };
     const int first = (I.tile0 + I.t0) * kChunkKeys + warp * kRqKeys, last = (I.tile0 + I.t1) * kChunkKeys;
-    int64_t block = -1, at = first < last ? place(first, block) : -1;
+    Group at{-1, -1};
+    if (first < last) at = place(first);
 #pragma unroll 1
-    for (int i = 0; i < kRqStages - 1; ++i) {
-      const int k0 = first + i * kRqSpan;
-      if (k0 < last) fetch(at, block, i);
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      const int k0 = first + i * S::kSpan;
+      if (k0 < last) fetch(at, k0, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (k0 + kRqSpan < last) at = place(k0 + kRqSpan, block);
+      if (k0 + S::kSpan < last) at = place(k0 + S::kSpan);
     }
-    // q of rows g and g + 8: values 16 c and on of each 64, scaled and as fp16
-    uint32_t q[kSteps][4];
-    float rs[2];
-    int lo[2], hi[2];
+    // q of rows 8 x + g: values 16 c and on of each 64, scaled and as fp16
+    uint32_t q[NT][D / 8];
+    float rs[NT][2];           // of rows 8 x + 2 c and the next: what a score is multiplied by for base-2 exponents
+    int lo[NT][2], hi[NT][2];
+    // keys that every row sees (rows that are not there see all, and are not stored)
+    int all_lo = 0, all_hi = 0x7fffffff;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NT; ++x) {
       const int r = g + 8 * x, tok = r / p.tile_heads;
       uint4 v[D / 64][2];
       float top = 0.f;
@@ -173,113 +190,141 @@ __global__ void __launch_bounds__(kRqThreads, 1) chunk_quant_rows_kernel(const C
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const bool finite = top <= 3.4e38f;  // an infinity makes all of the row NaN
-      const int e = scale_exponent(finite ? top : 0.f);
-      const float f = finite ? power_of_two(-e) : __uint_as_float(0x7fffffffu);
-      rs[x] = power_of_two(e) * p.scale_log2;
+      const int ex = scale_exponent(finite ? top : 0.f);
+      const float f = finite ? power_of_two(-ex) : __uint_as_float(0x7fffffffu);
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // pair i of the 16: step 4 h + i / 2, its first or second pair
+        for (int i = 0; i < 8; ++i) {
           const uint4 u = v[h][i / 4];
           const uint32_t w = i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w;
-          uint32_t r16;
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r16) : "f"(bf16_hi(w) * f), "f"(bf16_lo(w) * f));
-          q[4 * h + i / 2][2 * (i & 1) + x] = r16;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[x][8 * h + i]) : "f"(bf16_hi(w) * f), "f"(bf16_lo(w) * f));
         }
       }
-      const KeyRange k = chunk_keys(p, I.qo, I.kv, I.first_tok + tok, I.first_tok + tok + 1);
-      lo[x] = k.lo;
-      hi[x] = r < rows ? k.hi : 0;
+      const float scaled = power_of_two(ex) * p.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rs[x][e] = __shfl_sync(0xffffffffu, scaled, 4 * (2 * c + e));
+        const int row = 8 * x + 2 * c + e, t = I.first_tok + row / p.tile_heads;
+        const KeyRange k = chunk_keys(p, I.qo, I.kv, t, t + 1);
+        lo[x][e] = k.lo;
+        hi[x][e] = k.hi;
+        if (row < rows) {
+          all_lo = max(all_lo, k.lo);
+          all_hi = min(all_hi, k.hi);
+        }
+      }
     }
-    float o[kTiles][4];
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    float o[NT][kTiles][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int x = 0; x < NT; ++x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][t][e] = 0.f;
+      m[x][0] = m[x][1] = -INFINITY;
+      l[x][0] = l[x][1] = 0.f;
+    }
     int stage = 0;
 #pragma unroll 1
-    for (int k0 = first; k0 < last; k0 += kRqSpan) {
-      const int ahead = k0 + (kRqStages - 1) * kRqSpan;
+    for (int k0 = first; k0 < last; k0 += S::kSpan) {
+      const int ahead = k0 + (S::kStages - 1) * S::kSpan;
       __syncwarp();  // the stage that is filled next has been read
-      if (ahead < last) fetch(at, block, stage == 0 ? kRqStages - 1 : stage - 1);
+      if (ahead < last) fetch(at, ahead, stage == 0 ? S::kStages - 1 : stage - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (ahead + kRqSpan < last) at = place(ahead + kRqSpan, block);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRqStages - 1) : "memory");
+      if (ahead + S::kSpan < last) at = place(ahead + S::kSpan);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
       __syncwarp();  // the other lanes' copies too
       const uint32_t from = ring + stage * S::kStage;
-      if (++stage == kRqStages) stage = 0;
+      if (++stage == S::kStages) stage = 0;
       float4 scale;  // K's of the two groups, V's of the two
       asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                    : "=f"(scale.x), "=f"(scale.y), "=f"(scale.z), "=f"(scale.w)
                    : "r"(from + 2 * S::kCodes)
                    : "memory");
-      // scores of the two groups of 8 keys: columns 2 c and 2 c + 1 of rows g and g + 8
-      float s[2][4];
+      // scores of keys g and g + 8 with rows 8 x + 2 c and the next
+      float s[NT][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int key = 8 * n + g;
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t k[2][8];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = 8 * n + g;
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"(from + key * D + k_chunk<D>(key, 4 * h + c) * 16)
                        : "memory");
-          uint32_t k[8];
-          to_f16(v, k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma_16816(s[n], q[4 * h + i], k[2 * i], k[2 * i + 1]);
+          to_f16(v, k[n]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+            mma_16816(s[x], k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[x][8 * h + 2 * i],
+                      q[x][8 * h + 2 * i + 1]);
       }
       const float lb[2] = {fast_log2(fmaxf(scale.z, kScaleMin)), fast_log2(fmaxf(scale.w, kScaleMin))};
+      const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
       bool raise = false;
-      float alpha[2] = {1.f, 1.f};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float top = -INFINITY;
+      for (int x = 0; x < NT; ++x) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          // (the factor is not 0: a masked score is -inf below, and a tiny one stays a number)
-          const float f = fmaf(n ? scale.y : scale.x, rs[x], 1e-37f);
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = k0 + 8 * n + 2 * c + e;
-            float& y = s[n][2 * x + e];
-            y = j >= lo[x] && j < hi[x] ? fmaf(y, f, lb[n]) : -INFINITY;
-            top = fmaxf(top, y);
+          for (int n = 0; n < 2; ++n) {
+            // (the factor is not 0: a tiny one stays a number)
+            float& y = s[x][2 * n + e];
+            y = fmaf(y, fmaf(n ? scale.y : scale.x, rs[x][e], 1e-37f), lb[n]);
+            if (masked) {
+              const int j = k0 + 8 * n + g;
+              if (j < lo[x][e] || j >= hi[x][e]) y = -INFINITY;
+            }
           }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) - kRqShift;
-        if (top > m[x] + kRqRaise || (m[x] == -INFINITY && top > -INFINITY)) {
-          alpha[x] = fast_exp2(m[x] - top);  // (0 for the first)
-          m[x] = top;
-          raise = true;
+          raise = raise || fmaxf(s[x][e], s[x][2 + e]) > m[x][e] + kRqRaise;
         }
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          l[x] *= alpha[x];
+        for (int x = 0; x < NT; ++x) {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            o[t][2 * x] *= alpha[x];
-            o[t][2 * x + 1] *= alpha[x];
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(s[x][e], s[x][2 + e]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (top > m[x][e] + kRqRaise) {
+              const float alpha = fast_exp2(m[x][e] - (top - kRqShift));  // (0 for the first)
+              m[x][e] = top - kRqShift;
+              l[x][e] *= alpha;
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                o[x][t][e] *= alpha;
+                o[x][t][2 + e] *= alpha;
+              }
+            }
           }
         }
       }
-      uint32_t w[4];
+      uint32_t w[NT][2];
+      const float inverse[2] = {fast_exp2(-lb[0]), fast_exp2(-lb[1])};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float base = m[x] == -INFINITY ? 0.f : m[x];
+      for (int x = 0; x < NT; ++x) {
+        const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float a = fast_exp2(s[n][2 * x] - base), b = fast_exp2(s[n][2 * x + 1] - base);
-          l[x] = fmaf(a + b, fast_exp2(-lb[n]), l[x]);
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[2 * n + x]) : "f"(b), "f"(a));
+          const float a = fast_exp2(s[x][2 * n] - b0), b = fast_exp2(s[x][2 * n + 1] - b1);
+          l[x][0] = fmaf(a, inverse[n], l[x][0]);
+          l[x][1] = fmaf(b, inverse[n], l[x][1]);
+          uint32_t pair;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(b), "f"(a));
+          w[x][n] = turned(pair);
         }
       }
       // values: rows of keys 2 c, 2 c + 1, 2 c + 8 and 2 c + 9, values D / 8 g and on
@@ -298,48 +343,52 @@ __global__ void __launch_bounds__(kRqThreads, 1) chunk_quant_rows_kernel(const C
       }
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
-        uint32_t b0[4], b1[4];  // of four columns
-        pairs_to_f16(__byte_perm(v[0][e], v[1][e], 0x5140), __byte_perm(v[0][e], v[1][e], 0x7362), b0);
-        pairs_to_f16(__byte_perm(v[2][e], v[3][e], 0x5140), __byte_perm(v[2][e], v[3][e], 0x7362), b1);
+        uint32_t a[4], b[4];  // of four values, of keys 2 c and 2 c + 1, and of the other two
+        pairs_to_f16(__byte_perm(v[0][e], v[1][e], 0x5140), __byte_perm(v[0][e], v[1][e], 0x7362), a);
+        pairs_to_f16(__byte_perm(v[2][e], v[3][e], 0x5140), __byte_perm(v[2][e], v[3][e], 0x7362), b);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) mma_16816(o[4 * e + t], w, b0[t], b1[t]);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+            mma_16816(o[x][2 * e + t], a[2 * t], a[2 * t + 1], b[2 * t], b[2 * t + 1], w[x][0], w[x][1]);
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the warps' outputs go where their keys were
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if (c == 0) {
-        sM[warp * kRqRows + g + 8 * x] = m[x];
-        sL[warp * kRqRows + g + 8 * x] = l[x];
-      }
-      // columns 2 c and 2 c + 1 of tile t are values D / 8 * (2 c) + t and D / 8 * (2 c + 1) + t
-      float* to = sAcc + (warp * kRqRows + g + 8 * x) * D + (D / 8) * 2 * c;
+    for (int x = 0; x < NT; ++x) {
 #pragma unroll
-      for (int t = 0; t < kTiles; t += 4) {
-        *reinterpret_cast<float4*>(to + t) =
-            make_float4(o[t][2 * x], o[t + 1][2 * x], o[t + 2][2 * x], o[t + 3][2 * x]);
-        *reinterpret_cast<float4*>(to + D / 8 + t) =
-            make_float4(o[t][2 * x + 1], o[t + 1][2 * x + 1], o[t + 2][2 * x + 1], o[t + 3][2 * x + 1]);
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * x + 2 * c + e;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
+        if (g == 0) {
+          sM[warp * S::kRows + row] = m[x][e];
+          sL[warp * S::kRows + row] = l[x][e];
+        }
+        // tile t has values D / 8 g + 2 t and the next
+        float* to = sAcc + (warp * S::kRows + row) * D + (D / 8) * g;
+#pragma unroll
+        for (int t = 0; t < kTiles; t += 2)
+          *reinterpret_cast<float4*>(to + 2 * t) =
+              make_float4(o[x][t][e], o[x][t][2 + e], o[x][t + 1][e], o[x][t + 1][2 + e]);
       }
     }
     __syncthreads();
-    // the eight warps' outputs of 4 columns of a row
+    // the warps' outputs of 4 columns of a row
     const int64_t part = part_slot(I, blockIdx.x);
-    for (int i = tid; i < rows * (D / 4); i += kRqThreads) {
+    for (int i = tid; i < rows * (D / 4); i += S::kThreads) {
       const int r = i / (D / 4), col = 4 * (i - r * (D / 4));
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kRqWarps; ++w) top = fmaxf(top, sM[w * kRqRows + r]);
+      for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, sM[w * S::kRows + r]);
       const float base = top == -INFINITY ? 0.f : top;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kRqWarps; ++w) {
-        const float f = fast_exp2(sM[w * kRqRows + r] - base);
-        const float4 a = *reinterpret_cast<const float4*>(sAcc + (w * kRqRows + r) * D + col);
-        sum = fmaf(sL[w * kRqRows + r], f, sum);
+      for (int w = 0; w < S::kWarps; ++w) {
+        const float f = fast_exp2(sM[w * S::kRows + r] - base);
+        const float4 a = *reinterpret_cast<const float4*>(sAcc + (w * S::kRows + r) * D + col);
+        sum = fmaf(sL[w * S::kRows + r], f, sum);
         y.x = fmaf(a.x, f, y.x);
         y.y = fmaf(a.y, f, y.y);
         y.z = fmaf(a.z, f, y.z);
@@ -367,11 +416,12 @@ __global__ void __launch_bounds__(kRqThreads, 1) chunk_quant_rows_kernel(const C
 // ------------------------------------------------------------------- host
 namespace {
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D>>(RowsQuantShape<D>::kSmem);
+  using S = RowsQuantShape<D, NT>;
+  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D, NT>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_quant_rows_kernel<D>, dim3((unsigned)p.grid), kRqThreads, RowsQuantShape<D>::kSmem, stream, p);
+  return launch_dependent(chunk_quant_rows_kernel<D, NT>, dim3((unsigned)p.grid), S::kThreads, S::kSmem, stream, p);
 }
 
 }  // namespace
@@ -379,7 +429,9 @@ cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
 cudaError_t launch_chunk_quant_rows(const ChunkParams& p, cudaStream_t stream) {
   last_kernel() = "chunk_quant_rows_kernel";
   profile_begin(stream);
-  const cudaError_t e = p.head_dim == 64 ? launch_rows<64>(p, stream) : launch_rows<128>(p, stream);
+  cudaError_t e;
+  if (p.rows == 8) e = p.head_dim == 64 ? launch_rows<64, 1>(p, stream) : launch_rows<128, 1>(p, stream);
+  else e = p.head_dim == 64 ? launch_rows<64, 2>(p, stream) : launch_rows<128, 2>(p, stream);
   profile_end(stream);
   return e;
 }
