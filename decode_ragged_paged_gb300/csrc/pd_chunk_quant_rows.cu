@@ -106,8 +106,17 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   }
   const int blocks = p.page_size / p.scale_block, block_shift = 31 - __clz(p.scale_block);
-  // what a lane copies: 16-byte chunk `chunk` of key key0 and of every (32 / chunks of a row)th from there on
+  // What a lane copies of 16 keys: 16-byte chunk `chunk` of key key0 and of every kStep-th from there on, kPer / kPer2
+  // of each group of 8; where from, after the group's first row, and where to in a stage. (K's place in the swizzle is the
+  // same for all of them, V's for every other.)
+  constexpr int kStep = 32 / kChunks, kPer2 = 2;
+  const uint8_t* k_pool = static_cast<const uint8_t*>(p.k_pool);
+  const uint8_t* v_pool = static_cast<const uint8_t*>(p.v_pool);
   const int key0 = lane / kChunks, chunk = lane % kChunks, row_step = p.nhd ? p.hkv : 1;
+  const int64_t from0 = (int64_t)key0 * row_step * D + chunk * 16, step = (int64_t)kStep * row_step * D;
+  const uint32_t to_k = key0 * D + k_chunk<D>(key0, chunk) * 16;
+  const uint32_t to_v[2] = {(uint32_t)(S::kCodes + key0 * D + v_chunk<D>(key0, chunk) * 16),
+                            (uint32_t)(S::kCodes + key0 * D + v_chunk<D>(key0 + kStep, chunk) * 16)};
   ChunkItem I;
   while (walk.next(p, I)) {
     __syncthreads();  // the line, or the last item's outputs, have been read
@@ -135,18 +144,25 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
     auto fetch = [&](const Group& at, int k0, int stage) {
       const uint32_t to = ring + stage * S::kStage;
       const int64_t r0 = __shfl_sync(0xffffffffu, at.row, 0), r1 = __shfl_sync(0xffffffffu, at.row, 1);
-      const bool whole = k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0;
+      if (k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0) {
+        const int64_t f0 = r0 * D + from0, f1 = r1 * D + from0;
+        const uint8_t* src[4] = {k_pool + f0, k_pool + f1, v_pool + f0, v_pool + f1};  // K and V of either group
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        constexpr int kStep = 32 / kChunks;  // keys of 32 lanes
-        const int key = key0 + i * kStep;    // (of a group: i * kStep / 8)
-        const int64_t base = i * kStep < 8 ? r0 : r1;
-        bool there = true;
-        if (!whole) there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
-        const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
-        copy_async<16>(to + key * D + k_chunk<D>(key, chunk) * 16, static_cast<const uint8_t*>(p.k_pool) + from, there);
-        copy_async<16>(to + S::kCodes + key * D + v_chunk<D>(key, chunk) * 16,
-                       static_cast<const uint8_t*>(p.v_pool) + from, there);
+        for (int i = 0; i < kPer; ++i) {
+          const int n = i * kPer2 / kPer, x = i - n * (kPer / kPer2);  // group, and number in it
+          copy_async<16>(to + to_k + i * (kStep * D), src[n] + x * step, true);
+          copy_async<16>(to + to_v[i & 1] + i * (kStep * D), src[2 + n] + x * step, true);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int key = key0 + i * kStep;
+          const int64_t base = key < 8 ? r0 : r1;
+          const bool there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
+          const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
+          copy_async<16>(to + to_k + i * (kStep * D), k_pool + from, there);
+          copy_async<16>(to + to_v[i & 1] + i * (kStep * D), v_pool + from, there);
+        }
       }
       if (lane < 4)  // K's scales of the two groups, and V's
         copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
