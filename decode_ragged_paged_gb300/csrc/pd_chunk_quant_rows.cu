@@ -37,9 +37,9 @@ constexpr float kRqShift = 4.0f, kRqRaise = 12.0f;
 template <int D, int NT>
 struct RowsQuantShape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = NT == 1 ? 16 : 8, kThreads = 32 * kWarps;
+  static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
   static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
-  static constexpr int kStages = NT == 1 ? 3 : 6;
+  static constexpr int kStages = NT == 1 ? 4 : 6;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
   static constexpr int kStage = 2 * kCodes + 16;                  // and four scales
   static constexpr int kWarp = kStages * kStage;
