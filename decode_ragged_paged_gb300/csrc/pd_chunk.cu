@@ -661,8 +661,10 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   const bool quant = p.scale_block > 0;
   const int64_t most = (int64_t)p.max_qo_len * p.group;  // rows of a request's KV head
   p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && p.scale_block % 8 == 0;
-  // Few rows of an 8-bit cache have a kernel of their own.
-  p.few = quant && p.tc && most <= 16;
+  // Few rows of an 8-bit cache have a kernel of their own: up to 8, the columns of its products. Measured against the
+  // tensor-core kernel, 8 KV heads, D 128: 4 rows, 4 requests of up to 255 keys 7.1 and 9.5 us, 128 of 512 to 4096 keys 132
+  // and 160 us; 16 rows (8 columns twice) 207 and 164 us.
+  p.few = quant && p.tc && most <= 8;
   p.tc = p.tc && !p.few;
   if (p.tc) {
     p.tile_heads = p.group <= 128 ? p.group : 1;
@@ -674,14 +676,17 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.max_parts = device_sm_count();
   } else {
     // Rows of an item: 4 or 16 where that takes a request's rows in one go or in a
-    // few (the kernel for few rows), else 64. Of 8-bit pools the tiled kernel takes any
-    // number of rows that theirs does not; in it 16 cost a fourth of 64.
-    if (p.few) p.rows = most <= 8 ? 8 : 16;
+    // few (the kernel for few rows), else 64. Of 8-bit pools the tiled kernel takes what
+    // theirs does not; in it 16 cost a fourth of 64.
+    if (p.few) p.rows = 8;
     else if (quant) p.rows = most <= 16 && p.group <= 16 ? 16 : 64;
     else p.rows = most <= 4 ? 4 : most <= 64 && p.group <= 16 ? 16 : 64;
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
-    p.item_cost = 1;
+    // In the kernel for few rows of 8-bit pools an item's ends (its first copies' latency, and the meeting of the warps)
+    // cost what 8 tiles do: 128 decodes of 512 to 4096 keys take 140, 135, 133, 132 and 131 us counted as 1, 4, 6, 8
+    // and 10, 24 of them 40.1, -, 36.6, 36.4 and 36.9.
+    p.item_cost = p.few ? 8 : 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
     p.max_parts = device_sm_count() * (p.rows == 64 || (quant && !p.few) ? 2 : 1);  // CTAs that an SM holds
   }

@@ -1,23 +1,28 @@
 // pd_chunk_quant_rows.cu -- chunk attention over a cache held in 8 bits, for few query
-// rows (single tokens, a few drafted ones; bf16 queries, pages and blocks of a multiple of 8 tokens).
+// rows (single tokens, a drafted one or two; bf16 queries, pages and blocks of a multiple of 8 tokens).
 //
-// HBM bound: an item has at most 8 or 16 query rows (tokens x heads of a KV head), and its
-// keys pass once. Tiles of 128 rows through tensor memory would keep 4 of them busy, a
-// softmax warp of 4 and every wait between the roles for them (128 decodes of 512 to 4096 keys:
-// 160 us); so here a warp does all of it by itself, as the fp32 kernel for few rows does, with
-// products of 8 columns (mma.m16n8k16, fp16 in, fp32 out) that are the query rows, and the
-// CTA's warps meet at an item's end only:
+// An item has at most 8 query rows (tokens x heads of a KV head), and its keys pass once, so the cache's bytes
+// are the floor. Tiles of 128 rows through tensor memory would keep 8 of them busy at most, a
+// softmax warp of 4 and every wait between the roles for them; so here a warp does all of it by itself,
+// with products of 8 columns (mma.m16n8k16, fp16 in, fp32 out) that are the query rows, and the CTA's warps
+// meet at an item's end only:
 //   16 keys a warp in turn: their 8-bit rows come through a ring of its own in shared memory by
 //     cp.async, the scales of their two 8-key groups with them;
-//   scores, K q^T: q as fp16 (scaled by a power of two a row, exact), k as fp16 by one conversion a
-//     pair. The products' inner index may be any order of the head's values, so a lane takes 16
-//     neighbouring bytes of a key and not 2 here and there;
+//   scores, K q^T: q as fp16 (scaled by a power of two a row, so that its largest lies in (224, 448]; exact but for
+//     values under 2^-25 of the largest, off by 2^-32 of it at most), k as fp16 by one conversion a pair, exact. The products' inner index may be any
+//     order of the head's values, so a lane takes 16 neighbouring bytes of a key and not 2 here and there;
 //   weights W = 2^(s + log2 b - m), b the key's scale of V and m the row's running maximum of s + log2 b, fp16 with
 //     the largest from 2^4 to 2^12: only a score over that raises m, and has the lanes' maxima
-//     exchanged. Their sum over b is the softmax's;
+//     exchanged. Their sum over b, in fp32, is the softmax's;
 //   o, V^T W: the weights' 8 x 8 blocks turned by movmatrix; a lane takes 16 neighbouring values of 4 keys, and a byte
 //     of two keys is one pair.
-// (With the rows as the 16 of the products, 8 of them empty, a turn took twice the products and registers,
+// An item's first copies are under way while the outputs of the one before are joined (139 us, 144 after them).
+//
+// 128 requests of 512 to 4096 keys, 32 query and 8 KV heads of 128: 132 us, 4.3 TB/s; the cache's bytes take 84 at the
+// copy rate. What holds it is each warp's chain from a key's bytes to its weights, at 3 warps a scheduler
+// (1.8 instructions a cycle and SM; a third of the stalls wait for the instruction before): its 168 registers allow 12
+// warps. 8, 10 and 16 warps (of 128 registers): 166, 148 and 153 us when 12 took 144; 3 CTAs of 4 warps 182.
+// (With the rows as the 16 of the products, half of them empty, a turn took twice the products and registers,
 // and 8 warps an SM: 210 us.)
 #include <math.h>
 
@@ -33,19 +38,18 @@ namespace {
 constexpr int kRqKeys = 16;  // of a warp's turn
 constexpr float kRqShift = 4.0f, kRqRaise = 12.0f;
 
-// NT: 8 query rows each.
-template <int D, int NT>
+template <int D>
 struct RowsQuantShape {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
+  static constexpr int kRows = 8;
+  static constexpr int kWarps = 12, kThreads = 32 * kWarps;
   static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
-  static constexpr int kStages = NT == 1 ? 4 : 6;
+  static constexpr int kStages = 3;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
   static constexpr int kStage = 2 * kCodes + 16;                  // and four scales
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kJoin = kRows * D * 4;                     // a warp's output
-  static constexpr int kRing = kWarps * (kWarp > kJoin ? kWarp : kJoin);
-  static constexpr size_t kSmem = kRing + 2 * kWarps * kRows * sizeof(float);
+  static constexpr int kRing = kWarps * kWarp;
+  static constexpr size_t kSmem = kRing + kWarps * kJoin + 2 * kWarps * kRows * sizeof(float);
   static_assert(kSelfBytes <= kRing && kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -75,6 +79,9 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool t
                  : "memory");
 }
 
+// Two bf16 of eight.
+__device__ __forceinline__ uint32_t q_pair(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 // Where 16-byte chunk `c` of a key's row lies in a stage, so that the lanes that read together meet in no bank (of
 // V with D = 64 two do).
 template <int D>
@@ -84,9 +91,9 @@ __device__ __forceinline__ int v_chunk(int key, int c) { return D == 128 ? c ^ (
 
 }  // namespace
 
-template <int D, int NT>
-__global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quant_rows_kernel(const ChunkParams p) {
-  using S = RowsQuantShape<D, NT>;
+template <int D>
+__global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_rows_kernel(const ChunkParams p) {
+  using S = RowsQuantShape<D>;
   constexpr int kTiles = D / 16;       // of 16 values of the output
   constexpr int kChunks = D / 16;      // 16-byte chunks of a row
   constexpr int kPer = kRqKeys * kChunks / 32;  // chunks of K (or V) that a lane copies
@@ -94,8 +101,8 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(rq_smem) + warp * S::kWarp;
-  float* sAcc = reinterpret_cast<float*>(rq_smem);                // [warp][row][D]
-  float* sM = reinterpret_cast<float*>(rq_smem + S::kRing);       // [warp][row] maxima, then sums
+  float* sAcc = reinterpret_cast<float*>(rq_smem + S::kRing);     // [warp][row][D]
+  float* sM = sAcc + S::kWarps * S::kRows * D;                    // [warp][row] maxima, then sums
   float* sL = sM + S::kWarps * S::kRows;
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -117,60 +124,77 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
   const uint32_t to_k = key0 * D + k_chunk<D>(key0, chunk) * 16;
   const uint32_t to_v[2] = {(uint32_t)(S::kCodes + key0 * D + v_chunk<D>(key0, chunk) * 16),
                             (uint32_t)(S::kCodes + key0 * D + v_chunk<D>(key0 + kStep, chunk) * 16)};
-  ChunkItem I;
-  while (walk.next(p, I)) {
-    __syncthreads();  // the line, or the last item's outputs, have been read
-    const int rows = I.tokens * p.tile_heads;
-    const int kv_head = I.h / p.group;
-    // A warp's 16 keys from k0 on are two groups of 8, a run of slots of one page each. An odd lane has the second, an
-    // even one the first: its first row in the pools, and its block of the scales; -1 where no row of the item sees it.
-    struct Group {
-      int64_t row, block;
-    };
-    auto place = [&](int k0) -> Group {
-      const int j = k0 + 8 * (lane & 1);
-      if (j + 8 <= I.keys.lo || j >= I.keys.hi) return Group{-1, -1};
-      const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-      const int page = p.page_indices[I.pbase + idx], slot = j - idx * p.page_size;
-      if (page < 0 || page >= p.num_pages) {
-        report(p.status, PD_DEV_BAD_PAGE_TABLE);
-        return Group{-1, -1};
-      }
-      const int64_t head = (int64_t)page * p.hkv + kv_head;
-      return Group{p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head : head * p.page_size + slot,
-                   head * blocks + (p.page_shift >= 0 ? slot >> block_shift : slot / p.scale_block)};
-    };
-    // Starts the copies of the keys from k0 on into a stage; those that no row of the item sees become zeros.
-    auto fetch = [&](const Group& at, int k0, int stage) {
-      const uint32_t to = ring + stage * S::kStage;
-      const int64_t r0 = __shfl_sync(0xffffffffu, at.row, 0), r1 = __shfl_sync(0xffffffffu, at.row, 1);
-      if (k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0) {
-        const int64_t f0 = r0 * D + from0, f1 = r1 * D + from0;
-        const uint8_t* src[4] = {k_pool + f0, k_pool + f1, v_pool + f0, v_pool + f1};  // K and V of either group
+  __syncthreads();  // the line has been read
+  ChunkItem I{};
+  int kv_head = 0, first = 0, last = 0;  // of the item: its KV head, the warp's first key, the end
+  uint4 raw[D / 64][2];                  // row g's values 16 c and on of each 64
+  // A warp's 16 keys from k0 on are two groups of 8, a run of slots of one page each. An odd lane has the second, an
+  // even one the first: its first row in the pools, and its block of the scales; -1 where no row of the item sees it.
+  struct Group {
+    int64_t row, block;
+  };
+  auto place = [&](int k0) -> Group {
+    const int j = k0 + 8 * (lane & 1);
+    if (j + 8 <= I.keys.lo || j >= I.keys.hi) return Group{-1, -1};
+    const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+    const int page = p.page_indices[I.pbase + idx], slot = j - idx * p.page_size;
+    if (page < 0 || page >= p.num_pages) {
+      report(p.status, PD_DEV_BAD_PAGE_TABLE);
+      return Group{-1, -1};
+    }
+    const int64_t head = (int64_t)page * p.hkv + kv_head;
+    return Group{p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head : head * p.page_size + slot,
+                 head * blocks + (p.page_shift >= 0 ? slot >> block_shift : slot / p.scale_block)};
+  };
+  // Starts the copies of the keys from k0 on into a stage; those that no row of the item sees become zeros.
+  auto fetch = [&](const Group& at, int k0, int stage) {
+    const uint32_t to = ring + stage * S::kStage;
+    const int64_t r0 = __shfl_sync(0xffffffffu, at.row, 0), r1 = __shfl_sync(0xffffffffu, at.row, 1);
+    if (k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0) {
+      const int64_t f0 = r0 * D + from0, f1 = r1 * D + from0;
+      const uint8_t* src[4] = {k_pool + f0, k_pool + f1, v_pool + f0, v_pool + f1};  // K and V of either group
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int n = i * kPer2 / kPer, x = i - n * (kPer / kPer2);  // group, and number in it
-          copy_async<16>(to + to_k + i * (kStep * D), src[n] + x * step, true);
-          copy_async<16>(to + to_v[i & 1] + i * (kStep * D), src[2 + n] + x * step, true);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int key = key0 + i * kStep;
-          const int64_t base = key < 8 ? r0 : r1;
-          const bool there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
-          const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
-          copy_async<16>(to + to_k + i * (kStep * D), k_pool + from, there);
-          copy_async<16>(to + to_v[i & 1] + i * (kStep * D), v_pool + from, there);
-        }
+      for (int i = 0; i < kPer; ++i) {
+        const int n = i * kPer2 / kPer, x = i - n * (kPer / kPer2);  // group, and number in it
+        copy_async<16>(to + to_k + i * (kStep * D), src[n] + x * step, true);
+        copy_async<16>(to + to_v[i & 1] + i * (kStep * D), src[2 + n] + x * step, true);
       }
-      if (lane < 4)  // K's scales of the two groups, and V's
-        copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
-                      at.block >= 0);
-    };
-    const int first = (I.tile0 + I.t0) * kChunkKeys + warp * kRqKeys, last = (I.tile0 + I.t1) * kChunkKeys;
-    Group at{-1, -1};
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int key = key0 + i * kStep;
+        const int64_t base = key < 8 ? r0 : r1;
+        const bool there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
+        const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
+        copy_async<16>(to + to_k + i * (kStep * D), k_pool + from, there);
+        copy_async<16>(to + to_v[i & 1] + i * (kStep * D), v_pool + from, there);
+      }
+    }
+    if (lane < 4)  // K's scales of the two groups, and V's
+      copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
+                    at.block >= 0);
+  };
+  Group at{-1, -1};
+  // The walk's next item: starts its first turns' copies, and reads q. False: there is none.
+  auto start = [&]() -> bool {
+    if (!walk.next(p, I)) return false;
+    kv_head = I.h / p.group;
+    first = (I.tile0 + I.t0) * kChunkKeys + warp * kRqKeys;
+    last = (I.tile0 + I.t1) * kChunkKeys;
+    at = Group{-1, -1};
     if (first < last) at = place(first);
+    const int tok = g / p.tile_heads;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        raw[h][e] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < I.tokens)
+          raw[h][e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                           (int64_t)(I.q0 + tok) * p.q_stride +
+                                                           (int64_t)(I.h + g - tok * p.tile_heads) * D + 64 * h + 16 * c) + e);
+      }
+    __syncwarp();  // the last item's stages have been read
 #pragma unroll 1
     for (int i = 0; i < S::kStages - 1; ++i) {
       const int k0 = first + i * S::kSpan;
@@ -178,72 +202,54 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (k0 + S::kSpan < last) at = place(k0 + S::kSpan);
     }
-    // q of rows 8 x + g: values 16 c and on of each 64, scaled and as fp16
-    uint32_t q[NT][D / 8];
-    float rs[NT][2];           // of rows 8 x + 2 c and the next: what a score is multiplied by for base-2 exponents
-    int lo[NT][2], hi[NT][2];
+    return true;
+  };
+  bool more = start();
+  while (more) {
+    const int rows = I.tokens * p.tile_heads;
+    // q as fp16, scaled
+    uint32_t q[D / 8];
+    float rs[2];        // of rows 2 c and the next: what a score is multiplied by for base-2 exponents
+    int lo[2], hi[2];
     // keys that every row sees (rows that are not there see all, and are not stored)
     int all_lo = 0, all_hi = 0x7fffffff;
+    float top = 0.f;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      const int r = g + 8 * x, tok = r / p.tile_heads;
-      uint4 v[D / 64][2];
-      float top = 0.f;
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t w = q_pair(raw[i / 8][i / 4 % 2], i % 4);
+      top = fmaxf(top, fmaxf(fabsf(bf16_lo(w)), fabsf(bf16_hi(w))));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool finite = top <= 3.4e38f;  // an infinity makes all of the row NaN
+    const int ex = scale_exponent(finite ? top : 0.f);
+    const float f = finite ? power_of_two(-ex) : __uint_as_float(0x7fffffffu);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t w = q_pair(raw[i / 8][i / 4 % 2], i % 4);
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(bf16_hi(w) * f), "f"(bf16_lo(w) * f));
+    }
+    const float scaled = power_of_two(ex) * p.scale_log2;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[h][e] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows)
-            v[h][e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                           (int64_t)(I.q0 + tok) * p.q_stride +
-                                                           (int64_t)(I.h + r - tok * p.tile_heads) * D + 64 * h + 16 * c) + e);
-          const uint32_t w[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-        }
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const bool finite = top <= 3.4e38f;  // an infinity makes all of the row NaN
-      const int ex = scale_exponent(finite ? top : 0.f);
-      const float f = finite ? power_of_two(-ex) : __uint_as_float(0x7fffffffu);
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 u = v[h][i / 4];
-          const uint32_t w = i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w;
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[x][8 * h + i]) : "f"(bf16_hi(w) * f), "f"(bf16_lo(w) * f));
-        }
-      }
-      const float scaled = power_of_two(ex) * p.scale_log2;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        rs[x][e] = __shfl_sync(0xffffffffu, scaled, 4 * (2 * c + e));
-        const int row = 8 * x + 2 * c + e, t = I.first_tok + row / p.tile_heads;
-        const KeyRange k = chunk_keys(p, I.qo, I.kv, t, t + 1);
-        lo[x][e] = k.lo;
-        hi[x][e] = k.hi;
-        if (row < rows) {
-          all_lo = max(all_lo, k.lo);
-          all_hi = min(all_hi, k.hi);
-        }
+    for (int e = 0; e < 2; ++e) {
+      rs[e] = __shfl_sync(0xffffffffu, scaled, 4 * (2 * c + e));
+      const int row = 2 * c + e, t = I.first_tok + row / p.tile_heads;
+      const KeyRange k = chunk_keys(p, I.qo, I.kv, t, t + 1);
+      lo[e] = k.lo;
+      hi[e] = k.hi;
+      if (row < rows) {
+        all_lo = max(all_lo, k.lo);
+        all_hi = min(all_hi, k.hi);
       }
     }
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    float o[NT][kTiles][4];
-    float m[NT][2], l[NT][2];
+    float o[kTiles][4];
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][t][e] = 0.f;
-      m[x][0] = m[x][1] = -INFINITY;
-      l[x][0] = l[x][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     int stage = 0;
 #pragma unroll 1
     for (int k0 = first; k0 < last; k0 += S::kSpan) {
@@ -261,12 +267,8 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
                    : "=f"(scale.x), "=f"(scale.y), "=f"(scale.z), "=f"(scale.w)
                    : "r"(from + 2 * S::kCodes)
                    : "memory");
-      // scores of keys g and g + 8 with rows 8 x + 2 c and the next
-      float s[NT][4];
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
+      // scores of keys g and g + 8 with rows 2 c and the next
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint32_t k[2][8];
@@ -282,66 +284,54 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-            mma_16816(s[x], k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[x][8 * h + 2 * i],
-                      q[x][8 * h + 2 * i + 1]);
+          mma_16816(s, k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[8 * h + 2 * i], q[8 * h + 2 * i + 1]);
       }
       const float lb[2] = {fast_log2(fmaxf(scale.z, kScaleMin)), fast_log2(fmaxf(scale.w, kScaleMin))};
       const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
       bool raise = false;
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            // (the factor is not 0: a tiny one stays a number)
-            float& y = s[x][2 * n + e];
-            y = fmaf(y, fmaf(n ? scale.y : scale.x, rs[x][e], 1e-37f), lb[n]);
-            if (masked) {
-              const int j = k0 + 8 * n + g;
-              if (j < lo[x][e] || j >= hi[x][e]) y = -INFINITY;
-            }
+        for (int n = 0; n < 2; ++n) {
+          // (the factor is not 0: a tiny one stays a number)
+          float& y = s[2 * n + e];
+          y = fmaf(y, fmaf(n ? scale.y : scale.x, rs[e], 1e-37f), lb[n]);
+          if (masked) {
+            const int j = k0 + 8 * n + g;
+            if (j < lo[e] || j >= hi[e]) y = -INFINITY;
           }
-          raise = raise || fmaxf(s[x][e], s[x][2 + e]) > m[x][e] + kRqRaise;
         }
+        raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + kRqRaise;
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
+        for (int e = 0; e < 2; ++e) {
+          float best = fmaxf(s[e], s[2 + e]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[x][e], s[x][2 + e]);
+          for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+          if (best > m[e] + kRqRaise) {
+            const float alpha = fast_exp2(m[e] - (best - kRqShift));  // (0 for the first)
+            m[e] = best - kRqShift;
+            l[e] *= alpha;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (top > m[x][e] + kRqRaise) {
-              const float alpha = fast_exp2(m[x][e] - (top - kRqShift));  // (0 for the first)
-              m[x][e] = top - kRqShift;
-              l[x][e] *= alpha;
-#pragma unroll
-              for (int t = 0; t < kTiles; ++t) {
-                o[x][t][e] *= alpha;
-                o[x][t][2 + e] *= alpha;
-              }
+            for (int t = 0; t < kTiles; ++t) {
+              o[t][e] *= alpha;
+              o[t][2 + e] *= alpha;
             }
           }
         }
       }
-      uint32_t w[NT][2];
+      uint32_t w[2];
       const float inverse[2] = {fast_exp2(-lb[0]), fast_exp2(-lb[1])};
+      const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float a = fast_exp2(s[x][2 * n] - b0), b = fast_exp2(s[x][2 * n + 1] - b1);
-          l[x][0] = fmaf(a, inverse[n], l[x][0]);
-          l[x][1] = fmaf(b, inverse[n], l[x][1]);
-          uint32_t pair;
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(b), "f"(a));
-          w[x][n] = turned(pair);
-        }
+      for (int n = 0; n < 2; ++n) {
+        const float a = fast_exp2(s[2 * n] - b0), b = fast_exp2(s[2 * n + 1] - b1);
+        l[0] = fmaf(a, inverse[n], l[0]);
+        l[1] = fmaf(b, inverse[n], l[1]);
+        uint32_t pair;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(b), "f"(a));
+        w[n] = turned(pair);
       }
       // values: rows of keys 2 c, 2 c + 1, 2 c + 8 and 2 c + 9, values D / 8 g and on
       uint32_t v[4][D / 32];
@@ -363,36 +353,31 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
         pairs_to_f16(__byte_perm(v[0][e], v[1][e], 0x5140), __byte_perm(v[0][e], v[1][e], 0x7362), a);
         pairs_to_f16(__byte_perm(v[2][e], v[3][e], 0x5140), __byte_perm(v[2][e], v[3][e], 0x7362), b);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-            mma_16816(o[x][2 * e + t], a[2 * t], a[2 * t + 1], b[2 * t], b[2 * t + 1], w[x][0], w[x][1]);
+        for (int t = 0; t < 2; ++t) mma_16816(o[2 * e + t], a[2 * t], a[2 * t + 1], b[2 * t], b[2 * t + 1], w[0], w[1]);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the warps' outputs go where their keys were
+    const int64_t part = part_slot(I, blockIdx.x);
+    const int64_t q0 = I.q0;
+    const int h0 = I.h;
+    more = start();   // its copies are under way while the warps' outputs are joined
+    __syncthreads();  // the last item's outputs have been read
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
+    for (int e = 0; e < 2; ++e) {
+      const int row = 2 * c + e;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * x + 2 * c + e;
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
-        if (g == 0) {
-          sM[warp * S::kRows + row] = m[x][e];
-          sL[warp * S::kRows + row] = l[x][e];
-        }
-        // tile t has values D / 8 g + 2 t and the next
-        float* to = sAcc + (warp * S::kRows + row) * D + (D / 8) * g;
-#pragma unroll
-        for (int t = 0; t < kTiles; t += 2)
-          *reinterpret_cast<float4*>(to + 2 * t) =
-              make_float4(o[x][t][e], o[x][t][2 + e], o[x][t + 1][e], o[x][t + 1][2 + e]);
+      for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+      if (g == 0) {
+        sM[warp * S::kRows + row] = m[e];
+        sL[warp * S::kRows + row] = l[e];
       }
+      // tile t has values D / 8 g + 2 t and the next
+      float* to = sAcc + (warp * S::kRows + row) * D + (D / 8) * g;
+#pragma unroll
+      for (int t = 0; t < kTiles; t += 2)
+        *reinterpret_cast<float4*>(to + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
     }
     __syncthreads();
     // the warps' outputs of 4 columns of a row
-    const int64_t part = part_slot(I, blockIdx.x);
     for (int i = tid; i < rows * (D / 4); i += S::kThreads) {
       const int r = i / (D / 4), col = 4 * (i - r * (D / 4));
       float top = -INFINITY, sum = 0.f;
@@ -413,7 +398,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
       const float inv = sum != 0.f ? 1.f / sum : 0.f;
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       const int tok = r / p.tile_heads;
-      const int64_t row = (int64_t)(I.q0 + tok) * p.hq + I.h + r - tok * p.tile_heads;
+      const int64_t row = (q0 + tok) * p.hq + h0 + r - tok * p.tile_heads;
       if (part < 0 && p.o_dtype == PD_BF16)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + col) =
             make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
@@ -432,12 +417,12 @@ __global__ void __launch_bounds__(RowsQuantShape<D, NT>::kThreads, 1) chunk_quan
 // ------------------------------------------------------------------- host
 namespace {
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
-  using S = RowsQuantShape<D, NT>;
-  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D, NT>>(S::kSmem);
+  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D>>(RowsQuantShape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_quant_rows_kernel<D, NT>, dim3((unsigned)p.grid), S::kThreads, S::kSmem, stream, p);
+  return launch_dependent(chunk_quant_rows_kernel<D>, dim3((unsigned)p.grid), RowsQuantShape<D>::kThreads,
+                          RowsQuantShape<D>::kSmem, stream, p);
 }
 
 }  // namespace
@@ -445,9 +430,7 @@ cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
 cudaError_t launch_chunk_quant_rows(const ChunkParams& p, cudaStream_t stream) {
   last_kernel() = "chunk_quant_rows_kernel";
   profile_begin(stream);
-  cudaError_t e;
-  if (p.rows == 8) e = p.head_dim == 64 ? launch_rows<64, 1>(p, stream) : launch_rows<128, 1>(p, stream);
-  else e = p.head_dim == 64 ? launch_rows<64, 2>(p, stream) : launch_rows<128, 2>(p, stream);
+  const cudaError_t e = p.head_dim == 64 ? launch_rows<64>(p, stream) : launch_rows<128>(p, stream);
   profile_end(stream);
   return e;
 }
