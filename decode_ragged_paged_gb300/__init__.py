@@ -5,7 +5,7 @@ in-tree by ``decode_ragged_paged_gb300.build``). The functions carry the C
 names and only marshal arguments: torch tensors give device pointers, shapes
 and the current CUDA stream; every step of the computation runs in the
 library's CUDA kernels. The calls of a serving step (pd_batch_tables,
-pd_qk_norm_rope*, pd_attn_chunk) are checked and marshalled by a small extension
+pd_qk_norm_rope*, pd_kv_append_quant, pd_attn_chunk, pd_attn_chunk_quant) are checked and marshalled by a small extension
 module (``csrc/pd_bind.cpp``), as a short step's calls would otherwise take longer
 in Python than on the GPU. There is no CPU path: if ``libpd.so`` is missing or a
 call fails, an exception is raised.
@@ -17,7 +17,10 @@ Tensor layouts (see ``include/pd.h``):
     qo_indptr       int32 [B+1]; kv_len int32 [B]; page_indptr int32 [B+1];
     page_indices    int32 [nnz]
     lse             fp32 [total_qo][Hq], natural log
-    positions       int32 [total_qo]; slot_map int64 [total_qo] (page * P + slot, -1: padding)
+    positions       int32 [total_qo]; slot_map int64 [total_qo] (page * P + slot, -1: padding);
+                    with several axes [axes][total_qo]
+    8-bit pools     torch.float8_e4m3fn (or uint8), shaped as above; k_scale, v_scale fp32
+                    [num_pages][Hkv][P / block]
 """
 from __future__ import annotations
 

@@ -425,7 +425,8 @@ int pd_kv_append_quant(const pd_kv_quant_desc* d, const pd_batch* b, const void*
     return PD_ERR_INVALID_ARG;
   if (d->layout != PD_LAYOUT_HND && d->layout != PD_LAYOUT_NHD) return PD_ERR_INVALID_ARG;
   if (b->batch_size < 0 || b->total_qo < 0 || b->max_kv_len < 0) return PD_ERR_INVALID_ARG;
-  if (d->head_dim % 8 != 0 || d->head_dim > 1024 || d->num_kv_heads > (1 << 14)) return PD_ERR_UNSUPPORTED;
+  if (d->head_dim % 8 != 0 || d->head_dim > 1024 || d->num_kv_heads > (1 << 14) || d->scale_block > (1 << 20))
+    return PD_ERR_UNSUPPORTED;  // (a block's values are counted in 32 bits)
   if (b->batch_size == 0 || b->total_qo == 0) return PD_OK;
   if (b->num_pages <= 0 || b->qo_indptr == nullptr || b->kv_len == nullptr || b->page_indptr == nullptr ||
       b->page_indices == nullptr)

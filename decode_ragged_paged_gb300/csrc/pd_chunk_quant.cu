@@ -1,26 +1,34 @@
 // pd_chunk_quant.cu -- the tensor-core kernel of the chunk attention over a cache held
-// in 8 bits (bf16 queries; pages and blocks of a multiple of 8 tokens).
+// in 8 bits (bf16 queries; pages and blocks of a multiple of 8 tokens; more than 8 query rows a KV head).
 //
 // For a block of tokens with scales a of K and b of V, and e4m3 values k, v:
 //   s_j = scale a_j <q, k_j>,  o = sum_j softmax(s)_j b_j v_j
-// How the work is dealt, what the two groups of softmax warps share, and the softmax
-// itself are those of pd_chunk_tc.cu. What the 8 bits change:
+// How the work is dealt and what the two groups of softmax warps share are those of pd_chunk_tc.cu.
+// What the 8 bits change:
 //   K enters the products as it is in memory (kind::f8f6f4), and so q has to be e4m3
 //     too: x = h + l of the row's scaled values, h = rn(x), l = rn(x - h). With the row's
 //     largest value in (224, 448], bf16's 8 bits are two times e4m3's 4, so h + l is x itself
 //     from 1/4 up and off by at most 2^-10 below (2^-17 of the row's largest value). [h | l]
-//     [k | k]^T takes as long as bf16's product and reads half the bytes; K is not
-//     converted. The scales a_j are the same for 8 columns of the scores at least: they are
-//     multiplied into the softmax's own factor.
-//   V becomes bf16, v b rounded (exact for a power of two), by four warps of their own, on
-//     its way from the ring of its 8-bit rows to a short one of the products' operands. As a
-//     second e4m3 operand it would want the weights as two e4m3 terms, which is
-//     more work for the softmax warps, and they are what a long prefill waits for.
-// Warps: 0 loads K, 2 V and 4 Q; 1 and 5 issue the products with K of group 0 and 1,
-// 3 and 7 those with V; 6 finds the work; 8-11 and 12-15 are the groups; 16-19
-// split q and convert V. The scales of a tile's 8-token groups are fetched by
-// cp.async of the loaders' lanes, counted on the barrier of the tile that they belong to;
-// those of K are kept for 32 tiles, as the softmax reads them after K's slot is free.
+//     [k | k]^T takes as long as bf16's product and reads half the bytes; K is not converted.
+//   V becomes fp16, exactly and without its scale, on its way from the ring of its 8-bit rows to
+//     a short one of the products' operands, by four warps of their own.
+//   Both scales belong to 8 tokens at least, and act on the scores: with m the row's running maximum
+//     of s_j + log2 b_j (base 2) the weights are W_j = 2^(s_j + log2 b_j - m), o = sum W_j v_j / sum (W_j / b_j).
+//     An exponent is one product and sum either way, so the scales cost a load and a sum for each 8.
+//   W is fp16, as V is. A row's largest is 2^3 when m is set, and m stays until a tile's weights add up to
+//     2^15 or more: then m is raised out of that sum, the output so far scaled, and the tile done again. At 2^3
+//     the rounding of weights below 2^-14 is at most 2^-28 of the largest contribution. The sums are fp32.
+// Warps (20, of 96 registers: the softmax's tile of 64 scores and its weights want them): 0 finds the work; 6 loads K
+// and makes a tile's factors out of its scales, 2 loads V and 4 Q; 1 and 5 issue the products with K of group 0 and
+// 1, 3 and 7 those with V; 8-11 and 12-15 are the groups; 16-19 split q and convert V. A tile's factors are kept for
+// 32 tiles, as the softmax reads them after K's slot is free.
+//
+// Bound (D 128, 152 SMs): tiles of 64 keys are what fits tensor memory twice beside two outputs, and so the
+// products read 32 KB of q for 16 of K. With V's way through the converters a pair of tiles moves about 170 KB through
+// shared memory, some 1300 cycles at 128 bytes each; 1650 are taken, 10 % of the whole by raised maxima where scales
+// differ much. 4 x 2048 tokens over 14000 to 20000 keys: 1372 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
+// pages: 1015 to 1090); 500 tokens over 32700 keys 232 us; 32 requests of 2 to 8 tokens 53 us (55), there
+// a tile's chain of waits bounds it. Without the exponentials none of them gets shorter.
 //
 // Every wait is bounded; on a timeout the CTA records PD_DEV_TIMEOUT, drains
 // and frees its TMEM.
@@ -38,9 +46,9 @@ constexpr int kCqThreads = 640;
 constexpr int kScaleTiles = 32;  // tiles whose factors are kept
 constexpr int kGroups = kN / 8;  // 8-token groups of a tile
 constexpr int kCqItems = 6;      // items that the scheduler is ahead
-constexpr float kShift = 3.0f;             // log2 of the weight of a row's largest key
+constexpr float kShift = 3.0f;            // log2 of the weight of a row's largest key
 constexpr float kSumShift = kShift + 6;   // and of the sum of 64 alike
-constexpr float kWeightLimit = 32768.0f;  // 2^15: largest row sum of weights taken with a stale maximum
+constexpr float kWeightLimit = 32768.0f;  // 2^15, half of fp16's largest: row sum of weights taken with a stale maximum
 
 // A tile's scales as the softmax takes them.
 struct Factors {
@@ -53,11 +61,11 @@ template <int D>
 struct QuantShape {
   static constexpr uint32_t kQHalf = kM * 128, kQTile = D / 64 * kQHalf;  // query tiles: bf16, then [h | l]
   static constexpr uint32_t kCodes = kN * D;                              // a tile of 8-bit K or V
-  static constexpr uint32_t kVHalf = kN * 128, kVTile = D / 64 * kVHalf;  // a tile of bf16 V
+  static constexpr uint32_t kVHalf = kN * 128, kVTile = D / 64 * kVHalf;  // a tile of fp16 V
   static constexpr int kQ = D == 128 ? 2 : 4;       // slots of the Q ring
   static constexpr int kK = D == 128 ? 7 : 8;       // of K's
   static constexpr int kC = D == 128 ? 6 : 8;       // of V's 8-bit rows
-  static constexpr int kV = D == 128 ? 3 : 4;       // of V's bf16 tiles
+  static constexpr int kV = D == 128 ? 3 : 4;       // of V's fp16 tiles
   static constexpr uint32_t kOffK = kQ * kQTile, kOffC = kOffK + kK * kCodes, kOffV = kOffC + kC * kCodes;
   static constexpr uint32_t kOffBar = kOffV + kV * kVTile;
   static constexpr uint32_t kOffML = kOffBar + 1024;                       // group 1's maxima and sums

@@ -16,6 +16,12 @@
 // lane); larger blocks take 2, 4 or 8. The CTA's first warp finds the blocks that
 // its rows begin: a request's row is looked for with 32 probes at a time, as one
 // after another they would cost a decode more than everything else.
+//
+// Bound: HBM, every new value read once and half or a quarter of that written. Measured (cold caches): 4096
+// tokens of 2 x 40 heads of 128, bf16, 126 MB, 29 us (4.3 TB/s, 65 % of the copy rate); 24 requests of 37 to 700 fp32
+// tokens, 2 x 8 heads of 64, 37 MB, 14 us, two rounds of CTAs that each wait for their places, values and
+// maximum in turn; 128 decodes 4.1 us, the launch. 80 registers, 3 CTAs an SM: with 64 and 4 the three take 29, 14.8
+// and 4.6 us; CTAs of 128 threads 35, 19 and 4.0.
 #include <cfloat>
 #include <type_traits>
 
@@ -205,8 +211,7 @@ __global__ void __launch_bounds__(kQaThreads, 3) kv_append_quant_kernel(const Kv
     const int page = __ldg(p.page_indices + w.entry);  // (on its way with the new values)
     const int vecs = w.count * vpr;
     Vec8<T> x[NV];
-    // vector i of the block: its row and its first element there (where a row's vectors divide a team's lanes, a lane
-    // stays in its column)
+    // vector i of the block: its row
     auto row_of = [&](int i) { return p.vpr_shift >= 0 ? i >> p.vpr_shift : i / vpr; };
     auto load = [&](int i0) {
 #pragma unroll

@@ -13,7 +13,9 @@
 // Positions with several axes (AXES: time, height and width of a token of an image or a
 // video): frequency i turns by the position of its axis, positions[axis(i)][token]. Every lane
 // reads the positions of the frequencies that it makes the cosines of, an item ahead as the
-// single position is; the axes are two bits each of the launch's parameters.
+// single position is; the axes are two bits each of the launch's parameters. Each lane has a position
+// for each of its cosines and not one for all: 16384 tokens of 32 + 2 x 8 heads 85 us with three axes, 79 with one;
+// 4099 tokens of 28 + 2 x 4 heads 25 us, 128 of 32 + 2 x 8 5.5 us.
 //
 // Angle. t in turns is position * (inv_freq / 2 pi) mod 1: the frequency is
 // held as a 64-bit fraction of a turn and multiplied by the position in

@@ -305,10 +305,14 @@ PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_
  * token of the request sees may hold anything, their blocks' scales too.
  *   k_scale, v_scale  device fp32 [num_pages][num_kv_heads][page_size / scale_block]
  *   workspace         pd_attn_chunk_quant_workspace_size(desc, batch, scale_block) bytes
- * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores: a
- * query enters the products with K as two e4m3 terms of its row's scale, which leaves at
- * most 2^-17 of the row's largest value, and the softmax weights, times their keys' scales of
- * V, enter the product with V as fp16. Other calls run in fp32 on the CUDA cores.
+ * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores. A
+ * query is rounded to what 2^-17 of its row's largest value allows (as two e4m3 terms; with
+ * max_qo_len * num_qo_heads / num_kv_heads <= 8 as fp16, to 2^-32). The softmax weights, times
+ * their keys' scales of V, enter the product with V as fp16, the row's largest as 8 or more:
+ * each is off by 2^-11 of itself and 2^-28 of the largest at most, and the sums are fp32. Other
+ * calls run in fp32 on the CUDA cores. On the tensor cores a key whose weight times its scale
+ * of V is below 2^-126 of the row's largest such product counts as none, in lse too (which
+ * matters only where a row sees scales of V more than 2^100 apart).
  */
 PD_API size_t pd_attn_chunk_quant_workspace_size(const pd_attn_desc *desc, const pd_batch *batch,
                                                  int32_t scale_block);
@@ -508,8 +512,9 @@ PD_API int pd_kv_append(const pd_kv_desc *desc, const pd_batch *batch, const voi
  *   k_new, v_new  device, row i at + i * stride elements, [num_kv_heads][head_dim] (dtype);
  *                 stride 0: contiguous; times the element size a multiple of 16 bytes
  * The same call again gives the same cache. Requests with a bad indptr or length are skipped
- * and reported, tokens whose page id is out of range dropped and reported. Supported: head_dim a multiple of 8 up to 1024, at most 16384
- * heads (PD_ERR_UNSUPPORTED).
+ * and reported, tokens whose page id is out of range dropped and reported. Supported: head_dim
+ * a multiple of 8 up to 1024, at most 16384 heads, blocks of at most 2^20 tokens; otherwise
+ * PD_ERR_UNSUPPORTED.
  */
 typedef struct {
   int32_t num_kv_heads; /* Hkv */

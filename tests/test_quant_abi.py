@@ -51,6 +51,7 @@ def _append(lib, **kw):
     (dict(head_dim=100), UNSUPPORTED),        # not whole vectors of 8
     (dict(head_dim=1032), UNSUPPORTED),
     (dict(num_kv_heads=16385), UNSUPPORTED),
+    (dict(page_size=1 << 21, scale_block=1 << 21), UNSUPPORTED),
     (dict(num_pages=0), INVALID),
     (dict(qo_indptr=None), INVALID),
     (dict(kv_len=None), INVALID),
