@@ -5,9 +5,9 @@ in-tree by ``decode_ragged_paged_gb300.build``). The functions carry the C
 names and only marshal arguments: torch tensors give device pointers, shapes
 and the current CUDA stream; every step of the computation runs in the
 library's CUDA kernels. The calls of a serving step (pd_batch_tables,
-pd_qk_norm_rope*, pd_kv_append_quant, pd_attn_chunk, pd_attn_chunk_quant) are checked and marshalled by a small extension
-module (``csrc/pd_bind.cpp``), as a short step's calls would otherwise take longer
-in Python than on the GPU. There is no CPU path: if ``libpd.so`` is missing or a
+pd_qk_norm_rope*, pd_kv_append_quant, pd_attn_chunk, pd_attn_chunk_quant) are
+checked and marshalled by a small extension module (``csrc/pd_bind.cpp``), as a
+short step's calls would otherwise take longer in Python than on the GPU. There is no CPU path: if ``libpd.so`` is missing or a
 call fails, an exception is raised.
 
 Tensor layouts (see ``include/pd.h``):
@@ -211,10 +211,12 @@ def _load_bind():
             if built_for != torch.__version__:  # it reads torch's objects in place
                 raise PdError(f"_pd_bind was built for torch {built_for}, not {torch.__version__}; run "
                               "`python -m decode_ragged_paged_gb300.build`")
-            _pd_bind.init(PdError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-                "pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
-                "pd_attn_chunk_workspace_size", "pd_qk_norm_rope_axes", "pd_qk_norm_rope_axes_append",
-                "pd_kv_append_quant", "pd_attn_chunk_quant", "pd_attn_chunk_quant_workspace_size")))
+            def at(*names):
+                return (ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)
+            _pd_bind.init(PdError, *at("pd_batch_tables", "pd_qk_norm_rope", "pd_qk_norm_rope_append", "pd_attn_chunk",
+                                       "pd_attn_chunk_workspace_size"))
+            _pd_bind.init_more(*at("pd_qk_norm_rope_axes", "pd_qk_norm_rope_axes_append", "pd_kv_append_quant",
+                                   "pd_attn_chunk_quant", "pd_attn_chunk_quant_workspace_size"))
             _bind = _pd_bind
         return _bind
 

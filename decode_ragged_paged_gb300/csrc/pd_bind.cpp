@@ -437,11 +437,16 @@ PyObject* init(PyObject* const* o) {
   g_norm_rope_append = reinterpret_cast<decltype(g_norm_rope_append)>(integer(o[3]));
   g_attn_chunk = reinterpret_cast<decltype(g_attn_chunk)>(integer(o[4]));
   g_chunk_workspace = reinterpret_cast<decltype(g_chunk_workspace)>(integer(o[5]));
-  g_norm_rope_axes = reinterpret_cast<decltype(g_norm_rope_axes)>(integer(o[6]));
-  g_norm_rope_axes_append = reinterpret_cast<decltype(g_norm_rope_axes_append)>(integer(o[7]));
-  g_kv_append_quant = reinterpret_cast<decltype(g_kv_append_quant)>(integer(o[8]));
-  g_chunk_quant = reinterpret_cast<decltype(g_chunk_quant)>(integer(o[9]));
-  g_chunk_quant_workspace = reinterpret_cast<decltype(g_chunk_quant_workspace)>(integer(o[10]));
+  Py_RETURN_NONE;
+}
+
+// init_more(addresses of the other entry points in the order below)
+PyObject* init_more(PyObject* const* o) {
+  g_norm_rope_axes = reinterpret_cast<decltype(g_norm_rope_axes)>(integer(o[0]));
+  g_norm_rope_axes_append = reinterpret_cast<decltype(g_norm_rope_axes_append)>(integer(o[1]));
+  g_kv_append_quant = reinterpret_cast<decltype(g_kv_append_quant)>(integer(o[2]));
+  g_chunk_quant = reinterpret_cast<decltype(g_chunk_quant)>(integer(o[3]));
+  g_chunk_quant_workspace = reinterpret_cast<decltype(g_chunk_quant_workspace)>(integer(o[4]));
   Py_RETURN_NONE;
 }
 
@@ -450,7 +455,8 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<init, 11>("init"),
+PyMethodDef g_methods[] = {method<init, 6>("init"),
+                           method<init_more, 5>("init_more"),
                            method<batch_tables, 20>("batch_tables"),
                            method<norm_rope<false>, 12>("norm_rope"),
                            method<norm_rope<true>, 13>("norm_rope_axes"),

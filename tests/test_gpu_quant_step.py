@@ -1,7 +1,10 @@
 """A serving step over a cache held in 8 bits, as it is used: tables from lengths, norm and rotation with a
 time, a height and a width, append to the 8-bit pages, attention of the new tokens; over several steps of a ragged
 batch, and captured. Each call against its 64-bit form over what the calls before it left."""
+import ctypes
 import random
+import subprocess
+import threading
 
 import pytest
 import torch
@@ -171,6 +174,50 @@ def test_lengths_are_read_on_the_stream_of_the_call(handle):
         torch.cuda.synchronize()
         assert int(status.item()) == 0
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_other_threads_run_during_a_call(tmp_path):
+    """A call that takes long on the host (here: entry points that sleep, in the library's place) does not keep
+    the interpreter's lock."""
+    src = tmp_path / "slow.c"
+    src.write_text("#include <unistd.h>\nint slow(void) { usleep(300000); return 0; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", tmp_path / "slow.so", src], check=True)
+    slow = ctypes.cast(ctypes.CDLL(str(tmp_path / "slow.so")).slow, ctypes.c_void_p).value
+    x, pool = torch.zeros(4, 8, 64, device="cuda"), torch.zeros(4, 8, 16, 64, device="cuda")
+    codes, scale = pool.to(E4M3), torch.ones(4, 8, 1, device="cuda")
+    n, ids, px, f = i32([4]), i32([0, 4]), i32([0, 1, 2, 3]), torch.ones(32, device="cuda")
+    slot, ws = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(64, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(x), torch.empty(4, 8, device="cuda")
+    calls = [
+        lambda: pd.pd_qk_norm_rope_axes(x, x, None, None, f, bytes(32), px.view(1, 4), q_out=x, k_out=x),
+        lambda: pd.pd_qk_norm_rope_axes_append(x, x, x, None, None, f, bytes(32), px.view(1, 4), slot, pool, pool,
+                                               q_out=x),
+        lambda: pd.pd_kv_append_quant(x, x, codes, codes, scale, scale, ids, n, ids, px, max_kv_len=4),
+        lambda: pd.pd_attn_chunk_quant(x, codes, codes, scale, scale, n, ids, px, ids, max_qo_len=4, max_kv_len=4, o=o,
+                                       lse=lse, workspace=ws),
+    ]
+    ticks, stop = [0], threading.Event()
+
+    def count():
+        while not stop.wait(0.002):
+            ticks[0] += 1
+
+    thread = threading.Thread(target=count)
+    thread.start()
+    bind = pd._load_bind()
+    try:
+        bind.init_more(*[slow] * 5)
+        during = []
+        for call in calls:
+            before = ticks[0]
+            call()
+            during.append(ticks[0] - before)
+    finally:
+        pd._bind = None
+        pd._load_bind()  # the library's own again
+        stop.set()
+        thread.join()
+    assert min(during) >= 20, during  # of about 150; two at most with the lock held
 
 
 @pytest.mark.parametrize("hq,hkv,d,page,block,layout", [(8, 2, 128, 16, 16, "HND"), (16, 2, 64, 32, 8, "NHD"),
