@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         const int key = group_key(i0), off = key - (POW2 ? key >> p.page_shift : key / p.page_size) * p.page_size;
         const int next = checked(ahead, i0 + 4);
         ahead = read_page(i0 + 8);
-        const float a = scale_k, b = scale_v;
+        const float a = fmaxf(scale_k, kScaleMin), b = fmaxf(scale_v, kScaleMin);
         if (!is_v) read_scales(next, i0 + 4);
         const int tiles = min(4, nt - i0);
         for (int x = 0; x < tiles; ++x) {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           __syncwarp();
           if (!is_v && x == 0) {
             Factors& f = sFactors[(count + i0 + lane / 8) & (kScaleTiles - 1)];
-            const float lb = fast_log2(fmaxf(b, kScaleMin));
+            const float lb = fast_log2(b);
             if (lane / 8 < tiles) {
               reinterpret_cast<float*>(f.k)[lane & 7] = a;
               reinterpret_cast<float*>(f.log_v)[lane & 7] = lb;

@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
         for (int i = 0; i < 4; ++i)
           mma_16816(s, k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[8 * h + 2 * i], q[8 * h + 2 * i + 1]);
       }
+      const float a[2] = {fmaxf(scale.x, kScaleMin), fmaxf(scale.y, kScaleMin)};
       const float lb[2] = {fast_log2(fmaxf(scale.z, kScaleMin)), fast_log2(fmaxf(scale.w, kScaleMin))};
       const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
       bool raise = false;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
         for (int n = 0; n < 2; ++n) {
           // (the factor is not 0: a tiny one stays a number)
           float& y = s[2 * n + e];
-          y = fmaf(y, fmaf(n ? scale.y : scale.x, rs[e], 1e-37f), lb[n]);
+          y = fmaf(y, fmaf(a[n], rs[e], 1e-37f), lb[n]);
           if (masked) {
             const int j = k0 + 8 * n + g;
             if (j < lo[e] || j >= hi[e]) y = -INFINITY;
@@ -326,11 +327,11 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
       const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const float a = fast_exp2(s[2 * n] - b0), b = fast_exp2(s[2 * n + 1] - b1);
-        l[0] = fmaf(a, inverse[n], l[0]);
-        l[1] = fmaf(b, inverse[n], l[1]);
+        const float w0 = fast_exp2(s[2 * n] - b0), w1 = fast_exp2(s[2 * n + 1] - b1);
+        l[0] = fmaf(w0, inverse[n], l[0]);
+        l[1] = fmaf(w1, inverse[n], l[1]);
         uint32_t pair;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(b), "f"(a));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(w1), "f"(w0));
         w[n] = turned(pair);
       }
       // values: rows of keys 2 c, 2 c + 1, 2 c + 8 and 2 c + 9, values D / 8 g and on

@@ -221,6 +221,20 @@ def test_blocks_of_zeros_and_scales_of_zero(dt, d, page, block):
 
 
 @pytest.mark.parametrize("dt,d,page,block", TYPES)
+@pytest.mark.parametrize("new,kv", [([40, 3], [300, 128]), ([1, 1], [300, 128])])
+def test_scales_below_the_smallest(dt, d, page, block, new, kv):
+    # of any sign they count as 2^-100: the scores of such a block of K are 0 (but for 2^-80), what is masked stays so
+    b = Batch(35, new, kv, 8, 2, d, page, block, dt)
+    for t in (b.ks, b.vs):
+        t.copy_(torch.where(torch.rand_like(t) < 0.3, torch.full_like(t, -0.5), t))
+    b.ks[torch.rand_like(b.ks) < 0.1] = 1e-38
+    b.ks[torch.isnan(b.vs)] = float("nan")
+    b.vs[torch.isnan(b.ks)] = float("nan")
+    b.check()
+    b.check(window=50)
+
+
+@pytest.mark.parametrize("dt,d,page,block", TYPES)
 def test_dead_keys_may_hold_anything(dt, d, page, block):
     # before every row's window: values and scales of NaN
     b = Batch(10, [3], [500], 8, 2, d, page, block, dt)
