@@ -35,17 +35,19 @@ namespace pd {
 
 namespace {
 
-constexpr int kRqKeys = 16;  // of a warp's turn
+constexpr int kRqHalves = 2;              // of a warp's turn, 16 keys each: while one waits, the other is worked on
+constexpr int kRqKeys = 16 * kRqHalves;
+constexpr int kRqGroups = kRqKeys / 8;    // of 8 keys
 constexpr float kRqShift = 4.0f, kRqRaise = 12.0f;
 
 template <int D>
 struct RowsQuantShape {
   static constexpr int kRows = 8;
-  static constexpr int kWarps = 12, kThreads = 32 * kWarps;
+  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
-  static constexpr int kStage = 2 * kCodes + 16;                  // and four scales
+  static constexpr int kStage = 2 * kCodes + 8 * kRqGroups;       // and the groups' scales
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kJoin = kRows * D * 4;                     // a warp's output
   static constexpr int kRing = kWarps * kWarp;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
   // What a lane copies of 16 keys: 16-byte chunk `chunk` of key key0 and of every kStep-th from there on, kPer / kPer2
   // of each group of 8; where from, after the group's first row, and where to in a stage. (K's place in the swizzle is the
   // same for all of them, V's for every other.)
-  constexpr int kStep = 32 / kChunks, kPer2 = 2;
+  constexpr int kStep = 32 / kChunks, kEach = kPer / kRqGroups;
   const uint8_t* k_pool = static_cast<const uint8_t*>(p.k_pool);
   const uint8_t* v_pool = static_cast<const uint8_t*>(p.v_pool);
   const int key0 = lane / kChunks, chunk = lane % kChunks, row_step = p.nhd ? p.hkv : 1;
@@ -128,20 +130,26 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
   ChunkItem I{};
   int kv_head = 0, first = 0, last = 0;  // of the item: its KV head, the warp's first key, the end
   uint4 raw[D / 64][2];                  // row g's values 16 c and on of each 64
-  // A warp's 16 keys from k0 on are two groups of 8, a run of slots of one page each. An odd lane has the second, an
-  // even one the first: its first row in the pools, and its block of the scales; -1 where no row of the item sees it.
+  // A warp's keys from k0 on are groups of 8, a run of slots of one page each; lane n has group n % kRqGroups: its page's
+  // id, read a turn ahead and looked at only where it is used, then its first row in the pools and its block of the
+  // scales (-1: no row of the item sees it).
   struct Group {
     int64_t row, block;
   };
-  auto place = [&](int k0) -> Group {
-    const int j = k0 + 8 * (lane & 1);
-    if (j + 8 <= I.keys.lo || j >= I.keys.hi) return Group{-1, -1};
-    const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-    const int page = p.page_indices[I.pbase + idx], slot = j - idx * p.page_size;
+  auto group_key = [&](int k0) { return k0 + 8 * (lane & (kRqGroups - 1)); };
+  auto seen = [&](int j) { return j + 8 > I.keys.lo && j < I.keys.hi; };
+  auto read_page = [&](int k0) {
+    const int j = group_key(k0);
+    return seen(j) ? __ldg(p.page_indices + I.pbase + (p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size)) : 0;
+  };
+  auto place = [&](int page, int k0) -> Group {
+    const int j = group_key(k0);
+    if (!seen(j)) return Group{-1, -1};
     if (page < 0 || page >= p.num_pages) {
       report(p.status, PD_DEV_BAD_PAGE_TABLE);
       return Group{-1, -1};
     }
+    const int slot = p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
     const int64_t head = (int64_t)page * p.hkv + kv_head;
     return Group{p.nhd ? ((int64_t)page * p.page_size + slot) * p.hkv + kv_head : head * p.page_size + slot,
                  head * blocks + (p.page_shift >= 0 ? slot >> block_shift : slot / p.scale_block)};
@@ -149,40 +157,48 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
   // Starts the copies of the keys from k0 on into a stage; those that no row of the item sees become zeros.
   auto fetch = [&](const Group& at, int k0, int stage) {
     const uint32_t to = ring + stage * S::kStage;
-    const int64_t r0 = __shfl_sync(0xffffffffu, at.row, 0), r1 = __shfl_sync(0xffffffffu, at.row, 1);
-    if (k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && r0 >= 0 && r1 >= 0) {
-      const int64_t f0 = r0 * D + from0, f1 = r1 * D + from0;
-      const uint8_t* src[4] = {k_pool + f0, k_pool + f1, v_pool + f0, v_pool + f1};  // K and V of either group
+    int64_t r[kRqGroups];
+    bool all = true;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int n = i * kPer2 / kPer, x = i - n * (kPer / kPer2);  // group, and number in it
-        copy_async<16>(to + to_k + i * (kStep * D), src[n] + x * step, true);
-        copy_async<16>(to + to_v[i & 1] + i * (kStep * D), src[2 + n] + x * step, true);
+    for (int n = 0; n < kRqGroups; ++n) {
+      r[n] = __shfl_sync(0xffffffffu, at.row, n);
+      all = all && r[n] >= 0;
+    }
+    if (k0 >= I.keys.lo && k0 + kRqKeys <= I.keys.hi && all) {
+#pragma unroll
+      for (int n = 0; n < kRqGroups; ++n) {
+        const int64_t from = r[n] * D + from0;
+        const uint8_t *k = k_pool + from, *v = v_pool + from;
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+          const int i = n * kEach + x;
+          copy_async<16>(to + to_k + i * (kStep * D), k + x * step, true);
+          copy_async<16>(to + to_v[i & 1] + i * (kStep * D), v + x * step, true);
+        }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int key = key0 + i * kStep;
-        const int64_t base = key < 8 ? r0 : r1;
+        const int64_t base = r[i / kEach];
         const bool there = base >= 0 && k0 + key >= I.keys.lo && k0 + key < I.keys.hi;
         const int64_t from = there ? (base + (int64_t)((key & 7) * row_step)) * D + chunk * 16 : 0;
         copy_async<16>(to + to_k + i * (kStep * D), k_pool + from, there);
         copy_async<16>(to + to_v[i & 1] + i * (kStep * D), v_pool + from, there);
       }
     }
-    if (lane < 4)  // K's scales of the two groups, and V's
-      copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < 2 ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
+    if (lane < 2 * kRqGroups)  // K's scales of the groups, and V's
+      copy_async<4>(to + 2 * S::kCodes + 4 * lane, (lane < kRqGroups ? p.k_scale : p.v_scale) + (at.block >= 0 ? at.block : 0),
                     at.block >= 0);
   };
-  Group at{-1, -1};
+  int page = 0;  // of the turn that is fetched next
   // The walk's next item: starts its first turns' copies, and reads q. False: there is none.
   auto start = [&]() -> bool {
     if (!walk.next(p, I)) return false;
     kv_head = I.h / p.group;
     first = (I.tile0 + I.t0) * kChunkKeys + warp * kRqKeys;
     last = (I.tile0 + I.t1) * kChunkKeys;
-    at = Group{-1, -1};
-    if (first < last) at = place(first);
+    page = read_page(first);
     const int tok = g / p.tile_heads;
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
@@ -198,9 +214,9 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
 #pragma unroll 1
     for (int i = 0; i < S::kStages - 1; ++i) {
       const int k0 = first + i * S::kSpan;
-      if (k0 < last) fetch(at, k0, i);
+      if (k0 < last) fetch(place(page, k0), k0, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (k0 + S::kSpan < last) at = place(k0 + S::kSpan);
+      page = read_page(k0 + S::kSpan);
     }
     return true;
   };
@@ -255,25 +271,36 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
     for (int k0 = first; k0 < last; k0 += S::kSpan) {
       const int ahead = k0 + (S::kStages - 1) * S::kSpan;
       __syncwarp();  // the stage that is filled next has been read
-      if (ahead < last) fetch(at, ahead, stage == 0 ? S::kStages - 1 : stage - 1);
+      if (ahead < last) fetch(place(page, ahead), ahead, stage == 0 ? S::kStages - 1 : stage - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (ahead + S::kSpan < last) at = place(ahead + S::kSpan);
+      page = read_page(ahead + S::kSpan);
       asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
       __syncwarp();  // the other lanes' copies too
       const uint32_t from = ring + stage * S::kStage;
       if (++stage == S::kStages) stage = 0;
-      float4 scale;  // K's of the two groups, V's of the two
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(scale.x), "=f"(scale.y), "=f"(scale.z), "=f"(scale.w)
-                   : "r"(from + 2 * S::kCodes)
-                   : "memory");
-      // scores of keys g and g + 8 with rows 2 c and the next
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float a[kRqGroups], sv[kRqGroups];  // the groups' scales of K and V
+#pragma unroll
+      for (int n = 0; n < kRqGroups; n += 4) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(a[n]), "=f"(a[n + 1]), "=f"(a[n + 2]), "=f"(a[n + 3])
+                     : "r"(from + 2 * S::kCodes + 4 * n)
+                     : "memory");
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(sv[n]), "=f"(sv[n + 1]), "=f"(sv[n + 2]), "=f"(sv[n + 3])
+                     : "r"(from + 2 * S::kCodes + 4 * (kRqGroups + n))
+                     : "memory");
+      }
+      // scores of keys 16 x + g and 16 x + g + 8 with rows 2 c and the next
+      float s[kRqHalves][4];
+#pragma unroll
+      for (int x = 0; x < kRqHalves; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        uint32_t k[2][8];
+        uint32_t k[2 * kRqHalves][8];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 2 * kRqHalves; ++n) {
           const int key = 8 * n + g;
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -284,35 +311,41 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          mma_16816(s, k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[8 * h + 2 * i], q[8 * h + 2 * i + 1]);
+#pragma unroll
+          for (int x = 0; x < kRqHalves; ++x)
+            mma_16816(s[x], k[2 * x][2 * i], k[2 * x + 1][2 * i], k[2 * x][2 * i + 1], k[2 * x + 1][2 * i + 1],
+                      q[8 * h + 2 * i], q[8 * h + 2 * i + 1]);
       }
-      const float a[2] = {fmaxf(scale.x, kScaleMin), fmaxf(scale.y, kScaleMin)};
-      const float lb[2] = {fast_log2(fmaxf(scale.z, kScaleMin)), fast_log2(fmaxf(scale.w, kScaleMin))};
+      float lb[kRqGroups];
+#pragma unroll
+      for (int n = 0; n < kRqGroups; ++n) {
+        a[n] = fmaxf(a[n], kScaleMin);
+        lb[n] = fast_log2(fmaxf(sv[n], kScaleMin));
+      }
       const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
-      bool raise = false;
+      float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kRqGroups; ++n) {
           // (the factor is not 0: a tiny one stays a number)
-          float& y = s[2 * n + e];
+          float& y = s[n >> 1][2 * (n & 1) + e];
           y = fmaf(y, fmaf(a[n], rs[e], 1e-37f), lb[n]);
           if (masked) {
             const int j = k0 + 8 * n + g;
             if (j < lo[e] || j >= hi[e]) y = -INFINITY;
           }
+          best[e] = fmaxf(best[e], y);
         }
-        raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + kRqRaise;
       }
-      if (__any_sync(0xffffffffu, raise)) {
+      if (__any_sync(0xffffffffu, best[0] > m[0] + kRqRaise || best[1] > m[1] + kRqRaise)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float best = fmaxf(s[e], s[2 + e]);
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-          if (best > m[e] + kRqRaise) {
-            const float alpha = fast_exp2(m[e] - (best - kRqShift));  // (0 for the first)
-            m[e] = best - kRqShift;
+          for (int d = 4; d < 32; d <<= 1) best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], d));
+          if (best[e] > m[e] + kRqRaise) {
+            const float alpha = fast_exp2(m[e] - (best[e] - kRqShift));  // (0 for the first)
+            m[e] = best[e] - kRqShift;
             l[e] *= alpha;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
@@ -322,39 +355,42 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_ro
           }
         }
       }
-      uint32_t w[2];
-      const float inverse[2] = {fast_exp2(-lb[0]), fast_exp2(-lb[1])};
+      uint32_t w[kRqGroups];
       const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float w0 = fast_exp2(s[2 * n] - b0), w1 = fast_exp2(s[2 * n + 1] - b1);
-        l[0] = fmaf(w0, inverse[n], l[0]);
-        l[1] = fmaf(w1, inverse[n], l[1]);
+      for (int n = 0; n < kRqGroups; ++n) {
+        const float inverse = fast_exp2(-lb[n]);
+        const float w0 = fast_exp2(s[n >> 1][2 * (n & 1)] - b0), w1 = fast_exp2(s[n >> 1][2 * (n & 1) + 1] - b1);
+        l[0] = fmaf(w0, inverse, l[0]);
+        l[1] = fmaf(w1, inverse, l[1]);
         uint32_t pair;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pair) : "f"(w1), "f"(w0));
         w[n] = turned(pair);
       }
-      // values: rows of keys 2 c, 2 c + 1, 2 c + 8 and 2 c + 9, values D / 8 g and on
-      uint32_t v[4][D / 32];
+      // values: rows of a half's keys 2 c, 2 c + 1, 2 c + 8 and 2 c + 9, values D / 8 g and on
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 2 * c + (i & 1) + 8 * (i >> 1), byte = (D / 8) * g;
-        const uint32_t at = from + S::kCodes + key * D + v_chunk<D>(key, byte >> 4) * 16 + (byte & 15);
-        if constexpr (D == 128)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                       : "r"(at)
-                       : "memory");
-        else
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at) : "memory");
-      }
+      for (int x = 0; x < kRqHalves; ++x) {
+        uint32_t v[4][D / 32];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        uint32_t a[4], b[4];  // of four values, of keys 2 c and 2 c + 1, and of the other two
-        pairs_to_f16(__byte_perm(v[0][e], v[1][e], 0x5140), __byte_perm(v[0][e], v[1][e], 0x7362), a);
-        pairs_to_f16(__byte_perm(v[2][e], v[3][e], 0x5140), __byte_perm(v[2][e], v[3][e], 0x7362), b);
+        for (int i = 0; i < 4; ++i) {
+          const int key = 16 * x + 2 * c + (i & 1) + 8 * (i >> 1), byte = (D / 8) * g;
+          const uint32_t at = from + S::kCodes + key * D + v_chunk<D>(key, byte >> 4) * 16 + (byte & 15);
+          if constexpr (D == 128)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                         : "r"(at)
+                         : "memory");
+          else
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at) : "memory");
+        }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) mma_16816(o[2 * e + t], a[2 * t], a[2 * t + 1], b[2 * t], b[2 * t + 1], w[0], w[1]);
+        for (int e = 0; e < D / 32; ++e) {
+          uint32_t a[4], b[4];  // of four values, of keys 2 c and 2 c + 1, and of the other two
+          pairs_to_f16(__byte_perm(v[0][e], v[1][e], 0x5140), __byte_perm(v[0][e], v[1][e], 0x7362), a);
+          pairs_to_f16(__byte_perm(v[2][e], v[3][e], 0x5140), __byte_perm(v[2][e], v[3][e], 0x7362), b);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) mma_16816(o[2 * e + t], a[2 * t], a[2 * t + 1], b[2 * t], b[2 * t + 1], w[2 * x], w[2 * x + 1]);
+        }
       }
     }
     const int64_t part = part_slot(I, blockIdx.x);
