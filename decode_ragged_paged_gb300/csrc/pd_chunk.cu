@@ -690,9 +690,9 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     // In the kernel for few rows of 8-bit pools an item's ends (its first copies' latency, and the meeting of the warps)
     // cost what 8 tiles do: 128 decodes of 512 to 4096 keys take 140, 135, 133, 132 and 131 us counted as 1, 4, 6, 8
     // and 10, 24 of them 40.1, -, 36.6, 36.4 and 36.9.
-    p.item_cost = p.few ? 8 : 1;
+    p.item_cost = p.few ? 6 : 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * (p.rows == 64 || (quant && !p.few) ? 2 : 1);  // CTAs that an SM holds
+    p.max_parts = device_sm_count() * (p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)

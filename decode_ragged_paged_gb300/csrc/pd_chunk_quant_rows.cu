@@ -43,7 +43,7 @@ constexpr float kRqShift = 4.0f, kRqRaise = 12.0f;
 template <int D>
 struct RowsQuantShape {
   static constexpr int kRows = 8;
-  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
+  static constexpr int kWarps = 4, kThreads = 32 * kWarps;
   static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
   static constexpr int kStages = 2;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
@@ -94,7 +94,7 @@ __device__ __forceinline__ int v_chunk(int key, int c) { return D == 128 ? c ^ (
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 1) chunk_quant_rows_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 2) chunk_quant_rows_kernel(const ChunkParams p) {
   using S = RowsQuantShape<D>;
   constexpr int kTiles = D / 16;       // of 16 values of the output
   constexpr int kChunks = D / 16;      // 16-byte chunks of a row
