@@ -666,8 +666,8 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   const int64_t most = (int64_t)p.max_qo_len * p.group;  // rows of a request's KV head
   p.tc = kv_dtype == PD_BF16 && p.page_size % 8 == 0 && p.scale_block % 8 == 0;
   // Few rows of an 8-bit cache have a kernel of their own: up to 8, the columns of its products. Measured against the
-  // tensor-core kernel, 8 KV heads, D 128: 4 rows, 4 requests of up to 255 keys 7.1 and 9.5 us, 128 of 512 to 4096 keys 132
-  // and 160 us; 16 rows (8 columns twice) 207 and 164 us.
+  // tensor-core kernel, 8 KV heads, D 128: 4 rows, 4 requests of up to 255 keys 6.3 and 9.5 us, 128 of 512 to 4096 keys 104
+  // and 160 us; for 16 rows, its products twice, it took 207 us (when it took 144 for 4) and the other 164.
   p.few = quant && p.tc && most <= 8;
   p.tc = p.tc && !p.few;
   if (p.tc) {
@@ -688,8 +688,8 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     p.tile_heads = p.group <= p.rows ? p.group : 1;
     p.item_tokens = p.rows / p.tile_heads;
     // In the kernel for few rows of 8-bit pools an item's ends (its first copies' latency, and the meeting of the warps)
-    // cost what 8 tiles do: 128 decodes of 512 to 4096 keys take 140, 135, 133, 132 and 131 us counted as 1, 4, 6, 8
-    // and 10, 24 of them 40.1, -, 36.6, 36.4 and 36.9.
+    // cost what 6 tiles do: 128 decodes of 512 to 4096 keys take 105.8, 103.7, 103.5 and 104.3 us counted as 2, 4, 6 and 8,
+    // 24 of them 31.6, 31.0, 30.9 and 31.1.
     p.item_cost = p.few ? 6 : 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
     p.max_parts = device_sm_count() * (p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
@@ -725,11 +725,14 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
   // requests 8.9 / 15.0, 11.2 / 17.2, 15.8 / 20.5, 27.4 / 34.4; in fp32 4 requests
   // 10.4 / 10.5, 16.3 / 12.3, 27.9 / 15.8, 16 requests 10.8 / 16.7, 17.4 / 22.6,
   // 38.9 / 43.1, 69.7 / 70.0; fp32 items of 64 rows are better cut from two tiles
-  // on. `most_tiles` bounds what requests shorter than the longest lose by it.
+  // on. Few rows of 8-bit pools, over 256, 512, 1024 and 2048 keys: 4 requests 7.3 / 12.1, 9.1 / 12.9,
+  // 12.5 / 14.4, 18.8 / 15.3, 16 requests 8.4 / 13.4, 10.7 / 14.8, 16.0 / 18.3, 25.3 / 23.6, 32 requests 8.8 / 15.4,
+  // 12.0 / 18.3, 18.0 / 24.4, 28.7 / 34.1, but 16 of 10 to 2048 keys 22.6 / 18.6 (of up to 1024 14.7 / 15.8).
+  // `most_tiles` bounds what requests shorter than the longest lose by it.
   const int64_t all = ((int64_t)p.max_kv_len + kChunkKeys - 1) / kChunkKeys;
   const int64_t seen = ((int64_t)p.window + p.item_tokens) / kChunkKeys + 2;  // through a window
   const int64_t tiles = p.causal && p.window >= 0 && seen < all ? seen : all;
-  const int spare = p.tc ? 13 : p.rows == 64 ? 1 : 4, most_tiles = p.tc ? 16 : p.rows == 64 ? 1 : 8;
+  const int spare = p.tc ? 13 : p.few ? 16 : p.rows == 64 ? 1 : 4, most_tiles = p.tc || p.few ? 16 : p.rows == 64 ? 1 : 8;
   p.uncut = items <= p.max_parts && tiles <= most_tiles && tiles * (p.max_parts - items) <= (int64_t)spare * p.max_parts;
   p.grid = p.uncut ? (int32_t)items : p.max_parts;
   p.self_plan = p.batch <= kSelfBatch && (p.uncut || (p.max_blocks <= kSelfBlocks && p.max_parts <= kSelfParts));

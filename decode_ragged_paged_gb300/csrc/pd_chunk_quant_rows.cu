@@ -6,8 +6,8 @@
 // softmax warp of 4 and every wait between the roles for them; so here a warp does all of it by itself,
 // with products of 8 columns (mma.m16n8k16, fp16 in, fp32 out) that are the query rows, and the CTA's warps
 // meet at an item's end only:
-//   16 keys a warp in turn: their 8-bit rows come through a ring of its own in shared memory by
-//     cp.async, the scales of their two 8-key groups with them;
+//   32 keys a warp in turn, in two halves that do not wait for one another: their 8-bit rows come through a ring of
+//     its own in shared memory by cp.async, the scales of their four 8-key groups with them;
 //   scores, K q^T: q as fp16 (scaled by a power of two a row, so that its largest lies in (224, 448]; exact but for
 //     values under 2^-25 of the largest, off by 2^-32 of it at most), k as fp16 by one conversion a pair, exact. The products' inner index may be any
 //     order of the head's values, so a lane takes 16 neighbouring bytes of a key and not 2 here and there;
@@ -16,14 +16,16 @@
 //     exchanged. Their sum over b, in fp32, is the softmax's;
 //   o, V^T W: the weights' 8 x 8 blocks turned by movmatrix; a lane takes 16 neighbouring values of 4 keys, and a byte
 //     of two keys is one pair.
-// An item's first copies are under way while the outputs of the one before are joined (139 us, 144 after them).
+// An item's first copies are under way while the outputs of the one before are joined (139 us of the case below, 144
+// after them).
 //
-// 128 requests of 512 to 4096 keys, 32 query and 8 KV heads of 128: 132 us, 4.3 TB/s; the cache's bytes take 84 at the
-// copy rate. What holds it is each warp's chain from a key's bytes to its weights, at 3 warps a scheduler
-// (1.8 instructions a cycle and SM; a third of the stalls wait for the instruction before): its 168 registers allow 12
-// warps. 8, 10 and 16 warps (of 128 registers): 166, 148 and 153 us when 12 took 144; 3 CTAs of 4 warps 182.
-// (With the rows as the 16 of the products, half of them empty, a turn took twice the products and registers,
-// and 8 warps an SM: 210 us.)
+// 128 requests of 512 to 4096 keys, 32 query and 8 KV heads of 128: 104 us, 5.4 TB/s; the cache's bytes take 84 at the
+// copy rate. What holds it is each warp's chain from a key's bytes to its weights, at 2 warps a scheduler of 232
+// registers (1.6 instructions a cycle and SM; 28 % of the stalls wait for the instruction before, 22 % for what an item's
+// start reads). One half a turn and 12 warps took 132; a page's id looked at in the turn that reads it 116 for 109; one CTA
+// of 8 warps 109 for 104, of 6 and 7 128 and 119 for 117; three turns in the ring 105; the next item looked up while one is
+// worked off 104. (With the rows as the 16 of the products, half of them empty, a turn took twice the
+// products and registers: 210.)
 #include <math.h>
 
 #include "pd_chunk.cuh"
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 2) chunk_quant_ro
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   }
   const int blocks = p.page_size / p.scale_block, block_shift = 31 - __clz(p.scale_block);
-  // What a lane copies of 16 keys: 16-byte chunk `chunk` of key key0 and of every kStep-th from there on, kPer / kPer2
+  // What a lane copies of a turn's keys: 16-byte chunk `chunk` of key key0 and of every kStep-th from there on, kEach
   // of each group of 8; where from, after the group's first row, and where to in a stage. (K's place in the swizzle is the
   // same for all of them, V's for every other.)
   constexpr int kStep = 32 / kChunks, kEach = kPer / kRqGroups;
