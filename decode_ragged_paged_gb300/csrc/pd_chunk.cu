@@ -692,7 +692,7 @@ ChunkLayout chunk_layout(ChunkParams& p, int32_t kv_dtype) {
     // 24 of them 31.6, 31.0, 30.9 and 31.1.
     p.item_cost = p.few ? 6 : 1;
     p.min_units = 1;  // few tiles: one a CTA, as their latencies would add up
-    p.max_parts = device_sm_count() * (p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
+    p.max_parts = device_sm_count() * (p.few ? rows_quant_ctas(p.head_dim) : p.rows == 64 || quant ? 2 : 1);  // CTAs that an SM holds
   }
   p.page_shift = -1;
   if ((p.page_size & (p.page_size - 1)) == 0)

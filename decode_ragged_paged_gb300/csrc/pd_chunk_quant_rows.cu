@@ -9,8 +9,9 @@
 //   32 keys a warp in turn, in two halves that do not wait for one another: their 8-bit rows come through a ring of
 //     its own in shared memory by cp.async, the scales of their four 8-key groups with them;
 //   scores, K q^T: q as fp16 (scaled by a power of two a row, so that its largest lies in (224, 448]; exact but for
-//     values under 2^-25 of the largest, off by 2^-32 of it at most), k as fp16 by one conversion a pair, exact. The products' inner index may be any
-//     order of the head's values, so a lane takes 16 neighbouring bytes of a key and not 2 here and there;
+//     values under 2^-25 of the largest, off by 2^-32 of it at most), k as fp16 by one conversion a pair, exact. The
+//     products' inner index may be any order of the head's values, so a lane takes 16 neighbouring bytes of a key and not
+//     2 here and there;
 //   weights W = 2^(s + log2 b - m), b the key's scale of V and m the row's running maximum of s + log2 b, fp16 with
 //     the largest from 2^4 to 2^12: only a score over that raises m, and has the lanes' maxima
 //     exchanged. Their sum over b, in fp32, is the softmax's;
@@ -24,7 +25,8 @@
 // registers (1.6 instructions a cycle and SM; 28 % of the stalls wait for the instruction before, 22 % for what an item's
 // start reads). One half a turn and 12 warps took 132; a page's id looked at in the turn that reads it 116 for 109; one CTA
 // of 8 warps 109 for 104, of 6 and 7 128 and 119 for 117; three turns in the ring 105; the next item looked up while one is
-// worked off 104. (With the rows as the 16 of the products, half of them empty, a turn took twice the
+// worked off 104. D 64 fits three CTAs: 78 us with two of them, 68 with three (103 where the SMs had kept
+// less shared memory from the kernel before). (With the rows as the 16 of the products, half of them empty, a turn took twice the
 // products and registers: 210.)
 #include <math.h>
 
@@ -46,6 +48,7 @@ template <int D>
 struct RowsQuantShape {
   static constexpr int kRows = 8;
   static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+  static constexpr int kCtas = rows_quant_ctas(D);                // of an SM
   static constexpr int kSpan = kWarps * kRqKeys;                  // keys of the CTA's turn
   static constexpr int kStages = 2;
   static constexpr int kCodes = kRqKeys * D;                      // K or V of a warp's keys
@@ -54,7 +57,7 @@ struct RowsQuantShape {
   static constexpr int kJoin = kRows * D * 4;                     // a warp's output
   static constexpr int kRing = kWarps * kWarp;
   static constexpr size_t kSmem = kRing + kWarps * kJoin + 2 * kWarps * kRows * sizeof(float);
-  static_assert(kSelfBytes <= kRing && kSmem <= 232448, "shared memory of a CTA");
+  static_assert(kSelfBytes <= kRing && kCtas * (kSmem + 1024) <= 233472, "shared memory of an SM");
 };
 
 // An 8 x 8 block of 16-bit values, two of a row a lane, turned.
@@ -96,7 +99,7 @@ __device__ __forceinline__ int v_chunk(int key, int c) { return D == 128 ? c ^ (
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, 2) chunk_quant_rows_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>::kCtas) chunk_quant_rows_kernel(const ChunkParams p) {
   using S = RowsQuantShape<D>;
   constexpr int kTiles = D / 16;       // of 16 values of the output
   constexpr int kChunks = D / 16;      // 16-byte chunks of a row
@@ -458,7 +461,7 @@ namespace {
 
 template <int D>
 cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D>>(RowsQuantShape<D>::kSmem);
+  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D>, true>(RowsQuantShape<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(chunk_quant_rows_kernel<D>, dim3((unsigned)p.grid), RowsQuantShape<D>::kThreads,
                           RowsQuantShape<D>::kSmem, stream, p);

@@ -317,6 +317,8 @@ int launch_chunk(ChunkParams& p, int32_t kv_dtype, cudaStream_t stream);
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_quant_tc(const ChunkParams& p, cudaStream_t stream);
+// CTAs of the kernel for few rows that an SM holds.
+constexpr int rows_quant_ctas(int head_dim) { return head_dim == 64 ? 3 : 2; }
 cudaError_t launch_chunk_quant_rows(const ChunkParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ tensor maps
