@@ -27,8 +27,10 @@
 // products read 32 KB of q for 16 of K. With V's way through the converters a pair of tiles moves about 170 KB through
 // shared memory, some 1300 cycles at 128 bytes each; 1650 are taken, 10 % of the whole by raised maxima where scales
 // differ much. 4 x 2048 tokens over 14000 to 16384 keys: 1372 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
-// pages: 1015 to 1090); 500 tokens over 32700 keys 232 us; 32 requests of 2 to 8 tokens 53 us (55), there
-// a tile's chain of waits bounds it. Without the exponentials none of them gets shorter.
+// pages: 1015 to 1090); 500 tokens over 32700 keys 230 us (184). Without the exponentials neither gets shorter. With
+// one query tile (32 requests of 2 to 8 tokens: 52 us, bf16 55) a tile of keys takes 0.5 us, 5.0 TB/s, and an
+// item's ends 4.5: the last product, both groups' outputs joined, and the first tile's own maximum, each
+// after the other (152 x 4 tokens over 1024 keys 114 us, 38 over 4096, as many keys, 87).
 //
 // Every wait is bounded; on a timeout the CTA records PD_DEV_TIMEOUT, drains
 // and frees its TMEM.
