@@ -232,3 +232,13 @@ def test_other_threads_run_during_a_call(tmp_path):
 def test_few_rows(hq, hkv, d, page, block, layout, new, kv, window):
     from test_gpu_chunk_quant import Batch
     Batch(3, new, kv, hq, hkv, d, page, block, BF16, layout).check(window=window)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,most", [(140, 4, 1, 128, 1000), (300, 8, 1, 128, 1024), (304, 2, 1, 128, 200),
+                                             (456, 4, 1, 64, 1024), (457, 4, 1, 64, 700), (150, 6, 3, 64, 900)])
+def test_few_rows_of_as_many_requests_as_ctas(n, hq, hkv, d, most):
+    """An item a CTA, or just more than that; more requests than a CTA makes the line of by itself."""
+    from test_gpu_chunk_quant import Batch
+    rng = random.Random(n)
+    kv = [rng.choice([1, 31, 32, 33, 128, rng.randint(1, most)]) for _ in range(n - 1)] + [most]
+    Batch(4, [1] * n, kv, hq, hkv, d, 16, 16, BF16).check()
