@@ -15,9 +15,10 @@
 //   Both scales belong to 8 tokens at least, and act on the scores: with m the row's running maximum
 //     of s_j + log2 b_j (base 2) the weights are W_j = 2^(s_j + log2 b_j - m), o = sum W_j v_j / sum (W_j / b_j).
 //     An exponent is one product and sum either way, so the scales cost a load and a sum for each 8.
-//   W is fp16, as V is. A row's largest is 2^3 when m is set, and m stays until a tile's weights add up to
-//     2^15 or more: then m is raised out of that sum, the output so far scaled, and the tile done again. At 2^3
-//     the rounding of weights below 2^-14 is at most 2^-28 of the largest contribution. The sums are fp32.
+//   W is fp16, as V is. A row's largest is 2^3 to 2^8 when m is set, and m stays until 32 weights of a tile
+//     add up to more than fp16 holds: then m is raised out of that sum, the output so far scaled, and the tile done
+//     again. At 2^3 the rounding of weights below 2^-14 is at most 2^-28 of the largest contribution. The sums are
+//     fp32. (Of 64 weights and 2^15: 232 us where it takes 227; of 16 or 8 the registers did not do: 239.)
 // Warps (20, of 96 registers: the softmax's tile of 64 scores and its weights want them): 0 finds the work; 6 loads K
 // and makes a tile's factors out of its scales, 2 loads V and 4 Q; 1 and 5 issue the products with K of group 0 and
 // 1, 3 and 7 those with V; 8-11 and 12-15 are the groups; 16-19 split q and convert V. A tile's factors are kept for
@@ -26,9 +27,9 @@
 // Bound (D 128, 152 SMs): tiles of 64 keys are what fits tensor memory twice beside two outputs, and so the
 // products read 32 KB of q for 16 of K. With V's way through the converters a pair of tiles moves about 170 KB through
 // shared memory, some 1300 cycles at 128 bytes each; 1650 are taken, 10 % of the whole by raised maxima where scales
-// differ much. 4 x 2048 tokens over 14000 to 16384 keys: 1372 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
-// pages: 1015 to 1090); 500 tokens over 32700 keys 230 us (184). Without the exponentials neither gets shorter. With
-// one query tile (32 requests of 2 to 8 tokens: 52 us, bf16 55) a tile of keys takes 0.5 us, 5.0 TB/s, and an
+// differ much. 4 x 2048 tokens over 14000 to 16384 keys: 1360 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
+// pages: 1015 to 1090); 500 tokens over 32700 keys 227 us (184). Without the exponentials neither gets shorter. With
+// one query tile (32 requests of 2 to 8 tokens: 51 us, bf16 55) a tile of keys takes 0.5 us, 5.0 TB/s, and an
 // item's ends 4.5: the last product, both groups' outputs joined, and the first tile's own maximum, each
 // after the other (152 x 4 tokens over 1024 keys 114 us, 38 over 4096, as many keys, 87).
 //
@@ -49,8 +50,8 @@ constexpr int kScaleTiles = 32;  // tiles whose factors are kept
 constexpr int kGroups = kN / 8;  // 8-token groups of a tile
 constexpr int kCqItems = 6;      // items that the scheduler is ahead
 constexpr float kShift = 3.0f;            // log2 of the weight of a row's largest key
-constexpr float kSumShift = kShift + 6;   // and of the sum of 64 alike
-constexpr float kWeightLimit = 32768.0f;  // 2^15, half of fp16's largest: row sum of weights taken with a stale maximum
+constexpr float kSumShift = kShift + 5;   // and of the sum of 32 alike
+constexpr float kWeightLimit = 65504.0f;  // fp16's largest: sum of 32 weights taken with a stale maximum
 
 // A tile's scales as the softmax takes them.
 struct Factors {
@@ -538,10 +539,10 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           if (!full) hide_scores(t_s, c_lo, c_hi);
           const Factors& factors = sFactors[(count + i) & (kScaleTiles - 1)];
           uint32_t w[kN / 2];
-          float total, part;  // of the tile's weights, and of them over V's scales
+          float most, part;  // the largest sum of 32 of the tile's weights, and the sum of all over V's scales
           // weights of the tile, as fp16 pairs
           auto weights = [&](float nm) {
-            total = part = 0.f;
+            most = part = 0.f;
             uint32_t v[2][16];
             tmem_ld16(t_s, v[0]);
             // all of the tile's at once, while the scores are on their way
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
             for (int n = 0; n < kGroups / 4; ++n) {
               const float4 r = factors.inverse[n];
               const float* x = sums + 4 * n;
-              total += (x[0] + x[1]) + (x[2] + x[3]);
+              most = fmaxf(most, (x[0] + x[1]) + (x[2] + x[3]));
               part += fmaf(x[0], r.x, x[1] * r.y) + fmaf(x[2], r.z, x[3] * r.w);
             }
           };
@@ -588,14 +589,14 @@ __global__ void __launch_bounds__(kCqThreads, 1)
             if (stale) {
               weights(m == -INFINITY ? 0.f : -m);
               if (over) break;  // with the tile's own maximum
-              over = __any_sync(0xffffffffu, valid && total > kWeightLimit);
+              over = __any_sync(0xffffffffu, valid && most > kWeightLimit);
               if (!over) break;
             }
-            // the tile's own maximum: where weights were over the limit, out of their sum, which is between the
-            // largest and 2^6 times that; else out of the scores
+            // the tile's own maximum: where weights were over the limit, out of the largest sum of 32, which is between
+            // the largest and 2^5 times that; else out of the scores
             float ms = -INFINITY;
-            const bool summed = stale && __all_sync(0xffffffffu, !valid || total < 0x1p120f);
-            if (summed) ms = m + fast_log2(total) - kSumShift;
+            const bool summed = stale && __all_sync(0xffffffffu, !valid || most < 0x1p120f);
+            if (summed) ms = m + fast_log2(most) - kSumShift;
 #pragma unroll 1
             for (int c = 0; !summed && c < kN / 32; ++c) {
               uint32_t v[32];
