@@ -26,7 +26,7 @@
 //
 // Bound (D 128, 152 SMs): tiles of 64 keys are what fits tensor memory twice beside two outputs, and so the
 // products read 32 KB of q for 16 of K. With V's way through the converters a pair of tiles moves about 170 KB through
-// shared memory, some 1300 cycles at 128 bytes each; 1640 are taken, 7 % of the whole by raised maxima where scales
+// shared memory, some 1300 cycles at 128 bytes each; 1640 are taken, 8 % of the whole by raised maxima where scales
 // differ much. 4 x 2048 tokens over 14000 to 16384 keys: 1360 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
 // pages: 1015 to 1090); 500 tokens over 32700 keys 227 us (184). Without the exponentials neither gets shorter. With
 // one query tile (32 requests of 2 to 8 tokens: 51 us, bf16 55) a tile of keys takes 0.5 us, 5.0 TB/s, and an
