@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
             if (lane / 8 < tiles) {
               reinterpret_cast<float*>(f.k)[lane & 7] = a;
               reinterpret_cast<float*>(f.log_v)[lane & 7] = lb;
-              reinterpret_cast<float*>(f.inverse)[lane & 7] = fast_exp2(-lb);
+              reinterpret_cast<float*>(f.inverse)[lane & 7] = inverse_scale(lb);
             }
             __syncwarp();
           }
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (++q == S::kQ) q = 0, ++qturn;
       }
       if (!ok) break;
-      float m = valid ? -INFINITY : 0.f, l = 0.f;
+      float m = valid ? -INFINITY : 0.f, l = 0.f;  // (l below 0: minus the sum times kSumFactor)
       const int step = two ? 1 : 2, keys_end = (I.tile0 + I.t1) * kN;
       int k0 = (I.tile0 + I.t0 + I.rot + (two ? 0 : g) - step) * kN;  // first key of the tile before
       for (int i = two ? 0 : g; i < nt; i += step) {  // (with one query tile the others are the other group's)
@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
             stale = over = true;
           }
           if (!ok) break;
-          l += part;
+          l = fmaf(part, l < 0.f ? -kSumFactor : 1.f, l);
+          if (l > kSumHigh) l *= -kSumFactor;
           tmem_st32(t_s, w);
           tmem_wait_st();
           tc_fence_before();
@@ -687,12 +688,17 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         const float top = fmaxf(m, b.x), at = top == -INFINITY ? 0.f : top;
         f0 = exp2f(m - at);
         f1 = exp2f(b.x - at);
-        l = l * f0 + b.y * f1;
+        float l1 = b.y;
+        if (l < 0.f || l1 < 0.f) {  // both as the one that is held times the factor
+          if (l > 0.f) l *= -kSumFactor;
+          if (l1 > 0.f) l1 *= -kSumFactor;
+        }
+        l = l * f0 + l1 * f1;
         m = top;
       }
       tc_fence_after();
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      const float lse2 = l != 0.f ? m + log2f(l) : -INFINITY;
+      const float inv = l != 0.f ? (l < 0.f ? -kSumFactor : 1.f) / l : 0.f;
+      const float lse2 = l != 0.f ? m + (log2f(fabsf(l)) + (l < 0.f ? kSumLog : 0.f)) : -INFINITY;
       const int64_t slot = part_slot(I, blockIdx.x);
       const int mrow = tok0 * p.tile_heads + row;
       const int64_t orow = (int64_t)(I.q0 + tok0 + tok_row) * p.hq + I.h + head;

@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float sum_log = 0.f;  // kSumLog once a sum of the warp's is held times kSumFactor: all of them then
     int stage = 0;
 #pragma unroll 1
     for (int k0 = first; k0 < last; k0 += S::kSpan) {
@@ -343,7 +344,12 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
           best[e] = fmaxf(best[e], y);
         }
       }
-      if (__any_sync(0xffffffffu, best[0] > m[0] + kRqRaise || best[1] > m[1] + kRqRaise)) {
+      if (__any_sync(0xffffffffu, best[0] > m[0] + kRqRaise || best[1] > m[1] + kRqRaise || fmaxf(l[0], l[1]) > kSumHigh)) {
+        if (__any_sync(0xffffffffu, fmaxf(l[0], l[1]) > kSumHigh)) {
+          l[0] *= kSumFactor;
+          l[1] *= kSumFactor;
+          sum_log = kSumLog;
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
       const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
       for (int n = 0; n < kRqGroups; ++n) {
-        const float inverse = fast_exp2(-lb[n]);
+        const float inverse = inverse_scale(lb[n] + sum_log);
         const float w0 = fast_exp2(s[n >> 1][2 * (n & 1)] - b0), w1 = fast_exp2(s[n >> 1][2 * (n & 1) + 1] - b1);
         l[0] = fmaf(w0, inverse, l[0]);
         l[1] = fmaf(w1, inverse, l[1]);
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
       for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
       if (g == 0) {
         sM[warp * S::kRows + row] = m[e];
-        sL[warp * S::kRows + row] = l[e];
+        sL[warp * S::kRows + row] = sum_log == 0.f ? l[e] : -l[e];
       }
       // tile t has values D / 8 g + 2 t and the next
       float* to = sAcc + (warp * S::kRows + row) * D + (D / 8) * g;
@@ -422,22 +428,27 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
     // the warps' outputs of 4 columns of a row
     for (int i = tid; i < rows * (D / 4); i += S::kThreads) {
       const int r = i / (D / 4), col = 4 * (i - r * (D / 4));
-      float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, sum = 0.f, least = 0.f;
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, sM[w * S::kRows + r]);
+      for (int w = 0; w < S::kWarps; ++w) {
+        top = fmaxf(top, sM[w * S::kRows + r]);
+        least = fminf(least, sL[w * S::kRows + r]);
+      }
+      const float plain = least < 0.f ? kSumFactor : 1.f;  // what sums held as they are are multiplied by
       const float base = top == -INFINITY ? 0.f : top;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < S::kWarps; ++w) {
         const float f = fast_exp2(sM[w * S::kRows + r] - base);
         const float4 a = *reinterpret_cast<const float4*>(sAcc + (w * S::kRows + r) * D + col);
-        sum = fmaf(sL[w * S::kRows + r], f, sum);
+        const float l = sL[w * S::kRows + r];
+        sum = fmaf(l < 0.f ? -l : l * plain, f, sum);
         y.x = fmaf(a.x, f, y.x);
         y.y = fmaf(a.y, f, y.y);
         y.z = fmaf(a.z, f, y.z);
         y.w = fmaf(a.w, f, y.w);
       }
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const float inv = sum != 0.f ? plain / sum : 0.f;
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       const int tok = r / p.tile_heads;
       const int64_t row = (q0 + tok) * p.hq + h0 + r - tok * p.tile_heads;
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
         *reinterpret_cast<float4*>((part < 0 ? static_cast<float*>(p.o) + row * D : p.part_o + (part * p.rows + r) * D) +
                                    col) = y;
       if (col == 0) {
-        const float lse2 = sum != 0.f ? top + log2f(sum) : -INFINITY;
+        const float lse2 = sum != 0.f ? top + (log2f(sum) + (least < 0.f ? kSumLog : 0.f)) : -INFINITY;
         if (part >= 0) p.part_lse[part * p.rows + r] = lse2;
         else if (p.lse != nullptr) p.lse[row] = lse2 * kLn2;
       }

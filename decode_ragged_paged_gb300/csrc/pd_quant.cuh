@@ -53,6 +53,19 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+// 1 / b of a scale of V, given as log2 b: also above 2^126, where it is subnormal.
+__device__ __forceinline__ float inverse_scale(float log_b) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(-log_b));
+  return y;
+}
+
+// The softmax's sum is that of weights over their keys' scales of V. A row's largest weight is 2^3 or more and a scale
+// below 2^128, so the sum is above 2^-125. At the other end scales are 2^-100 or more and all weights of a row of 2^24
+// keys come to 2^36: more than fp32 holds. So where a sum has passed kSumHigh, it is held times kSumFactor from
+// there on, below 2^112 with all that may still come, and with a minus sign where others have to tell.
+constexpr float kSumHigh = 0x1p112f, kSumFactor = 0x1p-24f, kSumLog = 24.0f;
+
 // The exponent of the scale of values up to amax (finite, not negative): the smallest power of two,
 // at least 2^-100, times 448 is not below amax. 448 = 1.75 * 2^8. A power of two, because values
 // are then scaled without rounding, and what a block holds already keeps its value when the scale grows

@@ -300,9 +300,11 @@ PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_
 
 /*
  * pd_attn_chunk over a cache held in 8 bits (pools and scales as pd_kv_append_quant
- * leaves them; any finite scales will do, and below 2^-100 they count as that). desc->kv_dtype is q's
- * type. Rows, masks, empty rows, lengths, limits and capture as pd_attn_chunk; keys that no
- * token of the request sees may hold anything, their blocks' scales too.
+ * leaves them; any finite scales will do, and below 2^-100 they count as that; in the kernel
+ * for the CUDA cores the values times the keys that a row sees have to stay inside fp32).
+ * desc->kv_dtype is q's type. Rows, masks, empty rows, lengths, limits and capture as
+ * pd_attn_chunk; keys that no token of the request sees may hold anything, their blocks'
+ * scales too.
  *   k_scale, v_scale  device fp32 [num_pages][num_kv_heads][page_size / scale_block]
  *   workspace         pd_attn_chunk_quant_workspace_size(desc, batch, scale_block) bytes
  * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores. A
