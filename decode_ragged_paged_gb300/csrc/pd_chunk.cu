@@ -11,6 +11,7 @@
 #include <math.h>
 
 #include "pd_chunk.cuh"
+#include "pd_chunk_quant.cuh"
 #include "pd_launch.cuh"
 #include "pd_quant.cuh"
 
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
     };
     const bool has_rows = (tid >> 5) * 2 * RT < rows;  // of this warp's; the others only load
     uint4 kv[NV];
+    bool nan = false;
     if (I.t0 < I.t1) fetch(p.k_pool, p.k_scale, (I.tile0 + I.t0) * kSimtKeys, kv);
     for (int t = I.t0; t < I.t1; ++t) {
       const int k0 = (I.tile0 + t) * kSimtKeys;
@@ -314,6 +316,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
           for (int e = 0; e < CT * 4; ++e) acc[i][e] *= alpha;
         }
       }
+      if constexpr (QUANT) {
+        const KeyRange shared = shared_keys(p, I);
+        if (k0 < shared.lo || k0 + kSimtKeys > shared.hi) nan |= clear_nan(kv);
+      }
       __syncthreads();  // the scores have read K, and the weights are written
       put(kv);
       __syncthreads();
@@ -338,6 +344,21 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const Chunk
       }
     }
     const int64_t slot = part_slot(I, blockIdx.x);
+    if (QUANT && __syncthreads_or(nan)) {
+      const KeyRange shared = shared_keys(p, I), skip{shared.lo + kSimtKeys, shared.hi - kSimtKeys};
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int col = tx * 4 + 64 * c;
+          const uint32_t bad = nan_columns(p, I.pbase, kv_head, max(lo[i], (I.tile0 + I.t0) * kSimtKeys),
+                                           min(hi[i], (I.tile0 + I.t1) * kSimtKeys), skip, col / 16) >> (col & 15);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (bad >> e & 1u) acc[i][4 * c + e] = __uint_as_float(kNan);
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int m = ty * RT + i;

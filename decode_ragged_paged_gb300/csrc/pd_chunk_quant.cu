@@ -38,6 +38,7 @@
 #include <math.h>
 #include <stddef.h>
 
+#include "pd_chunk_quant.cuh"
 #include "pd_chunk_tc.cuh"
 #include "pd_quant.cuh"
 
@@ -81,6 +82,7 @@ struct QuantShape {
 
 struct QuantBars {
   ChunkItem items[kCqItems];  // no tokens: the end
+  int nan[kCqItems];          // V had a NaN where not all of the item's rows see it
   uint64_t item_full[kCqItems], item_empty[kCqItems];
   uint64_t q_full[4], q_ready[4], q_empty[4];
   uint64_t k_full[8], k_empty[8], c_full[8], c_empty[8], v_full[4], v_empty[4];
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       if (!wait(bar(offsetof(QuantBars, item_empty), slot), (turn & 1u) ^ 1u)) break;
       if (lane == 0) {
         bars->items[slot] = I;
+        bars->nan[slot] = 0;
         mbar_arrive(&bars->item_full[slot]);
       }
       __syncwarp();
@@ -748,6 +751,21 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       if (valid) {
         if (slot >= 0) p.part_lse[slot * p.rows + mrow] = lse2;
         else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
+        if (*static_cast<volatile const int*>(&bars->nan[item_slot]) != 0) {
+          const int tok = I.first_tok + tok0 + tok_row;
+          const KeyRange shared = shared_keys(p, I), k = chunk_keys(p, I.qo, I.kv, tok, tok + 1);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t bad = nan_columns(p, I.pbase, I.h / p.group, max(k.lo, (I.tile0 + I.t0) * kN),
+                                       min(k.hi, (I.tile0 + I.t1) * kN), KeyRange{shared.lo + kN, shared.hi - kN}, c);
+            for (int e = 16 * c; bad != 0; bad >>= 1, ++e) {
+              if ((bad & 1u) == 0) continue;
+              if (slot >= 0) p.part_o[(slot * p.rows + mrow) * D + e] = __uint_as_float(kNan);
+              else if (p.o_dtype == PD_BF16) static_cast<uint16_t*>(p.o)[orow * D + e] = (uint16_t)kNan;
+              else static_cast<float*>(p.o)[orow * D + e] = __uint_as_float(kNan);
+            }
+          }
+        }
       }
       tc_fence_before();
       leave_item();
@@ -770,9 +788,12 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     uint32_t q = 0, qturn = 0, cs = 0, cturn = 0, vs = 0, vturn = 0;
     bool ok = true;
     ChunkItem I;
-    while (ok && next_item(I)) {
+    while (ok) {
+      volatile int* nan = &bars->nan[item_slot];  // (the softmax warps keep the item until all of its V is used)
+      if (!next_item(I)) break;
       const int nt = I.t1 - I.t0;
       if (nt <= 0) continue;
+      const KeyRange shared = shared_keys(p, I);
       const int tiles = two_tiles(p, I) ? 2 : 1;
       for (int x = 0; ok && x < tiles; ++x) {
         ok = wait(bar(offsetof(QuantBars, q_full), q), qturn & 1u);
@@ -795,13 +816,14 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (lane == 0) mbar_arrive(&bars->c_empty[cs]);
         const int k0 = tile * kN;
         if (++tile == end) tile = I.tile0 + I.t0;
-        if (k0 < I.keys.lo || k0 + kN > I.keys.hi) {
-          // keys that no row sees: may be NaN, which a weight of 0 would not hide
+        if (k0 < shared.lo || k0 + kN > shared.hi) {
+          // a weight of 0 would not hide a NaN: none of keys that no row sees, and none for now of the others
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
             const int key = k0 + u * kStep + row0;
             if (key < I.keys.lo || key >= I.keys.hi) v[u] = make_uint4(0u, 0u, 0u, 0u);
           }
+          if (clear_nan(v)) *nan = 1;
         }
         ok = wait(bar(offsetof(QuantBars, v_empty), vs), (vturn & 1u) ^ 1u);
         if (!ok) break;

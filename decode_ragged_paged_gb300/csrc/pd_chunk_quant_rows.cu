@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "pd_chunk.cuh"
+#include "pd_chunk_quant.cuh"
 #include "pd_launch.cuh"
 #include "pd_quant.cuh"
 #include "pd_tc.cuh"
@@ -98,7 +99,9 @@ __device__ __forceinline__ int v_chunk(int key, int c) { return D == 128 ? c ^ (
 
 }  // namespace
 
-template <int D>
+// SINGLE: calls of at most one token a request. Rows of one token see the same keys, so no NaN of V has to be kept
+// from any of them (without the code for that four short requests take 6.2 us for 6.5, 128 decodes 102.9 for 103.7).
+template <int D, bool SINGLE>
 __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>::kCtas) chunk_quant_rows_kernel(const ChunkParams p) {
   using S = RowsQuantShape<D>;
   constexpr int kTiles = D / 16;       // of 16 values of the output
@@ -272,6 +275,7 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float sum_log = 0.f;  // kSumLog once a sum of the warp's is held times kSumFactor: all of them then
+    bool nan = false;
     int stage = 0;
 #pragma unroll 1
     for (int k0 = first; k0 < last; k0 += S::kSpan) {
@@ -284,6 +288,22 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
       __syncwarp();  // the other lanes' copies too
       const uint32_t from = ring + stage * S::kStage;
       if (++stage == S::kStages) stage = 0;
+      const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
+      if (!SINGLE && masked && rows > p.tile_heads) {
+#pragma unroll 1
+        for (uint32_t at = from + S::kCodes + 16 * lane; at < from + 2 * S::kCodes; at += 512) {
+          uint4 v[1];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w)
+                       : "r"(at)
+                       : "memory");
+          if (!clear_nan(v)) continue;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w)
+                       : "memory");
+          nan = true;
+        }
+        __syncwarp();
+      }
       float a[kRqGroups], sv[kRqGroups];  // the groups' scales of K and V
 #pragma unroll
       for (int n = 0; n < kRqGroups; n += 4) {
@@ -328,7 +348,6 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
         a[n] = fmaxf(a[n], kScaleMin);
         lb[n] = fast_log2(fmaxf(sv[n], kScaleMin));
       }
-      const bool masked = k0 < all_lo || k0 + kRqKeys > all_hi;
       float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -404,6 +423,20 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
         }
       }
     }
+    if (!SINGLE && __any_sync(0xffffffffu, nan)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // columns D / 8 g and on; turns of 32 keys inside [all_lo, all_hi) were multiplied as they are
+        const uint32_t bad = nan_columns(p, I.pbase, kv_head, max(lo[e], (I.tile0 + I.t0) * kChunkKeys), min(hi[e], last),
+                                         KeyRange{all_lo + kRqKeys, all_hi - kRqKeys}, D / 8 * g / 16) >>
+                             (D / 8 * g % 16);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (bad >> 2 * t & 1u) o[t][e] = __uint_as_float(kNan);
+          if (bad >> (2 * t + 1) & 1u) o[t][2 + e] = __uint_as_float(kNan);
+        }
+      }
+    }
     const int64_t part = part_slot(I, blockIdx.x);
     const int64_t q0 = I.q0;
     const int h0 = I.h;
@@ -470,11 +503,11 @@ __global__ void __launch_bounds__(RowsQuantShape<D>::kThreads, RowsQuantShape<D>
 // ------------------------------------------------------------------- host
 namespace {
 
-template <int D>
+template <int D, bool SINGLE>
 cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D>, true>(RowsQuantShape<D>::kSmem);
+  const cudaError_t e = allow_smem<chunk_quant_rows_kernel<D, SINGLE>, true>(RowsQuantShape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_quant_rows_kernel<D>, dim3((unsigned)p.grid), RowsQuantShape<D>::kThreads,
+  return launch_dependent(chunk_quant_rows_kernel<D, SINGLE>, dim3((unsigned)p.grid), RowsQuantShape<D>::kThreads,
                           RowsQuantShape<D>::kSmem, stream, p);
 }
 
@@ -483,7 +516,9 @@ cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
 cudaError_t launch_chunk_quant_rows(const ChunkParams& p, cudaStream_t stream) {
   last_kernel() = "chunk_quant_rows_kernel";
   profile_begin(stream);
-  const cudaError_t e = p.head_dim == 64 ? launch_rows<64>(p, stream) : launch_rows<128>(p, stream);
+  cudaError_t e;
+  if (p.max_qo_len <= 1) e = p.head_dim == 64 ? launch_rows<64, true>(p, stream) : launch_rows<128, true>(p, stream);
+  else e = p.head_dim == 64 ? launch_rows<64, false>(p, stream) : launch_rows<128, false>(p, stream);
   profile_end(stream);
   return e;
 }

@@ -304,7 +304,8 @@ PD_API int pd_attn_chunk(const pd_attn_desc *desc, const pd_batch *batch, int32_
  * for the CUDA cores the values times the keys that a row sees have to stay inside fp32).
  * desc->kv_dtype is q's type. Rows, masks, empty rows, lengths, limits and capture as
  * pd_attn_chunk; keys that no token of the request sees may hold anything, their blocks'
- * scales too.
+ * scales too. What is NaN in a key that some tokens see (the append makes it of what is not
+ * finite) reaches those tokens and no others: of K their whole rows, of V its column.
  *   k_scale, v_scale  device fp32 [num_pages][num_kv_heads][page_size / scale_block]
  *   workspace         pd_attn_chunk_quant_workspace_size(desc, batch, scale_block) bytes
  * bf16 queries with pages and blocks of a multiple of 8 tokens run on the tensor cores. A
