@@ -8,7 +8,8 @@
 //   scale s', and, if it grew, its earlier values c become rn(c s' / s);
 //   c = rn(x / s), rounded to the nearest e4m3 value, ties to even.
 // What is not finite does not count in amax and becomes NaN, so that one such value
-// spoils its own row and not its block. All of it is exact in fp32 but the one rounding.
+// spoils its own row and not its block. All of it is exact in fp32 but the one rounding: scales are powers of two, and
+// where a caller's own are not, quotient and product are rounded to odd first (odd()).
 //
 // A block has to be read whole before its first value can be written, so a team of warps
 // takes (block, head, K or V), holds its new values in registers, exchanges the
@@ -106,6 +107,12 @@ __device__ __noinline__ float largest_finite(const T* src, int64_t stride, int c
   return m;
 }
 
+// x, which is y cut towards 0, with its last bit set where y - x, `left`, is not 0: rounded from there to far fewer bits it
+// gives what y would, as a tie of those is never made and never lost.
+__device__ __forceinline__ float odd(float x, float left) {
+  return left != 0.f ? __uint_as_float(__float_as_uint(x) | 1u) : x;
+}
+
 // Stores a lane's share of a block's new values one by one, with a division: where some are not finite (what is
 // not becomes NaN), or the caller's own scale is no power of two, whose inverse would not be exact.
 template <typename T>
@@ -116,7 +123,13 @@ __device__ __noinline__ void store_slowly(const T* src, int64_t stride, int coun
     float x;
     if constexpr (sizeof(T) == 4) x = src[tok * stride + d];
     else x = bf16_lo(src[tok * stride + d]);
-    x = fabsf(x) <= FLT_MAX ? x / s : __uint_as_float(0x7fffffffu);
+    if (fabsf(x) <= FLT_MAX) {
+      // (s is not below |x| / 448; where both are small, what the quotient leaves would be below fp32's smallest)
+      const float up = s < 1.f ? 0x1p64f : 1.f, y = x * up, t = s * up, q = __fdiv_rz(y, t);
+      x = odd(q, fmaf(-q, t, y));
+    } else {
+      x = __uint_as_float(0x7fffffffu);
+    }
     to[tok * to_step + d] = (uint8_t)pack_e4m3x2(x, 0.f);
   }
 }
@@ -272,7 +285,8 @@ __global__ void __launch_bounds__(kQaThreads, 3) kv_append_quant_kernel(const Kv
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 y = unpack_e4m3x2(v[e]);
-          v[e] = pack_e4m3x2(y.x * f, y.y * f);
+          const float lo = __fmul_rz(y.x, f), hi = __fmul_rz(y.y, f);
+          v[e] = pack_e4m3x2(odd(lo, fmaf(y.x, f, -lo)), odd(hi, fmaf(y.y, f, -hi)));
         }
         *to = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
       }

@@ -1,11 +1,13 @@
 """pd_attn_chunk_quant held to what include/pd.h says of it: weights off by 2^-11 of themselves (quant_ref.attention
-allows the 2^-8 of bf16 weights), and pools whose offsets pass 32 bits in each of its kernels and in the append."""
+allows the 2^-8 of bf16 weights), and pools whose offsets pass 32 bits in each of its kernels and in the append; the
+append's one rounding where scales are a caller's own."""
 import pytest
 import torch
 
 import quant_ref as qref
 import step_ref as ref
 from test_gpu_chunk_quant import BF16, E4M3, F32, Batch, i32
+from test_gpu_kvquant import Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +85,16 @@ def test_append_past_32_bit_offsets(dt, layout):
     for pool, scale, (codes, scales) in ((k, ks, want[0]), (v, vs, want[1])):
         assert torch.equal(pool[px.long()].view(E4M3).double(), codes)
         assert torch.equal(scale[px.long()].double(), scales)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("factor", [1.3, 1.7, 300.0, 0.01])
+def test_append_to_callers_scales_rounds_once(dt, factor):
+    # scales that are no powers of two: values are those of the exact quotients, to the nearest e4m3
+    for seed in range(3):
+        c = Cache(64 + seed, [3, 5, 40, 7], [20, 30, 47, 8], 4, 128, 16, 16, dt)
+        c.ks *= factor
+        c.vs *= factor
+        want = c.want()
+        c.run()
+        c.check(want)
