@@ -113,3 +113,25 @@ def test_items_after_one_another_in_a_cta(dt, d, page, block):
     check(b, spoil(b, [p for p in places(b, rng, n=1) if p[0] % 2]))
     b = Batch(45, [2] * 700, kv, 4, 2, d, page, block, dt)
     check(b, spoil(b, [p for p in places(b, rng, n=1) if p[0] % 2]))
+
+
+@pytest.mark.parametrize("dt,d,page,block", TYPES)
+@pytest.mark.parametrize("new,kv,window", [([2, 2], [300, 40], -1), ([8, 40], [100, 333], -1), ([8, 40], [100, 333], 20),
+                                           ([300, 70], [700, 64], -1)])
+def test_a_nan_of_k_spoils_the_rows_that_see_it(dt, d, page, block, new, kv, window):
+    # in whole, their lse too, and no others
+    b = Batch(46, new, kv, 4, 2, d, page, block, dt)
+    rng = random.Random(d)
+    want = spoil(b, [])
+    bad, clean = want(True, window)
+    codes = b.k.view(torch.uint8)
+    for r, n in enumerate(kv):
+        for j in (n - 1, n - 1 - new[r] // 3):
+            h = rng.randrange(2)
+            codes[int(b.px[b.pp[r] + j // page]), h, j % page, rng.randrange(d)] = 0xff
+            pos = torch.arange(n - new[r], n, device="cuda")
+            sees = (j <= pos) & ((j >= pos - window) if window >= 0 else torch.ones_like(pos, dtype=torch.bool))
+            bad[b.qo[r]:b.qo[r + 1], 2 * h:2 * h + 2] |= sees[:, None, None]
+    o, lse = b.run(window_left=window)
+    assert torch.equal(torch.isnan(o), bad) and torch.equal(torch.isnan(lse), bad[..., 0])
+    ref.check_attention(torch.where(bad, clean[0].to(o.dtype), o), torch.where(bad[..., 0], clean[1].float(), lse), clean)
