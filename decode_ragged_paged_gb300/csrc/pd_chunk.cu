@@ -136,8 +136,8 @@ constexpr size_t simt_smem() {
 // QUANT: pools of 8-bit values with block scales (the value enters the tile as fp32, times its scale): fp32 queries, and
 // pages or blocks that are not of whole groups of 8 tokens. Its 64 keys a tile cost the same arithmetic whatever they
 // were held in, so it is bound as above, or, with few rows, by the keys' way through registers and shared memory: 32 / 8
-// heads of 128, 64 decodes of 2048 keys 385 us in fp32 and 416 in bf16 over pages of 6, 4 x 512 tokens 332
-// and 333 (the kernels for bf16 over pages of 16: 71 and 49).
+// heads of 128, 64 decodes of 2048 keys 396 us in fp32 and 409 in bf16 over pages of 6, 4 x 512 tokens 340
+// and 341 (the kernels for bf16 over pages of 16: 57 and 43).
 template <typename T, int R, int D, bool QUANT>
 __global__ void __launch_bounds__(kSimtThreads, 2) chunk_simt_kernel(const ChunkParams p) {
   constexpr int RT = R / 16, LD = D + 4, LP = R + 4, CT = D / 64;  // CT: float4 columns of a thread

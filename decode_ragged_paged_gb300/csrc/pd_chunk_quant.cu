@@ -24,11 +24,12 @@
 // 1, 3 and 7 those with V; 8-11 and 12-15 are the groups; 16-19 split q and convert V. A tile's factors are kept for
 // 32 tiles, as the softmax reads them after K's slot is free.
 //
-// Bound (D 128, 152 SMs): tiles of 64 keys are what fits tensor memory twice beside two outputs, and so the
-// products read 32 KB of q for 16 of K. With V's way through the converters a pair of tiles moves about 170 KB through
-// shared memory, some 1300 cycles at 128 bytes each; 1640 are taken, 8 % of the whole by raised maxima where scales
-// differ much. 4 x 2048 tokens over 14000 to 16384 keys: 1360 us, 70 % of the dense bf16 rate (pd_attn_chunk over bf16
-// pages: 1015 to 1090); 500 tokens over 32700 keys 227 us (184). Without the exponentials neither gets shorter. With
+// Bound (D 128, 152 SMs): the softmax warps. A pair of tiles (64 keys, two query tiles) is 1024 cycles of products, half of
+// them e4m3's, and the tensor cores are busy in 55 % of the cycles (over bf16, pd_chunk_tc.cu: 77 %); shared memory's
+// banks are read in 28 % of them and written in 7 (there 36 and 9). The scales and V's conversion make it 127
+// million instructions for 90 (500 tokens over 32700 keys), and warps wait longest for loads, of tensor memory above all.
+// That case takes 228 to 230 us (over bf16 184), without the softmax 172; 4 x 2048 tokens over 14000 to 16384 keys 1355 to 1385
+// (1140 to 1177), 69 % of the dense bf16 rate, 8 % of it raised maxima where scales differ much. With
 // one query tile (32 requests of 2 to 8 tokens: 51 us, bf16 55) a tile of keys takes 0.5 us, 5.0 TB/s, and an
 // item's ends 4.5: the last product, both groups' outputs joined, and the first tile's own maximum, each
 // after the other (152 x 4 tokens over 1024 keys 114 us, 38 over 4096, as many keys, 87).

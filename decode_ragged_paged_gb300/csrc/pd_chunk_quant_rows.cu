@@ -22,8 +22,8 @@
 //
 // 128 requests of 512 to 4096 keys, 32 query and 8 KV heads of 128: 104 us, 5.4 TB/s; the cache's bytes take 84 at the
 // copy rate. What holds it is each warp's chain from a key's bytes to its weights, at 2 warps a scheduler of 232
-// registers (1.6 instructions a cycle and SM; 28 % of the stalls wait for the instruction before, 22 % for what an item's
-// start reads). One half a turn and 12 warps took 132; a page's id looked at in the turn that reads it 116 for 109; one CTA
+// registers (1.6 instructions a cycle and SM; 27 % of the stalls wait for the instruction before, 24 % for global memory, what
+// an item's start reads above all). One half a turn and 12 warps took 132; a page's id looked at in the turn that reads it 116 for 109; one CTA
 // of 8 warps 109 for 104, of 6 and 7 128 and 119 for 117; three turns in the ring 105; the next item looked up while one is
 // worked off 104. D 64 fits three CTAs: 78 us with two of them, 68 with three (103 where the SMs had kept
 // less shared memory from the kernel before). (With the rows as the 16 of the products, half of them empty, a turn took twice the
